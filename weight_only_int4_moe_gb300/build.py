@@ -1,7 +1,7 @@
 """Build the CUDA library (``_build/libmoe_int4.so``) with nvcc for sm_103a.
 
 Each translation unit is compiled in parallel, then linked into one shared
-library exporting the C ABI of ``include/moe_int4.h``.  No CMake; nvcc only.
+library exporting the C ABI of ``include/moe_int4.h`` and ``include/moe_kv4.h``.  No CMake; nvcc only.
 
 ``build(debug_bounds=True)`` builds a second copy with ``-DMOE_DEBUG_BOUNDS``
 (``_build/debug_bounds/libmoe_int4.so``): the kernels check the indices they read
@@ -23,8 +23,9 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libmoe_int4.so")
 DEBUG_BUILD = os.path.join(BUILD, "debug_bounds")
 DEBUG_LIB = os.path.join(DEBUG_BUILD, "libmoe_int4.so")
-SOURCES = ["abi.cu", "align.cu", "pack.cu", "gemm.cu", "noalloc.cu", "ep.cu", "gemv.cu"]
-HEADERS = ["common.cuh", "kernels.cuh", "dequant.cuh", "gemv.cuh"]
+SOURCES = ["abi.cu", "align.cu", "pack.cu", "gemm.cu", "noalloc.cu", "ep.cu", "gemv.cu",
+           "kv4_abi.cu", "kv4_append.cu", "kv4_attn.cu", "kv4_pages.cu"]
+HEADERS = ["common.cuh", "kernels.cuh", "dequant.cuh", "gemv.cuh", "kv4.cuh", "kv4_launch.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
               "--expt-relaxed-constexpr", "-I" + os.path.join(ROOT, "include")]
@@ -39,7 +40,7 @@ def nvcc() -> str:
 
 def _inputs():
     files = [os.path.join(CSRC, f) for f in SOURCES + HEADERS]
-    files.append(os.path.join(ROOT, "include", "moe_int4.h"))
+    files += [os.path.join(ROOT, "include", f) for f in ("moe_int4.h", "moe_kv4.h")]
     return files
 
 

@@ -1,0 +1,85 @@
+// Shared by the kernels of the 4-bit paged key/value cache (kv4_*.cu): the
+// pool's geometry, the lookup of a token's request and page, and the code and
+// scale arithmetic of include/moe_kv4.h.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "common.cuh"
+#include "moe_kv4.h"
+
+namespace moe {
+
+constexpr float kKvScaleMin = 6.103515625e-05f;  // 2^-14
+constexpr float kKvScaleMax = 2720.0f;           // largest bf16 whose 24-fold fp16 holds
+constexpr float kKvSeventh = 1.0f / 7.0f;
+constexpr float kKvMax = 7.0f * kKvScaleMax;     // 19040
+
+// One layer of the pool.
+struct KvPool {
+    uint8_t *base;       // the layer's first page
+    int n_pages, hkv, ps;
+    uint32_t block;      // bytes of a block: ps * (D + D / 8)
+};
+
+struct KvBatch {
+    const int32_t *cu_q, *kv_len, *tables;
+    int requests, tokens, stride;
+};
+
+MOE_DEV void kv_report(uint32_t *err, uint32_t flag) {
+    if (err) {
+        atomicOr(err, flag);
+        atomicAdd(err + 1, 1u);
+    }
+}
+
+// The request that token t belongs to: the last b with cu_q[b] <= t.  A decode
+// batch has one token a request, so b = t is tried first.
+MOE_DEV int kv_request_of(const int32_t *cu_q, int requests, int t) {
+    const int guess = min(t, requests - 1);
+    if (cu_q[guess] <= t && t < cu_q[guess + 1]) return guess;
+    int lo = 0, hi = requests - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (cu_q[mid] <= t)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    return lo;
+}
+
+// The page of token j of a sequence, or -1 (and a report) where its table has
+// none.
+MOE_DEV int kv_page_of(const KvBatch &b, const KvPool &p, int request, int j, uint32_t *err) {
+    const int e = j / p.ps;
+    int page = -1;
+    if (e < b.stride) page = b.tables[(size_t)request * b.stride + e];
+    if ((unsigned)page >= (unsigned)p.n_pages) {
+        kv_report(err, MOE_KV4_DEVERR_PAGE);
+        return -1;
+    }
+    return page;
+}
+
+MOE_DEV uint8_t *kv_block(const KvPool &p, int page, int head) {
+    return p.base + ((size_t)page * p.hkv + head) * p.block;
+}
+
+// The scale of a group: bf16(amax / 7) in [2^-14, 2720] (also for amax = 0).
+MOE_DEV float kv_scale(float amax) {
+    const float s = __bfloat162float(__float2bfloat16_rn(__fmul_rn(amax, kKvSeventh)));
+    return fminf(fmaxf(s, kKvScaleMin), kKvScaleMax);
+}
+
+// rint(x / s) limited to -8..7, plus 8; the quotient is the IEEE one.
+MOE_DEV uint32_t kv_code(float x, float s) {
+    const float r = rintf(__fdiv_rn(x, s));
+    return (uint32_t)(int)(fminf(fmaxf(r, -8.0f), 7.0f) + 8.0f);
+}
+
+}  // namespace moe

@@ -1,0 +1,66 @@
+// Arguments and launchers of the cache kernels, between kv4_abi.cu and the
+// kernels' files.
+#pragma once
+
+#include "kernels.cuh"
+#include "kv4.cuh"
+
+namespace moe {
+
+struct KvAppendArgs {
+    const uint16_t *q, *k, *v;
+    int64_t q_stride, k_stride, v_stride;
+    const uint16_t *q_weight, *k_weight;
+    const float *cos, *sin;
+    const int32_t *positions;
+    float eps;
+    int max_pos, interleaved, q_heads;
+    uint16_t *q_out;
+    KvPool pool;
+    KvBatch batch;
+    uint32_t *err;
+};
+
+struct KvReadArgs {
+    KvPool pool;
+    KvBatch batch;
+    uint16_t *k_out, *v_out;
+    uint32_t *err;
+};
+
+struct KvAttnArgs {
+    const uint16_t *q;
+    int64_t q_stride;
+    KvPool pool;
+    KvBatch batch;
+    const uint64_t *tree;
+    uint16_t *out;
+    float *lse;
+    float scale_log2;  // scale * log2(e)
+    int q_heads, group, window;
+    uint32_t *err;
+};
+
+// The pool for page management (all layers).
+struct KvPages {
+    uint8_t *pages;
+    int layers, n_pages, hkv, D, ps;
+    uint32_t block;
+};
+
+cudaError_t launch_kv4_append(const KvAppendArgs &a, int D, cudaStream_t s);
+cudaError_t launch_kv4_read(const KvReadArgs &a, int D, cudaStream_t s);
+cudaError_t launch_kv4_attn(const KvAttnArgs &a, int D, cudaStream_t s);
+// new_lens null: fork (one page for each parent with a begun page), else reserve.
+cudaError_t launch_kv4_take(const KvPages &p, const moe_kv4_seqs &q, const int32_t *a,
+                            const int32_t *b, bool fork, int n, void *scratch, uint32_t *err,
+                            int sms, cudaStream_t s);
+cudaError_t launch_kv4_free(const KvPages &p, const moe_kv4_seqs &q, const int32_t *ids, int n,
+                            uint32_t *err, int sms, cudaStream_t s);
+cudaError_t launch_kv4_compact(const KvPages &p, const moe_kv4_seqs &q, int32_t *tables_out,
+                               int32_t *refs_out, int32_t *n_used, void *scratch, uint32_t *err,
+                               int sms, cudaStream_t s);
+cudaError_t launch_kv4_copy(const KvPages &p, const int32_t *src, const int32_t *dst, int n,
+                            uint32_t *err, int sms, cudaStream_t s);
+
+}  // namespace moe
