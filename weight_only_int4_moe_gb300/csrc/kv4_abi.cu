@@ -183,7 +183,7 @@ size_t moe_kv4_workspace_bytes(const moe_kv4_shape *shape, int q_heads) {
     if (!shape || !shape_ok(shape) || q_heads < 1 || q_heads % shape->kv_heads ||
         q_heads / shape->kv_heads > 64)
         return 0;
-    return MOE_KV4_WS_HEADER;
+    return MOE_KV4_WS_HEADER + kv4_decode_slot_bytes(shape->head_dim, kKvMaxCtas);
 }
 
 int moe_kv4_attention(const uint16_t *q, int64_t q_stride, int q_heads, const void *pages,
@@ -218,8 +218,16 @@ int moe_kv4_attention(const uint16_t *q, int64_t q_stride, int q_heads, const vo
     a.q_heads = q_heads;
     a.group = q_heads / shape->kv_heads;
     a.window = window;
-    a.err = reinterpret_cast<uint32_t *>(workspace);
-    return done(launch_kv4_attn(a, shape->head_dim, str(stream)));
+    uint8_t *ws = reinterpret_cast<uint8_t *>(workspace);
+    a.err = reinterpret_cast<uint32_t *>(ws);
+    a.counters = reinterpret_cast<int32_t *>(ws + kKvCounterByte);
+    a.max_kv = batch->max_kv;
+    a.rows_lo = 1;
+    a.rows_hi = INT32_MAX;
+    const long long rows = (long long)batch->max_q * a.group;
+    return done(launch_kv4_decode(a, shape->head_dim, rows > INT32_MAX ? INT32_MAX : (int)rows,
+                                  ws + MOE_KV4_WS_HEADER, sms < kKvMaxCtas ? sms : kKvMaxCtas,
+                                  str(stream)));
 }
 
 size_t moe_kv4_scratch_bytes(const moe_kv4_shape *shape, int n) {

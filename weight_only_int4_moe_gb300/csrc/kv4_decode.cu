@@ -1,0 +1,704 @@
+// Attention over the 4-bit cache for few query rows (include/moe_kv4.h): decode
+// and small verify batches, where the cache's bytes are the bound.
+//
+// The query rows that share a kv head (its group's heads of all new tokens) are
+// taken 8 NT at a time against tiles of 64 tokens.  The transposed products put
+// tokens, then head dimensions, on the 16-high side of mma.m16n8k16 and the few
+// rows on its 8-wide side, so that no instruction works on padding:
+//   S^T[token, row] = K Q^T        O^T[dim, row] = V^T P^T
+// The column of an accumulator is a row of the query in both, so the running
+// maximum and the rescaling need no exchange between the two products.
+//
+// Codes become operands without leaving the lane that loads them.  A K word holds
+// eight dimensions of one group for one token: masked and ORed with an fp16
+// exponent they are four operand registers.  With one row tile the group's scale
+// multiplies the group's fp32 partial score (four FMAs per 16 tokens and group
+// instead of eight fp16 ones), the operands are 64 + q and the accumulator starts
+// at -72 sum(q); with two the operands are (q - 8) scale, exact in fp16, as for the
+// expert weights.  V pieces of two tokens are interleaved by one byte permute into
+// (token, token + 1) pairs and take their two scales by the same exact FMA.
+//
+// Work is cut by tokens: all (request, row tile, kv head) items' tiles in one
+// list, every CTA an equal run of it, every warp of the CTA an equal part of the
+// run with a ring of tiles of its own, filled by bulk copies (a tile of a page
+// size of 64 is one contiguous block).  Warps of a CTA join their parts of an item
+// through shared memory, CTAs through the workspace, the last one to arrive adding
+// them up in list order.
+#include "kv4_launch.cuh"
+#include "dequant.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int kTile = 64;       // tokens of a unit of work
+constexpr int kChunks = 1024;   // entries of the prefix table over requests
+
+template <int D, int NT>
+struct Cfg {
+    static constexpr int NG = D / 32;
+    static constexpr int kTileBytes = kTile * (D + D / 8);
+    static constexpr int kStages = D == 128 ? 2 : 3;
+    static constexpr int kWarps = NT == 1 ? 12 : 8;
+    static constexpr int kRows = 8 * NT;
+    static constexpr int kPitch = D + 4;                   // floats of a partial's row
+    static constexpr int kSlot = kRows * kPitch;           // D sums, then m and l
+    static constexpr int kRing = kStages * kTileBytes;
+    static constexpr int kSmem = kWarps * kRing;
+    static_assert(kSlot * 4 <= kRing, "a warp's last partial reuses its ring");
+};
+
+struct Meta {        // where a warp's partial belongs
+    uint32_t u0, u1; // the item's units; u0 == u1: none
+    int b, h, r;
+};
+
+MOE_DEV void bulk_copy(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+            dst),
+        "l"(src), "r"(bytes), "r"(bar)
+        : "memory");
+}
+
+MOE_DEV void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                      uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+MOE_DEV uint32_t transpose8x8(uint32_t v) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+
+MOE_DEV float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+template <int N>
+MOE_DEV void lds_words(uint32_t addr, uint32_t (&w)[N]) {
+    if constexpr (N == 4) {
+        const uint4 v = lds128(addr);
+        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+    } else if constexpr (N == 2) {
+        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr) : "memory");
+    } else {
+        w[0] = lds32(addr);
+    }
+}
+
+// The four nibble pairs of a word as fp16 pairs 64 + q.
+MOE_DEV void codes64(uint32_t w, uint32_t (&x)[4]) {
+    x[0] = ((w << 4) & 0x00F000F0u) | 0x54005400u;
+    x[1] = (w & 0x00F000F0u) | 0x54005400u;
+    x[2] = ((w >> 4) & 0x00F000F0u) | 0x54005400u;
+    x[3] = ((w >> 8) & 0x00F000F0u) | 0x54005400u;
+}
+
+// The same as (q - 8) * s, exact: (16 + q) * s - 24 * s.
+MOE_DEV void codes_scaled(uint32_t w, uint32_t s, uint32_t m24s, uint32_t (&x)[4]) {
+    const uint32_t t[4] = {w << 6, w << 2, w >> 2, w >> 6};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        x[i] = as_u32(__hfma2(as_h2((t[i] & 0x03C003C0u) | 0x4C004C00u), as_h2(s), as_h2(m24s)));
+}
+
+MOE_DEV uint32_t times_m24(uint32_t s) { return as_u32(__hmul2(as_h2(s), as_h2(0xCE00CE00u))); }
+
+// What a request adds to the list of units.
+struct Request {
+    int q0, m, first, end, tile0, tiles, row_tiles;
+};
+
+MOE_DEV Request request_of(const KvAttnArgs &a, int b, int rows) {
+    Request r;
+    r.q0 = a.batch.cu_q[b];
+    r.m = a.batch.cu_q[b + 1] - r.q0;
+    const int len = a.batch.kv_len[b];
+    r.first = len - r.m;
+    r.end = (int)min((long long)len, (long long)a.batch.stride * a.pool.ps);
+    const int start = a.window > 0 ? max(0, r.first - a.window + 1) : 0;
+    r.tile0 = start / kTile;
+    r.tiles = max(1, (r.end + kTile - 1) / kTile - r.tile0);
+    const bool mine = r.m > 0 && r.m * a.group >= a.rows_lo && r.m * a.group <= a.rows_hi;
+    r.row_tiles = mine ? (r.m * a.group + rows - 1) / rows : 0;
+    return r;
+}
+
+MOE_DEV uint32_t units_of(const Request &r, int hkv) {
+    return (uint32_t)r.tiles * (uint32_t)r.row_tiles * (uint32_t)hkv;
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
+    kv4_decode_kernel(const KvAttnArgs a) {
+    using C = Cfg<D, NT>;
+    constexpr int NG = C::NG, W = C::kWarps, S = C::kStages, RB = D / 2;
+    extern __shared__ __align__(128) uint8_t ring[];
+    __shared__ uint32_t prefix[kChunks + 1];
+    __shared__ uint64_t bars[W * S];
+    __shared__ Meta meta[2 * W];
+    __shared__ int run_of[2 * W + 1], n_runs, abort_flag, last_of;
+    __shared__ uint32_t warp_tot[W];
+    pdl_wait();
+    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, g = lane >> 2, t = lane & 3;
+    const int hkv = a.pool.hkv, ps = a.pool.ps, G = a.group;
+    const float sl2 = fmaxf(fabsf(a.scale_log2), 1e-30f);
+    if (tid == 0) abort_flag = 0;
+    if (lane == 0)
+        for (int s = 0; s < S; ++s) mbar_init(smem_u32(&bars[w * S + s]), 1);
+    mbar_fence_init();
+    if (lane < 2) meta[2 * w + lane].u0 = meta[2 * w + lane].u1 = 0;
+
+    // prefix of units over chunks of requests, two or three chunks a thread
+    const int per_chunk = (a.batch.requests + kChunks - 1) / kChunks;
+    const int chunks = (a.batch.requests + per_chunk - 1) / per_chunk;
+    uint32_t carry = 0;
+    for (int c0 = 0; c0 < chunks; c0 += W * 32) {
+        uint32_t n = 0;
+        if (c0 + tid < chunks)
+            for (int b = (c0 + tid) * per_chunk; b < min(a.batch.requests, (c0 + tid + 1) * per_chunk); ++b) {
+                const Request r = request_of(a, b, C::kRows);
+                n += units_of(r, hkv);
+                if (blockIdx.x == 0 && r.row_tiles && r.end < r.first + r.m)
+                    kv_report(a.err, MOE_KV4_DEVERR_PAGE);  // beyond its table
+            }
+        uint32_t x = n;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const uint32_t y = __shfl_up_sync(0xffffffffu, x, d);
+            if (lane >= d) x += y;
+        }
+        if (lane == 31) warp_tot[w] = x;
+        __syncthreads();
+        uint32_t before = carry, all = carry;
+        for (int i = 0; i < W; ++i) {
+            if (i < w) before += warp_tot[i];
+            all += warp_tot[i];
+        }
+        if (c0 + tid < chunks) prefix[c0 + tid] = before + x - n;
+        carry = all;
+        __syncthreads();
+    }
+    if (tid == 0) prefix[chunks] = carry;
+    __syncthreads();
+    const uint32_t total = carry;
+    const uint32_t per = max((uint32_t)a.min_units, (total + gridDim.x - 1) / gridDim.x);
+    const uint32_t c_lo = min(total, blockIdx.x * per), c_hi = min(total, c_lo + per);
+    if (c_lo >= c_hi) return;
+    uint32_t u = c_lo + (uint32_t)((unsigned long long)(c_hi - c_lo) * w / W);
+    const uint32_t u_end = c_lo + (uint32_t)((unsigned long long)(c_hi - c_lo) * (w + 1) / W);
+
+    const uint32_t my_ring = smem_u32(ring) + w * C::kRing;
+    const uint32_t my_bar = smem_u32(&bars[w * S]);
+    Ring cons(S);
+    const int tau = (g & 1) ? 4 + ((g >> 1) ^ 1) : g >> 1;  // token of accumulator row g
+    float *warp_slot = a.warp_slots + ((size_t)blockIdx.x * W + w) * C::kSlot;
+
+    // the request that holds unit u
+    int b = 0;
+    uint32_t b_u0 = 0;
+    if (u < u_end) {
+        int lo = 0, hi = chunks - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (prefix[mid] <= u)
+                lo = mid;
+            else
+                hi = mid - 1;
+        }
+        b = lo * per_chunk;
+        b_u0 = prefix[lo];
+    }
+    bool aborted = false;
+    while (u < u_end && !aborted) {
+        Request rq = request_of(a, b, C::kRows);
+        uint32_t n_b = units_of(rq, hkv);
+        while (u >= b_u0 + n_b) {
+            b_u0 += n_b;
+            rq = request_of(a, ++b, C::kRows);
+            n_b = units_of(rq, hkv);
+        }
+        const uint32_t item = (u - b_u0) / rq.tiles;
+        const uint32_t i_u0 = b_u0 + item * rq.tiles, i_u1 = i_u0 + rq.tiles;
+        const int h = item % hkv, rt = item / hkv;
+        const uint32_t seg_end = min(u_end, i_u1);
+        const int tile_lo = rq.tile0 + (int)(u - i_u0), n_tiles = (int)(seg_end - u);
+        const int row0 = rt * C::kRows, rows = min(C::kRows, rq.m * G - row0);
+        const int32_t *table = a.batch.tables + (size_t)b * a.batch.stride;
+        const int ppt = kTile / ps;  // pages of a tile
+
+        // page ids of the next tiles: lane l holds table entry e_base + l
+        int e_base = tile_lo * ppt, ids = -1;
+        auto load_ids = [&](int from) {
+            e_base = from;
+            const int e = from + lane;
+            ids = -1;
+            if (e < (tile_lo + n_tiles) * ppt && (long long)e * ps < rq.end) {
+                ids = table[e];
+                if ((unsigned)ids >= (unsigned)a.pool.n_pages) {
+                    ids = -1;
+                    if (h == 0 && rt == 0) kv_report(a.err, MOE_KV4_DEVERR_PAGE);
+                }
+            }
+        };
+        load_ids(e_base);
+        // starts the copies of the segment's k-th tile; returns which of its four
+        // runs of 16 tokens have a page
+        auto fetch = [&](int k, uint32_t slot) -> uint32_t {
+            const int e = (tile_lo + k) * ppt;
+            if (e + ppt > e_base + 32) load_ids(e);
+            uint32_t ok = 0, bytes = 0;
+            for (int i = 0; i < ppt; ++i) {
+                const int id = __shfl_sync(0xffffffffu, ids, e - e_base + i);
+                if (id >= 0) {
+                    ok |= ((1u << (ps / 16)) - 1u) << (i * (ps / 16));
+                    bytes += a.pool.block;
+                }
+            }
+            if (lane == 0) mbar_arrive_expect_tx(my_bar + 8 * slot, bytes);
+            __syncwarp();
+            const int id = __shfl_sync(0xffffffffu, ids, min(31, e - e_base + lane));
+            if (lane < ppt && id >= 0)
+                bulk_copy(my_ring + slot * C::kTileBytes + lane * a.pool.block,
+                          kv_block(a.pool, id, h), a.pool.block, my_bar + 8 * slot);
+            return ok;
+        };
+        uint32_t ok_ring = 0;  // four bits a stage
+        const int ahead = min(S, n_tiles);
+        {
+            uint32_t slot = cons.idx;
+            for (int k = 0; k < ahead; ++k) {
+                ok_ring = (ok_ring & ~(15u << (4 * slot))) | fetch(k, slot) << (4 * slot);
+                if (++slot == S) slot = 0;
+            }
+        }
+
+        // the query rows as B operands: lane (g, t) holds dimensions 32G + 8t.. of row g
+        uint32_t q[NT][NG][4];
+        float bias[NT == 1 ? NG : 1][2];
+        bool bad = false;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int r = 8 * n + g;
+            const int i = (row0 + r) / G, hh = (row0 + r) - i * G;
+            const uint16_t *src = a.q + (size_t)(rq.q0 + i) * a.q_stride + (size_t)(h * G + hh) * D + 8 * t;
+#pragma unroll
+            for (int G4 = 0; G4 < NG; ++G4) {
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (r < rows) v = *reinterpret_cast<const uint4 *>(src + 32 * G4);
+                v = bf16x8_to_f16x8_sat(v, bad);
+                const uint32_t flip = a.scale_log2 < 0.0f ? 0x80008000u : 0u;
+                q[n][G4][0] = v.x ^ flip;
+                q[n][G4][1] = v.y ^ flip;
+                q[n][G4][2] = v.z ^ flip;
+                q[n][G4][3] = v.w ^ flip;
+                if (NT == 1) {
+                    float s = 0.0f;
+#pragma unroll
+                    for (int i4 = 0; i4 < 4; ++i4) {
+                        const float2 f = __half22float2(as_h2(q[n][G4][i4]));
+                        s += f.x + f.y;
+                    }
+                    s += __shfl_xor_sync(0xffffffffu, s, 1);
+                    s += __shfl_xor_sync(0xffffffffu, s, 2);
+                    bias[NT == 1 ? G4 : 0][0] = -72.0f * __shfl_sync(0xffffffffu, s, 8 * t);
+                    bias[NT == 1 ? G4 : 0][1] = -72.0f * __shfl_sync(0xffffffffu, s, 8 * t + 4);
+                }
+            }
+        }
+        if (__any_sync(0xffffffffu, bad) && lane == 0) kv_report(a.err, MOE_KV4_DEVERR_RANGE);
+
+        // tokens that every row sees: below `open`, and from `shut` on
+        const int i_lo = row0 / G, i_hi = (row0 + rows - 1) / G;
+        const int open = min(rq.end, a.tree ? rq.first : rq.first + i_lo + 1);
+        const int shut = a.window > 0 ? rq.first + i_hi - a.window + 1 : 0;
+
+        float m[NT][2], l[NT][2], acc[NG][2][NT][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) m[n][0] = m[n][1] = -INFINITY, l[n][0] = l[n][1] = 0.0f;
+#pragma unroll
+        for (int x = 0; x < NG * 2 * NT * 4; ++x) (&acc[0][0][0][0])[x] = 0.0f;
+
+        for (int k = 0; k < n_tiles; ++k) {
+            const uint32_t slot = cons.idx;
+            if (__any_sync(0xffffffffu, !mbar_wait(my_bar + 8 * slot, cons.ph, &abort_flag, a.err))) {
+                aborted = true;
+                break;
+            }
+            const uint32_t sb = my_ring + slot * C::kTileBytes;
+            const uint32_t ok = (ok_ring >> (4 * slot)) & 15u;
+            const int j0 = (tile_lo + k) * kTile;
+            const bool full = ok == 15u && j0 + kTile <= open && j0 >= shut;
+            // a run of 16 tokens: its block and its first row there
+            auto place = [&](int s, uint32_t &base, uint32_t &row) {
+                const int tok = 16 * s;
+                base = sb + (uint32_t)(tok / ps) * a.pool.block;
+                row = tok & (ps - 1);
+            };
+
+            float x[4][NT][4];
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                uint32_t base, row;
+                place(s, base, row);
+                const uint32_t kr = base + (row + tau) * RB + t * (NG * 4);
+                const uint32_t sc = base + ps * D + (row + tau) * (NG * 2);
+                uint32_t wa[NG], wb[NG], za[NG / 2], zb[NG / 2];
+                lds_words(kr, wa);
+                lds_words(kr + 8 * RB, wb);
+                lds_words(sc, za);
+                lds_words(sc + 8 * NG * 2, zb);
+                if (NT == 1) {
+#pragma unroll
+                    for (int G4 = 0; G4 < NG; ++G4) {
+                        uint32_t ca[4], cb[4];
+                        codes64(wa[G4], ca);
+                        codes64(wb[G4], cb);
+                        float c[4] = {bias[NT == 1 ? G4 : 0][0], bias[NT == 1 ? G4 : 0][1],
+                                      bias[NT == 1 ? G4 : 0][0], bias[NT == 1 ? G4 : 0][1]};
+                        mma16816(c, ca[0], cb[0], ca[1], cb[1], q[0][G4][0], q[0][G4][1]);
+                        mma16816(c, ca[2], cb[2], ca[3], cb[3], q[0][G4][2], q[0][G4][3]);
+                        const float2 fa = __half22float2(as_h2(za[G4 / 2]));
+                        const float2 fb = __half22float2(as_h2(zb[G4 / 2]));
+                        const float ya = G4 & 1 ? fa.y : fa.x, yb = G4 & 1 ? fb.y : fb.x;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float y = i < 2 ? ya : yb;
+                            x[s][0][i] = G4 ? fmaf(c[i], y, x[s][0][i]) : c[i] * y;
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) x[s][n][i] = 0.0f;
+#pragma unroll
+                    for (int G4 = 0; G4 < NG; ++G4) {
+                        const uint32_t ya = __byte_perm(za[G4 / 2], 0, G4 & 1 ? 0x3232 : 0x1010);
+                        const uint32_t yb = __byte_perm(zb[G4 / 2], 0, G4 & 1 ? 0x3232 : 0x1010);
+                        uint32_t ca[4], cb[4];
+                        codes_scaled(wa[G4], ya, times_m24(ya), ca);
+                        codes_scaled(wb[G4], yb, times_m24(yb), cb);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            mma16816(x[s][n], ca[0], cb[0], ca[1], cb[1], q[n][G4][0], q[n][G4][1]);
+                            mma16816(x[s][n], ca[2], cb[2], ca[3], cb[3], q[n][G4][2], q[n][G4][3]);
+                        }
+                    }
+                }
+            }
+            if (!full) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int r = 8 * n + 2 * t + e, i = (row0 + r) / G, p = rq.first + i;
+                        const int hi = r < rows ? min(p, rq.end - 1) : -1;
+                        const int lo = a.window > 0 ? p - a.window : -1;
+                        uint64_t word = 0;
+                        if (a.tree && r < rows) word = a.tree[rq.q0 + i];
+#pragma unroll
+                        for (int s = 0; s < 4; ++s)
+#pragma unroll
+                            for (int f = 0; f < 2; ++f) {
+                                const int j = j0 + 16 * s + 8 * f + tau;
+                                bool see = j <= hi && j > lo && ((ok >> s) & 1u);
+                                if (a.tree && j >= rq.first)
+                                    see = see && j - rq.first < 64 && ((word >> (j - rq.first)) & 1u);
+                                if (!see) x[s][n][2 * f + e] = -INFINITY;
+                            }
+                    }
+            }
+            // running maximum and sum of each row (a column here: over the lanes g)
+            uint32_t pb[4][NT][2];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                float top[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float v = fmaxf(x[0][n][e], x[0][n][2 + e]);
+#pragma unroll
+                    for (int s = 1; s < 4; ++s) v = fmaxf(v, fmaxf(x[s][n][e], x[s][n][2 + e]));
+                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+                    top[e] = fmaxf(v, m[n][e]);
+                }
+                if (__any_sync(0xffffffffu, top[0] > m[n][0] || top[1] > m[n][1])) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float r = top[e] > m[n][e] ? ex2((m[n][e] - top[e]) * sl2) : 1.0f;
+                        m[n][e] = top[e];
+                        l[n][e] *= r;
+#pragma unroll
+                        for (int G4 = 0; G4 < NG; ++G4)
+#pragma unroll
+                            for (int v = 0; v < 2; ++v) acc[G4][v][n][e] *= r, acc[G4][v][n][2 + e] *= r;
+                    }
+                }
+                const float o0 = m[n][0] == -INFINITY ? 0.0f : -m[n][0] * sl2;
+                const float o1 = m[n][1] == -INFINITY ? 0.0f : -m[n][1] * sl2;
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                    float p[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) p[i] = ex2(fmaf(x[s][n][i], sl2, i & 1 ? o1 : o0));
+                    l[n][0] += p[0] + p[2];
+                    l[n][1] += p[1] + p[3];
+                    pb[s][n][0] = transpose8x8(as_u32(__floats2half2_rn(p[0], p[1])));
+                    pb[s][n][1] = transpose8x8(as_u32(__floats2half2_rn(p[2], p[3])));
+                }
+            }
+            // O^T += V^T P^T: lane (g, t) loads tokens t, 4 + (t ^ 1) and eight on
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                uint32_t base, row;
+                place(s, base, row);
+                const uint32_t vr = base + ps * RB + row * RB + g * (NG * 2);
+                const uint32_t sc = base + ps * D + ps * (NG * 2) + row * (NG * 2);
+                const int tok[4] = {t, 4 + (t ^ 1), 8 + t, 12 + (t ^ 1)};
+                uint32_t vw[4][NG / 2], z[4][NG / 2];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    lds_words(vr + tok[i] * RB, vw[i]);
+                    lds_words(sc + tok[i] * (NG * 2), z[i]);
+                }
+                if (!full) {
+                    // slots past the sequence (or without a page) hold anything
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (j0 + 16 * s + tok[i] >= rq.end || !((ok >> s) & 1u)) {
+#pragma unroll
+                            for (int c = 0; c < NG / 2; ++c) z[i][c] = 0;
+                        }
+                }
+#pragma unroll
+                for (int G4 = 0; G4 < NG; ++G4) {
+                    const uint32_t sel = G4 & 1 ? 0x7632 : 0x5410;
+                    const uint32_t s0 = __byte_perm(z[0][G4 / 2], z[1][G4 / 2], sel);
+                    const uint32_t s1 = __byte_perm(z[2][G4 / 2], z[3][G4 / 2], sel);
+                    uint32_t va[4], vb[4];
+                    codes_scaled(__byte_perm(vw[0][G4 / 2], vw[1][G4 / 2], sel), s0, times_m24(s0), va);
+                    codes_scaled(__byte_perm(vw[2][G4 / 2], vw[3][G4 / 2], sel), s1, times_m24(s1), vb);
+#pragma unroll
+                    for (int v = 0; v < 2; ++v)
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+                            mma16816(acc[G4][v][n], va[2 * v], va[2 * v + 1], vb[2 * v], vb[2 * v + 1],
+                                     pb[s][n][0], pb[s][n][1]);
+                }
+            }
+            __syncwarp();
+            if (k + S < n_tiles)
+                ok_ring = (ok_ring & ~(15u << (4 * slot))) | fetch(k + S, slot) << (4 * slot);
+            cons.next();
+        }
+
+        // the segment's result
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 4);
+                l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 8);
+                l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 16);
+            }
+        const bool whole = u == i_u0 && seg_end == i_u1;
+        u = seg_end;
+        const bool last_seg = u >= u_end;
+        if (whole) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int r = 8 * n + 2 * t + e;
+                    if (r >= rows) continue;
+                    const int i = (row0 + r) / G, hh = (row0 + r) - i * G;
+                    const size_t o = (size_t)(rq.q0 + i) * a.q_heads + h * G + hh;
+                    const float inv = l[n][e] > 0.0f ? 1.0f / l[n][e] : 0.0f;
+#pragma unroll
+                    for (int G4 = 0; G4 < NG; ++G4) {
+                        const __nv_bfloat162 lo = __floats2bfloat162_rn(acc[G4][0][n][e] * inv,
+                                                                        acc[G4][0][n][2 + e] * inv);
+                        const __nv_bfloat162 hi = __floats2bfloat162_rn(acc[G4][1][n][e] * inv,
+                                                                        acc[G4][1][n][2 + e] * inv);
+                        *reinterpret_cast<uint2 *>(a.out + o * D + 32 * G4 + 4 * g) =
+                            make_uint2(*reinterpret_cast<const uint32_t *>(&lo),
+                                       *reinterpret_cast<const uint32_t *>(&hi));
+                    }
+                    if (a.lse && g == 0)
+                        a.lse[o] = l[n][e] > 0.0f
+                                       ? (m[n][e] * sl2 + log2f(l[n][e])) * 0.6931471805599453f
+                                       : -INFINITY;
+                }
+        } else {
+            // the last segment's ring is idle and takes the partial; an earlier one's
+            // goes to the workspace
+            __syncwarp();
+            float *slot = last_seg ? reinterpret_cast<float *>(ring + w * C::kRing) : warp_slot;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float *p = slot + (8 * n + 2 * t + e) * C::kPitch;
+#pragma unroll
+                    for (int G4 = 0; G4 < NG; ++G4)
+                        *reinterpret_cast<float4 *>(p + 32 * G4 + 4 * g) =
+                            make_float4(acc[G4][0][n][e], acc[G4][0][n][2 + e], acc[G4][1][n][e],
+                                        acc[G4][1][n][2 + e]);
+                    if (g == 0) p[D] = m[n][e], p[D + 1] = l[n][e];
+                }
+            if (lane == 0) meta[2 * w + (last_seg ? 1 : 0)] = Meta{i_u0, i_u1, b, h, rt};
+        }
+    }
+    __syncthreads();
+
+    // partials of the same item are neighbours in the list of slots
+    if (tid == 0) {
+        int n = 0;
+        uint32_t prev = 0xffffffffu;
+        int end = 0;
+        for (int i = 0; i < 2 * W; ++i) {
+            if (meta[i].u0 == meta[i].u1) continue;
+            if (meta[i].u0 != prev) run_of[n++] = i, prev = meta[i].u0;
+            end = i + 1;
+        }
+        run_of[n] = end;
+        n_runs = n;
+    }
+    __syncthreads();
+    auto slot_of = [&](int i) -> const float * {
+        return i & 1 ? reinterpret_cast<const float *>(ring + (i >> 1) * C::kRing)
+                     : a.warp_slots + ((size_t)blockIdx.x * W + (i >> 1)) * C::kSlot;
+    };
+    constexpr int kQuads = D / 4, kWork = C::kRows * kQuads;
+    // one row's four dimensions, all partials of an item: sum and final result
+    auto finish = [&](const Meta &me, int row, int d4, float mm, float ll, float4 s) {
+        const int rows_b = (a.batch.cu_q[me.b + 1] - a.batch.cu_q[me.b]) * G;
+        const int rr = me.r * C::kRows + row;
+        if (rr >= rows_b) return;
+        const int i = rr / G, hh = rr - i * G;
+        const size_t o = (size_t)(a.batch.cu_q[me.b] + i) * a.q_heads + me.h * G + hh;
+        const float inv = ll > 0.0f ? 1.0f / ll : 0.0f;
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(s.x * inv, s.y * inv);
+        const __nv_bfloat162 hi = __floats2bfloat162_rn(s.z * inv, s.w * inv);
+        *reinterpret_cast<uint2 *>(a.out + o * D + 4 * d4) = make_uint2(
+            *reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
+        if (a.lse && d4 == 0)
+            a.lse[o] = ll > 0.0f ? (mm * sl2 + log2f(ll)) * 0.6931471805599453f : -INFINITY;
+    };
+    auto add = [&](const float *p, int row, int d4, float &mm, float &ll, float4 &s) {
+        const float *r = p + row * C::kPitch;
+        const float pm = r[D], pl = r[D + 1];
+        const float4 v = *reinterpret_cast<const float4 *>(r + 4 * d4);
+        const float nm = fmaxf(mm, pm);
+        const float x = mm > -INFINITY ? ex2((mm - nm) * sl2) : 0.0f;
+        const float y = pm > -INFINITY ? ex2((pm - nm) * sl2) : 0.0f;
+        mm = nm;
+        ll = ll * x + pl * y;
+        s.x = s.x * x + v.x * y;
+        s.y = s.y * x + v.y * y;
+        s.z = s.z * x + v.z * y;
+        s.w = s.w * x + v.w * y;
+    };
+    const int runs = n_runs;
+    for (int e = tid; e < runs * kWork; e += W * 32) {
+        const int run = e / kWork, row = (e / kQuads) % C::kRows, d4 = e % kQuads;
+        const Meta me = meta[run_of[run]];
+        float mm = -INFINITY, ll = 0.0f;
+        float4 s = make_float4(0, 0, 0, 0);
+        for (int i = run_of[run]; i < run_of[run + 1]; ++i)
+            if (meta[i].u0 != meta[i].u1) add(slot_of(i), row, d4, mm, ll, s);
+        if (me.u0 >= c_lo && me.u1 <= c_hi) {
+            finish(me, row, d4, mm, ll, s);
+        } else {
+            // the CTA's first item, or its last
+            float *p = a.cta_slots + ((size_t)2 * blockIdx.x + (me.u0 > c_lo ? 1 : 0)) * C::kSlot +
+                       row * C::kPitch;
+            *reinterpret_cast<float4 *>(p + 4 * d4) = s;
+            if (d4 == 0) p[D] = mm, p[D + 1] = ll;
+        }
+    }
+    __threadfence();
+    __syncthreads();
+    for (int run = 0; run < runs; ++run) {
+        const Meta me = meta[run_of[run]];
+        if (me.u0 >= c_lo && me.u1 <= c_hi) continue;
+        const uint32_t c0 = me.u0 / per, c1 = (me.u1 - 1) / per;  // CTAs of the item
+        if (tid == 0) {
+            const int old = atomicAdd(a.counters + c0, 1);
+            last_of = old == (int)(c1 - c0);
+            if (last_of) a.counters[c0] = 0;
+        }
+        __syncthreads();
+        const bool mine = last_of;
+        __syncthreads();
+        if (!mine) continue;
+        __threadfence();
+        for (int e = tid; e < kWork; e += W * 32) {
+            const int row = e / kQuads, d4 = e % kQuads;
+            float mm = -INFINITY, ll = 0.0f;
+            float4 s = make_float4(0, 0, 0, 0);
+            for (uint32_t c = c0; c <= c1; ++c)
+                add(a.cta_slots + ((size_t)2 * c + (c == c0 && me.u0 > c0 * per ? 1 : 0)) * C::kSlot, row,
+                    d4, mm, ll, s);
+            finish(me, row, d4, mm, ll, s);
+        }
+    }
+}
+
+template <int D, int NT>
+cudaError_t launch(const KvAttnArgs &a, int grid, cudaStream_t s) {
+    using C = Cfg<D, NT>;
+    static bool set[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64 || !set[dev]) {
+        e = cudaFuncSetAttribute(kv4_decode_kernel<D, NT>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+        if (e != cudaSuccess) return e;
+        if (dev >= 0 && dev < 64) set[dev] = true;
+    }
+    auto c = pdl_config((unsigned)grid, C::kWarps * 32, C::kSmem, s);
+    cudaLaunchAttribute at{};
+    c.numAttrs = pdl_attr(at);
+    c.attrs = &at;
+    return cudaLaunchKernelEx(&c, kv4_decode_kernel<D, NT>, a);
+}
+
+}  // namespace
+
+size_t kv4_decode_slot_bytes(int D, int ctas) {
+    // NT = 2 has the larger slots, NT = 1 the more warps
+    const size_t one = (size_t)8 * (D + 4) * 4;
+    return (size_t)ctas * (2 * 2 * one + (size_t)16 * one);
+}
+
+cudaError_t launch_kv4_decode(KvAttnArgs a, int D, int max_rows, void *slots, int ctas,
+                              cudaStream_t s) {
+    const int nt = max_rows <= 8 ? 1 : 2;
+    const int warps = nt == 1 ? 12 : 8;
+    const size_t slot = (size_t)8 * nt * (D + 4);
+    a.cta_slots = reinterpret_cast<float *>(slots);
+    a.warp_slots = a.cta_slots + 2 * slot * ctas;
+    a.min_units = warps;
+    // no more CTAs than the largest possible list of units fills
+    const long long tiles = (long long)(a.max_kv + kTile - 1) / kTile + 1;
+    const long long row_tiles = ((long long)max_rows + 8 * nt - 1) / (8 * nt);
+    long long most = tiles * row_tiles * a.pool.hkv * a.batch.requests;
+    most = (most + a.min_units - 1) / a.min_units;
+    const int grid = (int)(most < 1 ? 1 : most < ctas ? most : ctas);
+    if (D == 128) return nt == 1 ? launch<128, 1>(a, grid, s) : launch<128, 2>(a, grid, s);
+    return nt == 1 ? launch<64, 1>(a, grid, s) : launch<64, 2>(a, grid, s);
+}
+
+}  // namespace moe

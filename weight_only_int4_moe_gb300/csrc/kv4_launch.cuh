@@ -38,8 +38,15 @@ struct KvAttnArgs {
     float *lse;
     float scale_log2;  // scale * log2(e)
     int q_heads, group, window;
+    int rows_lo, rows_hi;  // requests of this many rows (new tokens x group) are the kernel's
+    int max_kv, min_units;
+    int32_t *counters;     // [CTAs], zero between calls
+    float *warp_slots, *cta_slots;
     uint32_t *err;
 };
+
+constexpr int kKvMaxCtas = 160;     // slots of the workspace (a GB300 has 152 SMs)
+constexpr int kKvCounterByte = 256; // the counters' place in the workspace header
 
 // The pool for page management (all layers).
 struct KvPages {
@@ -50,7 +57,10 @@ struct KvPages {
 
 cudaError_t launch_kv4_append(const KvAppendArgs &a, int D, cudaStream_t s);
 cudaError_t launch_kv4_read(const KvReadArgs &a, int D, cudaStream_t s);
-cudaError_t launch_kv4_attn(const KvAttnArgs &a, int D, cudaStream_t s);
+// Attention of the requests with few rows; max_rows bounds a request's rows.
+size_t kv4_decode_slot_bytes(int D, int ctas);
+cudaError_t launch_kv4_decode(KvAttnArgs a, int D, int max_rows, void *slots, int ctas,
+                              cudaStream_t s);
 // new_lens null: fork (one page for each parent with a begun page), else reserve.
 cudaError_t launch_kv4_take(const KvPages &p, const moe_kv4_seqs &q, const int32_t *a,
                             const int32_t *b, bool fork, int n, void *scratch, uint32_t *err,
