@@ -183,7 +183,9 @@ size_t moe_kv4_workspace_bytes(const moe_kv4_shape *shape, int q_heads) {
     if (!shape || !shape_ok(shape) || q_heads < 1 || q_heads % shape->kv_heads ||
         q_heads / shape->kv_heads > 64)
         return 0;
-    return MOE_KV4_WS_HEADER + kv4_decode_slot_bytes(shape->head_dim, kKvMaxCtas);
+    const size_t few = kv4_decode_slot_bytes(shape->head_dim, kKvMaxCtas);
+    const size_t many = kv4_prefill_slot_bytes(shape->head_dim, kKvMaxCtas);
+    return MOE_KV4_WS_HEADER + (few > many ? few : many);
 }
 
 int moe_kv4_attention(const uint16_t *q, int64_t q_stride, int q_heads, const void *pages,
@@ -222,12 +224,26 @@ int moe_kv4_attention(const uint16_t *q, int64_t q_stride, int q_heads, const vo
     a.err = reinterpret_cast<uint32_t *>(ws);
     a.counters = reinterpret_cast<int32_t *>(ws + kKvCounterByte);
     a.max_kv = batch->max_kv;
-    a.rows_lo = 1;
-    a.rows_hi = INT32_MAX;
-    const long long rows = (long long)batch->max_q * a.group;
-    return done(launch_kv4_decode(a, shape->head_dim, rows > INT32_MAX ? INT32_MAX : (int)rows,
-                                  ws + MOE_KV4_WS_HEADER, sms < kKvMaxCtas ? sms : kKvMaxCtas,
-                                  str(stream)));
+    // Requests of up to kKvFewRows rows go to the decode kernel, others to the
+    // prefill kernel; where all have the same number of new tokens one is enough.
+    const int ctas = sms < kKvMaxCtas ? sms : kKvMaxCtas;
+    uint8_t *slots = ws + MOE_KV4_WS_HEADER;
+    const long long most = (long long)batch->max_q * a.group;
+    const bool even = (long long)batch->requests * batch->max_q == batch->tokens;
+    cudaStream_t s = str(stream);
+    if (most <= kKvFewRows || !even) {
+        a.rows_lo = 1;
+        a.rows_hi = kKvFewRows;
+        const cudaError_t e = launch_kv4_decode(
+            a, shape->head_dim, most < kKvFewRows ? (int)most : kKvFewRows, slots, ctas, s);
+        if (e != cudaSuccess) return MOE_ERR_CUDA;
+    }
+    if (most > kKvFewRows) {
+        a.rows_lo = kKvFewRows + 1;
+        a.rows_hi = INT32_MAX;
+        return done(launch_kv4_prefill(a, shape->head_dim, slots, ctas, s));
+    }
+    return MOE_OK;
 }
 
 size_t moe_kv4_scratch_bytes(const moe_kv4_shape *shape, int n) {

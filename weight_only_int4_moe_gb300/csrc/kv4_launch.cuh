@@ -46,6 +46,7 @@ struct KvAttnArgs {
 };
 
 constexpr int kKvMaxCtas = 160;     // slots of the workspace (a GB300 has 152 SMs)
+constexpr int kKvFewRows = 16;      // rows of a request up to which the decode kernel takes it
 constexpr int kKvCounterByte = 256; // the counters' place in the workspace header
 
 // The pool for page management (all layers).
@@ -61,6 +62,9 @@ cudaError_t launch_kv4_read(const KvReadArgs &a, int D, cudaStream_t s);
 size_t kv4_decode_slot_bytes(int D, int ctas);
 cudaError_t launch_kv4_decode(KvAttnArgs a, int D, int max_rows, void *slots, int ctas,
                               cudaStream_t s);
+// Attention of the requests with many rows (a.rows_lo and up).
+size_t kv4_prefill_slot_bytes(int D, int ctas);
+cudaError_t launch_kv4_prefill(KvAttnArgs a, int D, void *slots, int ctas, cudaStream_t s);
 // new_lens null: fork (one page for each parent with a begun page), else reserve.
 cudaError_t launch_kv4_take(const KvPages &p, const moe_kv4_seqs &q, const int32_t *a,
                             const int32_t *b, bool fork, int n, void *scratch, uint32_t *err,

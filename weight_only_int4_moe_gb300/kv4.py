@@ -11,7 +11,6 @@ management.
 from __future__ import annotations
 
 import ctypes
-import math
 
 import torch
 
@@ -23,6 +22,7 @@ MOE_KV4_DEVERR_RANGE = 0x40
 MOE_KV4_DEVERR_NO_PAGES = 0x80
 MOE_KV4_DEVERR_SEQ = 0x100
 MOE_KV4_WS_HEADER = 8192
+MAX_REQUESTS = 65536  # of one page call
 
 EXPORTED = [
     "moe_kv4_block_bytes", "moe_kv4_pool_bytes", "moe_kv4_append", "moe_kv4_read",
@@ -94,50 +94,57 @@ class _Here:
 
 
 _HERE = _Here()
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 
 
-def _on(device):
+def _on(index):
     """Makes the device that holds a call's tensors the current one."""
-    return _HERE if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+    return _HERE if torch._C._cuda_getDevice() == index else torch.cuda.device(index)
 
 
-def _raw_stream(stream, device):
-    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+def _raw_stream(stream, index):
+    """The cudaStream_t of `stream`, or of the device's current one."""
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
 
-def _ints(t, what, device, shape=None):
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32:
+# The checks below run before every launch and are kept short: a single-token step
+# is bound by what the host does per call (a tensor's get_device() costs a third
+# of comparing its .device).
+def _ints(t, what, index, shape=None):
+    if not isinstance(t, torch.Tensor) or t.dtype is not _I32:
         raise TypeError(f"{what}: expected an int32 tensor")
-    if t.device != device or not t.is_contiguous():
-        raise ValueError(f"{what}: expected a contiguous tensor on {device}")
-    if shape is not None and tuple(t.shape) != shape:
+    if t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{what}: expected a contiguous tensor on cuda:{index}")
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{what}: expected shape {shape}, got {tuple(t.shape)}")
     return t
 
 
-def _rows(t, what, device, tokens, dim, heads=None):
+def _rows(t, what, index, tokens, dim, heads=None):
     """(pointer, token stride, heads) of bf16 [tokens, heads, dim] whose heads are
     contiguous; the tokens may be further apart (a part of a projection)."""
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not _BF16:
         raise TypeError(f"{what}: expected bf16, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{what}: expected a tensor on {device}")
-    if t.dim() != 3 or t.shape[0] != tokens or t.shape[2] != dim or \
-            (heads is not None and t.shape[1] != heads):
+    if t.get_device() != index:
+        raise ValueError(f"{what}: expected a tensor on cuda:{index}")
+    shape = t.shape
+    if len(shape) != 3 or shape[0] != tokens or shape[2] != dim or \
+            (heads is not None and shape[1] != heads):
         raise ValueError(f"{what}: expected [{tokens}, {heads or 'heads'}, {dim}], got "
-                         f"{tuple(t.shape)}")
-    n = t.shape[1]
-    if tokens and (t.stride(2) != 1 or (n > 1 and t.stride(1) != dim)):
+                         f"{tuple(shape)}")
+    n = shape[1]
+    st, sh, sd = t.stride()
+    if tokens and (sd != 1 or (n > 1 and sh != dim)):
         raise ValueError(f"{what}: the heads of a token must be contiguous")
-    return t.data_ptr(), (t.stride(0) if tokens > 1 else n * dim), n
+    return t.data_ptr(), (st if tokens > 1 else n * dim), n
 
 
-def _like(t, what, device, dtype, shape):
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{what}: expected {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
-    if t.device != device or not t.is_contiguous():
-        raise ValueError(f"{what}: expected a contiguous tensor on {device}")
-    return t
+def _like(t, what, index, dtype, shape):
+    if t.dtype is not dtype or t.shape != shape:
+        raise ValueError(f"{what}: expected {dtype} {shape}, got {t.dtype} {tuple(t.shape)}")
+    if t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{what}: expected a contiguous tensor on cuda:{index}")
+    return t.data_ptr()
 
 
 def block_bytes(head_dim: int, page_size: int) -> int:
@@ -162,9 +169,10 @@ class Cache:
             raise ValueError(f"pages {tuple(pages.shape)} does not fit kv_heads {kv_heads}, "
                              f"head_dim {head_dim}, page_size {page_size}, or these are not "
                              "supported")
-        self.pages = pages
-        self.device = pages.device
+        self.pages, self.pages_ptr = pages, pages.data_ptr()
+        self.device, self.index = pages.device, pages.get_device()
         self.err = torch.zeros(2, dtype=torch.int32, device=pages.device)
+        self.err_ptr = self.err.data_ptr()
         self._scratch = None
 
     @classmethod
@@ -182,15 +190,14 @@ class Cache:
     def clear_errors(self):
         self.err.zero_()
 
-    def scratch(self, n):
-        """Device scratch for page calls of up to n requests, kept between calls
-        (calls that share it run one after the other on one stream)."""
-        need = load_library().moe_kv4_scratch_bytes(self.ref, n)
-        if need == 0:
-            raise ValueError(f"{n} requests in one call are not supported")
-        if self._scratch is None or self._scratch.numel() < need:
-            self._scratch = torch.empty(need, dtype=torch.uint8, device=self.device)
-        return self._scratch
+    def scratch(self):
+        """(pointer, bytes) of the device scratch of page calls, for any number of
+        requests: taken once and kept (calls that share it run one after the other
+        on one stream)."""
+        if self._scratch is None:
+            n = load_library().moe_kv4_scratch_bytes(self.ref, MAX_REQUESTS)
+            self._scratch = torch.empty(n, dtype=torch.uint8, device=self.device)
+        return self._scratch.data_ptr(), self._scratch.numel()
 
 
 class Batch:
@@ -200,10 +207,9 @@ class Batch:
     request's new tokens and length.  The tensors may change between calls."""
 
     def __init__(self, cu_q, kv_len, tables, tokens: int, max_q: int, max_kv: int):
-        dev = kv_len.device
-        if dev.type != "cuda":
+        if not kv_len.is_cuda:
             raise ValueError("kv_len: expected a CUDA tensor")
-        r = kv_len.numel()
+        dev, r = kv_len.get_device(), kv_len.numel()
         _ints(kv_len, "kv_len", dev, (r,))
         _ints(cu_q, "cu_q", dev, (r + 1,))
         if tables.dtype != torch.int32 or tables.dim() != 2 or tables.shape[0] != r:
@@ -212,7 +218,7 @@ class Batch:
         if tokens < 0 or max_q < 0 or max_kv < 0 or tokens > r * max_q:
             raise ValueError(f"{tokens} tokens in {r} requests of at most {max_q}")
         self.cu_q, self.kv_len, self.tables, self.tokens = cu_q, kv_len, tables, tokens
-        self.device = dev
+        self.index = dev
         self.struct = _Batch(r, tokens, max_q, max_kv, tables.shape[1], cu_q.data_ptr(),
                              kv_len.data_ptr(), tables.data_ptr())
         self.ref = ctypes.byref(self.struct)
@@ -223,15 +229,13 @@ class Sequences:
     sequence's pages), lens int32 [S], refs int32 [n_pages]."""
 
     def __init__(self, tables, lens, refs):
-        dev = tables.device
-        if tables.dim() != 2:
-            raise ValueError("tables: expected [sequences, capacity]")
+        if not tables.is_cuda or tables.dim() != 2:
+            raise ValueError("tables: expected a CUDA tensor [sequences, capacity]")
+        dev = tables.get_device()
         _ints(tables, "tables", dev)
         _ints(lens, "lens", dev, (tables.shape[0],))
         _ints(refs, "refs", dev)
-        if dev.type != "cuda":
-            raise ValueError("expected CUDA tensors")
-        self.tables, self.lens, self.refs, self.device = tables, lens, refs, dev
+        self.tables, self.lens, self.refs, self.index = tables, lens, refs, dev
         self.struct = _Seqs(tables.shape[0], tables.shape[1], tables.data_ptr(), lens.data_ptr(),
                             refs.data_ptr())
         self.ref = ctypes.byref(self.struct)
@@ -245,9 +249,9 @@ class Sequences:
 
 
 def _same(cache, other):
-    if other.device != cache.device:
-        raise ValueError(f"the cache is on {cache.device}, the batch or sequences on "
-                         f"{other.device}")
+    if other.index != cache.index:
+        raise ValueError(f"the cache is on cuda:{cache.index}, the batch or sequences on "
+                         f"cuda:{other.index}")
 
 
 # ------------------------------------------------------------------- tokens --
@@ -259,37 +263,36 @@ def moe_kv4_append(cache: Cache, batch: Batch, q, k, v, q_weight=None, k_weight=
     heads, D]; k and v go into the cache, q is returned (bf16, contiguous).  q may
     be None."""
     _same(cache, batch)
-    dev, d, t = cache.device, cache.shape.head_dim, batch.tokens
-    kp, ks, _ = _rows(k, "k", dev, t, d, cache.shape.kv_heads)
-    vp, vs, _ = _rows(v, "v", dev, t, d, cache.shape.kv_heads)
-    qp, qs, hq = (None, 0, 0) if q is None else _rows(q, "q", dev, t, d)
+    dev, d, t, hkv = cache.index, cache.shape.head_dim, batch.tokens, cache.shape.kv_heads
+    kp, ks, _ = _rows(k, "k", dev, t, d, hkv)
+    vp, vs, _ = _rows(v, "v", dev, t, d, hkv)
     if q is None:
-        q_out = None
-    elif q_out is None:
-        q_out = torch.empty((t, hq, d), dtype=torch.bfloat16, device=dev)
+        qp = op = q_out = None
+        qs = hq = 0
     else:
-        _like(q_out, "q_out", dev, torch.bfloat16, (t, hq, d))
-    for w, what in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            _like(w, what, dev, torch.bfloat16, (d,))
-    max_pos = 0
-    if (cos is None) != (sin is None):
-        raise ValueError("cos and sin are given together")
-    if cos is not None:
+        qp, qs, hq = _rows(q, "q", dev, t, d)
+        if q_out is None:
+            q_out = torch.empty((t, hq, d), dtype=_BF16, device=cache.device)
+            op = q_out.data_ptr()
+        else:
+            op = _like(q_out, "q_out", dev, _BF16, (t, hq, d))
+    qw = None if q_weight is None else _like(q_weight, "q_weight", dev, _BF16, (d,))
+    kw = None if k_weight is None else _like(k_weight, "k_weight", dev, _BF16, (d,))
+    max_pos, cp, sp = 0, None, None
+    if cos is not None and sin is not None:
         max_pos = cos.shape[0]
-        _like(cos, "cos", dev, torch.float32, (max_pos, d // 2))
-        _like(sin, "sin", dev, torch.float32, (max_pos, d // 2))
-    if positions is not None:
-        _ints(positions, "positions", dev, (t,))
+        cp = _like(cos, "cos", dev, _F32, (max_pos, d // 2))
+        sp = _like(sin, "sin", dev, _F32, (max_pos, d // 2))
+    elif cos is not None or sin is not None:
+        raise ValueError("cos and sin are given together")
+    pp = None if positions is None else _ints(positions, "positions", dev, (t,)).data_ptr()
     with _on(dev):
-        rc = load_library().moe_kv4_append(
-            qp, qs, kp, ks, vp, vs, None if q_weight is None else q_weight.data_ptr(),
-            None if k_weight is None else k_weight.data_ptr(), eps,
-            None if cos is None else cos.data_ptr(), None if sin is None else sin.data_ptr(),
-            None if positions is None else positions.data_ptr(), max_pos, int(bool(interleaved)),
-            hq, None if q_out is None else q_out.data_ptr(), cache.pages.data_ptr(), layer,
-            cache.ref, batch.ref, cache.err.data_ptr(), _raw_stream(stream, dev))
-    ops._check(rc, "moe_kv4_append")
+        rc = (_lib or load_library()).moe_kv4_append(
+            qp, qs, kp, ks, vp, vs, qw, kw, eps, cp, sp, pp, max_pos, 1 if interleaved else 0, hq,
+            op, cache.pages_ptr, layer, cache.ref, batch.ref, cache.err_ptr,
+            _raw_stream(stream, dev))
+    if rc:
+        ops._check(rc, "moe_kv4_append")
     return q_out
 
 
@@ -298,17 +301,19 @@ def moe_kv4_read(cache: Cache, batch: Batch, layer: int = 0, k_out=None, v_out=N
     kv_heads, D]."""
     _same(cache, batch)
     shape = (batch.tokens, cache.shape.kv_heads, cache.shape.head_dim)
-    out = []
-    for t, what in ((k_out, "k_out"), (v_out, "v_out")):
-        if t is None:
-            t = torch.empty(shape, dtype=torch.float16, device=cache.device)
-        out.append(_like(t, what, cache.device, torch.float16, shape))
-    with _on(cache.device):
-        rc = load_library().moe_kv4_read(
-            cache.pages.data_ptr(), layer, cache.ref, batch.ref, out[0].data_ptr(),
-            out[1].data_ptr(), cache.err.data_ptr(), _raw_stream(stream, cache.device))
-    ops._check(rc, "moe_kv4_read")
-    return out[0], out[1]
+    dev = cache.index
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=torch.float16, device=cache.device)
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=torch.float16, device=cache.device)
+    kp = _like(k_out, "k_out", dev, torch.float16, shape)
+    vp = _like(v_out, "v_out", dev, torch.float16, shape)
+    with _on(dev):
+        rc = (_lib or load_library()).moe_kv4_read(cache.pages_ptr, layer, cache.ref, batch.ref, kp,
+                                                   vp, cache.err_ptr, _raw_stream(stream, dev))
+    if rc:
+        ops._check(rc, "moe_kv4_read")
+    return k_out, v_out
 
 
 def alloc_workspace(cache: Cache, batch: Batch | None, q_heads: int) -> torch.Tensor:
@@ -332,38 +337,36 @@ def moe_kv4_attention(q, cache: Cache, batch: Batch, scale: float | None = None,
     tokens (0: all).  tree: int64 [tokens], bit i set where the i-th new token of
     the request is seen.  scale defaults to 1 / sqrt(D)."""
     _same(cache, batch)
-    dev, d, t = cache.device, cache.shape.head_dim, batch.tokens
+    dev, d, t = cache.index, cache.shape.head_dim, batch.tokens
     qp, qs, hq = _rows(q, "q", dev, t, d)
     if out is None:
-        out = torch.empty((t, hq, d), dtype=torch.bfloat16, device=dev)
+        out = torch.empty((t, hq, d), dtype=_BF16, device=cache.device)
+        op = out.data_ptr()
     else:
-        _like(out, "out", dev, torch.bfloat16, (t, hq, d))
-    if lse is not None:
-        _like(lse, "lse", dev, torch.float32, (t, hq))
-    elif return_lse:
-        lse = torch.empty((t, hq), dtype=torch.float32, device=dev)
-    if tree is not None:
-        _like(tree, "tree", dev, torch.int64, (t,))
+        op = _like(out, "out", dev, _BF16, (t, hq, d))
+    if lse is None and return_lse:
+        lse = torch.empty((t, hq), dtype=_F32, device=cache.device)
+    lp = None if lse is None else _like(lse, "lse", dev, _F32, (t, hq))
+    tp = None if tree is None else _like(tree, "tree", dev, torch.int64, (t,))
     if workspace is None:
         workspace = alloc_workspace(cache, batch, hq)
-    elif workspace.device != dev or workspace.dtype != torch.uint8 or \
+    elif workspace.get_device() != dev or workspace.dtype is not torch.uint8 or \
             not workspace.is_contiguous():
-        raise ValueError(f"workspace: expected a contiguous uint8 tensor on {dev}")
+        raise ValueError(f"workspace: expected a contiguous uint8 tensor on cuda:{dev}")
     with _on(dev):
-        rc = load_library().moe_kv4_attention(
-            qp, qs, hq, cache.pages.data_ptr(), layer, cache.ref, batch.ref,
-            1.0 / math.sqrt(d) if scale is None else scale, window,
-            None if tree is None else tree.data_ptr(), out.data_ptr(),
-            None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.numel(),
-            _raw_stream(stream, dev))
-    ops._check(rc, "moe_kv4_attention")
+        rc = (_lib or load_library()).moe_kv4_attention(
+            qp, qs, hq, cache.pages_ptr, layer, cache.ref, batch.ref,
+            d ** -0.5 if scale is None else scale, window, tp, op, lp, workspace.data_ptr(),
+            workspace.numel(), _raw_stream(stream, dev))
+    if rc:
+        ops._check(rc, "moe_kv4_attention")
     return out if lse is None else (out, lse)
 
 
 # -------------------------------------------------------------------- pages --
 def _ids(t, what, cache, n=None):
-    _ints(t, what, cache.device)
-    if t.dim() != 1 or (n is not None and t.numel() != n):
+    _ints(t, what, cache.index)
+    if len(t.shape) != 1 or (n is not None and t.numel() != n):
         raise ValueError(f"{what}: expected [{'n' if n is None else n}], got {tuple(t.shape)}")
     return t.data_ptr() if t.numel() else None
 
@@ -380,12 +383,13 @@ def moe_kv4_reserve(cache: Cache, seqs: Sequences, ids, new_lens, stream=None):
     _pool_of(cache, seqs)
     n = ids.numel()
     ip, lp = _ids(ids, "ids", cache), _ids(new_lens, "new_lens", cache, n)
-    s = cache.scratch(n)
-    with _on(cache.device):
-        rc = load_library().moe_kv4_reserve(cache.ref, seqs.ref, ip, lp, n, s.data_ptr(), s.numel(),
-                                            cache.err.data_ptr(),
-                                            _raw_stream(stream, cache.device))
-    ops._check(rc, "moe_kv4_reserve")
+    sp, sb = cache.scratch()
+    with _on(cache.index):
+        rc = (_lib or load_library()).moe_kv4_reserve(
+            cache.ref, seqs.ref, ip, lp, n, sp, sb, cache.err_ptr,
+            _raw_stream(stream, cache.index))
+    if rc:
+        ops._check(rc, "moe_kv4_reserve")
 
 
 def moe_kv4_fork(cache: Cache, seqs: Sequences, parents, children, stream=None):
@@ -394,12 +398,13 @@ def moe_kv4_fork(cache: Cache, seqs: Sequences, parents, children, stream=None):
     _pool_of(cache, seqs)
     n = parents.numel()
     pp, cp = _ids(parents, "parents", cache), _ids(children, "children", cache, n)
-    s = cache.scratch(n)
-    with _on(cache.device):
-        rc = load_library().moe_kv4_fork(cache.pages.data_ptr(), cache.ref, seqs.ref, pp, cp, n,
-                                         s.data_ptr(), s.numel(), cache.err.data_ptr(),
-                                         _raw_stream(stream, cache.device))
-    ops._check(rc, "moe_kv4_fork")
+    sp, sb = cache.scratch()
+    with _on(cache.index):
+        rc = (_lib or load_library()).moe_kv4_fork(
+            cache.pages_ptr, cache.ref, seqs.ref, pp, cp, n, sp, sb, cache.err_ptr,
+            _raw_stream(stream, cache.index))
+    if rc:
+        ops._check(rc, "moe_kv4_fork")
 
 
 def moe_kv4_free(cache: Cache, seqs: Sequences, ids, stream=None):
@@ -407,10 +412,11 @@ def moe_kv4_free(cache: Cache, seqs: Sequences, ids, stream=None):
     _pool_of(cache, seqs)
     n = ids.numel()
     ip = _ids(ids, "ids", cache)
-    with _on(cache.device):
-        rc = load_library().moe_kv4_free(cache.ref, seqs.ref, ip, n, cache.err.data_ptr(),
-                                         _raw_stream(stream, cache.device))
-    ops._check(rc, "moe_kv4_free")
+    with _on(cache.index):
+        rc = (_lib or load_library()).moe_kv4_free(cache.ref, seqs.ref, ip, n, cache.err_ptr,
+                                                   _raw_stream(stream, cache.index))
+    if rc:
+        ops._check(rc, "moe_kv4_free")
 
 
 def moe_kv4_compact(cache: Cache, seqs: Sequences, tables_out=None, refs_out=None, n_used=None,
@@ -419,22 +425,22 @@ def moe_kv4_compact(cache: Cache, seqs: Sequences, tables_out=None, refs_out=Non
     written in place, or to tables_out and refs_out.  Returns the number of pages
     in use (device int32 [1])."""
     _pool_of(cache, seqs)
-    dev = cache.device
+    dev = cache.index
     tables_out = seqs.tables if tables_out is None else \
-        _ints(tables_out, "tables_out", dev, tuple(seqs.tables.shape))
+        _ints(tables_out, "tables_out", dev, seqs.tables.shape)
     refs_out = seqs.refs if refs_out is None else \
-        _ints(refs_out, "refs_out", dev, tuple(seqs.refs.shape))
+        _ints(refs_out, "refs_out", dev, seqs.refs.shape)
     if n_used is None:
-        n_used = torch.empty(1, dtype=torch.int32, device=dev)
+        n_used = torch.empty(1, dtype=_I32, device=cache.device)
     else:
         _ints(n_used, "n_used", dev, (1,))
-    s = cache.scratch(0)
+    sp, sb = cache.scratch()
     with _on(dev):
-        rc = load_library().moe_kv4_compact(
-            cache.pages.data_ptr(), cache.ref, seqs.ref, tables_out.data_ptr(),
-            refs_out.data_ptr(), n_used.data_ptr(), s.data_ptr(), s.numel(), cache.err.data_ptr(),
-            _raw_stream(stream, dev))
-    ops._check(rc, "moe_kv4_compact")
+        rc = (_lib or load_library()).moe_kv4_compact(
+            cache.pages_ptr, cache.ref, seqs.ref, tables_out.data_ptr(), refs_out.data_ptr(),
+            n_used.data_ptr(), sp, sb, cache.err_ptr, _raw_stream(stream, dev))
+    if rc:
+        ops._check(rc, "moe_kv4_compact")
     return n_used
 
 
@@ -443,8 +449,9 @@ def moe_kv4_copy_pages(cache: Cache, src, dst, stream=None):
     skipped)."""
     n = src.numel()
     sp, dp = _ids(src, "src", cache), _ids(dst, "dst", cache, n)
-    with _on(cache.device):
-        rc = load_library().moe_kv4_copy_pages(cache.pages.data_ptr(), cache.ref, sp, dp, n,
-                                               cache.err.data_ptr(),
-                                               _raw_stream(stream, cache.device))
-    ops._check(rc, "moe_kv4_copy_pages")
+    with _on(cache.index):
+        rc = (_lib or load_library()).moe_kv4_copy_pages(
+            cache.pages_ptr, cache.ref, sp, dp, n, cache.err_ptr,
+            _raw_stream(stream, cache.index))
+    if rc:
+        ops._check(rc, "moe_kv4_copy_pages")
