@@ -70,6 +70,55 @@ MOE_DEV uint8_t *kv_block(const KvPool &p, int page, int head) {
     return p.base + ((size_t)page * p.hkv + head) * p.block;
 }
 
+// n / group for row numbers below 2^26 and groups of up to 64: one multiply by
+// magic = floor(2^32 / group) + 1 (whose error stays below n * group < 2^32).
+struct GroupDiv {
+    uint32_t magic;  // 0: group 1
+    int group;
+};
+MOE_DEV int div_group(int n, GroupDiv g) { return g.magic ? (int)__umulhi((uint32_t)n, g.magic) : n; }
+
+MOE_DEV float kv_ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// One row's four dimensions added up over several parts, in their order: each
+// holds sums o relative to a maximum m and their weight l.  U parts are loaded at
+// once (a part at a time would cost a memory round trip each).  at(i): the part's
+// row, D sums, then m and l; sl2 > 0 turns scores into powers of two.
+template <int D, int U, typename At>
+MOE_DEV void add_parts(int n, int d4, float sl2, At at, float &m, float &l, float4 &s) {
+    m = -INFINITY;
+    l = 0.0f;
+    s = make_float4(0, 0, 0, 0);
+    for (int i0 = 0; i0 < n; i0 += U) {
+        float pm[U], pl[U];
+        float4 v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const float *r = at(min(i0 + u, n - 1));
+            const float2 ml = *reinterpret_cast<const float2 *>(r + D);
+            v[u] = *reinterpret_cast<const float4 *>(r + 4 * d4);
+            pm[u] = i0 + u < n ? ml.x : -INFINITY;
+            pl[u] = ml.y;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const float nm = fmaxf(m, pm[u]);
+            const float x = m > -INFINITY ? kv_ex2((m - nm) * sl2) : 0.0f;
+            const float y = pm[u] > -INFINITY ? kv_ex2((pm[u] - nm) * sl2) : 0.0f;
+            m = nm;
+            l = l * x + pl[u] * y;
+            s.x = s.x * x + v[u].x * y;
+            s.y = s.y * x + v[u].y * y;
+            s.z = s.z * x + v[u].z * y;
+            s.w = s.w * x + v[u].w * y;
+        }
+    }
+}
+
 // The scale of a group: bf16(amax / 7) in [2^-14, 2720] (also for amax = 0).
 MOE_DEV float kv_scale(float amax) {
     const float s = __bfloat162float(__float2bfloat16_rn(__fmul_rn(amax, kKvSeventh)));

@@ -219,6 +219,8 @@ int moe_kv4_attention(const uint16_t *q, int64_t q_stride, int q_heads, const vo
     a.scale_log2 = scale * 1.4426950408889634f;
     a.q_heads = q_heads;
     a.group = q_heads / shape->kv_heads;
+    a.gdiv.group = a.group;
+    a.gdiv.magic = a.group == 1 ? 0u : (uint32_t)((1ull << 32) / a.group + 1);
     a.window = window;
     uint8_t *ws = reinterpret_cast<uint8_t *>(workspace);
     a.err = reinterpret_cast<uint32_t *>(ws);

@@ -76,12 +76,6 @@ MOE_DEV uint32_t transpose8x8(uint32_t v) {
     return r;
 }
 
-MOE_DEV float ex2(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-
 template <int N>
 MOE_DEV void lds_words(uint32_t addr, uint32_t (&w)[N]) {
     if constexpr (N == 4) {
@@ -145,7 +139,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
     __shared__ uint32_t prefix[kChunks + 1];
     __shared__ uint64_t bars[W * S];
     __shared__ Meta meta[2 * W];
-    __shared__ int run_of[2 * W + 1], n_runs, abort_flag, last_of;
+    __shared__ int run_of[2 * W + 1], list[2 * W], n_runs, abort_flag, last_of;
     __shared__ uint32_t warp_tot[W];
     pdl_wait();
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, g = lane >> 2, t = lane & 3;
@@ -288,7 +282,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const int r = 8 * n + g;
-            const int i = (row0 + r) / G, hh = (row0 + r) - i * G;
+            const int i = div_group(row0 + r, a.gdiv), hh = (row0 + r) - i * G;
             const uint16_t *src = a.q + (size_t)(rq.q0 + i) * a.q_stride + (size_t)(h * G + hh) * D + 8 * t;
 #pragma unroll
             for (int G4 = 0; G4 < NG; ++G4) {
@@ -317,7 +311,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
         if (__any_sync(0xffffffffu, bad) && lane == 0) kv_report(a.err, MOE_KV4_DEVERR_RANGE);
 
         // tokens that every row sees: below `open`, and from `shut` on
-        const int i_lo = row0 / G, i_hi = (row0 + rows - 1) / G;
+        const int i_lo = div_group(row0, a.gdiv), i_hi = div_group(row0 + rows - 1, a.gdiv);
         const int open = min(rq.end, a.tree ? rq.first : rq.first + i_lo + 1);
         const int shut = a.window > 0 ? rq.first + i_hi - a.window + 1 : 0;
 
@@ -400,7 +394,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const int r = 8 * n + 2 * t + e, i = (row0 + r) / G, p = rq.first + i;
+                        const int r = 8 * n + 2 * t + e, i = div_group(row0 + r, a.gdiv), p = rq.first + i;
                         const int hi = r < rows ? min(p, rq.end - 1) : -1;
                         const int lo = a.window > 0 ? p - a.window : -1;
                         uint64_t word = 0;
@@ -435,7 +429,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
                 if (__any_sync(0xffffffffu, top[0] > m[n][0] || top[1] > m[n][1])) {
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const float r = top[e] > m[n][e] ? ex2((m[n][e] - top[e]) * sl2) : 1.0f;
+                        const float r = top[e] > m[n][e] ? kv_ex2((m[n][e] - top[e]) * sl2) : 1.0f;
                         m[n][e] = top[e];
                         l[n][e] *= r;
 #pragma unroll
@@ -450,7 +444,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
                 for (int s = 0; s < 4; ++s) {
                     float p[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) p[i] = ex2(fmaf(x[s][n][i], sl2, i & 1 ? o1 : o0));
+                    for (int i = 0; i < 4; ++i) p[i] = kv_ex2(fmaf(x[s][n][i], sl2, i & 1 ? o1 : o0));
                     l[n][0] += p[0] + p[2];
                     l[n][1] += p[1] + p[3];
                     pb[s][n][0] = transpose8x8(as_u32(__floats2half2_rn(p[0], p[1])));
@@ -521,7 +515,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
                 for (int e = 0; e < 2; ++e) {
                     const int r = 8 * n + 2 * t + e;
                     if (r >= rows) continue;
-                    const int i = (row0 + r) / G, hh = (row0 + r) - i * G;
+                    const int i = div_group(row0 + r, a.gdiv), hh = (row0 + r) - i * G;
                     const size_t o = (size_t)(rq.q0 + i) * a.q_heads + h * G + hh;
                     const float inv = l[n][e] > 0.0f ? 1.0f / l[n][e] : 0.0f;
 #pragma unroll
@@ -561,18 +555,22 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
     }
     __syncthreads();
 
-    // partials of the same item are neighbours in the list of slots
-    if (tid == 0) {
-        int n = 0;
-        uint32_t prev = 0xffffffffu;
-        int end = 0;
-        for (int i = 0; i < 2 * W; ++i) {
-            if (meta[i].u0 == meta[i].u1) continue;
-            if (meta[i].u0 != prev) run_of[n++] = i, prev = meta[i].u0;
-            end = i + 1;
+    // the partials in list order; those of the same item are neighbours
+    if (w == 0) {
+        const Meta me = lane < 2 * W ? meta[lane] : Meta{0, 0, 0, 0, 0};
+        const bool has = me.u0 != me.u1;
+        const unsigned who = __ballot_sync(0xffffffffu, has);
+        const int at = __popc(who & ((1u << lane) - 1u));
+        if (has) list[at] = lane;
+        __syncwarp();
+        const int n = __popc(who);
+        const bool first = lane < n && (lane == 0 || meta[list[lane]].u0 != meta[list[lane - 1]].u0);
+        const unsigned firsts = __ballot_sync(0xffffffffu, first);
+        if (first) run_of[__popc(firsts & ((1u << lane) - 1u))] = lane;
+        if (lane == 0) {
+            n_runs = __popc(firsts);
+            run_of[__popc(firsts)] = n;
         }
-        run_of[n] = end;
-        n_runs = n;
     }
     __syncthreads();
     auto slot_of = [&](int i) -> const float * {
@@ -585,7 +583,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
         const int rows_b = (a.batch.cu_q[me.b + 1] - a.batch.cu_q[me.b]) * G;
         const int rr = me.r * C::kRows + row;
         if (rr >= rows_b) return;
-        const int i = rr / G, hh = rr - i * G;
+        const int i = div_group(rr, a.gdiv), hh = rr - i * G;
         const size_t o = (size_t)(a.batch.cu_q[me.b] + i) * a.q_heads + me.h * G + hh;
         const float inv = ll > 0.0f ? 1.0f / ll : 0.0f;
         const __nv_bfloat162 lo = __floats2bfloat162_rn(s.x * inv, s.y * inv);
@@ -595,28 +593,14 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
         if (a.lse && d4 == 0)
             a.lse[o] = ll > 0.0f ? (mm * sl2 + log2f(ll)) * 0.6931471805599453f : -INFINITY;
     };
-    auto add = [&](const float *p, int row, int d4, float &mm, float &ll, float4 &s) {
-        const float *r = p + row * C::kPitch;
-        const float pm = r[D], pl = r[D + 1];
-        const float4 v = *reinterpret_cast<const float4 *>(r + 4 * d4);
-        const float nm = fmaxf(mm, pm);
-        const float x = mm > -INFINITY ? ex2((mm - nm) * sl2) : 0.0f;
-        const float y = pm > -INFINITY ? ex2((pm - nm) * sl2) : 0.0f;
-        mm = nm;
-        ll = ll * x + pl * y;
-        s.x = s.x * x + v.x * y;
-        s.y = s.y * x + v.y * y;
-        s.z = s.z * x + v.z * y;
-        s.w = s.w * x + v.w * y;
-    };
     const int runs = n_runs;
     for (int e = tid; e < runs * kWork; e += W * 32) {
         const int run = e / kWork, row = (e / kQuads) % C::kRows, d4 = e % kQuads;
-        const Meta me = meta[run_of[run]];
-        float mm = -INFINITY, ll = 0.0f;
-        float4 s = make_float4(0, 0, 0, 0);
-        for (int i = run_of[run]; i < run_of[run + 1]; ++i)
-            if (meta[i].u0 != meta[i].u1) add(slot_of(i), row, d4, mm, ll, s);
+        const Meta me = meta[list[run_of[run]]];
+        float mm, ll;
+        float4 s;
+        add_parts<D, 4>(run_of[run + 1] - run_of[run], d4, sl2,
+                        [&](int i) { return slot_of(list[run_of[run] + i]) + row * C::kPitch; }, mm, ll, s);
         if (me.u0 >= c_lo && me.u1 <= c_hi) {
             finish(me, row, d4, mm, ll, s);
         } else {
@@ -630,7 +614,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
     __threadfence();
     __syncthreads();
     for (int run = 0; run < runs; ++run) {
-        const Meta me = meta[run_of[run]];
+        const Meta me = meta[list[run_of[run]]];
         if (me.u0 >= c_lo && me.u1 <= c_hi) continue;
         const uint32_t c0 = me.u0 / per, c1 = (me.u1 - 1) / per;  // CTAs of the item
         if (tid == 0) {
@@ -645,11 +629,15 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
         __threadfence();
         for (int e = tid; e < kWork; e += W * 32) {
             const int row = e / kQuads, d4 = e % kQuads;
-            float mm = -INFINITY, ll = 0.0f;
-            float4 s = make_float4(0, 0, 0, 0);
-            for (uint32_t c = c0; c <= c1; ++c)
-                add(a.cta_slots + ((size_t)2 * c + (c == c0 && me.u0 > c0 * per ? 1 : 0)) * C::kSlot, row,
-                    d4, mm, ll, s);
+            float mm, ll;
+            float4 s;
+            const int odd = me.u0 > c0 * per ? 1 : 0;  // in its first CTA the item is the last one
+            add_parts<D, 8>((int)(c1 - c0) + 1, d4, sl2,
+                            [&](int i) {
+                                return a.cta_slots + ((size_t)2 * (c0 + i) + (i ? 0 : odd)) * C::kSlot +
+                                       row * C::kPitch;
+                            },
+                            mm, ll, s);
             finish(me, row, d4, mm, ll, s);
         }
     }

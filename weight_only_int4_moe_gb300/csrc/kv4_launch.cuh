@@ -38,6 +38,7 @@ struct KvAttnArgs {
     float *lse;
     float scale_log2;  // scale * log2(e)
     int q_heads, group, window;
+    GroupDiv gdiv;
     int rows_lo, rows_hi;  // requests of this many rows (new tokens x group) are the kernel's
     int max_kv, min_units;
     int32_t *counters;     // [CTAs], zero between calls

@@ -5,17 +5,17 @@
 // consecutive tokens), two tiles of 128 for tcgen05.mma, against tiles of 128
 // tokens.  Per tile of tokens and rows,
 //   S = Q K^T   (128 x 128 x D, both operands fp16 in shared memory)
-//   P = 2^(S - m) in fp16, written over S in tensor memory
+//   P = 2^(S - m) in fp16, written over the second half of S in tensor memory
 //   O += P V    (128 x D x 128, P from tensor memory, V from shared memory)
 // with the running maximum m and the sum of a row in the one thread that owns the
 // row.  O is rescaled only when a row's maximum has grown by more than 2^8 since
 // its last rescale (the probabilities then stay below 2^8, far inside fp16, and
 // the quotient O / l does not depend on m).
 //
-// Roles of the 16 warps: two warpgroups each own one tile of rows (load its Q,
-// softmax, output); one warpgroup turns codes into fp16 operand tiles, its loads
-// one tile ahead in registers; one warp issues the MMAs, alternating between the
-// two tiles of rows so that the softmax of one runs under the products of the
+// Roles of the 20 warps: two warpgroups each own one tile of rows (load its Q,
+// softmax, output); one turns K's codes into fp16 operand tiles and one V's, their
+// loads one tile ahead in registers; one warp issues the MMAs, alternating between
+// the two tiles of rows so that the softmax of one runs under the products of the
 // other.  K tiles are K-major, V tiles are left in token order and read N-major;
 // the order of V's columns is the order in which its codes unpack, undone when
 // the output is written.
@@ -33,13 +33,18 @@ namespace {
 constexpr int kTok = 128;        // tokens of a unit
 constexpr int kRowsItem = 256;
 constexpr int kChunks = 1024;
-constexpr int kThreads = 512;
+constexpr int kThreads = 640;
 constexpr uint32_t kTmemCols = 512;
-// Registers a thread of each role (multiples of 8): a row of S is 128 of them.  The
-// four warpgroups' shares add up to what the block is launched with, 4 x 128.
-constexpr int kRegsLaunch = 128, kRegsSoftmax = 168, kRegsCodes = 120, kRegsMma = 56;
-static_assert(2 * kRegsSoftmax + kRegsCodes + kRegsMma == 4 * kRegsLaunch, "register shares");
-static_assert(kThreads * kRegsLaunch == 65536, "the block takes the whole register file");
+// Registers a thread of each role (multiples of 8).  The five warpgroups' shares add
+// up to what the block is launched with, 5 x 96.
+constexpr int kRegsLaunch = 96, kRegsSoftmax = 136, kRegsCodes = 72, kRegsMma = 64;
+static_assert(2 * kRegsSoftmax + 2 * kRegsCodes + kRegsMma == 5 * kRegsLaunch, "register shares");
+static_assert(kThreads * kRegsLaunch <= 65536, "the register file");
+// Before the block's common end every warp returns to kRegsLaunch.  Those that take
+// registers back wait at this barrier until those that give them up have done so,
+// and until the softmax warps have had theirs: a warp with no work that took its
+// share back early would keep it from a softmax warp that still waits for it.
+constexpr uint32_t kBarRegs = 1;
 
 template <int D>
 struct Cfg {
@@ -85,8 +90,8 @@ MOE_DEV Request request_of(const KvAttnArgs &a, int b) {
 
 // Token tiles of a row tile: [lo, lo + n).
 MOE_DEV int tiles_of(const KvAttnArgs &a, const Request &r, int rt, int &lo) {
-    const int i_lo = rt * kRowsItem / a.group;
-    const int i_hi = (min(r.rows, (rt + 1) * kRowsItem) - 1) / a.group;
+    const int i_lo = div_group(rt * kRowsItem, a.gdiv);
+    const int i_hi = div_group(min(r.rows, (rt + 1) * kRowsItem) - 1, a.gdiv);
     const int hi = max(0, min(r.end, r.first + i_hi + 1));
     lo = (a.window > 0 ? max(0, r.first + i_lo - a.window + 1) : 0) / kTok;
     return max(1, (hi + kTok - 1) / kTok - lo);
@@ -267,10 +272,28 @@ MOE_DEV void tmem_pass(uint32_t *v) {
     asm volatile("" : KV4_P8(v, 0), KV4_P8(v, 8), KV4_P8(v, 16), KV4_P8(v, 24)::"memory");
 }
 
-MOE_DEV float ex2(float x) {
+// One instruction of the ALU pipe, which has half the lanes of the FMA pipe.
+MOE_DEV float max3(float a, float b, float c) {
     float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
+}
+
+// Which of the tokens j0..j0+31 a row sees, as bits: lo < j <= hi, in a run of 16
+// that has a page, and by the row's word for the new tokens (from `first` on).
+MOE_DEV uint32_t visible32(int j0, int lo, int hi, uint32_t ok, bool tree, uint64_t word, int first) {
+    const int b = hi - j0, a = lo + 1 - j0;
+    uint32_t see = b < 0 ? 0u : b >= 31 ? 0xffffffffu : (2u << b) - 1u;
+    see &= a <= 0 ? 0xffffffffu : a >= 32 ? 0u : 0xffffffffu << a;
+    see &= (ok & 1u ? 0xffffu : 0u) | (ok & 2u ? 0xffff0000u : 0u);
+    if (tree) {
+        const int d = j0 - first;  // index of j0 among the new tokens
+        if (d >= 0)
+            see &= d < 64 ? (uint32_t)(word >> d) : 0u;
+        else if (d > -32)
+            see &= (uint32_t)(word << -d) | ((1u << -d) - 1u);
+    }
+    return see;
 }
 
 MOE_DEV uint64_t pack2(float a, float b) {
@@ -301,12 +324,149 @@ MOE_DEV void scaled_codes(uint32_t w, uint32_t s, uint32_t (&x)[4]) {
         x[i] = as_u32(__hfma2(as_h2((t[i] & 0x03C003C0u) | 0x4C004C00u), as_h2(s), m24));
 }
 
-// Codes and scales of a thread's part of one tile, on their way from global memory.
+MOE_DEV void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+        "%12, %13, %14, %15, %16};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+        "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
+
+// Multiplies the thread's row of O (rarely needed: see the file's head).
+template <int D>
+MOE_DEV void scale_o(uint32_t o_at, float f) {
+#pragma unroll 1
+    for (int c = 0; c < D / 16; ++c) {
+        float o[16];
+        tmem_ld_32x32b_x16_wait(o_at + 16 * c, o);
+        uint32_t v[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(o[e] * f);
+        tmem_st16(o_at + 16 * c, v);
+    }
+}
+
+// A thread's part of one tile of codes and scales, on its way from global memory,
+// and which of its rows hold a token.
 template <int D>
 struct Packed {
-    uint4 k[Cfg<D>::kLoads], v[Cfg<D>::kLoads];
-    uint32_t ks[Cfg<D>::kLoads][D / 64], vs[Cfg<D>::kLoads][D / 64];
+    uint4 c[Cfg<D>::kLoads];
+    uint32_t z[Cfg<D>::kLoads][D / 64];
+    uint32_t live;
 };
+
+// Requests the part (nothing waits for it here: rows without a token load page 0
+// and are zeroed when they are unpacked).  part: 0 K, 1 V.  id_at: the lane that
+// holds the tile's first page id; left: tokens of the sequence from the tile on.
+template <int D, int part>
+MOE_DEV void load_part(Packed<D> &p, const KvPool &pool, int head, int ids, int id_at, int row_l, int ch,
+                       int left) {
+    constexpr int kStep = 128 / (D == 128 ? 4 : 2), NG = D / 32;
+    const int ps = pool.ps;
+    p.live = 0;
+#pragma unroll
+    for (int i = 0; i < Cfg<D>::kLoads; ++i) {
+        const int row = i * kStep + row_l;
+        const int id = __shfl_sync(0xffffffffu, ids, id_at + row / ps);
+        const int slot = row & (ps - 1);
+        p.live |= (id >= 0 && row < left ? 1u : 0u) << i;
+        const uint8_t *blk = kv_block(pool, max(id, 0), head);
+        p.c[i] = *reinterpret_cast<const uint4 *>(blk + part * ps * (D / 2) + slot * (D / 2) + 16 * ch);
+        const uint8_t *sc = blk + ps * D + part * ps * (NG * 2) + slot * (NG * 2);
+        if constexpr (D == 128) {
+            const uint2 v = *reinterpret_cast<const uint2 *>(sc);
+            p.z[i][0] = v.x;
+            p.z[i][1] = v.y;
+        } else {
+            p.z[i][0] = *reinterpret_cast<const uint32_t *>(sc);
+        }
+    }
+}
+
+// The warpgroup that turns one side's codes (part 0: K, 1: V) into operand tiles.
+template <int D, int part>
+MOE_DEV void unpack_role(const KvAttnArgs &a, Shared &sh, uint32_t smem, Walk walk) {
+    using C = Cfg<D>;
+    constexpr int kLanesRow = D == 128 ? 4 : 2;  // 16-byte chunks of a row
+    constexpr int kStep = 128 / kLanesRow;       // rows of one load of the group
+    const int lane = threadIdx.x & 31, dt = threadIdx.x & 127, row_l = dt / kLanesRow, ch = dt % kLanesRow;
+    const int ps = a.pool.ps, ppt = kTok / ps;
+    const uint32_t full = smem_u32(&sh.bar[part ? kVFull : kKFull]);
+    const uint32_t empty = smem_u32(&sh.bar[part ? kVEmpty : kKEmpty]);
+    const uint32_t buf = smem + (part ? C::kV : C::kK);
+    Ring ring(2);
+    uint32_t tiles = 0;
+    Segment sg;
+    while (walk.next(a, sg)) {
+        const int32_t *table = a.batch.tables + (size_t)sg.b * a.batch.stride;
+        int e_base = 0, ids = -1;
+        // page ids of the next tiles: lane l holds table entry e_base + l
+        auto load_ids = [&](int from) {
+            e_base = from;
+            const int e = from + lane;
+            ids = -1;
+            if (e < (sg.tile0 + sg.n) * ppt && (long long)e * ps < sg.r.end) {
+                ids = table[e];
+                if ((unsigned)ids >= (unsigned)a.pool.n_pages) {
+                    ids = -1;
+                    if (part == 0 && sg.h == 0 && dt < 32) kv_report(a.err, MOE_KV4_DEVERR_PAGE);
+                }
+            }
+        };
+        Packed<D> pk;
+        uint32_t ok_next = 0;
+        auto request = [&](int k) {
+            const int e0 = (sg.tile0 + k) * ppt;
+            if (k == 0 || e0 + ppt > e_base + 32) load_ids(e0);
+            if (part == 0) {
+                const unsigned have = __ballot_sync(0xffffffffu, ids >= 0) >> (e0 - e_base);
+                ok_next = 0;
+                for (int i = 0; i < ppt; ++i)
+                    if ((have >> i) & 1u) ok_next |= ((1u << (ps / 16)) - 1u) << (i * (ps / 16));
+            }
+            load_part<D, part>(pk, a.pool, sg.h, ids, e0 - e_base, row_l, ch,
+                               sg.r.end - (sg.tile0 + k) * kTok);
+        };
+        request(0);
+        for (int k = 0; k < sg.n; ++k) {
+            if (__any_sync(0xffffffffu, !mbar_wait(empty + 8 * ring.idx, ring.ph ^ 1, &sh.abort_flag, a.err)))
+                return;
+            if (part == 0 && dt == 0) sh.ok[tiles & 7] = ok_next;
+            ++tiles;
+            const uint32_t dst = buf + ring.idx * C::kTileBytes;
+#pragma unroll
+            for (int i = 0; i < C::kLoads; ++i) {
+                const int row = i * kStep + row_l;
+                const uint32_t words[4] = {pk.c[i].x, pk.c[i].y, pk.c[i].z, pk.c[i].w};
+                const bool live = (pk.live >> i) & 1u;
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    uint32_t s;
+                    int chunk;
+                    if (part == 0) {
+                        // word (t, G): dimensions 32G + 8t.., the row's chunk 4G + t
+                        const int G = D == 128 ? u : u & 1, t = D == 128 ? ch : 2 * ch + (u >> 1);
+                        s = __byte_perm(pk.z[i][G / 2], 0, G & 1 ? 0x3232 : 0x1010);
+                        chunk = 4 * G + t;
+                    } else {
+                        // piece g of groups 2p and 2p + 1: column chunk 8p + g
+                        const int pp = D == 128 ? u & 1 : 0, g = D == 128 ? 2 * ch + (u >> 1) : 4 * ch + u;
+                        s = pk.z[i][pp];
+                        chunk = 8 * pp + g;
+                    }
+                    uint32_t x[4];
+                    scaled_codes(words[u], live ? s : 0u, x);
+                    sts128(dst + tile_at(row, chunk), x[0], x[1], x[2], x[3]);
+                }
+            }
+            fence_proxy_async_shared();
+            mbar_arrive(full + 8 * ring.idx);
+            ring.next();
+            if (k + 1 < sg.n) request(k + 1);
+        }
+    }
+}
 
 template <int N>
 MOE_DEV void more_regs() {
@@ -320,7 +480,6 @@ MOE_DEV void fewer_regs() {
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnArgs a) {
     using C = Cfg<D>;
-    constexpr int NG = C::NG;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     __shared__ Shared sh;
     const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -333,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnAr
         mbar_fence_init();
         sh.part_u0[0] = sh.part_u1[0] = sh.part_u0[1] = sh.part_u1[1] = 0;
     }
-    if (w == 15) {
+    if (w == 19) {
         tmem_alloc(smem_u32(&sh.tmem), kTmemCols);
         tmem_relinquish();
     }
@@ -390,8 +549,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnAr
     const uint32_t tmem = sh.tmem;
     const float sl2 = fmaxf(fabsf(a.scale_log2), 1e-30f);
     auto bar = [&](int i) { return smem_u32(&sh.bar[i]); };
-    // S (and P over it) of the two row tiles, then their O
+    // S (and P over its second half) of the two row tiles, then their O
     auto s_col = [&](int m) { return tmem + 128u * m; };
+    auto p_col = [&](int m) { return tmem + 128u * m + 64u; };
     auto o_col = [&](int m) { return tmem + 256u + 128u * m; };
     int *abort_flag = &sh.abort_flag;
 
@@ -415,23 +575,32 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnAr
                 const int row_base = sg.rt * kRowsItem + m * 128, n_rows = min(128, sg.rows - m * 128);
                 bool bad = false;
                 const uint32_t flip = a.scale_log2 < 0.0f ? 0x80008000u : 0u;
-                for (int c = r; c < 128 * (D / 8); c += 128) {
-                    const int qr = c / (D / 8), ch = c % (D / 8);
-                    uint4 v = make_uint4(0, 0, 0, 0);
-                    if (qr < n_rows) {
-                        const int i = (row_base + qr) / a.group, hh = row_base + qr - i * a.group;
-                        v = *reinterpret_cast<const uint4 *>(a.q + (size_t)(sg.r.q0 + i) * a.q_stride +
-                                                             (size_t)(sg.h * a.group + hh) * D + 8 * ch);
+#pragma unroll
+                for (int c0 = 0; c0 < D / 8; c0 += 8) {
+                    uint4 v[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int c = r + 128 * (c0 + e), qr = c / (D / 8), ch = c % (D / 8);
+                        const int i = div_group(row_base + qr, a.gdiv), hh = row_base + qr - i * a.group;
+                        v[e] = make_uint4(0, 0, 0, 0);
+                        if (qr < n_rows)
+                            v[e] = *reinterpret_cast<const uint4 *>(
+                                a.q + (size_t)(sg.r.q0 + i) * a.q_stride +
+                                (size_t)(sg.h * a.group + hh) * D + 8 * ch);
                     }
-                    v = bf16x8_to_f16x8_sat(v, bad);
-                    sts128(smem + C::kQ + m * C::kTileBytes + tile_at(qr, ch), v.x ^ flip, v.y ^ flip,
-                           v.z ^ flip, v.w ^ flip);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int c = r + 128 * (c0 + e), qr = c / (D / 8), ch = c % (D / 8);
+                        const uint4 x = bf16x8_to_f16x8_sat(v[e], bad);
+                        sts128(smem + C::kQ + m * C::kTileBytes + tile_at(qr, ch), x.x ^ flip, x.y ^ flip,
+                               x.z ^ flip, x.w ^ flip);
+                    }
                 }
                 if (__any_sync(0xffffffffu, bad) && lane == 0) kv_report(a.err, MOE_KV4_DEVERR_RANGE);
                 fence_proxy_async_shared();
                 mbar_arrive(bar(kQFull + m));
 
-                const int i = (row_base + r) / a.group, hh = row_base + r - i * a.group;
+                const int i = div_group(row_base + r, a.gdiv), hh = row_base + r - i * a.group;
                 const bool live = r < n_rows;
                 const int p = sg.r.first + i;
                 const int hi = live ? min(p, sg.r.end - 1) : -1;
@@ -454,74 +623,83 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnAr
                     tc_fence_after();
                     const uint32_t ok = sh.ok[tiles & 7];
                     ++tiles;
-                    uint32_t s[128];
                     if (any_live) {
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) tmem_ld32(s_at + 32 * c, s + 32 * c);
-                        tmem_wait_ld(s);
-                        tmem_pass(s + 32);
-                        tmem_pass(s + 64);
-                        tmem_pass(s + 96);
                         const int j0 = (sg.tile0 + k) * kTok;
-                        if (ok != 0xFFu || j0 + kTok > open || j0 < shut) {
+                        const bool masked = ok != 0xFFu || j0 + kTok > open || j0 < shut;
+                        auto mask = [&](uint32_t *v, int c) {
+                            if (!masked) return;
+                            const uint32_t see = visible32(j0 + 32 * c, lo, hi, ok >> (2 * c),
+                                                           a.tree != nullptr, word, sg.r.first);
 #pragma unroll
-                            for (int c = 0; c < 128; ++c) {
-                                const int j = j0 + c;
-                                bool see = j <= hi && j > lo && ((ok >> (c / 16)) & 1u);
-                                if (a.tree && j >= sg.r.first)
-                                    see = see && j - sg.r.first < 64 && ((word >> (j - sg.r.first)) & 1u);
-                                if (!see) s[c] = 0xff800000u;  // -inf
-                            }
-                        }
-                        float mx[4];
+                            for (int e = 0; e < 32; ++e)
+                                if (!((see >> e) & 1u)) v[e] = 0xff800000u;  // -inf
+                        };
+                        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                        auto maxima = [&](const uint32_t *v) {
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) mx[c] = __uint_as_float(s[c]);
+                            for (int e = 0; e < 32; e += 8)
 #pragma unroll
-                        for (int c = 4; c < 128; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(s[c]));
-                        const float now = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                                for (int f = 0; f < 4; ++f)
+                                    mx[f] = max3(mx[f], __uint_as_float(v[e + f]), __uint_as_float(v[e + f + 4]));
+                        };
+                        // columns 64.. stay in registers (P goes there), 0..63 are read twice
+                        uint32_t v0[32], v2[32], v3[32];
+                        tmem_ld32(s_at, v0);
+                        tmem_ld32(s_at + 64, v2);
+                        tmem_wait_ld(v0);
+                        tmem_pass(v2);
+                        mask(v0, 0);
+                        maxima(v0);
+                        tmem_ld32(s_at + 32, v0);
+                        tmem_ld32(s_at + 96, v3);
+                        mask(v2, 2);
+                        maxima(v2);
+                        tmem_wait_ld(v0);
+                        tmem_pass(v3);
+                        mask(v0, 1);
+                        maxima(v0);
+                        tmem_ld32(s_at, v0);
+                        mask(v3, 3);
+                        maxima(v3);
+                        const float now = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
                         // the first maximum of a run is taken as it is; later ones only when
                         // they have grown by more than 2^8
                         const bool grow = now > top && (top == -INFINITY || (now - top) * sl2 > 8.0f);
                         if (__any_sync(0xffffffffu, grow)) {
-                            const float f = grow ? ex2((top - now) * sl2) : 1.0f;
+                            const float f = grow ? kv_ex2((top - now) * sl2) : 1.0f;
                             if (grow) top = now;
                             sum *= f;
-                            if (k > 0 && __any_sync(0xffffffffu, f != 1.0f)) {
-#pragma unroll 1
-                                for (int c = 0; c < D / 16; ++c) {
-                                    float o[16];
-                                    tmem_ld_32x32b_x16_wait(o_at + 16 * c, o);
-                                    asm volatile(
-                                        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, "
-                                        "%5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(
-                                            o_at + 16 * c),
-                                        "f"(o[0] * f), "f"(o[1] * f), "f"(o[2] * f), "f"(o[3] * f),
-                                        "f"(o[4] * f), "f"(o[5] * f), "f"(o[6] * f), "f"(o[7] * f),
-                                        "f"(o[8] * f), "f"(o[9] * f), "f"(o[10] * f), "f"(o[11] * f),
-                                        "f"(o[12] * f), "f"(o[13] * f), "f"(o[14] * f), "f"(o[15] * f)
-                                        : "memory");
-                                }
-                            }
+                            if (k > 0) scale_o<D>(o_at, f);
                         }
                         const float off = top == -INFINITY ? 0.0f : -top * sl2;
                         const uint64_t sc2 = pack2(sl2, sl2), off2 = pack2(off, off);
                         uint64_t sum2[2] = {pack2(sum, 0.0f), 0};
+                        auto exps = [&](const uint32_t *v, int c) {
+                            uint32_t p[16];
 #pragma unroll
-                        for (int c = 0; c < 128; c += 2) {
-                            float x, y;
-                            unpack2(fma2(pack2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), sc2, off2),
-                                    x, y);
-                            x = ex2(x);
-                            y = ex2(y);
-                            sum2[(c >> 1) & 1] = add2(sum2[(c >> 1) & 1], pack2(x, y));
-                            s[c / 2] = as_u32(__floats2half2_rn(x, y));
-                        }
+                            for (int e = 0; e < 32; e += 2) {
+                                float x, y;
+                                unpack2(fma2(pack2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), sc2, off2),
+                                        x, y);
+                                x = kv_ex2(x);
+                                y = kv_ex2(y);
+                                sum2[(e >> 1) & 1] = add2(sum2[(e >> 1) & 1], pack2(x, y));
+                                p[e / 2] = as_u32(__floats2half2_rn(x, y));
+                            }
+                            tmem_st16(s_at + 64 + 16 * c, p);
+                        };
+                        exps(v2, 2);
+                        tmem_wait_ld(v0);
+                        mask(v0, 0);
+                        tmem_ld32(s_at + 32, v2);
+                        exps(v3, 3);
+                        exps(v0, 0);
+                        tmem_wait_ld(v2);
+                        mask(v2, 1);
+                        exps(v2, 1);
                         float x, y;
                         unpack2(add2(sum2[0], sum2[1]), x, y);
                         sum = x + y;
-                        uint32_t *s2 = s;
-                        tmem_st_32x32b_x32(s_at, *reinterpret_cast<const uint32_t(*)[32]>(s2));
-                        tmem_st_32x32b_x32(s_at + 32, *reinterpret_cast<const uint32_t(*)[32]>(s2 + 32));
                         tmem_wait_st();
                     }
                     tc_fence_before();
@@ -592,125 +770,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnAr
                 tc_fence_before();  // the reads of O before the next run's first product
             }
             fewer_regs<kRegsLaunch>();
-        } else if (w < 12) {
+            named_bar_sync(kBarRegs, kThreads);
+        } else if (w < 16) {
             // ----------------------------------------------- codes to operand tiles --
             fewer_regs<kRegsCodes>();
-            constexpr int kLanesRow = D == 128 ? 4 : 2;         // 16-byte chunks of a row
-            constexpr int kStep = 128 / kLanesRow;              // rows of one load of the group
-            const int dt = tid - 256, row_l = dt / kLanesRow, ch = dt % kLanesRow;
-            const int ps = a.pool.ps;
-            Ring kr(2), vr(2);
-            uint32_t tiles = 0;
-            bool gave_up = false;
-            while (!gave_up && walk.next(a, sg)) {
-                const int32_t *table = a.batch.tables + (size_t)sg.b * a.batch.stride;
-                const int ppt = kTok / ps;
-                int e_base = 0, ids = -1;
-                auto load_ids = [&](int from) {
-                    e_base = from;
-                    const int e = from + lane;
-                    ids = -1;
-                    if (e < (sg.tile0 + sg.n) * ppt && (long long)e * ps < sg.r.end) {
-                        ids = table[e];
-                        if ((unsigned)ids >= (unsigned)a.pool.n_pages) {
-                            ids = -1;
-                            if (sg.h == 0 && w == 8) kv_report(a.err, MOE_KV4_DEVERR_PAGE);
-                        }
-                    }
-                };
-                load_ids(sg.tile0 * ppt);
-                Packed<D> pk;
-                uint32_t ok_next = 0;
-                // requests the k-th tile's K (or V) part of this thread
-                auto load = [&](int k, bool key) {
-                    const int e0 = (sg.tile0 + k) * ppt;
-                    if (key && e0 + ppt > e_base + 32) load_ids(e0);
-                    if (key) {
-                        uint32_t ok = 0;
-                        for (int i = 0; i < ppt; ++i)
-                            if (__shfl_sync(0xffffffffu, ids, e0 - e_base + i) >= 0)
-                                ok |= ((1u << (ps / 16)) - 1u) << (i * (ps / 16));
-                        ok_next = ok;
-                    }
-#pragma unroll
-                    for (int i = 0; i < C::kLoads; ++i) {
-                        const int row = i * kStep + row_l;
-                        const int id = __shfl_sync(0xffffffffu, ids, e0 - e_base + row / ps);
-                        const bool live = id >= 0 && (sg.tile0 + k) * kTok + row < sg.r.end;
-                        const int slot = row & (ps - 1);
-                        const uint8_t *blk = kv_block(a.pool, live ? id : 0, sg.h);
-                        const uint8_t *code = blk + (key ? 0 : ps * (D / 2)) + slot * (D / 2) + 16 * ch;
-                        const uint32_t *sc = reinterpret_cast<const uint32_t *>(
-                            blk + ps * D + (key ? 0 : ps * (NG * 2)) + slot * (NG * 2));
-                        uint4 c = make_uint4(0, 0, 0, 0);
-                        uint32_t z[D / 64];
-#pragma unroll
-                        for (int x = 0; x < D / 64; ++x) z[x] = 0;
-                        if (live) {
-                            c = *reinterpret_cast<const uint4 *>(code);
-#pragma unroll
-                            for (int x = 0; x < D / 64; ++x) z[x] = sc[x];
-                        }
-                        (key ? pk.k[i] : pk.v[i]) = c;
-#pragma unroll
-                        for (int x = 0; x < D / 64; ++x) (key ? pk.ks[i][x] : pk.vs[i][x]) = z[x];
-                    }
-                };
-                load(0, true);
-                load(0, false);
-                for (int k = 0; k < sg.n; ++k) {
-                    // K: the chunk's words are (t, G) for its t's; a word is dimensions
-                    // 32G + 8t.., the row's 16-byte chunk 4G + t
-                    if (__any_sync(0xffffffffu,
-                                   !mbar_wait(bar(kKEmpty + kr.idx), kr.ph ^ 1, abort_flag, a.err))) {
-                        gave_up = true;
-                        break;
-                    }
-                    if (dt == 0) sh.ok[tiles & 7] = ok_next;
-                    ++tiles;
-                    const uint32_t kd = smem + C::kK + kr.idx * C::kTileBytes;
-#pragma unroll
-                    for (int i = 0; i < C::kLoads; ++i) {
-                        const int row = i * kStep + row_l;
-                        const uint32_t words[4] = {pk.k[i].x, pk.k[i].y, pk.k[i].z, pk.k[i].w};
-#pragma unroll
-                        for (int u = 0; u < 4; ++u) {
-                            const int G = D == 128 ? u : u & 1, t = D == 128 ? ch : 2 * ch + (u >> 1);
-                            const uint32_t s = __byte_perm(pk.ks[i][G / 2], 0, G & 1 ? 0x3232 : 0x1010);
-                            uint32_t x[4];
-                            scaled_codes(words[u], s, x);
-                            sts128(kd + tile_at(row, 4 * G + t), x[0], x[1], x[2], x[3]);
-                        }
-                    }
-                    fence_proxy_async_shared();
-                    mbar_arrive(bar(kKFull + kr.idx));
-                    kr.next();
-                    if (k + 1 < sg.n) load(k + 1, true);
-                    // V: a word is piece g of groups 2p and 2p + 1, column chunk 8p + g
-                    if (__any_sync(0xffffffffu,
-                                   !mbar_wait(bar(kVEmpty + vr.idx), vr.ph ^ 1, abort_flag, a.err))) {
-                        gave_up = true;
-                        break;
-                    }
-                    const uint32_t vd = smem + C::kV + vr.idx * C::kTileBytes;
-#pragma unroll
-                    for (int i = 0; i < C::kLoads; ++i) {
-                        const int row = i * kStep + row_l;
-                        const uint32_t words[4] = {pk.v[i].x, pk.v[i].y, pk.v[i].z, pk.v[i].w};
-#pragma unroll
-                        for (int u = 0; u < 4; ++u) {
-                            const int pp = D == 128 ? u & 1 : 0, g = D == 128 ? 2 * ch + (u >> 1) : 4 * ch + u;
-                            uint32_t x[4];
-                            scaled_codes(words[u], pk.vs[i][pp], x);
-                            sts128(vd + tile_at(row, 8 * pp + g), x[0], x[1], x[2], x[3]);
-                        }
-                    }
-                    fence_proxy_async_shared();
-                    mbar_arrive(bar(kVFull + vr.idx));
-                    vr.next();
-                    if (k + 1 < sg.n) load(k + 1, false);
-                }
-            }
+            if (w < 12)
+                unpack_role<D, 0>(a, sh, smem, walk);
+            else
+                unpack_role<D, 1>(a, sh, smem, walk);
+            named_bar_sync(kBarRegs, kThreads);
             more_regs<kRegsLaunch>();
         } else {
             fewer_regs<kRegsMma>();
@@ -725,7 +793,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnAr
                 tc_fence_after();
                 return !gave_up;
             };
-            while (w == 12 && !gave_up && walk.next(a, sg)) {
+            while (w == 16 && !gave_up && walk.next(a, sg)) {
                 const int nm = sg.rows > 128 ? 2 : 1;
                 for (int m = 0; m < nm; ++m) {
                     if (!wait(kQFull + m, q_ph[m])) break;
@@ -743,7 +811,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnAr
                     for (int m = 0; m < nm; ++m) {
                         if (!wait(kPFull + m, p_ph[m])) break;
                         p_ph[m] ^= 1;
-                        mma_pv(o_col(m), s_col(m), smem + C::kV + vr.idx * C::kTileBytes, id_o, k > 0);
+                        mma_pv(o_col(m), p_col(m), smem + C::kV + vr.idx * C::kTileBytes, id_o, k > 0);
                         tc_commit2_elect(k == sg.n - 1 ? bar(kOFull + m) : 0u,
                                          m == nm - 1 ? bar(kVEmpty + vr.idx) : 0u);
                         if (k + 1 < sg.n) {
@@ -757,6 +825,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnAr
                     if (k + 1 < sg.n) kr.next();
                 }
             }
+            named_bar_sync(kBarRegs, kThreads);
             more_regs<kRegsLaunch>();
         }
     }
@@ -764,7 +833,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnAr
     __threadfence();
     __syncthreads();
     tc_fence_after();
-    if (w == 15) tmem_dealloc(tmem, kTmemCols);
+    if (w == 19) tmem_dealloc(tmem, kTmemCols);
 
     // items shared with other CTAs: the last of them adds the parts up
     constexpr int kQuads = D / 4;
@@ -785,27 +854,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnAr
         const Request rq = request_of(a, sh.part_b[part]);
         const int rt = sh.part_rt[part], h = sh.part_h[part];
         const int rows = min(kRowsItem, rq.rows - rt * kRowsItem);
+        const int odd = u0 > c0 * per ? 1 : 0;  // in its first CTA the item is the last one
+#pragma unroll 4
         for (int e = tid; e < rows * kQuads; e += kThreads) {
             const int row = e / kQuads, d4 = e % kQuads;
-            float mm = -INFINITY, ll = 0.0f;
-            float4 s = make_float4(0, 0, 0, 0);
-            for (uint32_t c = c0; c <= c1; ++c) {
-                const float *pr = a.cta_slots +
-                                  ((size_t)2 * c + (c == c0 && u0 > c0 * per ? 1 : 0)) * C::kSlot +
-                                  row * C::kPitch;
-                const float pm = pr[D], pl = pr[D + 1];
-                const float4 v = *reinterpret_cast<const float4 *>(pr + 4 * d4);
-                const float nm = fmaxf(mm, pm);
-                const float x = mm > -INFINITY ? ex2((mm - nm) * sl2) : 0.0f;
-                const float y = pm > -INFINITY ? ex2((pm - nm) * sl2) : 0.0f;
-                mm = nm;
-                ll = ll * x + pl * y;
-                s.x = s.x * x + v.x * y;
-                s.y = s.y * x + v.y * y;
-                s.z = s.z * x + v.z * y;
-                s.w = s.w * x + v.w * y;
-            }
-            const int rr = rt * kRowsItem + row, i = rr / a.group, hh = rr - i * a.group;
+            float mm, ll;
+            float4 s;
+            add_parts<D, 2>((int)(c1 - c0) + 1, d4, sl2,
+                            [&](int i) {
+                                return a.cta_slots + ((size_t)2 * (c0 + i) + (i ? 0 : odd)) * C::kSlot +
+                                       row * C::kPitch;
+                            },
+                            mm, ll, s);
+            const int rr = rt * kRowsItem + row, i = div_group(rr, a.gdiv), hh = rr - i * a.group;
             const size_t o = (size_t)(rq.q0 + i) * a.q_heads + h * a.group + hh;
             const float inv = ll > 0.0f ? 1.0f / ll : 0.0f;
             const __nv_bfloat162 lo = __floats2bfloat162_rn(s.x * inv, s.y * inv);
