@@ -12,11 +12,16 @@
 // its last rescale (the probabilities then stay below 2^8, far inside fp16, and
 // the quotient O / l does not depend on m).
 //
-// Roles of the 20 warps: two warpgroups each own one tile of rows (load its Q,
-// softmax, output); one turns K's codes into fp16 operand tiles and one V's, their
-// loads one tile ahead in registers; one warp issues the MMAs, alternating between
-// the two tiles of rows so that the softmax of one runs under the products of the
-// other.  K tiles are K-major, V tiles are left in token order and read N-major;
+// Roles of the 28 warps: two warpgroups each own one tile of rows, a thread half of
+// a row's columns (they load its Q, do the softmax, write the output; the maximum
+// of a row passes between its two threads through shared memory); one warpgroup
+// turns K's codes into fp16 operand tiles and one V's, their loads one tile ahead in
+// registers; a warp for each tile of rows issues its MMAs, so that the softmax of one
+// runs under the products of the other.  A row in two
+// threads: with a thread a whole row (half the warps, twice the registers each) a
+// tile's softmax took about 1900 cycles, most of it latency, against 1024 for the
+// tensor pipe between a tile's P and its next S.
+// K tiles are K-major, V tiles are left in token order and read N-major;
 // the order of V's columns is the order in which its codes unpack, undone when
 // the output is written.
 //
@@ -33,22 +38,21 @@ namespace {
 constexpr int kTok = 128;        // tokens of a unit
 constexpr int kRowsItem = 256;
 constexpr int kChunks = 1024;
-constexpr int kThreads = 640;
+constexpr int kThreads = 896;
 constexpr uint32_t kTmemCols = 512;
-// Registers a thread of each role (multiples of 8).  The five warpgroups' shares add
-// up to what the block is launched with, 5 x 96.
-constexpr int kRegsLaunch = 96, kRegsSoftmax = 136, kRegsCodes = 72, kRegsMma = 64;
-static_assert(2 * kRegsSoftmax + 2 * kRegsCodes + kRegsMma == 5 * kRegsLaunch, "register shares");
+// Registers a thread of each role (multiples of 8).  The seven warpgroups' shares add
+// up to what the block is launched with, 7 x 72.
+constexpr int kRegsLaunch = 72, kRegsSoftmax = 88, kRegsCodes = 56, kRegsMma = 40;
+static_assert(4 * kRegsSoftmax + 2 * kRegsCodes + kRegsMma == 7 * kRegsLaunch, "register shares");
 static_assert(kThreads * kRegsLaunch <= 65536, "the register file");
 // Before the block's common end every warp returns to kRegsLaunch.  Those that take
 // registers back wait at this barrier until those that give them up have done so,
 // and until the softmax warps have had theirs: a warp with no work that took its
 // share back early would keep it from a softmax warp that still waits for it.
-constexpr uint32_t kBarRegs = 1;
+constexpr uint32_t kBarRegs = 1, kBarTile = 2;  // kBarTile + m: the 256 threads of row tile m
 
 template <int D>
 struct Cfg {
-    static constexpr int NG = D / 32;
     static constexpr int kTileBytes = kTok * D * 2;   // an operand tile
     static constexpr int kQ = 0;                      // two tiles of rows
     static constexpr int kK = 2 * kTileBytes;         // two K tiles, two V tiles
@@ -67,6 +71,7 @@ struct Shared {
     int abort_flag, last_of;
     uint32_t ok[8];              // runs of 16 tokens that have a page, by tile
     uint32_t prefix[kChunks + 1];
+    float top[2][2][2][128];     // a tile's row maxima: by parity, row tile, half
     uint32_t part_u0[2], part_u1[2];
     int part_b[2], part_h[2], part_rt[2];
 };
@@ -333,11 +338,11 @@ MOE_DEV void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
         : "memory");
 }
 
-// Multiplies the thread's row of O (rarely needed: see the file's head).
+// Multiplies the thread's half row of O (rarely needed: see the file's head).
 template <int D>
 MOE_DEV void scale_o(uint32_t o_at, float f) {
 #pragma unroll 1
-    for (int c = 0; c < D / 16; ++c) {
+    for (int c = 0; c < D / 32; ++c) {
         float o[16];
         tmem_ld_32x32b_x16_wait(o_at + 16 * c, o);
         uint32_t v[16];
@@ -384,13 +389,27 @@ MOE_DEV void load_part(Packed<D> &p, const KvPool &pool, int head, int ids, int 
     }
 }
 
+// The row that a thread unpacks first.  The eight lanes of a store phase hold two
+// rows (D = 64: four); their order puts the swizzled 16-byte chunks that the lanes
+// store at once into different banks: K stores chunks 4G + t of all t together, so
+// rows four apart, V stores every other chunk, so neighbouring rows.
+template <int D, int part>
+MOE_DEV int row_of_lane(int dt) {
+    const int warp = dt >> 5, l = dt & 31;
+    if (D == 128) return 8 * warp + (part == 0 ? (l >> 3) + 4 * ((l >> 2) & 1) : l >> 2);
+    if (part == 1) return 16 * warp + (l >> 1);
+    const int i = (l >> 1) & 3, j = l >> 3;
+    return 16 * warp + (i & 1) + 4 * (i >> 1) + 2 * (j & 1) + 8 * (j >> 1);
+}
+
 // The warpgroup that turns one side's codes (part 0: K, 1: V) into operand tiles.
 template <int D, int part>
 MOE_DEV void unpack_role(const KvAttnArgs &a, Shared &sh, uint32_t smem, Walk walk) {
     using C = Cfg<D>;
     constexpr int kLanesRow = D == 128 ? 4 : 2;  // 16-byte chunks of a row
     constexpr int kStep = 128 / kLanesRow;       // rows of one load of the group
-    const int lane = threadIdx.x & 31, dt = threadIdx.x & 127, row_l = dt / kLanesRow, ch = dt % kLanesRow;
+    const int lane = threadIdx.x & 31, dt = threadIdx.x & 127, ch = dt % kLanesRow;
+    const int row_l = row_of_lane<D, part>(dt);
     const int ps = a.pool.ps, ppt = kTok / ps;
     const uint32_t full = smem_u32(&sh.bar[part ? kVFull : kKFull]);
     const uint32_t empty = smem_u32(&sh.bar[part ? kVEmpty : kKEmpty]);
@@ -487,12 +506,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnAr
     pdl_wait();
     if (tid == 0) {
         sh.abort_flag = 0;
-        const int counts[8] = {128, 1, 128, 1, 128, 1, 128, 1};
+        const int counts[8] = {128, 2, 128, 2, 256, 1, 256, 1};
         for (int i = 0; i < kBars; ++i) mbar_init(smem_u32(&sh.bar[i]), counts[i / 2]);
         mbar_fence_init();
         sh.part_u0[0] = sh.part_u1[0] = sh.part_u0[1] = sh.part_u1[1] = 0;
     }
-    if (w == 19) {
+    if (w == 27) {
         tmem_alloc(smem_u32(&sh.tmem), kTmemCols);
         tmem_relinquish();
     }
@@ -559,13 +578,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnAr
         Walk walk;
         walk.start(a, sh.prefix, chunks, per_chunk, c_lo, c_hi);
         Segment sg;
-        if (w < 8) {
+        if (w < 16) {
             // ------------------------------------------- softmax of a tile of rows --
             more_regs<kRegsSoftmax>();
-            const int m = w >> 2, r = tid & 127;  // the thread's row in its tile
+            // the thread's row tile, half of the columns and row
+            const int m = w >> 3, half = (w >> 2) & 1, r = tid & 127;
             const uint32_t lane_off = (uint32_t)(32 * (w & 3)) << 16;
-            const uint32_t s_at = s_col(m) + lane_off, o_at = o_col(m) + lane_off;
+            const uint32_t s_at = s_col(m) + lane_off + 64u * half;
+            const uint32_t p_at = p_col(m) + lane_off + 32u * half;
+            const uint32_t o_at = o_col(m) + lane_off + (D / 2) * half;
             uint32_t s_ph = 0, o_ph = 0, tiles = 0;
+            bool dead = false;
             while (walk.next(a, sg)) {
                 if (m * 128 >= sg.rows) {
                     tiles += sg.n;
@@ -576,11 +599,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnAr
                 bool bad = false;
                 const uint32_t flip = a.scale_log2 < 0.0f ? 0x80008000u : 0u;
 #pragma unroll
-                for (int c0 = 0; c0 < D / 8; c0 += 8) {
-                    uint4 v[8];
+                for (int c0 = 0; c0 < D / 16; c0 += 4) {
+                    uint4 v[4];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int c = r + 128 * (c0 + e), qr = c / (D / 8), ch = c % (D / 8);
+                    for (int e = 0; e < 4; ++e) {
+                        const int c = (tid & 255) + 256 * (c0 + e), qr = c / (D / 8), ch = c % (D / 8);
                         const int i = div_group(row_base + qr, a.gdiv), hh = row_base + qr - i * a.group;
                         v[e] = make_uint4(0, 0, 0, 0);
                         if (qr < n_rows)
@@ -589,8 +612,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnAr
                                 (size_t)(sg.h * a.group + hh) * D + 8 * ch);
                     }
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int c = r + 128 * (c0 + e), qr = c / (D / 8), ch = c % (D / 8);
+                    for (int e = 0; e < 4; ++e) {
+                        const int c = (tid & 255) + 256 * (c0 + e), qr = c / (D / 8), ch = c % (D / 8);
                         const uint4 x = bf16x8_to_f16x8_sat(v[e], bad);
                         sts128(smem + C::kQ + m * C::kTileBytes + tile_at(qr, ch), x.x ^ flip, x.y ^ flip,
                                x.z ^ flip, x.w ^ flip);
@@ -610,127 +633,118 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnAr
                 const int open = __reduce_min_sync(0xffffffffu, live ? (a.tree ? min(hi + 1, sg.r.first) : hi + 1)
                                                                      : INT32_MAX);
                 const int shut = __reduce_max_sync(0xffffffffu, live ? lo + 1 : 0);
-                const bool any_live = __any_sync(0xffffffffu, live);
                 float top = -INFINITY, sum = 0.0f;
-                bool gave_up = false;
                 for (int k = 0; k < sg.n; ++k) {
-                    const bool ok_wait = mbar_wait(bar(kSFull + m), s_ph, abort_flag, a.err);
+                    // a wait that gave up (a kernel bug, reported) leaves the loop's shape
+                    // as it is: the tile's other warps count on this one at the barriers
+                    if (!dead) dead = __any_sync(0xffffffffu, !mbar_wait(bar(kSFull + m), s_ph, abort_flag, a.err));
                     s_ph ^= 1;
-                    if (__any_sync(0xffffffffu, !ok_wait)) {
-                        gave_up = true;
-                        break;
-                    }
                     tc_fence_after();
-                    const uint32_t ok = sh.ok[tiles & 7];
+                    const uint32_t ok = sh.ok[tiles & 7] >> (4 * half);
+                    float *swap = &sh.top[tiles & 1][m][0][r];
                     ++tiles;
-                    if (any_live) {
-                        const int j0 = (sg.tile0 + k) * kTok;
-                        const bool masked = ok != 0xFFu || j0 + kTok > open || j0 < shut;
-                        auto mask = [&](uint32_t *v, int c) {
-                            if (!masked) return;
+                    const int j0 = (sg.tile0 + k) * kTok + 64 * half;
+                    const bool masked = (ok & 15u) != 15u || j0 + 64 > open || j0 < shut;
+                    uint32_t v[64];
+                    tmem_ld32(s_at, v);
+                    tmem_ld32(s_at + 32, v + 32);
+                    tmem_wait_ld(v);
+                    tmem_pass(v + 32);
+                    if (masked) {
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
                             const uint32_t see = visible32(j0 + 32 * c, lo, hi, ok >> (2 * c),
                                                            a.tree != nullptr, word, sg.r.first);
 #pragma unroll
                             for (int e = 0; e < 32; ++e)
-                                if (!((see >> e) & 1u)) v[e] = 0xff800000u;  // -inf
-                        };
-                        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                        auto maxima = [&](const uint32_t *v) {
-#pragma unroll
-                            for (int e = 0; e < 32; e += 8)
-#pragma unroll
-                                for (int f = 0; f < 4; ++f)
-                                    mx[f] = max3(mx[f], __uint_as_float(v[e + f]), __uint_as_float(v[e + f + 4]));
-                        };
-                        // columns 64.. stay in registers (P goes there), 0..63 are read twice
-                        uint32_t v0[32], v2[32], v3[32];
-                        tmem_ld32(s_at, v0);
-                        tmem_ld32(s_at + 64, v2);
-                        tmem_wait_ld(v0);
-                        tmem_pass(v2);
-                        mask(v0, 0);
-                        maxima(v0);
-                        tmem_ld32(s_at + 32, v0);
-                        tmem_ld32(s_at + 96, v3);
-                        mask(v2, 2);
-                        maxima(v2);
-                        tmem_wait_ld(v0);
-                        tmem_pass(v3);
-                        mask(v0, 1);
-                        maxima(v0);
-                        tmem_ld32(s_at, v0);
-                        mask(v3, 3);
-                        maxima(v3);
-                        const float now = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
-                        // the first maximum of a run is taken as it is; later ones only when
-                        // they have grown by more than 2^8
-                        const bool grow = now > top && (top == -INFINITY || (now - top) * sl2 > 8.0f);
-                        if (__any_sync(0xffffffffu, grow)) {
-                            const float f = grow ? kv_ex2((top - now) * sl2) : 1.0f;
-                            if (grow) top = now;
-                            sum *= f;
-                            if (k > 0) scale_o<D>(o_at, f);
+                                if (!((see >> e) & 1u)) v[32 * c + e] = 0xff800000u;  // -inf
                         }
-                        const float off = top == -INFINITY ? 0.0f : -top * sl2;
-                        const uint64_t sc2 = pack2(sl2, sl2), off2 = pack2(off, off);
-                        uint64_t sum2[2] = {pack2(sum, 0.0f), 0};
-                        auto exps = [&](const uint32_t *v, int c) {
-                            uint32_t p[16];
+                    }
+                    float mx[4];
 #pragma unroll
-                            for (int e = 0; e < 32; e += 2) {
-                                float x, y;
-                                unpack2(fma2(pack2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), sc2, off2),
-                                        x, y);
-                                x = kv_ex2(x);
-                                y = kv_ex2(y);
-                                sum2[(e >> 1) & 1] = add2(sum2[(e >> 1) & 1], pack2(x, y));
-                                p[e / 2] = as_u32(__floats2half2_rn(x, y));
-                            }
-                            tmem_st16(s_at + 64 + 16 * c, p);
-                        };
-                        exps(v2, 2);
-                        tmem_wait_ld(v0);
-                        mask(v0, 0);
-                        tmem_ld32(s_at + 32, v2);
-                        exps(v3, 3);
-                        exps(v0, 0);
-                        tmem_wait_ld(v2);
-                        mask(v2, 1);
-                        exps(v2, 1);
+                    for (int e = 0; e < 4; ++e)
+                        mx[e] = fmaxf(__uint_as_float(v[e]), __uint_as_float(v[e + 4]));
+#pragma unroll
+                    for (int e = 8; e < 64; e += 8)
+#pragma unroll
+                        for (int f = 0; f < 4; ++f)
+                            mx[f] = max3(mx[f], __uint_as_float(v[e + f]), __uint_as_float(v[e + f + 4]));
+                    float now = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
+                    // the other half's maximum; after the barrier S has been read, too,
+                    // and P may be written over it
+                    swap[128 * half] = now;
+                    tc_fence_before();
+                    named_bar_sync(kBarTile + m, 256);
+                    tc_fence_after();
+                    now = fmaxf(now, swap[128 * (half ^ 1)]);
+                    // the first maximum of a run is taken as it is; later ones only when
+                    // they have grown by more than 2^8
+                    const bool grow = now > top && (top == -INFINITY || (now - top) * sl2 > 8.0f);
+                    if (__any_sync(0xffffffffu, grow)) {
+                        const float f = grow ? kv_ex2((top - now) * sl2) : 1.0f;
+                        if (grow) top = now;
+                        sum *= f;
+                        if (k > 0) scale_o<D>(o_at, f);
+                    }
+                    const float off = top == -INFINITY ? 0.0f : -top * sl2;
+                    const uint64_t sc2 = pack2(sl2, sl2), off2 = pack2(off, off);
+                    uint64_t sum2[2] = {pack2(sum, 0.0f), 0};
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        uint32_t p[16];
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            float x, y;
+                            unpack2(fma2(pack2(__uint_as_float(v[32 * c + e]),
+                                               __uint_as_float(v[32 * c + e + 1])),
+                                         sc2, off2),
+                                    x, y);
+                            x = kv_ex2(x);
+                            y = kv_ex2(y);
+                            sum2[(e >> 1) & 1] = add2(sum2[(e >> 1) & 1], pack2(x, y));
+                            p[e / 2] = as_u32(__floats2half2_rn(x, y));
+                        }
+                        tmem_st16(p_at + 16 * c, p);
+                    }
+                    {
                         float x, y;
                         unpack2(add2(sum2[0], sum2[1]), x, y);
                         sum = x + y;
-                        tmem_wait_st();
                     }
+                    tmem_wait_st();
                     tc_fence_before();
                     mbar_arrive(bar(kPFull + m));
                 }
-                if (gave_up) break;
                 // O of the run
-                const bool ok_wait = mbar_wait(bar(kOFull + m), o_ph, abort_flag, a.err);
+                if (!dead) dead = __any_sync(0xffffffffu, !mbar_wait(bar(kOFull + m), o_ph, abort_flag, a.err));
                 o_ph ^= 1;
-                if (__any_sync(0xffffffffu, !ok_wait)) break;
                 tc_fence_after();
-                if (any_live) {
+                {
+                    // the row's sum: its second half's part passes to both threads
+                    float *swap = &sh.top[0][m][0][r];
+                    swap[128 * half] = sum;
+                    named_bar_sync(kBarTile + m, 256);
+                    sum += swap[128 * (half ^ 1)];
+                    named_bar_sync(kBarTile + m, 256);  // read before the next run writes there
                     const float inv = sg.whole ? (sum > 0.0f ? 1.0f / sum : 0.0f) : 1.0f;
                     const size_t o_row = (size_t)(sg.r.q0 + i) * a.q_heads + sg.h * a.group + hh;
                     const int part = sg.i_u0 > c_lo ? 1 : 0;
                     float *slot = a.cta_slots + ((size_t)2 * blockIdx.x + part) * C::kSlot +
                                   (m * 128 + r) * C::kPitch;
 #pragma unroll 1
-                    for (int q = 0; q < D / 32; ++q) {
-                        // columns of four V pieces g = 4a..: two groups' 16 dimensions
+                    for (int q = 0; q < D / 64; ++q) {
+                        // 32 columns, four V pieces g = 4a..: two groups' 16 dimensions
                         uint32_t o[32];
                         tmem_ld32(o_at + 32 * q, o);
                         tmem_wait_ld(o);
-                        const int pp = q >> 1, d0 = 64 * pp + 16 * (q & 1);
+                        const int at = half * (D / 64) + q, d0 = 64 * (at >> 1) + 16 * (at & 1);
                         if (!live) continue;
 #pragma unroll
-                        for (int half = 0; half < 2; ++half) {
+                        for (int gr = 0; gr < 2; ++gr) {
                             float x[16];
 #pragma unroll
                             for (int e = 0; e < 16; ++e)
-                                x[e] = __uint_as_float(o[(e >> 2) * 8 + 2 * (e & 3) + half]) * inv;
+                                x[e] = __uint_as_float(o[(e >> 2) * 8 + 2 * (e & 3) + gr]) * inv;
                             if (sg.whole) {
                                 uint32_t y[8];
 #pragma unroll
@@ -738,18 +752,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnAr
                                     const __nv_bfloat162 z = __floats2bfloat162_rn(x[2 * e], x[2 * e + 1]);
                                     y[e] = *reinterpret_cast<const uint32_t *>(&z);
                                 }
-                                uint4 *dst = reinterpret_cast<uint4 *>(a.out + o_row * D + d0 + 32 * half);
+                                uint4 *dst = reinterpret_cast<uint4 *>(a.out + o_row * D + d0 + 32 * gr);
                                 dst[0] = make_uint4(y[0], y[1], y[2], y[3]);
                                 dst[1] = make_uint4(y[4], y[5], y[6], y[7]);
                             } else {
-                                float4 *dst = reinterpret_cast<float4 *>(slot + d0 + 32 * half);
+                                float4 *dst = reinterpret_cast<float4 *>(slot + d0 + 32 * gr);
 #pragma unroll
                                 for (int e = 0; e < 4; ++e)
                                     dst[e] = make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
                             }
                         }
                     }
-                    if (live) {
+                    if (live && half == 0) {
                         if (!sg.whole) {
                             slot[D] = top;
                             slot[D + 1] = sum;
@@ -771,10 +785,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnAr
             }
             fewer_regs<kRegsLaunch>();
             named_bar_sync(kBarRegs, kThreads);
-        } else if (w < 16) {
+        } else if (w < 24) {
             // ----------------------------------------------- codes to operand tiles --
             fewer_regs<kRegsCodes>();
-            if (w < 12)
+            if (w < 20)
                 unpack_role<D, 0>(a, sh, smem, walk);
             else
                 unpack_role<D, 1>(a, sh, smem, walk);
@@ -783,46 +797,55 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnAr
         } else {
             fewer_regs<kRegsMma>();
             // ----------------------------------------------------------------- MMAs --
+            // Warp 24 + m issues the products of row tile m.  The tensor pipe holds
+            // little more than the instruction it runs, so a warp's waits and commits
+            // would leave it idle; two warps fill each other's gaps.
+            const int m = w - 24;
             const uint32_t id_s = idesc_f16_m128(kTok);
             const uint32_t id_o = idesc_f16_m128(D) | (1u << 16);  // B N-major
+            const uint32_t q_at = smem + C::kQ + (uint32_t)m * C::kTileBytes;
             Ring kr(2), vr(2);
-            uint32_t p_ph[2] = {0, 0}, q_ph[2] = {0, 0};
-            bool gave_up = false;
+            uint32_t p_ph = 0, q_ph = 0;
+            bool ok = true;
             auto wait = [&](int b, uint32_t ph) {
-                if (__any_sync(0xffffffffu, !mbar_wait(bar(b), ph, abort_flag, a.err))) gave_up = true;
-                tc_fence_after();
-                return !gave_up;
+                ok = __all_sync(0xffffffffu, mbar_wait(bar(b), ph, abort_flag, a.err));
+                return ok;
             };
-            while (w == 16 && !gave_up && walk.next(a, sg)) {
-                const int nm = sg.rows > 128 ? 2 : 1;
-                for (int m = 0; m < nm; ++m) {
-                    if (!wait(kQFull + m, q_ph[m])) break;
-                    q_ph[m] ^= 1;
-                }
-                if (gave_up || !wait(kKFull + kr.idx, kr.ph)) break;
-                for (int m = 0; m < nm; ++m) {
-                    mma_qk<D>(s_col(m), smem + C::kQ + m * C::kTileBytes,
-                              smem + C::kK + kr.idx * C::kTileBytes, id_s);
-                    tc_commit2_elect(bar(kSFull + m), m == nm - 1 ? bar(kKEmpty + kr.idx) : 0u);
-                }
-                kr.next();
-                for (int k = 0; k < sg.n && !gave_up; ++k) {
-                    if (!wait(kVFull + vr.idx, vr.ph)) break;
-                    for (int m = 0; m < nm; ++m) {
-                        if (!wait(kPFull + m, p_ph[m])) break;
-                        p_ph[m] ^= 1;
-                        mma_pv(o_col(m), p_col(m), smem + C::kV + vr.idx * C::kTileBytes, id_o, k > 0);
-                        tc_commit2_elect(k == sg.n - 1 ? bar(kOFull + m) : 0u,
-                                         m == nm - 1 ? bar(kVEmpty + vr.idx) : 0u);
-                        if (k + 1 < sg.n) {
-                            if (m == 0 && !wait(kKFull + kr.idx, kr.ph)) break;
-                            mma_qk<D>(s_col(m), smem + C::kQ + m * C::kTileBytes,
-                                      smem + C::kK + kr.idx * C::kTileBytes, id_s);
-                            tc_commit2_elect(bar(kSFull + m), m == nm - 1 ? bar(kKEmpty + kr.idx) : 0u);
-                        }
+            while (m < 2 && ok && walk.next(a, sg)) {
+                if (m * 128 >= sg.rows) {
+                    // no rows: only lets the operand tiles pass
+                    for (int k = 0; k < sg.n; ++k) {
+                        if (!wait(kKFull + kr.idx, kr.ph)) break;
+                        if (lane == 0) mbar_arrive(bar(kKEmpty + kr.idx));
+                        kr.next();
+                        if (!wait(kVFull + vr.idx, vr.ph)) break;
+                        if (lane == 0) mbar_arrive(bar(kVEmpty + vr.idx));
+                        vr.next();
                     }
+                    continue;
+                }
+                if (!wait(kQFull + m, q_ph)) break;
+                q_ph ^= 1;
+                if (!wait(kKFull + kr.idx, kr.ph)) break;
+                tc_fence_after();
+                mma_qk<D>(s_col(m), q_at, smem + C::kK + kr.idx * C::kTileBytes, id_s);
+                tc_commit2_elect(bar(kSFull + m), bar(kKEmpty + kr.idx));
+                kr.next();
+                for (int k = 0; k < sg.n; ++k) {
+                    const bool more = k + 1 < sg.n;
+                    if (!wait(kVFull + vr.idx, vr.ph)) break;
+                    if (more && !wait(kKFull + kr.idx, kr.ph)) break;
+                    if (!wait(kPFull + m, p_ph)) break;
+                    p_ph ^= 1;
+                    tc_fence_after();
+                    mma_pv(o_col(m), p_col(m), smem + C::kV + vr.idx * C::kTileBytes, id_o, k > 0);
+                    if (more) {
+                        mma_qk<D>(s_col(m), q_at, smem + C::kK + kr.idx * C::kTileBytes, id_s);
+                        tc_commit2_elect(bar(kSFull + m), bar(kKEmpty + kr.idx));
+                        kr.next();
+                    }
+                    tc_commit2_elect(bar(kVEmpty + vr.idx), more ? 0u : bar(kOFull + m));
                     vr.next();
-                    if (k + 1 < sg.n) kr.next();
                 }
             }
             named_bar_sync(kBarRegs, kThreads);
@@ -833,7 +856,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnAr
     __threadfence();
     __syncthreads();
     tc_fence_after();
-    if (w == 19) tmem_dealloc(tmem, kTmemCols);
+    if (w == 27) tmem_dealloc(tmem, kTmemCols);
 
     // items shared with other CTAs: the last of them adds the parts up
     constexpr int kQuads = D / 4;
