@@ -33,6 +33,7 @@ namespace {
 
 constexpr int kTile = 64;       // tokens of a unit of work
 constexpr int kChunks = 1024;   // entries of the prefix table over requests
+constexpr float kSlack = 8.0f;
 
 template <int D, int NT>
 struct Cfg {
@@ -68,6 +69,12 @@ MOE_DEV void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint
         "{%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+MOE_DEV float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
 }
 
 MOE_DEV uint32_t transpose8x8(uint32_t v) {
@@ -130,7 +137,7 @@ MOE_DEV uint32_t units_of(const Request &r, int hkv) {
     return (uint32_t)r.tiles * (uint32_t)r.row_tiles * (uint32_t)hkv;
 }
 
-template <int D, int NT>
+template <int D, int NT, int PS>
 __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
     kv4_decode_kernel(const KvAttnArgs a) {
     using C = Cfg<D, NT>;
@@ -143,7 +150,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
     __shared__ uint32_t warp_tot[W];
     pdl_wait();
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, g = lane >> 2, t = lane & 3;
-    const int hkv = a.pool.hkv, ps = a.pool.ps, G = a.group;
+    const int hkv = a.pool.hkv, G = a.group;
+    constexpr int ps = PS, ppt = kTile / PS;          // pages of a tile
+    constexpr uint32_t kBlock = PS * (D + D / 8);     // bytes of a page of a head
     const float sl2 = fmaxf(fabsf(a.scale_log2), 1e-30f);
     if (tid == 0) abort_flag = 0;
     if (lane == 0)
@@ -227,8 +236,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
         const int tile_lo = rq.tile0 + (int)(u - i_u0), n_tiles = (int)(seg_end - u);
         const int row0 = rt * C::kRows, rows = min(C::kRows, rq.m * G - row0);
         const int32_t *table = a.batch.tables + (size_t)b * a.batch.stride;
-        const int ppt = kTile / ps;  // pages of a tile
 
+        const uint8_t *head_base = a.pool.base + (size_t)h * kBlock;
+        const size_t page_bytes = (size_t)hkv * kBlock;
         // page ids of the next tiles: lane l holds table entry e_base + l
         int e_base = tile_lo * ppt, ids = -1;
         auto load_ids = [&](int from) {
@@ -249,20 +259,22 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
         auto fetch = [&](int k, uint32_t slot) -> uint32_t {
             const int e = (tile_lo + k) * ppt;
             if (e + ppt > e_base + 32) load_ids(e);
-            uint32_t ok = 0, bytes = 0;
+            uint32_t ok = 0, have = 0;
+            int mine = -1;  // lane l < ppt copies the tile's page l
+#pragma unroll
             for (int i = 0; i < ppt; ++i) {
                 const int id = __shfl_sync(0xffffffffu, ids, e - e_base + i);
                 if (id >= 0) {
                     ok |= ((1u << (ps / 16)) - 1u) << (i * (ps / 16));
-                    bytes += a.pool.block;
+                    ++have;
                 }
+                if (lane == i) mine = id;
             }
-            if (lane == 0) mbar_arrive_expect_tx(my_bar + 8 * slot, bytes);
-            __syncwarp();
-            const int id = __shfl_sync(0xffffffffu, ids, min(31, e - e_base + lane));
-            if (lane < ppt && id >= 0)
-                bulk_copy(my_ring + slot * C::kTileBytes + lane * a.pool.block,
-                          kv_block(a.pool, id, h), a.pool.block, my_bar + 8 * slot);
+            if (lane == 0) mbar_arrive_expect_tx(my_bar + 8 * slot, have * kBlock);
+            if (ppt > 1) __syncwarp();
+            if (mine >= 0)
+                bulk_copy(my_ring + slot * C::kTileBytes + lane * kBlock,
+                          head_base + (size_t)mine * page_bytes, kBlock, my_bar + 8 * slot);
             return ok;
         };
         uint32_t ok_ring = 0;  // four bits a stage
@@ -315,9 +327,13 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
         const int open = min(rq.end, a.tree ? rq.first : rq.first + i_lo + 1);
         const int shut = a.window > 0 ? rq.first + i_hi - a.window + 1 : 0;
 
-        float m[NT][2], l[NT][2], acc[NG][2][NT][4];
+        // lim: the score from which a row's maximum moves
+        float m[NT][2], lim[NT][2], l[NT][2], acc[NG][2][NT][4];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) m[n][0] = m[n][1] = -INFINITY, l[n][0] = l[n][1] = 0.0f;
+        for (int n = 0; n < NT; ++n) {
+            m[n][0] = m[n][1] = lim[n][0] = lim[n][1] = -INFINITY;
+            l[n][0] = l[n][1] = 0.0f;
+        }
 #pragma unroll
         for (int x = 0; x < NG * 2 * NT * 4; ++x) (&acc[0][0][0][0])[x] = 0.0f;
 
@@ -333,9 +349,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
             const bool full = ok == 15u && j0 + kTile <= open && j0 >= shut;
             // a run of 16 tokens: its block and its first row there
             auto place = [&](int s, uint32_t &base, uint32_t &row) {
-                const int tok = 16 * s;
-                base = sb + (uint32_t)(tok / ps) * a.pool.block;
-                row = tok & (ps - 1);
+                base = sb + (uint32_t)(16 * s / ps) * kBlock;
+                row = 16 * s % ps;
             };
 
             float x[4][NT][4];
@@ -411,7 +426,10 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
                             }
                     }
             }
-            // running maximum and sum of each row (a column here: over the lanes g)
+            // Maximum and sum of each row (a column here: over the lanes g).  The maximum
+            // moves only when some score exceeds it by more than 2^kSlack: the
+            // probabilities then stay below that, far inside fp16, and neither the
+            // exchange between the lanes nor the rescaling is paid for every tile.
             uint32_t pb[4][NT][2];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
@@ -420,22 +438,25 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
                 for (int e = 0; e < 2; ++e) {
                     float v = fmaxf(x[0][n][e], x[0][n][2 + e]);
 #pragma unroll
-                    for (int s = 1; s < 4; ++s) v = fmaxf(v, fmaxf(x[s][n][e], x[s][n][2 + e]));
-                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
-                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
-                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-                    top[e] = fmaxf(v, m[n][e]);
+                    for (int s = 1; s < 4; ++s) v = max3(v, x[s][n][e], x[s][n][2 + e]);
+                    top[e] = v;
                 }
-                if (__any_sync(0xffffffffu, top[0] > m[n][0] || top[1] > m[n][1])) {
+                if (__any_sync(0xffffffffu, top[0] > lim[n][0] || top[1] > lim[n][1])) {
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const float r = top[e] > m[n][e] ? kv_ex2((m[n][e] - top[e]) * sl2) : 1.0f;
-                        m[n][e] = top[e];
+                        float v = top[e];
+                        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+                        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+                        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+                        v = fmaxf(v, m[n][e]);
+                        const float r = v > m[n][e] ? kv_ex2((m[n][e] - v) * sl2) : 1.0f;
+                        m[n][e] = v;
+                        lim[n][e] = v + kSlack / sl2;
                         l[n][e] *= r;
 #pragma unroll
                         for (int G4 = 0; G4 < NG; ++G4)
 #pragma unroll
-                            for (int v = 0; v < 2; ++v) acc[G4][v][n][e] *= r, acc[G4][v][n][2 + e] *= r;
+                            for (int c = 0; c < 2; ++c) acc[G4][c][n][e] *= r, acc[G4][c][n][2 + e] *= r;
                     }
                 }
                 const float o0 = m[n][0] == -INFINITY ? 0.0f : -m[n][0] * sl2;
@@ -643,7 +664,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
     }
 }
 
-template <int D, int NT>
+template <int D, int NT, int PS>
 cudaError_t launch(const KvAttnArgs &a, int grid, cudaStream_t s) {
     using C = Cfg<D, NT>;
     static bool set[64];
@@ -651,7 +672,7 @@ cudaError_t launch(const KvAttnArgs &a, int grid, cudaStream_t s) {
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64 || !set[dev]) {
-        e = cudaFuncSetAttribute(kv4_decode_kernel<D, NT>,
+        e = cudaFuncSetAttribute(kv4_decode_kernel<D, NT, PS>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) set[dev] = true;
@@ -660,7 +681,16 @@ cudaError_t launch(const KvAttnArgs &a, int grid, cudaStream_t s) {
     cudaLaunchAttribute at{};
     c.numAttrs = pdl_attr(at);
     c.attrs = &at;
-    return cudaLaunchKernelEx(&c, kv4_decode_kernel<D, NT>, a);
+    return cudaLaunchKernelEx(&c, kv4_decode_kernel<D, NT, PS>, a);
+}
+
+template <int D, int NT>
+cudaError_t launch_ps(const KvAttnArgs &a, int grid, cudaStream_t s) {
+    switch (a.pool.ps) {
+        case 16: return launch<D, NT, 16>(a, grid, s);
+        case 32: return launch<D, NT, 32>(a, grid, s);
+        default: return launch<D, NT, 64>(a, grid, s);
+    }
 }
 
 }  // namespace
@@ -685,8 +715,8 @@ cudaError_t launch_kv4_decode(KvAttnArgs a, int D, int max_rows, void *slots, in
     long long most = tiles * row_tiles * a.pool.hkv * a.batch.requests;
     most = (most + a.min_units - 1) / a.min_units;
     const int grid = (int)(most < 1 ? 1 : most < ctas ? most : ctas);
-    if (D == 128) return nt == 1 ? launch<128, 1>(a, grid, s) : launch<128, 2>(a, grid, s);
-    return nt == 1 ? launch<64, 1>(a, grid, s) : launch<64, 2>(a, grid, s);
+    if (D == 128) return nt == 1 ? launch_ps<128, 1>(a, grid, s) : launch_ps<128, 2>(a, grid, s);
+    return nt == 1 ? launch_ps<64, 1>(a, grid, s) : launch_ps<64, 2>(a, grid, s);
 }
 
 }  // namespace moe
