@@ -104,17 +104,21 @@ MOE_DEV void add_parts(int n, int d4, float sl2, At at, float &m, float &l, floa
             pm[u] = i0 + u < n ? ml.x : -INFINITY;
             pl[u] = ml.y;
         }
+        float nm = m;
+#pragma unroll
+        for (int u = 0; u < U; ++u) nm = fmaxf(nm, pm[u]);
+        const float x = m > -INFINITY ? kv_ex2((m - nm) * sl2) : 0.0f;
+        m = nm;
+        l *= x;
+        s.x *= x, s.y *= x, s.z *= x, s.w *= x;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const float nm = fmaxf(m, pm[u]);
-            const float x = m > -INFINITY ? kv_ex2((m - nm) * sl2) : 0.0f;
             const float y = pm[u] > -INFINITY ? kv_ex2((pm[u] - nm) * sl2) : 0.0f;
-            m = nm;
-            l = l * x + pl[u] * y;
-            s.x = s.x * x + v[u].x * y;
-            s.y = s.y * x + v[u].y * y;
-            s.z = s.z * x + v[u].z * y;
-            s.w = s.w * x + v[u].w * y;
+            l = fmaf(pl[u], y, l);
+            s.x = fmaf(v[u].x, y, s.x);
+            s.y = fmaf(v[u].y, y, s.y);
+            s.z = fmaf(v[u].z, y, s.z);
+            s.w = fmaf(v[u].w, y, s.w);
         }
     }
 }

@@ -34,6 +34,9 @@ namespace {
 constexpr int kTile = 64;       // tokens of a unit of work
 constexpr int kChunks = 1024;   // entries of the prefix table over requests
 constexpr float kSlack = 8.0f;
+// Units before an item's first tile that hold no work: what a warp spends on a new
+// item (its queries, the first copies' latency), in tiles.
+constexpr int kPad = 1;
 
 template <int D, int NT>
 struct Cfg {
@@ -50,7 +53,7 @@ struct Cfg {
 };
 
 struct Meta {        // where a warp's partial belongs
-    uint32_t u0, u1; // the item's units; u0 == u1: none
+    uint32_t u0, u1; // the item's tiles as units; u0 == u1: none
     int b, h, r;
 };
 
@@ -96,16 +99,19 @@ MOE_DEV void lds_words(uint32_t addr, uint32_t (&w)[N]) {
 }
 
 // The four nibble pairs of a word as fp16 pairs 64 + q.
-MOE_DEV void codes64(uint32_t w, uint32_t (&x)[4]) {
-    x[0] = ((w << 4) & 0x00F000F0u) | 0x54005400u;
+MOE_DEV void codes64(uint32_t w, uint32_t c16, uint32_t (&x)[4]) {
+    const uint32_t v = w >> 8;
+    x[0] = ((w * c16) & 0x00F000F0u) | 0x54005400u;
     x[1] = (w & 0x00F000F0u) | 0x54005400u;
-    x[2] = ((w >> 4) & 0x00F000F0u) | 0x54005400u;
-    x[3] = ((w >> 8) & 0x00F000F0u) | 0x54005400u;
+    x[2] = ((v * c16) & 0x00F000F0u) | 0x54005400u;
+    x[3] = (v & 0x00F000F0u) | 0x54005400u;
 }
 
-// The same as (q - 8) * s, exact: (16 + q) * s - 24 * s.
-MOE_DEV void codes_scaled(uint32_t w, uint32_t s, uint32_t m24s, uint32_t (&x)[4]) {
-    const uint32_t t[4] = {w << 6, w << 2, w >> 2, w >> 6};
+// The pairs of words lo (their low two nibbles) and hi (their low two) as
+// (q - 8) * s, exact: (16 + q) * s - 24 * s.
+MOE_DEV void codes_scaled(uint32_t lo, uint32_t hi, uint32_t c4, uint32_t c64, uint32_t s, uint32_t m24s,
+                          uint32_t (&x)[4]) {
+    const uint32_t t[4] = {lo * c64, lo * c4, hi * c64, hi * c4};
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         x[i] = as_u32(__hfma2(as_h2((t[i] & 0x03C003C0u) | 0x4C004C00u), as_h2(s), as_h2(m24s)));
@@ -118,11 +124,10 @@ struct Request {
     int q0, m, first, end, tile0, tiles, row_tiles;
 };
 
-MOE_DEV Request request_of(const KvAttnArgs &a, int b, int rows) {
+MOE_DEV Request request_of(const KvAttnArgs &a, int q0, int q1, int len, int rows) {
     Request r;
-    r.q0 = a.batch.cu_q[b];
-    r.m = a.batch.cu_q[b + 1] - r.q0;
-    const int len = a.batch.kv_len[b];
+    r.q0 = q0;
+    r.m = q1 - q0;
     r.first = len - r.m;
     r.end = (int)min((long long)len, (long long)a.batch.stride * a.pool.ps);
     const int start = a.window > 0 ? max(0, r.first - a.window + 1) : 0;
@@ -134,7 +139,7 @@ MOE_DEV Request request_of(const KvAttnArgs &a, int b, int rows) {
 }
 
 MOE_DEV uint32_t units_of(const Request &r, int hkv) {
-    return (uint32_t)r.tiles * (uint32_t)r.row_tiles * (uint32_t)hkv;
+    return (uint32_t)(r.tiles + kPad) * (uint32_t)r.row_tiles * (uint32_t)hkv;
 }
 
 template <int D, int NT, int PS>
@@ -149,6 +154,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
     __shared__ int run_of[2 * W + 1], list[2 * W], n_runs, abort_flag, last_of;
     __shared__ uint32_t warp_tot[W];
     pdl_wait();
+    pdl_launch_dependents();
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, g = lane >> 2, t = lane & 3;
     const int hkv = a.pool.hkv, G = a.group;
     constexpr int ps = PS, ppt = kTile / PS;          // pages of a tile
@@ -160,39 +166,75 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
     mbar_fence_init();
     if (lane < 2) meta[2 * w + lane].u0 = meta[2 * w + lane].u1 = 0;
 
-    // prefix of units over chunks of requests, two or three chunks a thread
+    // Units before each request.  Up to 32 requests: a lane of every warp holds one.
+    // More: a prefix table over chunks of requests in shared memory.
+    const bool few = a.batch.requests <= 32;
+    int my_q0 = 0, my_q1 = 0, my_len = 0;
+    uint32_t my_end = 0, total;
     const int per_chunk = (a.batch.requests + kChunks - 1) / kChunks;
     const int chunks = (a.batch.requests + per_chunk - 1) / per_chunk;
-    uint32_t carry = 0;
-    for (int c0 = 0; c0 < chunks; c0 += W * 32) {
+    auto load_request = [&](int b) {
+        return request_of(a, a.batch.cu_q[b], a.batch.cu_q[b + 1], a.batch.kv_len[b], C::kRows);
+    };
+    auto check = [&](const Request &r) {
+        if (blockIdx.x == 0 && r.row_tiles && r.end < r.first + r.m)
+            kv_report(a.err, MOE_KV4_DEVERR_PAGE);  // beyond its table
+    };
+    if (few) {
         uint32_t n = 0;
-        if (c0 + tid < chunks)
-            for (int b = (c0 + tid) * per_chunk; b < min(a.batch.requests, (c0 + tid + 1) * per_chunk); ++b) {
-                const Request r = request_of(a, b, C::kRows);
-                n += units_of(r, hkv);
-                if (blockIdx.x == 0 && r.row_tiles && r.end < r.first + r.m)
-                    kv_report(a.err, MOE_KV4_DEVERR_PAGE);  // beyond its table
-            }
-        uint32_t x = n;
+        if (lane < a.batch.requests) {
+            my_q0 = a.batch.cu_q[lane];
+            my_q1 = a.batch.cu_q[lane + 1];
+            my_len = a.batch.kv_len[lane];
+            const Request r = request_of(a, my_q0, my_q1, my_len, C::kRows);
+            n = units_of(r, hkv);
+            if (w == 0) check(r);
+        }
+        my_end = n;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
-            const uint32_t y = __shfl_up_sync(0xffffffffu, x, d);
-            if (lane >= d) x += y;
+            const uint32_t y = __shfl_up_sync(0xffffffffu, my_end, d);
+            if (lane >= d) my_end += y;
         }
-        if (lane == 31) warp_tot[w] = x;
-        __syncthreads();
-        uint32_t before = carry, all = carry;
-        for (int i = 0; i < W; ++i) {
-            if (i < w) before += warp_tot[i];
-            all += warp_tot[i];
+        total = __shfl_sync(0xffffffffu, my_end, 31);
+        __syncthreads();  // the barriers and flags set above
+    } else {
+        uint32_t carry = 0;
+        for (int c0 = 0; c0 < chunks; c0 += W * 32) {
+            uint32_t n = 0;
+            if (c0 + tid < chunks)
+                for (int b = (c0 + tid) * per_chunk;
+                     b < min(a.batch.requests, (c0 + tid + 1) * per_chunk); ++b) {
+                    const Request r = load_request(b);
+                    n += units_of(r, hkv);
+                    check(r);
+                }
+            uint32_t x = n;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const uint32_t y = __shfl_up_sync(0xffffffffu, x, d);
+                if (lane >= d) x += y;
+            }
+            if (lane == 31) warp_tot[w] = x;
+            __syncthreads();
+            uint32_t before = carry, all = carry;
+            for (int i = 0; i < W; ++i) {
+                if (i < w) before += warp_tot[i];
+                all += warp_tot[i];
+            }
+            if (c0 + tid < chunks) prefix[c0 + tid] = before + x - n;
+            carry = all;
+            __syncthreads();
         }
-        if (c0 + tid < chunks) prefix[c0 + tid] = before + x - n;
-        carry = all;
+        if (tid == 0) prefix[chunks] = carry;
         __syncthreads();
+        total = carry;
     }
-    if (tid == 0) prefix[chunks] = carry;
-    __syncthreads();
-    const uint32_t total = carry;
+    auto get_request = [&](int b) {
+        if (!few) return load_request(b);
+        return request_of(a, __shfl_sync(0xffffffffu, my_q0, b), __shfl_sync(0xffffffffu, my_q1, b),
+                          __shfl_sync(0xffffffffu, my_len, b), C::kRows);
+    };
     const uint32_t per = max((uint32_t)a.min_units, (total + gridDim.x - 1) / gridDim.x);
     const uint32_t c_lo = min(total, blockIdx.x * per), c_hi = min(total, c_lo + per);
     if (c_lo >= c_hi) return;
@@ -209,33 +251,54 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
     int b = 0;
     uint32_t b_u0 = 0;
     if (u < u_end) {
-        int lo = 0, hi = chunks - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (prefix[mid] <= u)
-                lo = mid;
-            else
-                hi = mid - 1;
+        if (few) {
+            b = __ffs(__ballot_sync(0xffffffffu, u < my_end)) - 1;
+            if (b) b_u0 = __shfl_sync(0xffffffffu, my_end, b - 1);
+        } else {
+            int lo = 0, hi = chunks - 1;
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (prefix[mid] <= u)
+                    lo = mid;
+                else
+                    hi = mid - 1;
+            }
+            b = lo * per_chunk;
+            b_u0 = prefix[lo];
         }
-        b = lo * per_chunk;
-        b_u0 = prefix[lo];
     }
     bool aborted = false;
     while (u < u_end && !aborted) {
-        Request rq = request_of(a, b, C::kRows);
+        Request rq = get_request(b);
         uint32_t n_b = units_of(rq, hkv);
         while (u >= b_u0 + n_b) {
             b_u0 += n_b;
-            rq = request_of(a, ++b, C::kRows);
+            rq = get_request(++b);
             n_b = units_of(rq, hkv);
         }
-        const uint32_t item = (u - b_u0) / rq.tiles;
-        const uint32_t i_u0 = b_u0 + item * rq.tiles, i_u1 = i_u0 + rq.tiles;
+        const uint32_t span = rq.tiles + kPad, item = (u - b_u0) / span;
+        const uint32_t i_u0 = b_u0 + item * span + kPad, i_u1 = i_u0 + rq.tiles;  // its tiles
+        u = max(u, i_u0);
+        if (u >= u_end) break;
         const int h = item % hkv, rt = item / hkv;
         const uint32_t seg_end = min(u_end, i_u1);
         const int tile_lo = rq.tile0 + (int)(u - i_u0), n_tiles = (int)(seg_end - u);
         const int row0 = rt * C::kRows, rows = min(C::kRows, rq.m * G - row0);
         const int32_t *table = a.batch.tables + (size_t)b * a.batch.stride;
+
+        // requested before the first tiles, behind which the queries would wait
+        uint4 q_raw[NT][NG];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int r = 8 * n + g, i = div_group(row0 + r, a.gdiv), hh = (row0 + r) - i * G;
+            const uint16_t *src =
+                a.q + (size_t)(rq.q0 + i) * a.q_stride + (size_t)(h * G + hh) * D + 8 * t;
+#pragma unroll
+            for (int G4 = 0; G4 < NG; ++G4) {
+                q_raw[n][G4] = make_uint4(0, 0, 0, 0);
+                if (r < rows) q_raw[n][G4] = *reinterpret_cast<const uint4 *>(src + 32 * G4);
+            }
+        }
 
         const uint8_t *head_base = a.pool.base + (size_t)h * kBlock;
         const size_t page_bytes = (size_t)hkv * kBlock;
@@ -291,17 +354,12 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
         uint32_t q[NT][NG][4];
         float bias[NT == 1 ? NG : 1][2];
         bool bad = false;
+        const uint32_t flip = a.scale_log2 < 0.0f ? 0x80008000u : 0u;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const int r = 8 * n + g;
-            const int i = div_group(row0 + r, a.gdiv), hh = (row0 + r) - i * G;
-            const uint16_t *src = a.q + (size_t)(rq.q0 + i) * a.q_stride + (size_t)(h * G + hh) * D + 8 * t;
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int G4 = 0; G4 < NG; ++G4) {
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (r < rows) v = *reinterpret_cast<const uint4 *>(src + 32 * G4);
-                v = bf16x8_to_f16x8_sat(v, bad);
-                const uint32_t flip = a.scale_log2 < 0.0f ? 0x80008000u : 0u;
+                const uint4 v = bf16x8_to_f16x8_sat(q_raw[n][G4], bad);
                 q[n][G4][0] = v.x ^ flip;
                 q[n][G4][1] = v.y ^ flip;
                 q[n][G4][2] = v.z ^ flip;
@@ -319,7 +377,6 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
                     bias[NT == 1 ? G4 : 0][1] = -72.0f * __shfl_sync(0xffffffffu, s, 8 * t + 4);
                 }
             }
-        }
         if (__any_sync(0xffffffffu, bad) && lane == 0) kv_report(a.err, MOE_KV4_DEVERR_RANGE);
 
         // tokens that every row sees: below `open`, and from `shut` on
@@ -369,8 +426,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
 #pragma unroll
                     for (int G4 = 0; G4 < NG; ++G4) {
                         uint32_t ca[4], cb[4];
-                        codes64(wa[G4], ca);
-                        codes64(wb[G4], cb);
+                        codes64(wa[G4], a.c16, ca);
+                        codes64(wb[G4], a.c16, cb);
                         float c[4] = {bias[NT == 1 ? G4 : 0][0], bias[NT == 1 ? G4 : 0][1],
                                       bias[NT == 1 ? G4 : 0][0], bias[NT == 1 ? G4 : 0][1]};
                         mma16816(c, ca[0], cb[0], ca[1], cb[1], q[0][G4][0], q[0][G4][1]);
@@ -394,8 +451,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
                         const uint32_t ya = __byte_perm(za[G4 / 2], 0, G4 & 1 ? 0x3232 : 0x1010);
                         const uint32_t yb = __byte_perm(zb[G4 / 2], 0, G4 & 1 ? 0x3232 : 0x1010);
                         uint32_t ca[4], cb[4];
-                        codes_scaled(wa[G4], ya, times_m24(ya), ca);
-                        codes_scaled(wb[G4], yb, times_m24(yb), cb);
+                        codes_scaled(wa[G4], wa[G4] >> 8, a.c4, a.c64, ya, times_m24(ya), ca);
+                        codes_scaled(wb[G4], wb[G4] >> 8, a.c4, a.c64, yb, times_m24(yb), cb);
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
                             mma16816(x[s][n], ca[0], cb[0], ca[1], cb[1], q[n][G4][0], q[n][G4][1]);
@@ -501,8 +558,14 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
                     const uint32_t s0 = __byte_perm(z[0][G4 / 2], z[1][G4 / 2], sel);
                     const uint32_t s1 = __byte_perm(z[2][G4 / 2], z[3][G4 / 2], sel);
                     uint32_t va[4], vb[4];
-                    codes_scaled(__byte_perm(vw[0][G4 / 2], vw[1][G4 / 2], sel), s0, times_m24(s0), va);
-                    codes_scaled(__byte_perm(vw[2][G4 / 2], vw[3][G4 / 2], sel), s1, times_m24(s1), vb);
+                    // the same with the bytes of each half exchanged: its high nibbles
+                    const uint32_t hsel = G4 & 1 ? 0x6723 : 0x4501;
+                    codes_scaled(__byte_perm(vw[0][G4 / 2], vw[1][G4 / 2], sel),
+                                 __byte_perm(vw[0][G4 / 2], vw[1][G4 / 2], hsel), a.c4, a.c64, s0,
+                                 times_m24(s0), va);
+                    codes_scaled(__byte_perm(vw[2][G4 / 2], vw[3][G4 / 2], sel),
+                                 __byte_perm(vw[2][G4 / 2], vw[3][G4 / 2], hsel), a.c4, a.c64, s1,
+                                 times_m24(s1), vb);
 #pragma unroll
                     for (int v = 0; v < 2; ++v)
 #pragma unroll
@@ -637,7 +700,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
     for (int run = 0; run < runs; ++run) {
         const Meta me = meta[list[run_of[run]]];
         if (me.u0 >= c_lo && me.u1 <= c_hi) continue;
-        const uint32_t c0 = me.u0 / per, c1 = (me.u1 - 1) / per;  // CTAs of the item
+        const uint32_t c0 = me.u0 / per, c1 = (me.u1 - 1) / per;  // CTAs of its tiles
         if (tid == 0) {
             const int old = atomicAdd(a.counters + c0, 1);
             last_of = old == (int)(c1 - c0);

@@ -41,6 +41,9 @@ struct KvAttnArgs {
     GroupDiv gdiv;
     int rows_lo, rows_hi;  // requests of this many rows (new tokens x group) are the kernel's
     int max_kv, min_units;
+    // 4, 16, 64: factors that the compiler does not see, so that left shifts of codes
+    // are multiplies of the FMA pipe, which has room where the ALU pipe has none
+    uint32_t c4, c16, c64;
     int32_t *counters;     // [CTAs], zero between calls
     float *warp_slots, *cta_slots;
     uint32_t *err;
