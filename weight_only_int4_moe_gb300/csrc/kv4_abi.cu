@@ -226,9 +226,6 @@ int moe_kv4_attention(const uint16_t *q, int64_t q_stride, int q_heads, const vo
     a.err = reinterpret_cast<uint32_t *>(ws);
     a.counters = reinterpret_cast<int32_t *>(ws + kKvCounterByte);
     a.max_kv = batch->max_kv;
-    a.c4 = 4;
-    a.c16 = 16;
-    a.c64 = 64;
     // Requests of up to kKvFewRows rows go to the decode kernel, others to the
     // prefill kernel; where all have the same number of new tokens one is enough.
     const int ctas = sms < kKvMaxCtas ? sms : kKvMaxCtas;

@@ -38,6 +38,7 @@ constexpr float kSlack = 8.0f;
 // item (its queries, the first copies' latency), in tiles.
 constexpr int kPad = 1;
 
+
 template <int D, int NT>
 struct Cfg {
     static constexpr int NG = D / 32;
@@ -63,6 +64,17 @@ MOE_DEV void bulk_copy(uint32_t dst, const void *src, uint32_t bytes, uint32_t b
             dst),
         "l"(src), "r"(bytes), "r"(bar)
         : "memory");
+}
+
+// The same with an accumulator to start from that stays as it is.
+MOE_DEV void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                      uint32_t b1, const float (&c)[4]) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%10, %11, %12, %13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]),
+          "f"(c[3]));
 }
 
 MOE_DEV void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -99,25 +111,23 @@ MOE_DEV void lds_words(uint32_t addr, uint32_t (&w)[N]) {
 }
 
 // The four nibble pairs of a word as fp16 pairs 64 + q.
-MOE_DEV void codes64(uint32_t w, uint32_t c16, uint32_t (&x)[4]) {
+MOE_DEV void codes64(uint32_t w, const KvConsts &k, uint32_t (&x)[4]) {
     const uint32_t v = w >> 8;
-    x[0] = ((w * c16) & 0x00F000F0u) | 0x54005400u;
-    x[1] = (w & 0x00F000F0u) | 0x54005400u;
-    x[2] = ((v * c16) & 0x00F000F0u) | 0x54005400u;
-    x[3] = (v & 0x00F000F0u) | 0x54005400u;
+    x[0] = ((w * k.c16) & k.nib4) | k.magic64;
+    x[1] = (w & k.nib4) | k.magic64;
+    x[2] = ((v * k.c16) & k.nib4) | k.magic64;
+    x[3] = (v & k.nib4) | k.magic64;
 }
 
-// The pairs of words lo (their low two nibbles) and hi (their low two) as
-// (q - 8) * s, exact: (16 + q) * s - 24 * s.
-MOE_DEV void codes_scaled(uint32_t lo, uint32_t hi, uint32_t c4, uint32_t c64, uint32_t s, uint32_t m24s,
-                          uint32_t (&x)[4]) {
-    const uint32_t t[4] = {lo * c64, lo * c4, hi * c64, hi * c4};
+// The pairs of words lo and hi (their low two nibbles each) as (q - 8) * s, exact:
+// (16 + q) * s - 24 * s.
+MOE_DEV void codes_scaled(uint32_t lo, uint32_t hi, const KvConsts &k, uint32_t s, uint32_t (&x)[4]) {
+    const __half2 m24 = __hmul2(as_h2(s), as_h2(k.cm24));
+    const uint32_t t[4] = {lo * k.c64, lo * k.c4, hi * k.c64, hi * k.c4};
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        x[i] = as_u32(__hfma2(as_h2((t[i] & 0x03C003C0u) | 0x4C004C00u), as_h2(s), as_h2(m24s)));
+        x[i] = as_u32(__hfma2(as_h2((t[i] & k.nib6) | k.magic16), as_h2(s), m24));
 }
-
-MOE_DEV uint32_t times_m24(uint32_t s) { return as_u32(__hmul2(as_h2(s), as_h2(0xCE00CE00u))); }
 
 // What a request adds to the list of units.
 struct Request {
@@ -151,7 +161,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
     __shared__ uint32_t prefix[kChunks + 1];
     __shared__ uint64_t bars[W * S];
     __shared__ Meta meta[2 * W];
-    __shared__ int run_of[2 * W + 1], list[2 * W], n_runs, abort_flag, last_of;
+    __shared__ int run_of[2 * W + 1], list[2 * W], n_runs, abort_flag, last_of[2];
     __shared__ uint32_t warp_tot[W];
     pdl_wait();
     pdl_launch_dependents();
@@ -352,7 +362,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
 
         // the query rows as B operands: lane (g, t) holds dimensions 32G + 8t.. of row g
         uint32_t q[NT][NG][4];
-        float bias[NT == 1 ? NG : 1][2];
+        float bias[NT == 1 ? NG : 1][4];  // what a group's scores start from
         bool bad = false;
         const uint32_t flip = a.scale_log2 < 0.0f ? 0x80008000u : 0u;
 #pragma unroll
@@ -375,6 +385,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
                     s += __shfl_xor_sync(0xffffffffu, s, 2);
                     bias[NT == 1 ? G4 : 0][0] = -72.0f * __shfl_sync(0xffffffffu, s, 8 * t);
                     bias[NT == 1 ? G4 : 0][1] = -72.0f * __shfl_sync(0xffffffffu, s, 8 * t + 4);
+                    bias[NT == 1 ? G4 : 0][2] = bias[NT == 1 ? G4 : 0][0];
+                    bias[NT == 1 ? G4 : 0][3] = bias[NT == 1 ? G4 : 0][1];
                 }
             }
         if (__any_sync(0xffffffffu, bad) && lane == 0) kv_report(a.err, MOE_KV4_DEVERR_RANGE);
@@ -426,11 +438,11 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
 #pragma unroll
                     for (int G4 = 0; G4 < NG; ++G4) {
                         uint32_t ca[4], cb[4];
-                        codes64(wa[G4], a.c16, ca);
-                        codes64(wb[G4], a.c16, cb);
-                        float c[4] = {bias[NT == 1 ? G4 : 0][0], bias[NT == 1 ? G4 : 0][1],
-                                      bias[NT == 1 ? G4 : 0][0], bias[NT == 1 ? G4 : 0][1]};
-                        mma16816(c, ca[0], cb[0], ca[1], cb[1], q[0][G4][0], q[0][G4][1]);
+                        codes64(wa[G4], a.k, ca);
+                        codes64(wb[G4], a.k, cb);
+                        float c[4];
+                        mma16816(c, ca[0], cb[0], ca[1], cb[1], q[0][G4][0], q[0][G4][1],
+                                 bias[NT == 1 ? G4 : 0]);
                         mma16816(c, ca[2], cb[2], ca[3], cb[3], q[0][G4][2], q[0][G4][3]);
                         const float2 fa = __half22float2(as_h2(za[G4 / 2]));
                         const float2 fb = __half22float2(as_h2(zb[G4 / 2]));
@@ -451,8 +463,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
                         const uint32_t ya = __byte_perm(za[G4 / 2], 0, G4 & 1 ? 0x3232 : 0x1010);
                         const uint32_t yb = __byte_perm(zb[G4 / 2], 0, G4 & 1 ? 0x3232 : 0x1010);
                         uint32_t ca[4], cb[4];
-                        codes_scaled(wa[G4], wa[G4] >> 8, a.c4, a.c64, ya, times_m24(ya), ca);
-                        codes_scaled(wb[G4], wb[G4] >> 8, a.c4, a.c64, yb, times_m24(yb), cb);
+                        codes_scaled(wa[G4], wa[G4] >> 8, a.k, ya, ca);
+                        codes_scaled(wb[G4], wb[G4] >> 8, a.k, yb, cb);
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
                             mma16816(x[s][n], ca[0], cb[0], ca[1], cb[1], q[n][G4][0], q[n][G4][1]);
@@ -561,11 +573,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
                     // the same with the bytes of each half exchanged: its high nibbles
                     const uint32_t hsel = G4 & 1 ? 0x6723 : 0x4501;
                     codes_scaled(__byte_perm(vw[0][G4 / 2], vw[1][G4 / 2], sel),
-                                 __byte_perm(vw[0][G4 / 2], vw[1][G4 / 2], hsel), a.c4, a.c64, s0,
-                                 times_m24(s0), va);
+                                 __byte_perm(vw[0][G4 / 2], vw[1][G4 / 2], hsel), a.k, s0, va);
                     codes_scaled(__byte_perm(vw[2][G4 / 2], vw[3][G4 / 2], sel),
-                                 __byte_perm(vw[2][G4 / 2], vw[3][G4 / 2], hsel), a.c4, a.c64, s1,
-                                 times_m24(s1), vb);
+                                 __byte_perm(vw[2][G4 / 2], vw[3][G4 / 2], hsel), a.k, s1, vb);
 #pragma unroll
                     for (int v = 0; v < 2; ++v)
 #pragma unroll
@@ -683,7 +693,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
         const Meta me = meta[list[run_of[run]]];
         float mm, ll;
         float4 s;
-        add_parts<D, 4>(run_of[run + 1] - run_of[run], d4, sl2,
+        add_parts<D, NT == 1 ? 12 : 8>(run_of[run + 1] - run_of[run], d4, sl2,
                         [&](int i) { return slot_of(list[run_of[run] + i]) + row * C::kPitch; }, mm, ll, s);
         if (me.u0 >= c_lo && me.u1 <= c_hi) {
             finish(me, row, d4, mm, ll, s);
@@ -697,19 +707,25 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
     }
     __threadfence();
     __syncthreads();
-    for (int run = 0; run < runs; ++run) {
-        const Meta me = meta[list[run_of[run]]];
-        if (me.u0 >= c_lo && me.u1 <= c_hi) continue;
-        const uint32_t c0 = me.u0 / per, c1 = (me.u1 - 1) / per;  // CTAs of its tiles
-        if (tid == 0) {
-            const int old = atomicAdd(a.counters + c0, 1);
-            last_of = old == (int)(c1 - c0);
-            if (last_of) a.counters[c0] = 0;
+    // at most two of the runs (the first and the last) are shared with other CTAs
+    if (tid < 2) {
+        bool last = false;
+        const int run = tid == 0 ? 0 : runs - 1;
+        if (runs > tid) {
+            const Meta me = meta[list[run_of[run]]];
+            if (!(me.u0 >= c_lo && me.u1 <= c_hi)) {
+                const uint32_t c0 = me.u0 / per, c1 = (me.u1 - 1) / per;  // CTAs of its tiles
+                last = atomicAdd(a.counters + c0, 1) == (int)(c1 - c0);
+                if (last) a.counters[c0] = 0;
+            }
         }
-        __syncthreads();
-        const bool mine = last_of;
-        __syncthreads();
-        if (!mine) continue;
+        last_of[tid] = last;
+    }
+    __syncthreads();
+    for (int k = 0; k < 2; ++k) {
+        if (!last_of[k]) continue;
+        const Meta me = meta[list[run_of[k == 0 ? 0 : runs - 1]]];
+        const uint32_t c0 = me.u0 / per, c1 = (me.u1 - 1) / per;
         __threadfence();
         for (int e = tid; e < kWork; e += W * 32) {
             const int row = e / kQuads, d4 = e % kQuads;
@@ -771,7 +787,7 @@ cudaError_t launch_kv4_decode(KvAttnArgs a, int D, int max_rows, void *slots, in
     const size_t slot = (size_t)8 * nt * (D + 4);
     a.cta_slots = reinterpret_cast<float *>(slots);
     a.warp_slots = a.cta_slots + 2 * slot * ctas;
-    a.min_units = warps;
+    a.min_units = 4;  // a tile for each quarter of an SM: short calls spread over the GPU
     // no more CTAs than the largest possible list of units fills
     const long long tiles = (long long)(a.max_kv + kTile - 1) / kTile + 1;
     const long long row_tiles = ((long long)max_rows + 8 * nt - 1) / (8 * nt);

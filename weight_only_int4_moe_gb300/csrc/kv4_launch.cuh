@@ -28,6 +28,17 @@ struct KvReadArgs {
     uint32_t *err;
 };
 
+// Constants of the unpacking, as kernel parameters: they stay constant-bank operands
+// where the compiler would put immediates into registers again for every use, and
+// shifts to the left become multiplies of the FMA pipe, which has room where the ALU
+// pipe has none.
+struct KvConsts {
+    uint32_t c4 = 4, c16 = 16, c64 = 64;
+    uint32_t nib4 = 0x00F000F0u, magic64 = 0x54005400u;   // a nibble at bits 4..7: fp16 64 + q
+    uint32_t nib6 = 0x03C003C0u, magic16 = 0x4C004C00u;   // at bits 6..9: 16 + q
+    uint32_t cm24 = 0xCE00CE00u;                          // fp16 pair (-24, -24)
+};
+
 struct KvAttnArgs {
     const uint16_t *q;
     int64_t q_stride;
@@ -41,9 +52,7 @@ struct KvAttnArgs {
     GroupDiv gdiv;
     int rows_lo, rows_hi;  // requests of this many rows (new tokens x group) are the kernel's
     int max_kv, min_units;
-    // 4, 16, 64: factors that the compiler does not see, so that left shifts of codes
-    // are multiplies of the FMA pipe, which has room where the ALU pipe has none
-    uint32_t c4, c16, c64;
+    KvConsts k;
     int32_t *counters;     // [CTAs], zero between calls
     float *warp_slots, *cta_slots;
     uint32_t *err;

@@ -320,13 +320,14 @@ MOE_DEV uint64_t add2(uint64_t a, uint64_t b) {
     return r;
 }
 
-// A word's four nibble pairs as (q - 8) * s in fp16, exact (see dequant_row).
-MOE_DEV void scaled_codes(uint32_t w, uint32_t s, uint32_t (&x)[4]) {
-    const __half2 m24 = __hmul2(as_h2(s), as_h2(0xCE00CE00u));
-    const uint32_t t[4] = {w << 6, w << 2, w >> 2, w >> 6};
+// A word's four nibble pairs as (q - 8) * s in fp16, exact: (16 + q) * s - 24 * s.
+MOE_DEV void scaled_codes(uint32_t w, const KvConsts &k, uint32_t s, uint32_t (&x)[4]) {
+    const __half2 m24 = __hmul2(as_h2(s), as_h2(k.cm24));
+    const uint32_t v = w >> 8;
+    const uint32_t t[4] = {w * k.c64, w * k.c4, v * k.c64, v * k.c4};
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        x[i] = as_u32(__hfma2(as_h2((t[i] & 0x03C003C0u) | 0x4C004C00u), as_h2(s), m24));
+        x[i] = as_u32(__hfma2(as_h2((t[i] & k.nib6) | k.magic16), as_h2(s), m24));
 }
 
 MOE_DEV void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
@@ -475,7 +476,7 @@ MOE_DEV void unpack_role(const KvAttnArgs &a, Shared &sh, uint32_t smem, Walk wa
                         chunk = 8 * pp + g;
                     }
                     uint32_t x[4];
-                    scaled_codes(words[u], live ? s : 0u, x);
+                    scaled_codes(words[u], a.k, live ? s : 0u, x);
                     sts128(dst + tile_at(row, chunk), x[0], x[1], x[2], x[3]);
                 }
             }
