@@ -84,43 +84,59 @@ MOE_DEV float kv_ex2(float x) {
     return r;
 }
 
-// One row's four dimensions added up over several parts, in their order: each
-// holds sums o relative to a maximum m and their weight l.  U parts are loaded at
-// once (a part at a time would cost a memory round trip each).  at(i): the part's
-// row, D sums, then m and l; sl2 > 0 turns scores into powers of two.
-template <int D, int U, typename At>
-MOE_DEV void add_parts(int n, int d4, float sl2, At at, float &m, float &l, float4 &s) {
-    m = -INFINITY;
-    l = 0.0f;
-    s = make_float4(0, 0, 0, 0);
+// Adds up several parts of the same rows, in their order: each part holds, for a
+// row, D sums relative to a maximum, then the maximum m and the weight l.  A whole
+// warp takes R rows at a time (D = 64: twice R, half a warp each), a lane four
+// dimensions, and requests U parts of all its rows at once: a row or a part at a
+// time would cost a memory round trip each.  at(i) is part i (rows of D + 4 floats);
+// sl2 > 0 turns scores into powers of two; done(row, d4, m, l, sums) takes a result.
+template <int D, int R, int U, typename At, typename Done>
+MOE_DEV void add_parts(int n, int row0, float sl2, At at, Done done) {
+    constexpr int kLanes = D / 4, kStep = 32 / kLanes;
+    const int lane = threadIdx.x & 31, d4 = lane % kLanes, first = row0 + lane / kLanes;
+    float m[R], l[R];
+    float4 s[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        m[r] = -INFINITY;
+        l[r] = 0.0f;
+        s[r] = make_float4(0, 0, 0, 0);
+    }
     for (int i0 = 0; i0 < n; i0 += U) {
-        float pm[U], pl[U];
-        float4 v[U];
+        float2 ml[U][R];
+        float4 v[U][R];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const float *r = at(min(i0 + u, n - 1));
-            const float2 ml = *reinterpret_cast<const float2 *>(r + D);
-            v[u] = *reinterpret_cast<const float4 *>(r + 4 * d4);
-            pm[u] = i0 + u < n ? ml.x : -INFINITY;
-            pl[u] = ml.y;
+            const float *p = at(min(i0 + u, n - 1)) + first * (D + 4);
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                ml[u][r] = *reinterpret_cast<const float2 *>(p + r * kStep * (D + 4) + D);
+                v[u][r] = *reinterpret_cast<const float4 *>(p + r * kStep * (D + 4) + 4 * d4);
+            }
         }
-        float nm = m;
 #pragma unroll
-        for (int u = 0; u < U; ++u) nm = fmaxf(nm, pm[u]);
-        const float x = m > -INFINITY ? kv_ex2((m - nm) * sl2) : 0.0f;
-        m = nm;
-        l *= x;
-        s.x *= x, s.y *= x, s.z *= x, s.w *= x;
+        for (int r = 0; r < R; ++r) {
+            float nm = m[r];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const float y = pm[u] > -INFINITY ? kv_ex2((pm[u] - nm) * sl2) : 0.0f;
-            l = fmaf(pl[u], y, l);
-            s.x = fmaf(v[u].x, y, s.x);
-            s.y = fmaf(v[u].y, y, s.y);
-            s.z = fmaf(v[u].z, y, s.z);
-            s.w = fmaf(v[u].w, y, s.w);
+            for (int u = 0; u < U; ++u) nm = fmaxf(nm, ml[u][r].x);  // a part twice: no harm
+            const float base = nm > -INFINITY ? nm * sl2 : 0.0f;
+            const float x = kv_ex2(m[r] * sl2 - base);
+            m[r] = nm;
+            l[r] *= x;
+            s[r].x *= x, s[r].y *= x, s[r].z *= x, s[r].w *= x;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const float y = i0 + u < n ? kv_ex2(ml[u][r].x * sl2 - base) : 0.0f;
+                l[r] = fmaf(ml[u][r].y, y, l[r]);
+                s[r].x = fmaf(v[u][r].x, y, s[r].x);
+                s[r].y = fmaf(v[u][r].y, y, s[r].y);
+                s[r].z = fmaf(v[u][r].z, y, s[r].z);
+                s[r].w = fmaf(v[u][r].w, y, s[r].w);
+            }
         }
     }
+#pragma unroll
+    for (int r = 0; r < R; ++r) done(first + r * kStep, d4, m[r], l[r], s[r]);
 }
 
 // The scale of a group: bf16(amax / 7) in [2^-14, 2720] (also for amax = 0).

@@ -55,7 +55,7 @@ struct Cfg {
 
 struct Meta {        // where a warp's partial belongs
     uint32_t u0, u1; // the item's tiles as units; u0 == u1: none
-    int b, h, r;
+    int q0, rows, h, row0; // the request's first token; the item's rows from row0 on
 };
 
 MOE_DEV void bulk_copy(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
     __shared__ uint32_t prefix[kChunks + 1];
     __shared__ uint64_t bars[W * S];
     __shared__ Meta meta[2 * W];
-    __shared__ int run_of[2 * W + 1], list[2 * W], n_runs, abort_flag, last_of[2];
+    __shared__ int run_of[2 * W + 1], n_runs, abort_flag, last_of[2];
     __shared__ uint32_t warp_tot[W];
     pdl_wait();
     pdl_launch_dependents();
@@ -248,8 +248,14 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
     const uint32_t per = max((uint32_t)a.min_units, (total + gridDim.x - 1) / gridDim.x);
     const uint32_t c_lo = min(total, blockIdx.x * per), c_hi = min(total, c_lo + per);
     if (c_lo >= c_hi) return;
-    uint32_t u = c_lo + (uint32_t)((unsigned long long)(c_hi - c_lo) * w / W);
-    const uint32_t u_end = c_lo + (uint32_t)((unsigned long long)(c_hi - c_lo) * (w + 1) / W);
+    // The warps' shares: one unit each to the first ones, or equal parts to all, so that
+    // an item's tiles always lie in neighbouring warps.
+    const uint32_t n_units = c_hi - c_lo;
+    auto share = [&](uint32_t i) {
+        return c_lo + (n_units < W ? min(i, n_units) : (uint32_t)((unsigned long long)n_units * i / W));
+    };
+    uint32_t u = share(w);
+    const uint32_t u_end = share(w + 1);
 
     const uint32_t my_ring = smem_u32(ring) + w * C::kRing;
     const uint32_t my_bar = smem_u32(&bars[w * S]);
@@ -644,41 +650,33 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
                                         acc[G4][1][n][2 + e]);
                     if (g == 0) p[D] = m[n][e], p[D + 1] = l[n][e];
                 }
-            if (lane == 0) meta[2 * w + (last_seg ? 1 : 0)] = Meta{i_u0, i_u1, b, h, rt};
+            if (lane == 0) meta[2 * w + (last_seg ? 1 : 0)] = Meta{i_u0, i_u1, rq.q0, rows, h, row0};
         }
     }
     __syncthreads();
 
-    // the partials in list order; those of the same item are neighbours
+    // The partials in list order; those of one item are a run of neighbouring warps,
+    // all in their rings but the run's last, which may be the first of its warp.
     if (w == 0) {
-        const Meta me = lane < 2 * W ? meta[lane] : Meta{0, 0, 0, 0, 0};
+        const Meta me = lane < 2 * W ? meta[lane] : Meta{0, 0, 0, 0, 0, 0};
         const bool has = me.u0 != me.u1;
         const unsigned who = __ballot_sync(0xffffffffu, has);
-        const int at = __popc(who & ((1u << lane) - 1u));
-        if (has) list[at] = lane;
-        __syncwarp();
-        const int n = __popc(who);
-        const bool first = lane < n && (lane == 0 || meta[list[lane]].u0 != meta[list[lane - 1]].u0);
-        const unsigned firsts = __ballot_sync(0xffffffffu, first);
-        if (first) run_of[__popc(firsts & ((1u << lane) - 1u))] = lane;
+        const unsigned below = who & ((1u << lane) - 1u);
+        const int prev = below ? 31 - __clz(below) : 0;
+        const uint32_t prev_u0 = __shfl_sync(0xffffffffu, me.u0, prev);
+        const unsigned firsts = __ballot_sync(0xffffffffu, has && (!below || prev_u0 != me.u0));
+        if ((firsts >> lane) & 1u) run_of[__popc(firsts & ((1u << lane) - 1u))] = lane;
         if (lane == 0) {
             n_runs = __popc(firsts);
-            run_of[__popc(firsts)] = n;
+            run_of[__popc(firsts)] = 32 - __clz(who);
         }
     }
     __syncthreads();
-    auto slot_of = [&](int i) -> const float * {
-        return i & 1 ? reinterpret_cast<const float *>(ring + (i >> 1) * C::kRing)
-                     : a.warp_slots + ((size_t)blockIdx.x * W + (i >> 1)) * C::kSlot;
-    };
-    constexpr int kQuads = D / 4, kWork = C::kRows * kQuads;
-    // one row's four dimensions, all partials of an item: sum and final result
+    // four dimensions of a row, all parts of its item added up
     auto finish = [&](const Meta &me, int row, int d4, float mm, float ll, float4 s) {
-        const int rows_b = (a.batch.cu_q[me.b + 1] - a.batch.cu_q[me.b]) * G;
-        const int rr = me.r * C::kRows + row;
-        if (rr >= rows_b) return;
-        const int i = div_group(rr, a.gdiv), hh = rr - i * G;
-        const size_t o = (size_t)(a.batch.cu_q[me.b] + i) * a.q_heads + me.h * G + hh;
+        if (row >= me.rows) return;
+        const int rr = me.row0 + row, i = div_group(rr, a.gdiv), hh = rr - i * G;
+        const size_t o = (size_t)(me.q0 + i) * a.q_heads + me.h * G + hh;
         const float inv = ll > 0.0f ? 1.0f / ll : 0.0f;
         const __nv_bfloat162 lo = __floats2bfloat162_rn(s.x * inv, s.y * inv);
         const __nv_bfloat162 hi = __floats2bfloat162_rn(s.z * inv, s.w * inv);
@@ -688,22 +686,33 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
             a.lse[o] = ll > 0.0f ? (mm * sl2 + log2f(ll)) * 0.6931471805599453f : -INFINITY;
     };
     const int runs = n_runs;
-    for (int e = tid; e < runs * kWork; e += W * 32) {
-        const int run = e / kWork, row = (e / kQuads) % C::kRows, d4 = e % kQuads;
-        const Meta me = meta[list[run_of[run]]];
-        float mm, ll;
-        float4 s;
-        add_parts<D, NT == 1 ? 12 : 8>(run_of[run + 1] - run_of[run], d4, sl2,
-                        [&](int i) { return slot_of(list[run_of[run] + i]) + row * C::kPitch; }, mm, ll, s);
-        if (me.u0 >= c_lo && me.u1 <= c_hi) {
-            finish(me, row, d4, mm, ll, s);
-        } else {
-            // the CTA's first item, or its last
-            float *p = a.cta_slots + ((size_t)2 * blockIdx.x + (me.u0 > c_lo ? 1 : 0)) * C::kSlot +
-                       row * C::kPitch;
-            *reinterpret_cast<float4 *>(p + 4 * d4) = s;
-            if (d4 == 0) p[D] = mm, p[D + 1] = ll;
-        }
+    // a warp's share: two rows (D = 64: four) of one item at a time
+    constexpr int kGroup = 2 * (32 / (D / 4)), kGroups = C::kRows / kGroup;
+    for (int e = w; e < runs * kGroups; e += W) {
+        const int run = e / kGroups, from = run_of[run];
+        const Meta me = meta[from];
+        const int w0 = from >> 1;
+        // the run's last slot: the next run's predecessor that is in use
+        int to = run_of[run + 1] - 1;
+        while (meta[to].u0 != me.u0) --to;
+        const int n = (to >> 1) - w0 + 1;
+        const float *tail = to & 1 ? nullptr : a.warp_slots + ((size_t)blockIdx.x * W + (to >> 1)) * C::kSlot;
+        float *own = me.u0 >= c_lo && me.u1 <= c_hi
+                         ? nullptr
+                         // the CTA's first item, or its last
+                         : a.cta_slots + ((size_t)2 * blockIdx.x + (me.u0 > c_lo ? 1 : 0)) * C::kSlot;
+        add_parts<D, 2, 6>(
+            n, (e % kGroups) * kGroup, sl2,
+            [&](int i) {
+                return i == n - 1 && tail ? tail
+                                          : reinterpret_cast<const float *>(ring + (w0 + i) * C::kRing);
+            },
+            [&](int row, int d4, float mm, float ll, float4 s) {
+                if (!own) return finish(me, row, d4, mm, ll, s);
+                float *p = own + row * C::kPitch;
+                *reinterpret_cast<float4 *>(p + 4 * d4) = s;
+                if (d4 == 0) *reinterpret_cast<float2 *>(p + D) = make_float2(mm, ll);
+            });
     }
     __threadfence();
     __syncthreads();
@@ -712,7 +721,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
         bool last = false;
         const int run = tid == 0 ? 0 : runs - 1;
         if (runs > tid) {
-            const Meta me = meta[list[run_of[run]]];
+            const Meta me = meta[run_of[run]];
             if (!(me.u0 >= c_lo && me.u1 <= c_hi)) {
                 const uint32_t c0 = me.u0 / per, c1 = (me.u1 - 1) / per;  // CTAs of its tiles
                 last = atomicAdd(a.counters + c0, 1) == (int)(c1 - c0);
@@ -724,22 +733,16 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
     __syncthreads();
     for (int k = 0; k < 2; ++k) {
         if (!last_of[k]) continue;
-        const Meta me = meta[list[run_of[k == 0 ? 0 : runs - 1]]];
+        const Meta me = meta[run_of[k == 0 ? 0 : runs - 1]];
         const uint32_t c0 = me.u0 / per, c1 = (me.u1 - 1) / per;
         __threadfence();
-        for (int e = tid; e < kWork; e += W * 32) {
-            const int row = e / kQuads, d4 = e % kQuads;
-            float mm, ll;
-            float4 s;
-            const int odd = me.u0 > c0 * per ? 1 : 0;  // in its first CTA the item is the last one
-            add_parts<D, 8>((int)(c1 - c0) + 1, d4, sl2,
-                            [&](int i) {
-                                return a.cta_slots + ((size_t)2 * (c0 + i) + (i ? 0 : odd)) * C::kSlot +
-                                       row * C::kPitch;
-                            },
-                            mm, ll, s);
-            finish(me, row, d4, mm, ll, s);
-        }
+        const int odd = me.u0 > c0 * per ? 1 : 0;  // in its first CTA the item is the last one
+        constexpr int kStep = 32 / (D / 4);
+        for (int row = w * kStep; row < C::kRows; row += W * kStep)
+            add_parts<D, 1, 12>(
+                (int)(c1 - c0) + 1, row, sl2,
+                [&](int i) { return a.cta_slots + ((size_t)2 * (c0 + i) + (i ? 0 : odd)) * C::kSlot; },
+                [&](int r, int d4, float mm, float ll, float4 s) { finish(me, r, d4, mm, ll, s); });
     }
 }
 
@@ -783,7 +786,6 @@ size_t kv4_decode_slot_bytes(int D, int ctas) {
 cudaError_t launch_kv4_decode(KvAttnArgs a, int D, int max_rows, void *slots, int ctas,
                               cudaStream_t s) {
     const int nt = max_rows <= 8 ? 1 : 2;
-    const int warps = nt == 1 ? 12 : 8;
     const size_t slot = (size_t)8 * nt * (D + 4);
     a.cta_slots = reinterpret_cast<float *>(slots);
     a.warp_slots = a.cta_slots + 2 * slot * ctas;

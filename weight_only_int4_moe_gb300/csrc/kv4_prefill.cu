@@ -860,7 +860,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnAr
     if (w == 27) tmem_dealloc(tmem, kTmemCols);
 
     // items shared with other CTAs: the last of them adds the parts up
-    constexpr int kQuads = D / 4;
     for (int part = 0; part < 2; ++part) {
         const uint32_t u0 = sh.part_u0[part], u1 = sh.part_u1[part];
         if (u0 == u1) continue;
@@ -879,27 +878,24 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnAr
         const int rt = sh.part_rt[part], h = sh.part_h[part];
         const int rows = min(kRowsItem, rq.rows - rt * kRowsItem);
         const int odd = u0 > c0 * per ? 1 : 0;  // in its first CTA the item is the last one
-#pragma unroll 4
-        for (int e = tid; e < rows * kQuads; e += kThreads) {
-            const int row = e / kQuads, d4 = e % kQuads;
-            float mm, ll;
-            float4 s;
-            add_parts<D, 2>((int)(c1 - c0) + 1, d4, sl2,
-                            [&](int i) {
-                                return a.cta_slots + ((size_t)2 * (c0 + i) + (i ? 0 : odd)) * C::kSlot +
-                                       row * C::kPitch;
-                            },
-                            mm, ll, s);
-            const int rr = rt * kRowsItem + row, i = div_group(rr, a.gdiv), hh = rr - i * a.group;
-            const size_t o = (size_t)(rq.q0 + i) * a.q_heads + h * a.group + hh;
-            const float inv = ll > 0.0f ? 1.0f / ll : 0.0f;
-            const __nv_bfloat162 lo = __floats2bfloat162_rn(s.x * inv, s.y * inv);
-            const __nv_bfloat162 hi = __floats2bfloat162_rn(s.z * inv, s.w * inv);
-            *reinterpret_cast<uint2 *>(a.out + o * D + 4 * d4) = make_uint2(
-                *reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
-            if (a.lse && d4 == 0)
-                a.lse[o] = ll > 0.0f ? (mm * sl2 + log2f(ll)) * 0.6931471805599453f : -INFINITY;
-        }
+        constexpr int kGroup = 2 * (32 / (D / 4));
+        for (int row = w * kGroup; row < rows; row += kThreads / 32 * kGroup)
+            add_parts<D, 2, 2>(
+                (int)(c1 - c0) + 1, row, sl2,
+                [&](int i) { return a.cta_slots + ((size_t)2 * (c0 + i) + (i ? 0 : odd)) * C::kSlot; },
+                [&](int r, int d4, float mm, float ll, float4 s) {
+                    if (r >= rows) return;
+                    const int rr = rt * kRowsItem + r, i = div_group(rr, a.gdiv), hh = rr - i * a.group;
+                    const size_t o = (size_t)(rq.q0 + i) * a.q_heads + h * a.group + hh;
+                    const float inv = ll > 0.0f ? 1.0f / ll : 0.0f;
+                    const __nv_bfloat162 x = __floats2bfloat162_rn(s.x * inv, s.y * inv);
+                    const __nv_bfloat162 y = __floats2bfloat162_rn(s.z * inv, s.w * inv);
+                    *reinterpret_cast<uint2 *>(a.out + o * D + 4 * d4) =
+                        make_uint2(*reinterpret_cast<const uint32_t *>(&x),
+                                   *reinterpret_cast<const uint32_t *>(&y));
+                    if (a.lse && d4 == 0)
+                        a.lse[o] = ll > 0.0f ? (mm * sl2 + log2f(ll)) * 0.6931471805599453f : -INFINITY;
+                });
     }
 }
 
