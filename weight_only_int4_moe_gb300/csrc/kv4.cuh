@@ -145,10 +145,4 @@ MOE_DEV float kv_scale(float amax) {
     return fminf(fmaxf(s, kKvScaleMin), kKvScaleMax);
 }
 
-// rint(x / s) limited to -8..7, plus 8; the quotient is the IEEE one.
-MOE_DEV uint32_t kv_code(float x, float s) {
-    const float r = rintf(__fdiv_rn(x, s));
-    return (uint32_t)(int)(fminf(fmaxf(r, -8.0f), 7.0f) + 8.0f);
-}
-
 }  // namespace moe

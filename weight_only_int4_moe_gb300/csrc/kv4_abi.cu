@@ -155,7 +155,7 @@ int moe_kv4_append(const uint16_t *q, int64_t q_stride, const uint16_t *k, int64
     a.pool = pool_of(pages, layer, shape);
     a.batch = batch_of(batch);
     a.err = err;
-    return done(launch_kv4_append(a, D, str(stream)));
+    return done(launch_kv4_append(a, D, sms, str(stream)));
 }
 
 int moe_kv4_read(const void *pages, int layer, const moe_kv4_shape *shape,

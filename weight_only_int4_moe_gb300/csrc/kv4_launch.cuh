@@ -15,6 +15,7 @@ struct KvAppendArgs {
     const int32_t *positions;
     float eps;
     int max_pos, interleaved, q_heads;
+    int split;  // warps of a token
     uint16_t *q_out;
     KvPool pool;
     KvBatch batch;
@@ -69,7 +70,7 @@ struct KvPages {
     uint32_t block;
 };
 
-cudaError_t launch_kv4_append(const KvAppendArgs &a, int D, cudaStream_t s);
+cudaError_t launch_kv4_append(KvAppendArgs a, int D, int sms, cudaStream_t s);
 cudaError_t launch_kv4_read(const KvReadArgs &a, int D, cudaStream_t s);
 // Attention of the requests with few rows; max_rows bounds a request's rows.
 size_t kv4_decode_slot_bytes(int D, int ctas);
