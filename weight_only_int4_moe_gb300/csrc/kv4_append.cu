@@ -19,37 +19,67 @@ namespace moe {
 
 namespace {
 
-MOE_DEV void unpack8(const uint4 v, float (&x)[8]) {
+// Two floats in one register pair; every operation rounds each on its own, as the
+// scalar ones do, in half the instructions.
+MOE_DEV uint64_t pair(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+MOE_DEV float2 both(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+MOE_DEV uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+MOE_DEV uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+// a - b: b * -1 is exact, so the one rounding is the difference's.
+MOE_DEV uint64_t sub2(uint64_t a, uint64_t b, uint64_t minus1) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(b), "l"(minus1), "l"(a));
+    return r;
+}
+MOE_DEV void unpack8(const uint4 v, uint64_t (&x)[4]) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(w[i] << 16);
-        x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
+    for (int i = 0; i < 4; ++i)
+        x[i] = pair(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
 }
-
-MOE_DEV uint4 pack8(const float (&x)[8]) {
+MOE_DEV uint4 pack8(const uint64_t (&x)[4]) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+        const float2 f = both(x[i]);
+        const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
         w[i] = *reinterpret_cast<const uint32_t *>(&h);
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
-
-MOE_DEV void load8(const float *p, float (&x)[8]) {
-    const float4 a = *reinterpret_cast<const float4 *>(p);
-    const float4 b = *reinterpret_cast<const float4 *>(p + 4);
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-    x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+MOE_DEV void load8(const float *p, uint64_t (&x)[4]) {
+    const ulonglong2 a = *reinterpret_cast<const ulonglong2 *>(p);
+    const ulonglong2 b = *reinterpret_cast<const ulonglong2 *>(p + 4);
+    x[0] = a.x, x[1] = a.y, x[2] = b.x, x[3] = b.y;
 }
 
-// (a, b) -> (a c - b s, b c + a s), every operation rounded on its own.
-MOE_DEV void turn(float &a, float &b, float c, float s) {
-    const float x = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
-    b = __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
+// Pairs (a, b) -> (a c - b s, b c + a s), two at a time.
+MOE_DEV void turn2(uint64_t &a, uint64_t &b, uint64_t c, uint64_t s, uint64_t minus1) {
+    const uint64_t x = sub2(mul2(a, c), mul2(b, s), minus1);
+    b = add2(mul2(b, c), mul2(a, s));
     a = x;
+}
+// One pair whose members are the two halves of v.
+MOE_DEV uint64_t turn1(uint64_t v, float c, float s) {
+    const float2 f = both(v);
+    return pair(__fsub_rn(__fmul_rn(f.x, c), __fmul_rn(f.y, s)),
+                __fadd_rn(__fmul_rn(f.y, c), __fmul_rn(f.x, s)));
 }
 
 // A row's eight values of one group of 32 (four lanes hold a group): codes and
@@ -86,118 +116,104 @@ MOE_DEV float quantise8(float (&x)[8], uint32_t (&q)[8], bool limited) {
     return s;
 }
 
-template <int D>
-__global__ void __launch_bounds__(256) kv4_append_kernel(const KvAppendArgs a) {
-    constexpr int kLanes = D / 16;      // lanes of a row
-    constexpr int kRows = 32 / kLanes;  // rows of a warp
-    constexpr int NG = D / 32;
-    pdl_wait();
+// Where a token's k and v rows go.
+struct Place {
+    uint8_t *page;  // its page's first block; null: nowhere
+    int slot;
+};
+
+// The steps [from, to) of a token's heads of one kind (0: q, 1: k, 2: v), kRows heads
+// a step.  c, z: the rotation.
+template <int D, int kind>
+MOE_DEV void append_heads(const KvAppendArgs &a, int t, int from, int to, const uint64_t (&c)[4],
+                          const uint64_t (&z)[4], Place place) {
+    constexpr int kLanes = D / 16, kRows = 32 / kLanes, NG = D / 32;
+    if (from >= to) return;
     const int lane = threadIdx.x & 31, l = lane % kLanes, sub = lane / kLanes;
-    const int warp = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-    const int t = warp / a.split, share = warp - t * a.split;
-    if (t >= a.batch.tokens) return;
-    const int hkv = a.pool.hkv, ps = a.pool.ps;
-    // the token's steps of kRows heads: q, then k, then v; this warp's part of them
-    const int nq = (a.q_heads + kRows - 1) / kRows, nk = (hkv + kRows - 1) / kRows;
-    const int steps = nq + 2 * nk;
-    const int from = steps * share / a.split, to = steps * (share + 1) / a.split;
-    auto source = [&](int step, int &kind, int &head) -> const uint16_t * {
-        kind = step < nq ? 0 : step < nq + nk ? 1 : 2;  // q, k, v
-        head = (step - (kind == 0 ? 0 : kind == 1 ? nq : nq + nk)) * kRows + sub;
-        const uint16_t *p = kind == 0   ? a.q + (size_t)t * a.q_stride
+    const int heads = kind == 0 ? a.q_heads : a.pool.hkv, ps = a.pool.ps;
+    const uint16_t *base = (kind == 0   ? a.q + (size_t)t * a.q_stride
                             : kind == 1 ? a.k + (size_t)t * a.k_stride
-                                        : a.v + (size_t)t * a.v_stride;
-        // lanes past the last head repeat it and write nothing
-        return p + (size_t)min(head, (kind == 0 ? a.q_heads : hkv) - 1) * D + 8 * l;
-    };
-    int kind, head;
-    const uint16_t *src = source(from, kind, head);
-    uint4 nx = *reinterpret_cast<const uint4 *>(src), ny = *reinterpret_cast<const uint4 *>(src + D / 2);
-
-    // the token's place, its rotation and the weights
-    const int b = kv_request_of(a.batch.cu_q, a.batch.requests, t);
-    const int at = a.batch.kv_len[b] - (a.batch.cu_q[b + 1] - t);
-    int page = -1;
-    // more new tokens than the sequence's length: not stored
-    if (to > nq && at >= 0) page = kv_page_of(a.batch, a.pool, b, at, lane == 0 && to == steps ? a.err : nullptr);
-    const int slot = at >= 0 ? at % ps : 0;
-    float c[8], z[8];
-    if (a.cos && from < nq + nk) {
-        int pos = a.positions ? a.positions[t] : at;
-        if (pos < 0 || pos >= a.max_pos) {
-            if (lane == 0 && share == 0) kv_report(a.err, MOE_KV4_DEVERR_POSITION);
-            pos = min(max(pos, 0), a.max_pos - 1);
-        }
-        const float *cs = a.cos + (size_t)pos * (D / 2), *sn = a.sin + (size_t)pos * (D / 2);
-        if (!a.interleaved) {
-            load8(cs + 8 * l, c);
-            load8(sn + 8 * l, z);
-        } else {
-            // pairs of the row's first half, then of its second
-            *reinterpret_cast<float4 *>(c) = *reinterpret_cast<const float4 *>(cs + 4 * l);
-            *reinterpret_cast<float4 *>(c + 4) = *reinterpret_cast<const float4 *>(cs + D / 4 + 4 * l);
-            *reinterpret_cast<float4 *>(z) = *reinterpret_cast<const float4 *>(sn + 4 * l);
-            *reinterpret_cast<float4 *>(z + 4) = *reinterpret_cast<const float4 *>(sn + D / 4 + 4 * l);
-        }
+                                        : a.v + (size_t)t * a.v_stride) + 8 * l;
+    // lanes past the last head repeat it and write nothing
+    auto row = [&](int step) { return base + min(step * kRows + sub, heads - 1) * D; };
+    const uint16_t *w = kind == 0 ? a.q_weight : kind == 1 ? a.k_weight : nullptr;
+    uint64_t w0[4], w1[4];
+    if (kind < 2 && w) {
+        unpack8(*reinterpret_cast<const uint4 *>(w + 8 * l), w0);
+        unpack8(*reinterpret_cast<const uint4 *>(w + D / 2 + 8 * l), w1);
     }
-    uint4 w0 = make_uint4(0, 0, 0, 0), w1 = w0;
-    int weights_of = -1;  // the kind whose weights w0, w1 are
-
-    for (int step = from; step < to; ++step) {
-        const int kd = kind, hd = head;
-        float x[8], y[8];
-        unpack8(nx, x);
-        unpack8(ny, y);
-        if (step + 1 < to) {
-            src = source(step + 1, kind, head);
-            nx = *reinterpret_cast<const uint4 *>(src);
-            ny = *reinterpret_cast<const uint4 *>(src + D / 2);
-        }
-        const uint16_t *w = kd == 0 ? a.q_weight : kd == 1 ? a.k_weight : nullptr;
-        if (w) {
-            if (weights_of != kd) {
-                weights_of = kd;
-                w0 = *reinterpret_cast<const uint4 *>(w + 8 * l);
-                w1 = *reinterpret_cast<const uint4 *>(w + D / 2 + 8 * l);
-            }
-            // sum of squares of the row, in the documented order
-            float s[8];
+    const uint64_t minus1 = pair(-1.0f, -1.0f);
+    // the rows of this step and of the next kAhead, so that enough bytes are on their way
+    constexpr int kAhead = 2;
+    uint4 nx[kAhead], ny[kAhead];
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                s[j] = __fadd_rn(__fmul_rn(x[j], x[j]), __fmul_rn(y[j], y[j]));
-            float sum = __fadd_rn(__fadd_rn(__fadd_rn(s[0], s[4]), __fadd_rn(s[2], s[6])),
-                                  __fadd_rn(__fadd_rn(s[1], s[5]), __fadd_rn(s[3], s[7])));
+    for (int i = 0; i < kAhead; ++i) {
+        const uint16_t *src = row(min(from + i, to - 1));
+        nx[i] = *reinterpret_cast<const uint4 *>(src);
+        ny[i] = *reinterpret_cast<const uint4 *>(src + D / 2);
+    }
+#pragma unroll 1
+    for (int step = from; step < to; ++step) {
+        const int head = step * kRows + sub;
+        uint64_t x2[4], y2[4];
+        unpack8(nx[0], x2);
+        unpack8(ny[0], y2);
+#pragma unroll
+        for (int i = 0; i + 1 < kAhead; ++i) {
+            nx[i] = nx[i + 1];
+            ny[i] = ny[i + 1];
+        }
+        if (step + kAhead < to) {
+            const uint16_t *src = row(step + kAhead);
+            nx[kAhead - 1] = *reinterpret_cast<const uint4 *>(src);
+            ny[kAhead - 1] = *reinterpret_cast<const uint4 *>(src + D / 2);
+        }
+        if (kind < 2 && w) {
+            // sum of squares of the row, in the documented order
+            uint64_t s[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[j] = add2(mul2(x2[j], x2[j]), mul2(y2[j], y2[j]));
+            const float2 f = both(add2(add2(s[0], s[2]), add2(s[1], s[3])));
+            float sum = __fadd_rn(f.x, f.y);
 #pragma unroll
             for (int m = 1; m < kLanes; m <<= 1)
                 sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, m));
             const float r = __frcp_rn(__fsqrt_rn(__fadd_rn(__fmul_rn(sum, 1.0f / D), a.eps)));
-            float g[8];
-            unpack8(w0, g);
+            const uint64_t r2 = pair(r, r);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = __fmul_rn(__fmul_rn(x[j], r), g[j]);
-            unpack8(w1, g);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] = __fmul_rn(__fmul_rn(y[j], r), g[j]);
+            for (int j = 0; j < 4; ++j) {
+                x2[j] = mul2(mul2(x2[j], r2), w0[j]);
+                y2[j] = mul2(mul2(y2[j], r2), w1[j]);
+            }
         }
-        if (kd < 2 && a.cos) {
+        if (kind < 2 && a.cos) {
             if (!a.interleaved) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) turn(x[j], y[j], c[j], z[j]);
+                for (int j = 0; j < 4; ++j) turn2(x2[j], y2[j], c[j], z[j], minus1);
             } else {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    turn(x[2 * j], x[2 * j + 1], c[j], z[j]);
-                    turn(y[2 * j], y[2 * j + 1], c[4 + j], z[4 + j]);
+                    const float2 cx = both(c[j / 2]), zx = both(z[j / 2]);
+                    const float2 cy = both(c[2 + j / 2]), zy = both(z[2 + j / 2]);
+                    x2[j] = turn1(x2[j], j & 1 ? cx.y : cx.x, j & 1 ? zx.y : zx.x);
+                    y2[j] = turn1(y2[j], j & 1 ? cy.y : cy.x, j & 1 ? zy.y : zy.x);
                 }
             }
         }
-        if (kd == 0) {
-            if (hd < a.q_heads) {
-                uint16_t *dst = a.q_out + ((size_t)t * a.q_heads + hd) * D + 8 * l;
-                *reinterpret_cast<uint4 *>(dst) = pack8(x);
-                *reinterpret_cast<uint4 *>(dst + D / 2) = pack8(y);
+        if (kind == 0) {
+            if (head < heads) {
+                uint16_t *dst = a.q_out + ((size_t)t * heads + head) * D + 8 * l;
+                *reinterpret_cast<uint4 *>(dst) = pack8(x2);
+                *reinterpret_cast<uint4 *>(dst + D / 2) = pack8(y2);
             }
             continue;
+        }
+        float x[8], y[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 f = both(x2[j]), g = both(y2[j]);
+            x[2 * j] = f.x, x[2 * j + 1] = f.y;
+            y[2 * j] = g.x, y[2 * j + 1] = g.y;
         }
         // 0 * v is 0 for finite values and NaN for others
         float odd = 0.0f, big = 0.0f;
@@ -209,12 +225,12 @@ __global__ void __launch_bounds__(256) kv4_append_kernel(const KvAppendArgs a) {
         const bool limited = odd != 0.0f || big > kKvMax;
         uint32_t qx[8], qy[8];
         const float sx = quantise8(x, qx, limited), sy = quantise8(y, qy, limited);
-        const bool mine = hd < hkv && page >= 0;
+        const bool mine = head < heads && place.page;
         if (limited && mine) kv_report(a.err, MOE_KV4_DEVERR_RANGE);
         // the lane's eighth of its two groups G and NG/2 + G
         const int tq = l & 3, G = l >> 2, G2 = NG / 2 + G;
         uint32_t first, second;
-        if (kd == 1) {
+        if (kind == 1) {
             // K words (tq, G); D = 128: lanes four apart exchange one, so that each
             // stores two neighbours
             uint32_t wx = 0, wy = 0;
@@ -249,9 +265,10 @@ __global__ void __launch_bounds__(256) kv4_append_kernel(const KvAppendArgs a) {
             }
         }
         if (!mine) continue;
-        uint8_t *blk = kv_block(a.pool, page, hd);
-        uint8_t *codes = blk + (kd == 1 ? 0 : ps * (D / 2)) + slot * (D / 2);
-        uint16_t *sc = reinterpret_cast<uint16_t *>(blk + ps * D) + (kd == 1 ? 0 : ps * NG) + slot * NG;
+        uint8_t *blk = place.page + (size_t)head * a.pool.block;
+        uint8_t *codes = blk + (kind == 1 ? 0 : ps * (D / 2)) + place.slot * (D / 2);
+        uint16_t *sc =
+            reinterpret_cast<uint16_t *>(blk + ps * D) + (kind == 1 ? 0 : ps * NG) + place.slot * NG;
         // D = 128: K word pairs (tq, 0..1) and (tq, 2..3), V pieces of g = 2 tq + G;
         // D = 64: both of the lane's words
         *reinterpret_cast<uint2 *>(codes + (D == 128 ? 16 * tq + 8 * G : 8 * tq)) =
@@ -261,6 +278,56 @@ __global__ void __launch_bounds__(256) kv4_append_kernel(const KvAppendArgs a) {
             sc[G2] = __half_as_ushort(__float2half_rn(sy));
         }
     }
+}
+
+template <int D>
+__global__ void __launch_bounds__(256, 3) kv4_append_kernel(const KvAppendArgs a) {
+    constexpr int kLanes = D / 16, kRows = 32 / kLanes;
+    pdl_wait();
+    const int lane = threadIdx.x & 31, l = lane % kLanes;
+    const int warp = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+    const int t = warp / a.split, share = warp - t * a.split;
+    if (t >= a.batch.tokens) return;
+    // the token's steps of kRows heads: q, then k, then v; this warp's part of them
+    const int nq = (a.q_heads + kRows - 1) / kRows, nk = (a.pool.hkv + kRows - 1) / kRows;
+    const int steps = nq + 2 * nk;
+    const int from = steps * share / a.split, to = steps * (share + 1) / a.split;
+    Place place{nullptr, 0};
+    int at = 0;
+    if (to > nq || (a.cos && !a.positions)) {
+        const int b = kv_request_of(a.batch.cu_q, a.batch.requests, t);
+        at = a.batch.kv_len[b] - (a.batch.cu_q[b + 1] - t);
+        // more new tokens than the sequence's length: not stored
+        if (to > nq && at >= 0) {
+            const int page =
+                kv_page_of(a.batch, a.pool, b, at, lane == 0 && to == steps ? a.err : nullptr);
+            if (page >= 0) place = Place{kv_block(a.pool, page, 0), at % a.pool.ps};
+        }
+    }
+    uint64_t c[4] = {}, z[4] = {};
+    if (a.cos && from < nq + nk) {
+        int pos = a.positions ? a.positions[t] : at;
+        if (pos < 0 || pos >= a.max_pos) {
+            if (lane == 0 && share == 0) kv_report(a.err, MOE_KV4_DEVERR_POSITION);
+            pos = min(max(pos, 0), a.max_pos - 1);
+        }
+        const float *cs = a.cos + (size_t)pos * (D / 2), *sn = a.sin + (size_t)pos * (D / 2);
+        if (!a.interleaved) {
+            load8(cs + 8 * l, c);
+            load8(sn + 8 * l, z);
+        } else {
+            // pairs of the row's first half, then of its second
+            const ulonglong2 c0 = *reinterpret_cast<const ulonglong2 *>(cs + 4 * l);
+            const ulonglong2 c1 = *reinterpret_cast<const ulonglong2 *>(cs + D / 4 + 4 * l);
+            const ulonglong2 z0 = *reinterpret_cast<const ulonglong2 *>(sn + 4 * l);
+            const ulonglong2 z1 = *reinterpret_cast<const ulonglong2 *>(sn + D / 4 + 4 * l);
+            c[0] = c0.x, c[1] = c0.y, c[2] = c1.x, c[3] = c1.y;
+            z[0] = z0.x, z[1] = z0.y, z[2] = z1.x, z[3] = z1.y;
+        }
+    }
+    append_heads<D, 0>(a, t, from, min(to, nq), c, z, place);
+    append_heads<D, 1>(a, t, max(from, nq) - nq, min(to, nq + nk) - nq, c, z, place);
+    append_heads<D, 2>(a, t, max(from, nq + nk) - nq - nk, to - nq - nk, c, z, place);
 }
 
 // One row (token, head, K or V) per D/16 lanes, as in the append.
