@@ -60,7 +60,7 @@ struct KvAttnArgs {
 };
 
 constexpr int kKvMaxCtas = 160;     // slots of the workspace (a GB300 has 152 SMs)
-constexpr int kKvFewRows = 16;      // rows of a request up to which the decode kernel takes it
+constexpr int kKvFewRows = 128;      // rows of a request up to which the decode kernel takes it
 constexpr int kKvCounterByte = 256; // the counters' place in the workspace header
 
 // The pool for page management (all layers).
