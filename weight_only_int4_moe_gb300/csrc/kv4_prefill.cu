@@ -17,7 +17,9 @@
 // of a row passes between its two threads through shared memory); one warpgroup
 // turns K's codes into fp16 operand tiles and one V's, their loads one tile ahead in
 // registers; a warp for each tile of rows issues its MMAs, so that the softmax of one
-// runs under the products of the other.  A row in two
+// runs under the products of the other.  An item of up to 128 rows has one tile of
+// rows: both pairs of warpgroups take it, each every other tile of tokens, and the
+// first adds up their two results.  A row in two
 // threads: with a thread a whole row (half the warps, twice the registers each) a
 // tile's softmax took about 1900 cycles, most of it latency, against 1024 for the
 // tensor pipe between a tile's P and its next S.
@@ -36,6 +38,11 @@ namespace moe {
 namespace {
 
 constexpr int kTok = 128;        // tokens of a unit
+// Units before an item's first tile that hold no work: what a new item costs (its
+// queries, filling the pipeline, its output) in tiles.  Without them a CTA whose run
+// is many short items ends long after the others (a verify batch of ragged lengths:
+// 119 us against a median of 42 us).
+constexpr int kPad = 4;
 constexpr int kRowsItem = 256;
 constexpr int kChunks = 1024;
 constexpr int kThreads = 896;
@@ -50,6 +57,7 @@ static_assert(kThreads * kRegsLaunch <= 65536, "the register file");
 // and until the softmax warps have had theirs: a warp with no work that took its
 // share back early would keep it from a softmax warp that still waits for it.
 constexpr uint32_t kBarRegs = 1, kBarTile = 2;  // kBarTile + m: the 256 threads of row tile m
+constexpr uint32_t kBarBoth = 4;                // both row tiles' threads
 
 template <int D>
 struct Cfg {
@@ -63,7 +71,7 @@ struct Cfg {
     static constexpr int kLoads = D == 128 ? 4 : 2;   // 16-byte loads a thread for K (and V)
 };
 
-enum Bar { kKFull = 0, kKEmpty = 2, kVFull = 4, kVEmpty = 6, kQFull = 8, kSFull = 10, kPFull = 12, kOFull = 14, kBars = 16 };
+enum Bar { kKFull = 0, kKEmpty = 2, kVFull = 4, kVEmpty = 6, kQFull = 8, kSFull = 10, kPFull = 12, kOFull = 14, kQEmpty = 16, kBars = 17 };
 
 struct Shared {
     uint64_t bar[kBars];
@@ -71,6 +79,8 @@ struct Shared {
     int abort_flag, last_of;
     uint32_t ok[8];              // runs of 16 tokens that have a page, by tile
     uint32_t prefix[kChunks + 1];
+    int4 see[2][2][128];         // by row tile, half and row: lo, hi, first new token
+    uint64_t word[2][2][128];    // and the row's word of the tree
     float top[2][2][2][128];     // a tile's row maxima: by parity, row tile, half
     uint32_t part_u0[2], part_u1[2];
     int part_b[2], part_h[2], part_rt[2];
@@ -106,7 +116,7 @@ MOE_DEV int tiles_of(const KvAttnArgs &a, const Request &r, int rt, int &lo) {
 MOE_DEV uint32_t request_units(const KvAttnArgs &a, const Request &r) {
     uint32_t n = 0;
     int lo;
-    for (int rt = threadIdx.x & 31; rt < r.row_tiles; rt += 32) n += tiles_of(a, r, rt, lo);
+    for (int rt = threadIdx.x & 31; rt < r.row_tiles; rt += 32) n += tiles_of(a, r, rt, lo) + kPad;
     return __reduce_add_sync(0xffffffffu, n) * a.pool.hkv;
 }
 
@@ -115,7 +125,7 @@ MOE_DEV uint32_t request_units(const KvAttnArgs &a, const Request &r) {
 struct Segment {
     Request r;
     int b, rt, h, tile0, n;       // tile0: the first token tile of the run
-    uint32_t i_u0, i_u1;
+    uint32_t i_u0, i_u1;          // the item's tiles as units
     int rows;                     // of the item
     bool whole;
 };
@@ -144,49 +154,54 @@ struct Walk {
     }
 
     MOE_DEV bool next(const KvAttnArgs &a, Segment &s) {
-        if (u >= u_end) return false;
-        s.r = request_of(a, b);
-        while (true) {
-            const uint32_t n = per_chunk == 1 ? prefix[b + 1] - prefix[b] : request_units(a, s.r);
-            if (u < b_u0 + n) break;
-            b_u0 += n;
-            s.r = request_of(a, ++b);
-        }
-        // the row tile: 32 at a time
-        const int lane = threadIdx.x & 31, hkv = a.pool.hkv;
-        uint32_t at = u - b_u0, base = 0;
-        for (int rt0 = 0;; rt0 += 32) {
-            int lo = 0;
-            const int rt = rt0 + lane;
-            const uint32_t n = rt < s.r.row_tiles ? (uint32_t)tiles_of(a, s.r, rt, lo) : 0u;
-            uint32_t x = n * hkv;
+        while (u < u_end) {
+            s.r = request_of(a, b);
+            while (true) {
+                const uint32_t n = per_chunk == 1 ? prefix[b + 1] - prefix[b] : request_units(a, s.r);
+                if (u < b_u0 + n) break;
+                b_u0 += n;
+                s.r = request_of(a, ++b);
+            }
+            // the row tile: 32 at a time
+            const int lane = threadIdx.x & 31, hkv = a.pool.hkv;
+            uint32_t at = u - b_u0, base = 0;
+            for (int rt0 = 0;; rt0 += 32) {
+                int lo = 0;
+                const int rt = rt0 + lane;
+                const uint32_t n = rt < s.r.row_tiles ? (uint32_t)(tiles_of(a, s.r, rt, lo) + kPad) : 0u;
+                uint32_t x = n * hkv;
 #pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const uint32_t y = __shfl_up_sync(0xffffffffu, x, d);
-                if (lane >= d) x += y;
+                for (int d = 1; d < 32; d <<= 1) {
+                    const uint32_t y = __shfl_up_sync(0xffffffffu, x, d);
+                    if (lane >= d) x += y;
+                }
+                const unsigned who = __ballot_sync(0xffffffffu, at < base + x);
+                if (!who) {
+                    base += __shfl_sync(0xffffffffu, x, 31);
+                    continue;
+                }
+                const int l = __ffs(who) - 1;
+                s.rt = rt0 + l;
+                const uint32_t span = __shfl_sync(0xffffffffu, n, l);
+                const uint32_t rt_u0 = base + __shfl_sync(0xffffffffu, x, l) - span * hkv;
+                s.h = (int)((at - rt_u0) / span);
+                s.i_u0 = b_u0 + rt_u0 + s.h * span + kPad;  // its tiles
+                s.i_u1 = s.i_u0 - kPad + span;
+                s.tile0 = __shfl_sync(0xffffffffu, lo, l);
+                break;
             }
-            const unsigned who = __ballot_sync(0xffffffffu, at < base + x);
-            if (!who) {
-                base += __shfl_sync(0xffffffffu, x, 31);
-                continue;
-            }
-            const int l = __ffs(who) - 1;
-            s.rt = rt0 + l;
-            const uint32_t tiles = __shfl_sync(0xffffffffu, n, l);
-            const uint32_t rt_u0 = base + __shfl_sync(0xffffffffu, x, l) - tiles * hkv;
-            s.h = (int)((at - rt_u0) / tiles);
-            s.i_u0 = b_u0 + rt_u0 + s.h * tiles;
-            s.i_u1 = s.i_u0 + tiles;
-            s.tile0 = __shfl_sync(0xffffffffu, lo, l) + (int)(u - s.i_u0);
-            break;
+            u = max(u, s.i_u0);
+            if (u >= u_end) return false;
+            s.tile0 += (int)(u - s.i_u0);
+            s.b = b;
+            const uint32_t end = min(u_end, s.i_u1);
+            s.n = (int)(end - u);
+            s.whole = u == s.i_u0 && end == s.i_u1;
+            s.rows = min(kRowsItem, s.r.rows - s.rt * kRowsItem);
+            u = end;
+            return true;
         }
-        s.b = b;
-        const uint32_t end = min(u_end, s.i_u1);
-        s.n = (int)(end - u);
-        s.whole = u == s.i_u0 && end == s.i_u1;
-        s.rows = min(kRowsItem, s.r.rows - s.rt * kRowsItem);
-        u = end;
-        return true;
+        return false;
     }
 };
 
@@ -497,6 +512,35 @@ MOE_DEV void fewer_regs() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// A tile of up to 128 query rows, from row_base of the request on: 16-byte chunks,
+// converted to fp16 and swizzled, by 256 threads (id).
+template <int D>
+MOE_DEV void load_q(const KvAttnArgs &a, const Segment &sg, uint32_t dst, int row_base, int n_rows, int id) {
+    bool bad = false;
+    const uint32_t flip = a.scale_log2 < 0.0f ? 0x80008000u : 0u;
+#pragma unroll
+    for (int c0 = 0; c0 < D / 16; c0 += 4) {
+        uint4 v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int c = id + 256 * (c0 + e), qr = c / (D / 8), ch = c % (D / 8);
+            const int i = div_group(row_base + qr, a.gdiv), hh = row_base + qr - i * a.group;
+            v[e] = make_uint4(0, 0, 0, 0);
+            if (qr < n_rows)
+                v[e] = *reinterpret_cast<const uint4 *>(a.q + (size_t)(sg.r.q0 + i) * a.q_stride +
+                                                        (size_t)(sg.h * a.group + hh) * D + 8 * ch);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int c = id + 256 * (c0 + e), qr = c / (D / 8), ch = c % (D / 8);
+            const uint4 x = bf16x8_to_f16x8_sat(v[e], bad);
+            sts128(dst + tile_at(qr, ch), x.x ^ flip, x.y ^ flip, x.z ^ flip, x.w ^ flip);
+        }
+    }
+    if (__any_sync(0xffffffffu, bad) && (id & 31) == 0) kv_report(a.err, MOE_KV4_DEVERR_RANGE);
+    fence_proxy_async_shared();
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnArgs a) {
     using C = Cfg<D>;
@@ -507,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnAr
     pdl_wait();
     if (tid == 0) {
         sh.abort_flag = 0;
-        const int counts[8] = {128, 2, 128, 2, 256, 1, 256, 1};
+        const int counts[9] = {128, 2, 128, 2, 256, 1, 256, 1, 2};
         for (int i = 0; i < kBars; ++i) mbar_init(smem_u32(&sh.bar[i]), counts[i / 2]);
         mbar_fence_init();
         sh.part_u0[0] = sh.part_u1[0] = sh.part_u0[1] = sh.part_u1[1] = 0;
@@ -532,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnAr
             const bool big = r.row_tiles > 4;
             int lo;
             if (!big)
-                for (int rt = 0; rt < r.row_tiles; ++rt) n += (uint32_t)tiles_of(a, r, rt, lo) * hkv;
+                for (int rt = 0; rt < r.row_tiles; ++rt) n += (uint32_t)(tiles_of(a, r, rt, lo) + kPad) * hkv;
             unsigned who = __ballot_sync(0xffffffffu, big);
             while (who) {
                 const int l = __ffs(who) - 1;
@@ -588,74 +632,59 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnAr
             const uint32_t s_at = s_col(m) + lane_off + 64u * half;
             const uint32_t p_at = p_col(m) + lane_off + 32u * half;
             const uint32_t o_at = o_col(m) + lane_off + (D / 2) * half;
-            uint32_t s_ph = 0, o_ph = 0, tiles = 0;
+            uint32_t s_ph = 0, o_ph = 0, e_ph = 0, t0 = 0;  // t0: tiles of earlier runs
             bool dead = false;
-            while (walk.next(a, sg)) {
-                if (m * 128 >= sg.rows) {
-                    tiles += sg.n;
-                    continue;
-                }
-                // Q: 16-byte chunks of the tile's rows, converted and swizzled
-                const int row_base = sg.rt * kRowsItem + m * 128, n_rows = min(128, sg.rows - m * 128);
-                bool bad = false;
-                const uint32_t flip = a.scale_log2 < 0.0f ? 0x80008000u : 0u;
-#pragma unroll
-                for (int c0 = 0; c0 < D / 16; c0 += 4) {
-                    uint4 v[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int c = (tid & 255) + 256 * (c0 + e), qr = c / (D / 8), ch = c % (D / 8);
-                        const int i = div_group(row_base + qr, a.gdiv), hh = row_base + qr - i * a.group;
-                        v[e] = make_uint4(0, 0, 0, 0);
-                        if (qr < n_rows)
-                            v[e] = *reinterpret_cast<const uint4 *>(
-                                a.q + (size_t)(sg.r.q0 + i) * a.q_stride +
-                                (size_t)(sg.h * a.group + hh) * D + 8 * ch);
-                    }
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int c = (tid & 255) + 256 * (c0 + e), qr = c / (D / 8), ch = c % (D / 8);
-                        const uint4 x = bf16x8_to_f16x8_sat(v[e], bad);
-                        sts128(smem + C::kQ + m * C::kTileBytes + tile_at(qr, ch), x.x ^ flip, x.y ^ flip,
-                               x.z ^ flip, x.w ^ flip);
-                    }
-                }
-                if (__any_sync(0xffffffffu, bad) && lane == 0) kv_report(a.err, MOE_KV4_DEVERR_RANGE);
-                fence_proxy_async_shared();
+            // the queries of this warpgroup pair's rows, where it loads any
+            auto queries = [&](const Segment &x) {
+                load_q<D>(a, x, smem + C::kQ + m * C::kTileBytes, x.rt * kRowsItem + m * 128,
+                          min(128, x.rows - m * 128), tid & 255);
                 mbar_arrive(bar(kQFull + m));
-
+            };
+            bool more = walk.next(a, sg);
+            if (more && m * 128 < sg.rows) queries(sg);
+            while (more) {
+                // up to 128 rows: both pairs take them, every other tile of tokens each
+                const bool narrow = sg.rows <= 128;
+                const int first = narrow ? m : 0, step = narrow ? 2 : 1;
+                const int row_base = sg.rt * kRowsItem + (narrow ? 0 : m * 128);
+                const int n_rows = min(128, sg.rows - (narrow ? 0 : m * 128));
                 const int i = div_group(row_base + r, a.gdiv), hh = row_base + r - i * a.group;
                 const bool live = r < n_rows;
                 const int p = sg.r.first + i;
                 const int hi = live ? min(p, sg.r.end - 1) : -1;
                 const int lo = a.window > 0 ? p - a.window : -1;
-                const uint64_t word = a.tree && live ? a.tree[sg.r.q0 + i] : 0;
+                // for the tiles at the edges only: not kept in registers
+                sh.see[m][half][r] = make_int4(lo, hi, sg.r.first, 0);
+                if (a.tree) sh.word[m][half][r] = live ? a.tree[sg.r.q0 + i] : 0;
                 // tokens that every row of the warp sees
                 const int open = __reduce_min_sync(0xffffffffu, live ? (a.tree ? min(hi + 1, sg.r.first) : hi + 1)
                                                                      : INT32_MAX);
                 const int shut = __reduce_max_sync(0xffffffffu, live ? lo + 1 : 0);
                 float top = -INFINITY, sum = 0.0f;
-                for (int k = 0; k < sg.n; ++k) {
+                int j0 = (sg.tile0 + first) * kTok + 64 * half;
+                uint32_t at = t0 + first;  // the tile among all of the CTA's
+                const int mine = sg.n > first ? (sg.n - first + step - 1) / step : 0;
+#pragma unroll 1
+                for (int left = mine; left > 0; --left, j0 += step * kTok, at += step) {
                     // a wait that gave up (a kernel bug, reported) leaves the loop's shape
                     // as it is: the tile's other warps count on this one at the barriers
                     if (!dead) dead = __any_sync(0xffffffffu, !mbar_wait(bar(kSFull + m), s_ph, abort_flag, a.err));
                     s_ph ^= 1;
                     tc_fence_after();
-                    const uint32_t ok = sh.ok[tiles & 7] >> (4 * half);
-                    float *swap = &sh.top[tiles & 1][m][0][r];
-                    ++tiles;
-                    const int j0 = (sg.tile0 + k) * kTok + 64 * half;
-                    const bool masked = (ok & 15u) != 15u || j0 + 64 > open || j0 < shut;
+                    const uint32_t ok = sh.ok[at & 7] >> (4 * half);
+                    float *swap = &sh.top[left & 1][m][0][r];
                     uint32_t v[64];
                     tmem_ld32(s_at, v);
                     tmem_ld32(s_at + 32, v + 32);
                     tmem_wait_ld(v);
                     tmem_pass(v + 32);
-                    if (masked) {
+                    if ((ok & 15u) != 15u || j0 + 64 > open || j0 < shut) {
+                        const int4 edge = sh.see[m][half][r];
+                        const uint64_t word = a.tree ? sh.word[m][half][r] : 0;
 #pragma unroll
                         for (int c = 0; c < 2; ++c) {
-                            const uint32_t see = visible32(j0 + 32 * c, lo, hi, ok >> (2 * c),
-                                                           a.tree != nullptr, word, sg.r.first);
+                            const uint32_t see = visible32(j0 + 32 * c, edge.x, edge.y, ok >> (2 * c),
+                                                           a.tree != nullptr, word, edge.z);
 #pragma unroll
                             for (int e = 0; e < 32; ++e)
                                 if (!((see >> e) & 1u)) v[32 * c + e] = 0xff800000u;  // -inf
@@ -685,7 +714,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnAr
                         const float f = grow ? kv_ex2((top - now) * sl2) : 1.0f;
                         if (grow) top = now;
                         sum *= f;
-                        if (k > 0) scale_o<D>(o_at, f);
+                        if (left != mine) scale_o<D>(o_at, f);
                     }
                     const float off = top == -INFINITY ? 0.0f : -top * sl2;
                     const uint64_t sc2 = pack2(sl2, sl2), off2 = pack2(off, off);
@@ -716,36 +745,87 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnAr
                     tc_fence_before();
                     mbar_arrive(bar(kPFull + m));
                 }
+                // the next run's queries, once the products of this one have read theirs:
+                // its first scores are then on their way while this one's output is written
+                t0 += sg.n;
+                Segment nx;
+                const bool another = walk.next(a, nx);
+                if (another && m * 128 < nx.rows) {
+                    // (only a pair that loads may wait here: without its load the barrier
+                    // cannot run a phase ahead of the one it waits for)
+                    if (!dead) dead = __any_sync(0xffffffffu, !mbar_wait(bar(kQEmpty), e_ph, abort_flag, a.err));
+                    queries(nx);
+                }
+                e_ph ^= 1;
                 // O of the run
-                if (!dead) dead = __any_sync(0xffffffffu, !mbar_wait(bar(kOFull + m), o_ph, abort_flag, a.err));
-                o_ph ^= 1;
-                tc_fence_after();
+                if (mine) {
+                    if (!dead) dead = __any_sync(0xffffffffu, !mbar_wait(bar(kOFull + m), o_ph, abort_flag, a.err));
+                    o_ph ^= 1;
+                }
                 {
-                    // the row's sum: its second half's part passes to both threads
+                    // the row's sum passes between its two threads
                     float *swap = &sh.top[0][m][0][r];
                     swap[128 * half] = sum;
                     named_bar_sync(kBarTile + m, 256);
                     sum += swap[128 * (half ^ 1)];
                     named_bar_sync(kBarTile + m, 256);  // read before the next run writes there
+                    // narrow: the second pair hands its maximum, sum and O to the first
+                    float mix = 1.0f, mix1 = 0.0f;
+                    if (narrow) {
+                        if (m == 1 && half == 0) {
+                            sh.top[0][1][0][r] = top;
+                            sh.top[0][1][1][r] = sum;
+                        }
+                        tc_fence_before();
+                        named_bar_sync(kBarBoth, 512);
+                        if (m == 0) {
+                            const float top1 = sh.top[0][1][0][r], sum1 = sh.top[0][1][1][r];
+                            const float both = fmaxf(top, top1);
+                            mix = top > -INFINITY ? kv_ex2((top - both) * sl2) : 0.0f;
+                            mix1 = top1 > -INFINITY ? kv_ex2((top1 - both) * sl2) : 0.0f;
+                            top = both;
+                            sum = sum * mix + sum1 * mix1;
+                        }
+                    }
+                    tc_fence_after();
+                    const bool join = narrow && sg.n > 1;
+                    const bool writes = live && !(narrow && m == 1);
                     const float inv = sg.whole ? (sum > 0.0f ? 1.0f / sum : 0.0f) : 1.0f;
+                    mix *= inv;
+                    mix1 *= inv;
                     const size_t o_row = (size_t)(sg.r.q0 + i) * a.q_heads + sg.h * a.group + hh;
                     const int part = sg.i_u0 > c_lo ? 1 : 0;
                     float *slot = a.cta_slots + ((size_t)2 * blockIdx.x + part) * C::kSlot +
-                                  (m * 128 + r) * C::kPitch;
+                                  ((narrow ? 0 : m * 128) + r) * C::kPitch;
 #pragma unroll 1
-                    for (int q = 0; q < D / 64; ++q) {
+                    for (int q = 0; q < (narrow && m == 1 ? 0 : D / 64); ++q) {
                         // 32 columns, four V pieces g = 4a..: two groups' 16 dimensions
                         uint32_t o[32];
                         tmem_ld32(o_at + 32 * q, o);
                         tmem_wait_ld(o);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * mix);
+                        if (join) {
+#pragma unroll
+                            for (int c = 0; c < 2; ++c) {
+                                float o1[16];
+                                tmem_ld_32x32b_x16_wait(o_at + 128 + 32 * q + 16 * c, o1);
+                                if (mix1 > 0.0f) {
+#pragma unroll
+                                    for (int e = 0; e < 16; ++e)
+                                        o[16 * c + e] = __float_as_uint(
+                                            fmaf(o1[e], mix1, __uint_as_float(o[16 * c + e])));
+                                }
+                            }
+                        }
                         const int at = half * (D / 64) + q, d0 = 64 * (at >> 1) + 16 * (at & 1);
-                        if (!live) continue;
+                        if (!writes) continue;
 #pragma unroll
                         for (int gr = 0; gr < 2; ++gr) {
                             float x[16];
 #pragma unroll
                             for (int e = 0; e < 16; ++e)
-                                x[e] = __uint_as_float(o[(e >> 2) * 8 + 2 * (e & 3) + gr]) * inv;
+                                x[e] = __uint_as_float(o[(e >> 2) * 8 + 2 * (e & 3) + gr]);
                             if (sg.whole) {
                                 uint32_t y[8];
 #pragma unroll
@@ -764,7 +844,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnAr
                             }
                         }
                     }
-                    if (live && half == 0) {
+                    if (writes && half == 0) {
                         if (!sg.whole) {
                             slot[D] = top;
                             slot[D + 1] = sum;
@@ -783,6 +863,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnAr
                     sh.part_rt[part] = sg.rt;
                 }
                 tc_fence_before();  // the reads of O before the next run's first product
+                if (narrow) named_bar_sync(kBarBoth, 512);
+                sg = nx;
+                more = another;
             }
             fewer_regs<kRegsLaunch>();
             named_bar_sync(kBarRegs, kThreads);
@@ -805,49 +888,55 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnAr
             const uint32_t id_s = idesc_f16_m128(kTok);
             const uint32_t id_o = idesc_f16_m128(D) | (1u << 16);  // B N-major
             const uint32_t q_at = smem + C::kQ + (uint32_t)m * C::kTileBytes;
-            Ring kr(2), vr(2);
-            uint32_t p_ph = 0, q_ph = 0;
+            uint32_t p_ph = 0, q_ph[2] = {0, 0}, t0 = 0;  // t0: tiles of earlier runs
             bool ok = true;
             auto wait = [&](int b, uint32_t ph) {
                 ok = __all_sync(0xffffffffu, mbar_wait(bar(b), ph, abort_flag, a.err));
                 return ok;
             };
+            // a tile's slot in the rings of two, and its phase
+            auto slot = [&](int k) { return (t0 + k) & 1u; };
+            auto phase = [&](int k) { return ((t0 + k) >> 1) & 1u; };
             while (m < 2 && ok && walk.next(a, sg)) {
-                if (m * 128 >= sg.rows) {
-                    // no rows: only lets the operand tiles pass
-                    for (int k = 0; k < sg.n; ++k) {
-                        if (!wait(kKFull + kr.idx, kr.ph)) break;
-                        if (lane == 0) mbar_arrive(bar(kKEmpty + kr.idx));
-                        kr.next();
-                        if (!wait(kVFull + vr.idx, vr.ph)) break;
-                        if (lane == 0) mbar_arrive(bar(kVEmpty + vr.idx));
-                        vr.next();
-                    }
-                    continue;
+                // narrow: warp m takes every other tile, for the same rows, and lets go
+                // of a tile for both
+                const bool narrow = sg.rows <= 128;
+                const int first = narrow ? m : 0, step = narrow ? 2 : 1;
+                const uint32_t q_at = smem + C::kQ + (narrow ? 0u : (uint32_t)m * C::kTileBytes);
+                if (!wait(kQFull, q_ph[0])) break;
+                q_ph[0] ^= 1;
+                if (!narrow) {
+                    if (m == 1 && !wait(kQFull + 1, q_ph[1])) break;
+                    q_ph[1] ^= 1;
                 }
-                if (!wait(kQFull + m, q_ph)) break;
-                q_ph ^= 1;
-                if (!wait(kKFull + kr.idx, kr.ph)) break;
-                tc_fence_after();
-                mma_qk<D>(s_col(m), q_at, smem + C::kK + kr.idx * C::kTileBytes, id_s);
-                tc_commit2_elect(bar(kSFull + m), bar(kKEmpty + kr.idx));
-                kr.next();
-                for (int k = 0; k < sg.n; ++k) {
-                    const bool more = k + 1 < sg.n;
-                    if (!wait(kVFull + vr.idx, vr.ph)) break;
-                    if (more && !wait(kKFull + kr.idx, kr.ph)) break;
+                auto scores = [&](int k) {
+                    const uint32_t done = bar(kKEmpty + slot(k));
+                    mma_qk<D>(s_col(m), q_at, smem + C::kK + slot(k) * C::kTileBytes, id_s);
+                    tc_commit2_elect(bar(kSFull + m), done);
+                    // the last scores of the run have read the queries
+                    tc_commit2_elect(narrow ? done : 0u, k + step >= sg.n ? bar(kQEmpty) : 0u);
+                };
+                if (first < sg.n) {
+                    if (!wait(kKFull + slot(first), phase(first))) break;
+                    tc_fence_after();
+                    scores(first);
+                } else if (lane == 0) {
+                    mbar_arrive(bar(kQEmpty));
+                }
+                for (int k = first; k < sg.n; k += step) {
+                    const bool again = k + step < sg.n;
+                    if (!wait(kVFull + slot(k), phase(k))) break;
+                    if (again && !wait(kKFull + slot(k + step), phase(k + step))) break;
                     if (!wait(kPFull + m, p_ph)) break;
                     p_ph ^= 1;
                     tc_fence_after();
-                    mma_pv(o_col(m), p_col(m), smem + C::kV + vr.idx * C::kTileBytes, id_o, k > 0);
-                    if (more) {
-                        mma_qk<D>(s_col(m), q_at, smem + C::kK + kr.idx * C::kTileBytes, id_s);
-                        tc_commit2_elect(bar(kSFull + m), bar(kKEmpty + kr.idx));
-                        kr.next();
-                    }
-                    tc_commit2_elect(bar(kVEmpty + vr.idx), more ? 0u : bar(kOFull + m));
-                    vr.next();
+                    mma_pv(o_col(m), p_col(m), smem + C::kV + slot(k) * C::kTileBytes, id_o, k > first);
+                    if (again) scores(k + step);
+                    const uint32_t done = bar(kVEmpty + slot(k));
+                    tc_commit2_elect(done, again ? 0u : bar(kOFull + m));
+                    if (narrow) tc_commit_elect(done);
                 }
+                t0 += sg.n;
             }
             named_bar_sync(kBarRegs, kThreads);
             more_regs<kRegsLaunch>();
