@@ -49,7 +49,7 @@ constexpr int kThreads = 896;
 constexpr uint32_t kTmemCols = 512;
 // Registers a thread of each role (multiples of 8).  The seven warpgroups' shares add
 // up to what the block is launched with, 7 x 72.
-constexpr int kRegsLaunch = 72, kRegsSoftmax = 88, kRegsCodes = 56, kRegsMma = 40;
+constexpr int kRegsLaunch = 72, kRegsSoftmax = 80, kRegsCodes = 64, kRegsMma = 56;
 static_assert(4 * kRegsSoftmax + 2 * kRegsCodes + kRegsMma == 7 * kRegsLaunch, "register shares");
 static_assert(kThreads * kRegsLaunch <= 65536, "the register file");
 // Before the block's common end every warp returns to kRegsLaunch.  Those that take
@@ -71,7 +71,8 @@ struct Cfg {
     static constexpr int kLoads = D == 128 ? 4 : 2;   // 16-byte loads a thread for K (and V)
 };
 
-enum Bar { kKFull = 0, kKEmpty = 2, kVFull = 4, kVEmpty = 6, kQFull = 8, kSFull = 10, kPFull = 12, kOFull = 14, kQEmpty = 16, kBars = 17 };
+// S and P: by row tile and half tile (2 m + sub); kPv: by row tile, after every P V.
+enum Bar { kKFull = 0, kKEmpty = 2, kVFull = 4, kVEmpty = 6, kQFull = 8, kPv = 10, kSFull = 12, kPFull = 16, kQEmpty = 20, kOFull = 22, kBars = 24 };
 
 struct Shared {
     uint64_t bar[kBars];
@@ -226,7 +227,8 @@ MOE_DEV uint64_t desc_n_major(uint32_t saddr) {
            ((uint64_t)(1024u >> 4) << 32) | ((uint64_t)1u << 46) | ((uint64_t)2u << 61);
 }
 
-// S = Q K^T: D / 16 MMAs, operands in column blocks of 64 dimensions; then commits.
+// S = Q K^T for half a tile of tokens: D / 16 MMAs, operands in column blocks of 64
+// dimensions.
 template <int D>
 MOE_DEV void mma_qk(uint32_t d_tmem, uint32_t q, uint32_t k, uint32_t idesc) {
 #pragma unroll
@@ -247,24 +249,20 @@ MOE_DEV void mma_qk(uint32_t d_tmem, uint32_t q, uint32_t k, uint32_t idesc) {
     }
 }
 
-// O (+)= P V: kTok / 16 MMAs; P's columns advance by 8, V's tokens by 16 rows.
+// O (+)= P V for half a tile: four MMAs; P's columns advance by 8, V's tokens by 16 rows.
 MOE_DEV void mma_pv(uint32_t d_tmem, uint32_t p_tmem, uint32_t v, uint32_t idesc, uint32_t accumulate) {
-#pragma unroll
-    for (int s = 0; s < kTok / 64; ++s) {
-        const uint64_t vd = desc_n_major(v + s * 64 * 128);
-        asm volatile(
-            "{\n\t.reg .pred p, t, e;\n\t.reg .b32 a1, a2, a3;\n\t.reg .b64 b1, b2, b3;\n\t"
-            "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, %4, %4;\n\t"
-            "add.u32 a1, %1, 8;\n\tadd.u32 a2, %1, 16;\n\tadd.u32 a3, %1, 24;\n\t"
-            "add.u64 b1, %2, 128;\n\tadd.u64 b2, %2, 256;\n\tadd.u64 b3, %2, 384;\n\t"
-            "elect.sync _|e, 0xffffffff;\n\t"
-            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
-            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n\t"
-            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, t;\n\t"
-            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, t;\n\t}" ::"r"(d_tmem),
-            "r"(p_tmem + 32 * s), "l"(vd), "r"(idesc), "r"(s ? 1u : accumulate)
-            : "memory");
-    }
+    asm volatile(
+        "{\n\t.reg .pred p, t, e;\n\t.reg .b32 a1, a2, a3;\n\t.reg .b64 b1, b2, b3;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, %4, %4;\n\t"
+        "add.u32 a1, %1, 8;\n\tadd.u32 a2, %1, 16;\n\tadd.u32 a3, %1, 24;\n\t"
+        "add.u64 b1, %2, 128;\n\tadd.u64 b2, %2, 256;\n\tadd.u64 b3, %2, 384;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, t;\n\t}" ::"r"(d_tmem),
+        "r"(p_tmem), "l"(desc_n_major(v)), "r"(idesc), "r"(accumulate)
+        : "memory");
 }
 
 #define KV4_R8(v, o) "=r"(v[o]), "=r"(v[o + 1]), "=r"(v[o + 2]), "=r"(v[o + 3]), "=r"(v[o + 4]), \
@@ -282,14 +280,11 @@ MOE_DEV void tmem_ld32(uint32_t taddr, uint32_t *v) {
         : "r"(taddr)
         : "memory");
 }
-// Waits for the thread's loads; the registers of one pass through, so that no use
-// of them can come before the wait (tmem_pass: for the further ones).
+// Waits for the thread's loads; the registers pass through, so that no use of them can
+// come before the wait.
 MOE_DEV void tmem_wait_ld(uint32_t *v) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
                  : KV4_P8(v, 0), KV4_P8(v, 8), KV4_P8(v, 16), KV4_P8(v, 24)::"memory");
-}
-MOE_DEV void tmem_pass(uint32_t *v) {
-    asm volatile("" : KV4_P8(v, 0), KV4_P8(v, 8), KV4_P8(v, 16), KV4_P8(v, 24)::"memory");
 }
 
 // One instruction of the ALU pipe, which has half the lanes of the FMA pipe.
@@ -551,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnAr
     pdl_wait();
     if (tid == 0) {
         sh.abort_flag = 0;
-        const int counts[9] = {128, 2, 128, 2, 256, 1, 256, 1, 2};
+        const int counts[12] = {128, 2, 128, 2, 256, 1, 1, 1, 256, 256, 2, 1};
         for (int i = 0; i < kBars; ++i) mbar_init(smem_u32(&sh.bar[i]), counts[i / 2]);
         mbar_fence_init();
         sh.part_u0[0] = sh.part_u1[0] = sh.part_u0[1] = sh.part_u1[1] = 0;
@@ -613,9 +608,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnAr
     const uint32_t tmem = sh.tmem;
     const float sl2 = fmaxf(fabsf(a.scale_log2), 1e-30f);
     auto bar = [&](int i) { return smem_u32(&sh.bar[i]); };
-    // S (and P over its second half) of the two row tiles, then their O
-    auto s_col = [&](int m) { return tmem + 128u * m; };
-    auto p_col = [&](int m) { return tmem + 128u * m + 64u; };
+    // S (and P over its second half) of the row tiles' half tiles, then their O
+    auto s_col = [&](int m, int sub) { return tmem + 128u * m + 64u * sub; };
+    auto p_col = [&](int m, int sub) { return s_col(m, sub) + 32u; };
     auto o_col = [&](int m) { return tmem + 256u + 128u * m; };
     int *abort_flag = &sh.abort_flag;
 
@@ -629,10 +624,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnAr
             // the thread's row tile, half of the columns and row
             const int m = w >> 3, half = (w >> 2) & 1, r = tid & 127;
             const uint32_t lane_off = (uint32_t)(32 * (w & 3)) << 16;
-            const uint32_t s_at = s_col(m) + lane_off + 64u * half;
-            const uint32_t p_at = p_col(m) + lane_off + 32u * half;
+            const uint32_t s_at = s_col(m, 0) + lane_off + 32u * half;
+            const uint32_t p_at = p_col(m, 0) + lane_off + 16u * half;
             const uint32_t o_at = o_col(m) + lane_off + (D / 2) * half;
-            uint32_t s_ph = 0, o_ph = 0, e_ph = 0, t0 = 0;  // t0: tiles of earlier runs
+            // s_ph: phase of S; pv: products with V so far; t0: tiles of earlier runs
+            uint32_t s_ph = 0, o_ph = 0, pv = 0, e_ph = 0, t0 = 0;
             bool dead = false;
             // the queries of this warpgroup pair's rows, where it loads any
             auto queries = [&](const Segment &x) {
@@ -661,41 +657,37 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnAr
                                                                      : INT32_MAX);
                 const int shut = __reduce_max_sync(0xffffffffu, live ? lo + 1 : 0);
                 float top = -INFINITY, sum = 0.0f;
-                int j0 = (sg.tile0 + first) * kTok + 64 * half;
+                int j0 = (sg.tile0 + first) * kTok + 32 * half;
                 uint32_t at = t0 + first;  // the tile among all of the CTA's
                 const int mine = sg.n > first ? (sg.n - first + step - 1) / step : 0;
 #pragma unroll 1
-                for (int left = mine; left > 0; --left, j0 += step * kTok, at += step) {
+                for (int left = 2 * mine; left > 0; --left) {
+                    // half a tile: the first of a tile where left is even
+                    const uint32_t sub = left & 1, s_sub = s_at + 64u * sub, p_sub = p_at + 64u * sub;
                     // a wait that gave up (a kernel bug, reported) leaves the loop's shape
                     // as it is: the tile's other warps count on this one at the barriers
-                    if (!dead) dead = __any_sync(0xffffffffu, !mbar_wait(bar(kSFull + m), s_ph, abort_flag, a.err));
-                    s_ph ^= 1;
+                    if (!dead)
+                        dead = __any_sync(0xffffffffu, !mbar_wait(bar(kSFull + 2 * m + sub), s_ph, abort_flag, a.err));
                     tc_fence_after();
-                    const uint32_t ok = sh.ok[at & 7] >> (4 * half);
-                    float *swap = &sh.top[left & 1][m][0][r];
-                    uint32_t v[64];
-                    tmem_ld32(s_at, v);
-                    tmem_ld32(s_at + 32, v + 32);
+                    const uint32_t ok = sh.ok[at & 7] >> (4 * sub + 2 * half);
+                    float *swap = &sh.top[sub][m][0][r];
+                    uint32_t v[32];
+                    tmem_ld32(s_sub, v);
                     tmem_wait_ld(v);
-                    tmem_pass(v + 32);
-                    if ((ok & 15u) != 15u || j0 + 64 > open || j0 < shut) {
+                    if ((ok & 3u) != 3u || j0 + 32 > open || j0 < shut) {
                         const int4 edge = sh.see[m][half][r];
-                        const uint64_t word = a.tree ? sh.word[m][half][r] : 0;
+                        const uint32_t see = visible32(j0, edge.x, edge.y, ok, a.tree != nullptr,
+                                                       a.tree ? sh.word[m][half][r] : 0, edge.z);
 #pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            const uint32_t see = visible32(j0 + 32 * c, edge.x, edge.y, ok >> (2 * c),
-                                                           a.tree != nullptr, word, edge.z);
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                if (!((see >> e) & 1u)) v[32 * c + e] = 0xff800000u;  // -inf
-                        }
+                        for (int e = 0; e < 32; ++e)
+                            if (!((see >> e) & 1u)) v[e] = 0xff800000u;  // -inf
                     }
                     float mx[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         mx[e] = fmaxf(__uint_as_float(v[e]), __uint_as_float(v[e + 4]));
 #pragma unroll
-                    for (int e = 8; e < 64; e += 8)
+                    for (int e = 8; e < 32; e += 8)
 #pragma unroll
                         for (int f = 0; f < 4; ++f)
                             mx[f] = max3(mx[f], __uint_as_float(v[e + f]), __uint_as_float(v[e + f + 4]));
@@ -714,28 +706,29 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnAr
                         const float f = grow ? kv_ex2((top - now) * sl2) : 1.0f;
                         if (grow) top = now;
                         sum *= f;
-                        if (left != mine) scale_o<D>(o_at, f);
+                        if (left != 2 * mine) {
+                            // O is free once the last product with V is done
+                            if (!dead)
+                                dead = __any_sync(0xffffffffu, !mbar_wait(bar(kPv + m), (pv - 1) & 1u, abort_flag, a.err));
+                            tc_fence_after();
+                            scale_o<D>(o_at, f);
+                        }
                     }
+                    ++pv;
                     const float off = top == -INFINITY ? 0.0f : -top * sl2;
                     const uint64_t sc2 = pack2(sl2, sl2), off2 = pack2(off, off);
                     uint64_t sum2[2] = {pack2(sum, 0.0f), 0};
+                    uint32_t p[16];
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        uint32_t p[16];
-#pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
-                            float x, y;
-                            unpack2(fma2(pack2(__uint_as_float(v[32 * c + e]),
-                                               __uint_as_float(v[32 * c + e + 1])),
-                                         sc2, off2),
-                                    x, y);
-                            x = kv_ex2(x);
-                            y = kv_ex2(y);
-                            sum2[(e >> 1) & 1] = add2(sum2[(e >> 1) & 1], pack2(x, y));
-                            p[e / 2] = as_u32(__floats2half2_rn(x, y));
-                        }
-                        tmem_st16(p_at + 16 * c, p);
+                    for (int e = 0; e < 32; e += 2) {
+                        float x, y;
+                        unpack2(fma2(pack2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), sc2, off2), x, y);
+                        x = kv_ex2(x);
+                        y = kv_ex2(y);
+                        sum2[(e >> 1) & 1] = add2(sum2[(e >> 1) & 1], pack2(x, y));
+                        p[e / 2] = as_u32(__floats2half2_rn(x, y));
                     }
+                    tmem_st16(p_sub, p);
                     {
                         float x, y;
                         unpack2(add2(sum2[0], sum2[1]), x, y);
@@ -743,7 +736,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnAr
                     }
                     tmem_wait_st();
                     tc_fence_before();
-                    mbar_arrive(bar(kPFull + m));
+                    mbar_arrive(bar(kPFull + 2 * m + sub));
+                    j0 += 64;
+                    if (sub) {
+                        j0 += (step - 1) * kTok;
+                        at += step;
+                        s_ph ^= 1;
+                    }
                 }
                 // the next run's queries, once the products of this one have read theirs:
                 // its first scores are then on their way while this one's output is written
@@ -885,9 +884,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnAr
             // little more than the instruction it runs, so a warp's waits and commits
             // would leave it idle; two warps fill each other's gaps.
             const int m = w - 24;
-            const uint32_t id_s = idesc_f16_m128(kTok);
+            const uint32_t id_s = idesc_f16_m128(kTok / 2);
             const uint32_t id_o = idesc_f16_m128(D) | (1u << 16);  // B N-major
-            const uint32_t q_at = smem + C::kQ + (uint32_t)m * C::kTileBytes;
             uint32_t p_ph = 0, q_ph[2] = {0, 0}, t0 = 0;  // t0: tiles of earlier runs
             bool ok = true;
             auto wait = [&](int b, uint32_t ph) {
@@ -909,32 +907,39 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnAr
                     if (m == 1 && !wait(kQFull + 1, q_ph[1])) break;
                     q_ph[1] ^= 1;
                 }
-                auto scores = [&](int k) {
-                    const uint32_t done = bar(kKEmpty + slot(k));
-                    mma_qk<D>(s_col(m), q_at, smem + C::kK + slot(k) * C::kTileBytes, id_s);
-                    tc_commit2_elect(bar(kSFull + m), done);
-                    // the last scores of the run have read the queries
-                    tc_commit2_elect(narrow ? done : 0u, k + step >= sg.n ? bar(kQEmpty) : 0u);
+                // the scores of one half of tile k; the tile's second half lets go of it,
+                // the run's last one of the queries
+                auto scores = [&](int k, uint32_t sub) {
+                    mma_qk<D>(s_col(m, sub), q_at, smem + C::kK + slot(k) * C::kTileBytes + sub * (kTok / 2 * 128),
+                              id_s);
+                    const uint32_t done = sub ? bar(kKEmpty + slot(k)) : 0u;
+                    tc_commit2_elect(bar(kSFull + 2 * m + sub), done);
+                    if (sub)
+                        tc_commit2_elect(narrow ? done : 0u, k + step >= sg.n ? bar(kQEmpty) : 0u);
                 };
                 if (first < sg.n) {
                     if (!wait(kKFull + slot(first), phase(first))) break;
                     tc_fence_after();
-                    scores(first);
+                    scores(first, 0);
+                    scores(first, 1);
                 } else if (lane == 0) {
                     mbar_arrive(bar(kQEmpty));
                 }
-                for (int k = first; k < sg.n; k += step) {
+                for (int k = first; ok && k < sg.n; k += step) {
                     const bool again = k + step < sg.n;
                     if (!wait(kVFull + slot(k), phase(k))) break;
                     if (again && !wait(kKFull + slot(k + step), phase(k + step))) break;
-                    if (!wait(kPFull + m, p_ph)) break;
+                    const uint32_t v_at = smem + C::kV + slot(k) * C::kTileBytes, done = bar(kVEmpty + slot(k));
+#pragma unroll
+                    for (uint32_t sub = 0; sub < 2; ++sub) {
+                        if (!wait(kPFull + 2 * m + sub, p_ph)) break;
+                        tc_fence_after();
+                        mma_pv(o_col(m), p_col(m, sub), v_at + sub * (kTok / 2 * 128), id_o, k > first || sub);
+                        tc_commit2_elect(bar(kPv + m), sub ? done : 0u);
+                        if (again) scores(k + step, sub);
+                    }
+                    tc_commit2_elect(narrow ? done : 0u, again ? 0u : bar(kOFull + m));
                     p_ph ^= 1;
-                    tc_fence_after();
-                    mma_pv(o_col(m), p_col(m), smem + C::kV + slot(k) * C::kTileBytes, id_o, k > first);
-                    if (again) scores(k + step);
-                    const uint32_t done = bar(kVEmpty + slot(k));
-                    tc_commit2_elect(done, again ? 0u : bar(kOFull + m));
-                    if (narrow) tc_commit_elect(done);
                 }
                 t0 += sg.n;
             }
