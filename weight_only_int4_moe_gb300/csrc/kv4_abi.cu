@@ -232,16 +232,23 @@ int moe_kv4_attention(const uint16_t *q, int64_t q_stride, int q_heads, const vo
     uint8_t *slots = ws + MOE_KV4_WS_HEADER;
     const long long most = (long long)batch->max_q * a.group;
     const bool even = (long long)batch->requests * batch->max_q == batch->tokens;
+    const bool few = most <= kKvFewRows || !even, many = most > kKvFewRows;
+    // the kernels count their units of work in 32 bits
+    const double few_rows = most < kKvFewRows ? (double)most : (double)kKvFewRows;
+    const double tiles = batch->max_kv / 64.0 + 8.0;
+    if ((few && batch->requests * (few_rows / 8 + 1) * shape->kv_heads * tiles > 4e9) ||
+        (many && ((double)batch->tokens * a.group / 256 + batch->requests) * shape->kv_heads * tiles > 4e9))
+        return MOE_ERR_SHAPE;
     cudaStream_t s = str(stream);
-    if (most <= kKvFewRows || !even) {
+    if (few) {
         a.rows_lo = 1;
-        a.rows_hi = kKvFewRows;
+        a.rows_hi = many ? kKvFewRows : INT32_MAX;
         const cudaError_t e = launch_kv4_decode(
             a, shape->head_dim, most < kKvFewRows ? (int)most : kKvFewRows, slots, ctas, s);
         if (e != cudaSuccess) return MOE_ERR_CUDA;
     }
-    if (most > kKvFewRows) {
-        a.rows_lo = kKvFewRows + 1;
+    if (many) {
+        a.rows_lo = few ? kKvFewRows + 1 : 1;
         a.rows_hi = INT32_MAX;
         return done(launch_kv4_prefill(a, shape->head_dim, slots, ctas, s));
     }

@@ -24,8 +24,10 @@
 // size of 64 is one contiguous block).  Warps of a CTA join their parts of an item
 // through shared memory, CTAs through the workspace, the last one to arrive adding
 // them up in list order.
-#include "kv4_launch.cuh"
+#include <atomic>
+
 #include "dequant.cuh"
+#include "kv4_launch.cuh"
 
 namespace moe {
 
@@ -143,7 +145,9 @@ MOE_DEV Request request_of(const KvAttnArgs &a, int q0, int q1, int len, int row
     const int start = a.window > 0 ? max(0, r.first - a.window + 1) : 0;
     r.tile0 = start / kTile;
     r.tiles = max(1, (r.end + kTile - 1) / kTile - r.tile0);
-    const bool mine = r.m > 0 && r.m * a.group >= a.rows_lo && r.m * a.group <= a.rows_hi;
+    // (a row range outside the batch's tokens is no request)
+    const bool mine = r.m > 0 && q0 >= 0 && q1 <= a.batch.tokens && r.m * a.group >= a.rows_lo &&
+                      r.m * a.group <= a.rows_hi;
     r.row_tiles = mine ? (r.m * a.group + rows - 1) / rows : 0;
     return r;
 }
@@ -287,11 +291,12 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
     while (u < u_end && !aborted) {
         Request rq = get_request(b);
         uint32_t n_b = units_of(rq, hkv);
-        while (u >= b_u0 + n_b) {
+        while (u >= b_u0 + n_b && b + 1 < a.batch.requests) {
             b_u0 += n_b;
             rq = get_request(++b);
             n_b = units_of(rq, hkv);
         }
+        if (u >= b_u0 + n_b) break;  // the lengths changed under the call
         const uint32_t span = rq.tiles + kPad, item = (u - b_u0) / span;
         const uint32_t i_u0 = b_u0 + item * span + kPad, i_u1 = i_u0 + rq.tiles;  // its tiles
         u = max(u, i_u0);
@@ -749,7 +754,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
 template <int D, int NT, int PS>
 cudaError_t launch(const KvAttnArgs &a, int grid, cudaStream_t s) {
     using C = Cfg<D, NT>;
-    static bool set[64];
+    static std::atomic<bool> set[64];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;

@@ -5,7 +5,7 @@
 // consecutive tokens), two tiles of 128 for tcgen05.mma, against tiles of 128
 // tokens.  Per tile of tokens and rows,
 //   S = Q K^T   (128 x 128 x D, both operands fp16 in shared memory)
-//   P = 2^(S - m) in fp16, written over the second half of S in tensor memory
+//   P = 2^(S - m) in fp16, written over S in tensor memory
 //   O += P V    (128 x D x 128, P from tensor memory, V from shared memory)
 // with the running maximum m and the sum of a row in the one thread that owns the
 // row.  O is rescaled only when a row's maximum has grown by more than 2^8 since
@@ -30,6 +30,8 @@
 // The list of (request, row tile, kv head) items' token tiles is cut into equal
 // runs, one a CTA; parts of an item are joined through the workspace by the last
 // CTA to arrive, in list order.
+#include <atomic>
+
 #include "dequant.cuh"
 #include "kv4_launch.cuh"
 
@@ -56,8 +58,8 @@ static_assert(kThreads * kRegsLaunch <= 65536, "the register file");
 // registers back wait at this barrier until those that give them up have done so,
 // and until the softmax warps have had theirs: a warp with no work that took its
 // share back early would keep it from a softmax warp that still waits for it.
-constexpr uint32_t kBarRegs = 1, kBarTile = 2;  // kBarTile + m: the 256 threads of row tile m
-constexpr uint32_t kBarBoth = 4;                // both row tiles' threads
+constexpr uint32_t kBarRegs = 1, kBarBoth = 2;  // kBarBoth: both row tiles' threads
+constexpr uint32_t kBarPair = 3;                // + 0..7: the two warps that share 32 rows
 
 template <int D>
 struct Cfg {
@@ -99,7 +101,9 @@ MOE_DEV Request request_of(const KvAttnArgs &a, int b) {
     r.first = len - r.m;
     r.end = (int)min((long long)len, (long long)a.batch.stride * a.pool.ps);
     r.rows = r.m * a.group;
-    const bool mine = r.m > 0 && r.rows >= a.rows_lo && r.rows <= a.rows_hi;
+    // (a row range outside the batch's tokens is no request)
+    const bool mine = r.m > 0 && r.q0 >= 0 && r.q0 + r.m <= a.batch.tokens && r.rows >= a.rows_lo &&
+                      r.rows <= a.rows_hi;
     r.row_tiles = mine ? (r.rows + kRowsItem - 1) / kRowsItem : 0;
     return r;
 }
@@ -160,6 +164,7 @@ struct Walk {
             while (true) {
                 const uint32_t n = per_chunk == 1 ? prefix[b + 1] - prefix[b] : request_units(a, s.r);
                 if (u < b_u0 + n) break;
+                if (b + 1 >= a.batch.requests) return false;  // the lengths changed under the call
                 b_u0 += n;
                 s.r = request_of(a, ++b);
             }
@@ -178,6 +183,7 @@ struct Walk {
                 }
                 const unsigned who = __ballot_sync(0xffffffffu, at < base + x);
                 if (!who) {
+                    if (rt0 >= s.r.row_tiles) return false;
                     base += __shfl_sync(0xffffffffu, x, 31);
                     continue;
                 }
@@ -249,12 +255,13 @@ MOE_DEV void mma_qk(uint32_t d_tmem, uint32_t q, uint32_t k, uint32_t idesc) {
     }
 }
 
-// O (+)= P V for half a tile: four MMAs; P's columns advance by 8, V's tokens by 16 rows.
+// O (+)= P V for half a tile: four MMAs of 16 tokens each; P's columns are 0..15 for
+// the first 32 tokens and 32..47 for the others.
 MOE_DEV void mma_pv(uint32_t d_tmem, uint32_t p_tmem, uint32_t v, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
         "{\n\t.reg .pred p, t, e;\n\t.reg .b32 a1, a2, a3;\n\t.reg .b64 b1, b2, b3;\n\t"
         "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, %4, %4;\n\t"
-        "add.u32 a1, %1, 8;\n\tadd.u32 a2, %1, 16;\n\tadd.u32 a3, %1, 24;\n\t"
+        "add.u32 a1, %1, 8;\n\tadd.u32 a2, %1, 32;\n\tadd.u32 a3, %1, 40;\n\t"
         "add.u64 b1, %2, 128;\n\tadd.u64 b2, %2, 256;\n\tadd.u64 b3, %2, 384;\n\t"
         "elect.sync _|e, 0xffffffff;\n\t"
         "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
@@ -608,9 +615,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnAr
     const uint32_t tmem = sh.tmem;
     const float sl2 = fmaxf(fabsf(a.scale_log2), 1e-30f);
     auto bar = [&](int i) { return smem_u32(&sh.bar[i]); };
-    // S (and P over its second half) of the row tiles' half tiles, then their O
+    // S of the row tiles' half tiles, then their O; P lies over the first half of either
+    // 32 columns of S
     auto s_col = [&](int m, int sub) { return tmem + 128u * m + 64u * sub; };
-    auto p_col = [&](int m, int sub) { return s_col(m, sub) + 32u; };
     auto o_col = [&](int m) { return tmem + 256u + 128u * m; };
     int *abort_flag = &sh.abort_flag;
 
@@ -624,8 +631,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnAr
             // the thread's row tile, half of the columns and row
             const int m = w >> 3, half = (w >> 2) & 1, r = tid & 127;
             const uint32_t lane_off = (uint32_t)(32 * (w & 3)) << 16;
-            const uint32_t s_at = s_col(m, 0) + lane_off + 32u * half;
-            const uint32_t p_at = p_col(m, 0) + lane_off + 16u * half;
+            const uint32_t s_at = s_col(m, 0) + lane_off + 32u * half;  // P over its first half
+            const uint32_t pair_bar = kBarPair + 4 * m + (w & 3);
             const uint32_t o_at = o_col(m) + lane_off + (D / 2) * half;
             // s_ph: phase of S; pv: products with V so far; t0: tiles of earlier runs
             uint32_t s_ph = 0, o_ph = 0, pv = 0, e_ph = 0, t0 = 0;
@@ -663,7 +670,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnAr
 #pragma unroll 1
                 for (int left = 2 * mine; left > 0; --left) {
                     // half a tile: the first of a tile where left is even
-                    const uint32_t sub = left & 1, s_sub = s_at + 64u * sub, p_sub = p_at + 64u * sub;
+                    const uint32_t sub = left & 1, s_sub = s_at + 64u * sub;
                     // a wait that gave up (a kernel bug, reported) leaves the loop's shape
                     // as it is: the tile's other warps count on this one at the barriers
                     if (!dead)
@@ -692,12 +699,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnAr
                         for (int f = 0; f < 4; ++f)
                             mx[f] = max3(mx[f], __uint_as_float(v[e + f]), __uint_as_float(v[e + f + 4]));
                     float now = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
-                    // the other half's maximum; after the barrier S has been read, too,
-                    // and P may be written over it
+                    // the other half's maximum
                     swap[128 * half] = now;
-                    tc_fence_before();
-                    named_bar_sync(kBarTile + m, 256);
-                    tc_fence_after();
+                    named_bar_sync(pair_bar, 64);
                     now = fmaxf(now, swap[128 * (half ^ 1)]);
                     // the first maximum of a run is taken as it is; later ones only when
                     // they have grown by more than 2^8
@@ -728,7 +732,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnAr
                         sum2[(e >> 1) & 1] = add2(sum2[(e >> 1) & 1], pack2(x, y));
                         p[e / 2] = as_u32(__floats2half2_rn(x, y));
                     }
-                    tmem_st16(p_sub, p);
+                    tmem_st16(s_sub, p);
                     {
                         float x, y;
                         unpack2(add2(sum2[0], sum2[1]), x, y);
@@ -765,9 +769,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnAr
                     // the row's sum passes between its two threads
                     float *swap = &sh.top[0][m][0][r];
                     swap[128 * half] = sum;
-                    named_bar_sync(kBarTile + m, 256);
+                    named_bar_sync(pair_bar, 64);
                     sum += swap[128 * (half ^ 1)];
-                    named_bar_sync(kBarTile + m, 256);  // read before the next run writes there
+                    named_bar_sync(pair_bar, 64);  // read before the next run writes there
                     // narrow: the second pair hands its maximum, sum and O to the first
                     float mix = 1.0f, mix1 = 0.0f;
                     if (narrow) {
@@ -934,7 +938,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnAr
                     for (uint32_t sub = 0; sub < 2; ++sub) {
                         if (!wait(kPFull + 2 * m + sub, p_ph)) break;
                         tc_fence_after();
-                        mma_pv(o_col(m), p_col(m, sub), v_at + sub * (kTok / 2 * 128), id_o, k > first || sub);
+                        mma_pv(o_col(m), s_col(m, sub), v_at + sub * (kTok / 2 * 128), id_o, k > first || sub);
                         tc_commit2_elect(bar(kPv + m), sub ? done : 0u);
                         if (again) scores(k + step, sub);
                     }
@@ -995,7 +999,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnAr
 
 template <int D>
 cudaError_t launch(const KvAttnArgs &a, int grid, cudaStream_t s) {
-    static bool set[64];
+    static std::atomic<bool> set[64];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
