@@ -379,34 +379,6 @@ struct Packed {
     uint32_t live;
 };
 
-// Requests the part (nothing waits for it here: rows without a token load page 0
-// and are zeroed when they are unpacked).  part: 0 K, 1 V.  id_at: the lane that
-// holds the tile's first page id; left: tokens of the sequence from the tile on.
-template <int D, int part>
-MOE_DEV void load_part(Packed<D> &p, const KvPool &pool, int head, int ids, int id_at, int row_l, int ch,
-                       int left) {
-    constexpr int kStep = 128 / (D == 128 ? 4 : 2), NG = D / 32;
-    const int ps = pool.ps;
-    p.live = 0;
-#pragma unroll
-    for (int i = 0; i < Cfg<D>::kLoads; ++i) {
-        const int row = i * kStep + row_l;
-        const int id = __shfl_sync(0xffffffffu, ids, id_at + row / ps);
-        const int slot = row & (ps - 1);
-        p.live |= (id >= 0 && row < left ? 1u : 0u) << i;
-        const uint8_t *blk = kv_block(pool, max(id, 0), head);
-        p.c[i] = *reinterpret_cast<const uint4 *>(blk + part * ps * (D / 2) + slot * (D / 2) + 16 * ch);
-        const uint8_t *sc = blk + ps * D + part * ps * (NG * 2) + slot * (NG * 2);
-        if constexpr (D == 128) {
-            const uint2 v = *reinterpret_cast<const uint2 *>(sc);
-            p.z[i][0] = v.x;
-            p.z[i][1] = v.y;
-        } else {
-            p.z[i][0] = *reinterpret_cast<const uint32_t *>(sc);
-        }
-    }
-}
-
 // The row that a thread unpacks first.  The eight lanes of a store phase hold two
 // rows (D = 64: four); their order puts the swizzled 16-byte chunks that the lanes
 // store at once into different banks: K stores chunks 4G + t of all t together, so
@@ -428,80 +400,123 @@ MOE_DEV void unpack_role(const KvAttnArgs &a, Shared &sh, uint32_t smem, Walk wa
     constexpr int kStep = 128 / kLanesRow;       // rows of one load of the group
     const int lane = threadIdx.x & 31, dt = threadIdx.x & 127, ch = dt % kLanesRow;
     const int row_l = row_of_lane<D, part>(dt);
-    const int ps = a.pool.ps, ppt = kTok / ps;
+    constexpr int NG = D / 32;
+    const int ps = a.pool.ps, ppt = kTok >> (31 - __clz(ps)), hkv = a.pool.hkv;
     const uint32_t full = smem_u32(&sh.bar[part ? kVFull : kKFull]);
     const uint32_t empty = smem_u32(&sh.bar[part ? kVEmpty : kKEmpty]);
     const uint32_t buf = smem + (part ? C::kV : C::kK);
+    // The tile whose loads are requested.  Each of them goes out as soon as the tile
+    // before has left its registers.  Kept from the run: the head's blocks (from the
+    // thread's chunk on), the tiles left, the tokens left, the table's next entry and end.
+    const int ps_log = 31 - __clz(ps);
+    const uint32_t page_bytes = a.pool.block * hkv;
+    const uint8_t *head = nullptr;
+    const int32_t *table = nullptr;
+    int tiles_left = 0, left = 0, id_at = 0, entry = 0, entries = 0, ids = -1, ids_next = -1;
+    bool reports = false;
+    // page ids: lane l holds the tile's and the following ones, 32 in all, then 32 more
+    auto next_ids = [&] {
+        ids = ids_next;
+        if ((unsigned)ids >= (unsigned)a.pool.n_pages) {
+            if (reports && entry + lane < entries) kv_report(a.err, MOE_KV4_DEVERR_PAGE);
+            ids = -1;
+        }
+        entry += 32;
+        ids_next = entry + lane < entries ? table[entry + lane] : -1;
+        id_at = 0;
+    };
+    uint32_t ok_next = 0;
+    auto advance = [&]() -> bool {
+        if (tiles_left == 0) {
+            Segment sg;
+            if (!walk.next(a, sg)) return false;
+            table = a.batch.tables + (size_t)sg.b * a.batch.stride;
+            head = a.pool.base + (size_t)sg.h * a.pool.block;
+            reports = part == 0 && sg.h == 0 && dt < 32;
+            tiles_left = sg.n;
+            left = sg.r.end - sg.tile0 * kTok;
+            entry = sg.tile0 * ppt;
+            entries = min((sg.tile0 + sg.n) * ppt, (sg.r.end + ps - 1) >> ps_log);
+            ids_next = entry + lane < entries ? table[entry + lane] : -1;
+            next_ids();
+        } else {
+            left -= kTok;
+            id_at += ppt;
+            if (id_at == 32) next_ids();
+        }
+        --tiles_left;
+        if (part == 0) {
+            const unsigned have = __ballot_sync(0xffffffffu, ids >= 0) >> id_at;
+            ok_next = 0;
+            for (int i = 0; i < ppt; ++i)
+                if ((have >> i) & 1u) ok_next |= ((1u << (ps / 16)) - 1u) << (i * (ps / 16));
+        }
+        return true;
+    };
+    Packed<D> pk;
+    pk.live = 0;
+    // (nothing waits for a load here: rows without a token load page 0 and are zeroed when
+    // they are unpacked)
+    auto request = [&](int i) {
+        const int row = i * kStep + row_l, slot = row & (ps - 1);
+        const int id = __shfl_sync(0xffffffffu, ids, id_at + (row >> ps_log));
+        pk.live = (pk.live & ~(1u << i)) | (id >= 0 && row < left ? 1u : 0u) << i;
+        const uint8_t *blk = head + (size_t)(uint32_t)max(id, 0) * page_bytes;
+        pk.c[i] = *reinterpret_cast<const uint4 *>(blk + (part * ps + slot) * (D / 2) + 16 * ch);
+        const uint8_t *sc = blk + ps * D + (part * ps + slot) * (NG * 2);
+        if constexpr (D == 128) {
+            const uint2 v = *reinterpret_cast<const uint2 *>(sc);
+            pk.z[i][0] = v.x;
+            pk.z[i][1] = v.y;
+        } else {
+            pk.z[i][0] = *reinterpret_cast<const uint32_t *>(sc);
+        }
+    };
     Ring ring(2);
     uint32_t tiles = 0;
-    Segment sg;
-    while (walk.next(a, sg)) {
-        const int32_t *table = a.batch.tables + (size_t)sg.b * a.batch.stride;
-        int e_base = 0, ids = -1;
-        // page ids of the next tiles: lane l holds table entry e_base + l
-        auto load_ids = [&](int from) {
-            e_base = from;
-            const int e = from + lane;
-            ids = -1;
-            if (e < (sg.tile0 + sg.n) * ppt && (long long)e * ps < sg.r.end) {
-                ids = table[e];
-                if ((unsigned)ids >= (unsigned)a.pool.n_pages) {
-                    ids = -1;
-                    if (part == 0 && sg.h == 0 && dt < 32) kv_report(a.err, MOE_KV4_DEVERR_PAGE);
-                }
-            }
-        };
-        Packed<D> pk;
-        uint32_t ok_next = 0;
-        auto request = [&](int k) {
-            const int e0 = (sg.tile0 + k) * ppt;
-            if (k == 0 || e0 + ppt > e_base + 32) load_ids(e0);
-            if (part == 0) {
-                const unsigned have = __ballot_sync(0xffffffffu, ids >= 0) >> (e0 - e_base);
-                ok_next = 0;
-                for (int i = 0; i < ppt; ++i)
-                    if ((have >> i) & 1u) ok_next |= ((1u << (ps / 16)) - 1u) << (i * (ps / 16));
-            }
-            load_part<D, part>(pk, a.pool, sg.h, ids, e0 - e_base, row_l, ch,
-                               sg.r.end - (sg.tile0 + k) * kTok);
-        };
-        request(0);
-        for (int k = 0; k < sg.n; ++k) {
-            if (__any_sync(0xffffffffu, !mbar_wait(empty + 8 * ring.idx, ring.ph ^ 1, &sh.abort_flag, a.err)))
-                return;
-            if (part == 0 && dt == 0) sh.ok[tiles & 7] = ok_next;
-            ++tiles;
-            const uint32_t dst = buf + ring.idx * C::kTileBytes;
+    bool more = advance();
+    if (more) {
 #pragma unroll
-            for (int i = 0; i < C::kLoads; ++i) {
-                const int row = i * kStep + row_l;
-                const uint32_t words[4] = {pk.c[i].x, pk.c[i].y, pk.c[i].z, pk.c[i].w};
-                const bool live = (pk.live >> i) & 1u;
+        for (int i = 0; i < C::kLoads; ++i) request(i);
+    }
+    while (more) {
+        const uint32_t ok = ok_next;
+        more = advance();
+        if (__any_sync(0xffffffffu, !mbar_wait(empty + 8 * ring.idx, ring.ph ^ 1, &sh.abort_flag, a.err)))
+            return;
+        if (part == 0 && dt == 0) sh.ok[tiles & 7] = ok;
+        ++tiles;
+        const uint32_t dst = buf + ring.idx * C::kTileBytes;
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    uint32_t s;
-                    int chunk;
-                    if (part == 0) {
-                        // word (t, G): dimensions 32G + 8t.., the row's chunk 4G + t
-                        const int G = D == 128 ? u : u & 1, t = D == 128 ? ch : 2 * ch + (u >> 1);
-                        s = __byte_perm(pk.z[i][G / 2], 0, G & 1 ? 0x3232 : 0x1010);
-                        chunk = 4 * G + t;
-                    } else {
-                        // piece g of groups 2p and 2p + 1: column chunk 8p + g
-                        const int pp = D == 128 ? u & 1 : 0, g = D == 128 ? 2 * ch + (u >> 1) : 4 * ch + u;
-                        s = pk.z[i][pp];
-                        chunk = 8 * pp + g;
-                    }
-                    uint32_t x[4];
-                    scaled_codes(words[u], a.k, live ? s : 0u, x);
-                    sts128(dst + tile_at(row, chunk), x[0], x[1], x[2], x[3]);
+        for (int i = 0; i < C::kLoads; ++i) {
+            const int row = i * kStep + row_l;
+            const uint32_t words[4] = {pk.c[i].x, pk.c[i].y, pk.c[i].z, pk.c[i].w};
+            const bool live = (pk.live >> i) & 1u;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                uint32_t s;
+                int chunk;
+                if (part == 0) {
+                    // word (t, G): dimensions 32G + 8t.., the row's chunk 4G + t
+                    const int G = D == 128 ? u : u & 1, t = D == 128 ? ch : 2 * ch + (u >> 1);
+                    s = __byte_perm(pk.z[i][G / 2], 0, G & 1 ? 0x3232 : 0x1010);
+                    chunk = 4 * G + t;
+                } else {
+                    // piece g of groups 2p and 2p + 1: column chunk 8p + g
+                    const int pp = D == 128 ? u & 1 : 0, g = D == 128 ? 2 * ch + (u >> 1) : 4 * ch + u;
+                    s = pk.z[i][pp];
+                    chunk = 8 * pp + g;
                 }
+                uint32_t x[4];
+                scaled_codes(words[u], a.k, live ? s : 0u, x);
+                sts128(dst + tile_at(row, chunk), x[0], x[1], x[2], x[3]);
             }
-            fence_proxy_async_shared();
-            mbar_arrive(full + 8 * ring.idx);
-            ring.next();
-            if (k + 1 < sg.n) request(k + 1);
         }
+        fence_proxy_async_shared();
+        mbar_arrive(full + 8 * ring.idx);
+#pragma unroll
+        for (int i = 0; i < C::kLoads; ++i) request(i);
+        ring.next();
     }
 }
 
