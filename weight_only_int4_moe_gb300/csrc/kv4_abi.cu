@@ -185,7 +185,7 @@ size_t moe_kv4_workspace_bytes(const moe_kv4_shape *shape, int q_heads) {
         return 0;
     const size_t few = kv4_decode_slot_bytes(shape->head_dim, kKvMaxCtas);
     const size_t many = kv4_prefill_slot_bytes(shape->head_dim, kKvMaxCtas);
-    return MOE_KV4_WS_HEADER + (few > many ? few : many);
+    return MOE_KV4_WS_HEADER + few + many;
 }
 
 int moe_kv4_attention(const uint16_t *q, int64_t q_stride, int q_heads, const void *pages,
@@ -224,7 +224,6 @@ int moe_kv4_attention(const uint16_t *q, int64_t q_stride, int q_heads, const vo
     a.window = window;
     uint8_t *ws = reinterpret_cast<uint8_t *>(workspace);
     a.err = reinterpret_cast<uint32_t *>(ws);
-    a.counters = reinterpret_cast<int32_t *>(ws + kKvCounterByte);
     a.max_kv = batch->max_kv;
     // Requests of up to kKvFewRows rows go to the decode kernel, others to the
     // prefill kernel; where all have the same number of new tokens one is enough.
@@ -240,17 +239,24 @@ int moe_kv4_attention(const uint16_t *q, int64_t q_stride, int q_heads, const vo
         (many && ((double)batch->tokens * a.group / 256 + batch->requests) * shape->kv_heads * tiles > 4e9))
         return MOE_ERR_SHAPE;
     cudaStream_t s = str(stream);
+    // Both: the prefill kernel first; the decode kernel's blocks then start on the SMs
+    // that it leaves, with slots and counters of their own.
+    a.beside = few && many;
+    if (many) {
+        a.counters = reinterpret_cast<int32_t *>(ws + kKvCounterByte) + kKvMaxCtas;
+        a.rows_lo = few ? kKvFewRows + 1 : 1;
+        a.rows_hi = INT32_MAX;
+        const cudaError_t e = launch_kv4_prefill(
+            a, shape->head_dim, slots + kv4_decode_slot_bytes(shape->head_dim, kKvMaxCtas), ctas, s);
+        if (e != cudaSuccess) return MOE_ERR_CUDA;
+    }
     if (few) {
+        a.counters = reinterpret_cast<int32_t *>(ws + kKvCounterByte);
         a.rows_lo = 1;
         a.rows_hi = many ? kKvFewRows : INT32_MAX;
         const cudaError_t e = launch_kv4_decode(
             a, shape->head_dim, most < kKvFewRows ? (int)most : kKvFewRows, slots, ctas, s);
         if (e != cudaSuccess) return MOE_ERR_CUDA;
-    }
-    if (many) {
-        a.rows_lo = few ? kKvFewRows + 1 : 1;
-        a.rows_hi = INT32_MAX;
-        return done(launch_kv4_prefill(a, shape->head_dim, slots, ctas, s));
     }
     return MOE_OK;
 }

@@ -167,7 +167,10 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
     __shared__ Meta meta[2 * W];
     __shared__ int run_of[2 * W + 1], n_runs, abort_flag, last_of[2];
     __shared__ uint32_t warp_tot[W];
-    pdl_wait();
+    // Beside the prefill kernel nothing here depends on it, and what came before it is
+    // complete (its blocks let this kernel start after their own wait): the wait moves to
+    // the end, so that whatever follows finds both complete.
+    if (!a.beside) pdl_wait();
     pdl_launch_dependents();
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, g = lane >> 2, t = lane & 3;
     const int hkv = a.pool.hkv, G = a.group;
@@ -251,7 +254,10 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
     };
     const uint32_t per = max((uint32_t)a.min_units, (total + gridDim.x - 1) / gridDim.x);
     const uint32_t c_lo = min(total, blockIdx.x * per), c_hi = min(total, c_lo + per);
-    if (c_lo >= c_hi) return;
+    if (c_lo >= c_hi) {
+        if (a.beside) pdl_wait();
+        return;
+    }
     // The warps' shares: one unit each to the first ones, or equal parts to all, so that
     // an item's tiles always lie in neighbouring warps.
     const uint32_t n_units = c_hi - c_lo;
@@ -749,6 +755,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
                 [&](int i) { return a.cta_slots + ((size_t)2 * (c0 + i) + (i ? 0 : odd)) * C::kSlot; },
                 [&](int r, int d4, float mm, float ll, float4 s) { finish(me, r, d4, mm, ll, s); });
     }
+    if (a.beside) pdl_wait();
 }
 
 template <int D, int NT, int PS>

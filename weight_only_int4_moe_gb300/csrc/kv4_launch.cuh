@@ -33,7 +33,7 @@ struct KvReadArgs {
 // where the compiler would put immediates into registers again for every use, and
 // shifts to the left become multiplies of the FMA pipe, which has room where the ALU
 // pipe has none.
-struct KvConsts {
+struct alignas(16) KvConsts {
     uint32_t c4 = 4, c16 = 16, c64 = 64;
     uint32_t nib4 = 0x00F000F0u, magic64 = 0x54005400u;   // a nibble at bits 4..7: fp16 64 + q
     uint32_t nib6 = 0x03C003C0u, magic16 = 0x4C004C00u;   // at bits 6..9: 16 + q
@@ -57,6 +57,7 @@ struct KvAttnArgs {
     int32_t *counters;     // [CTAs], zero between calls
     float *warp_slots, *cta_slots;
     uint32_t *err;
+    bool beside;           // both kernels take part: the decode kernel runs beside the other
 };
 
 constexpr int kKvMaxCtas = 160;     // slots of the workspace (a GB300 has 152 SMs)

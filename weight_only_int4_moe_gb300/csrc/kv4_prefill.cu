@@ -79,14 +79,14 @@ enum Bar { kKFull = 0, kKEmpty = 2, kVFull = 4, kVEmpty = 6, kQFull = 8, kPv = 1
 struct Shared {
     uint64_t bar[kBars];
     uint32_t tmem, warp_tot[kThreads / 32];
-    int abort_flag, last_of;
+    int abort_flag, last_of[2];
     uint32_t ok[8];              // runs of 16 tokens that have a page, by tile
     uint32_t prefix[kChunks + 1];
     int4 see[2][2][128];         // by row tile, half and row: lo, hi, first new token
     uint64_t word[2][2][128];    // and the row's word of the tree
     float top[2][2][2][128];     // a tile's row maxima: by parity, row tile, half
     uint32_t part_u0[2], part_u1[2];
-    int part_b[2], part_h[2], part_rt[2];
+    int part_q0[2], part_h[2], part_row0[2], part_rows[2];
 };
 
 struct Request {
@@ -566,6 +566,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnAr
     const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, hkv = a.pool.hkv;
     pdl_wait();
+    if (a.beside) pdl_launch_dependents();
     if (tid == 0) {
         sh.abort_flag = 0;
         const int counts[12] = {128, 2, 128, 2, 256, 1, 1, 1, 256, 256, 2, 1};
@@ -876,9 +877,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnAr
                     const int part = sg.i_u0 > c_lo ? 1 : 0;
                     sh.part_u0[part] = sg.i_u0;
                     sh.part_u1[part] = sg.i_u1;
-                    sh.part_b[part] = sg.b;
+                    sh.part_q0[part] = sg.r.q0;
                     sh.part_h[part] = sg.h;
-                    sh.part_rt[part] = sg.rt;
+                    sh.part_row0[part] = sg.rt * kRowsItem;
+                    sh.part_rows[part] = sg.rows;
                 }
                 tc_fence_before();  // the reads of O before the next run's first product
                 if (narrow) named_bar_sync(kBarBoth, 512);
@@ -973,23 +975,23 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnAr
     if (w == 27) tmem_dealloc(tmem, kTmemCols);
 
     // items shared with other CTAs: the last of them adds the parts up
-    for (int part = 0; part < 2; ++part) {
-        const uint32_t u0 = sh.part_u0[part], u1 = sh.part_u1[part];
-        if (u0 == u1) continue;
-        const uint32_t c0 = u0 / per, c1 = (u1 - 1) / per;
-        if (tid == 0) {
-            const int old = atomicAdd(a.counters + c0, 1);
-            sh.last_of = old == (int)(c1 - c0);
-            if (sh.last_of) a.counters[c0] = 0;
+    if (tid < 2) {
+        const uint32_t u0 = sh.part_u0[tid], u1 = sh.part_u1[tid];
+        bool last = false;
+        if (u0 != u1) {
+            const uint32_t c0 = u0 / per, c1 = (u1 - 1) / per;
+            last = atomicAdd(a.counters + c0, 1) == (int)(c1 - c0);
+            if (last) a.counters[c0] = 0;
         }
-        __syncthreads();
-        const bool mine = sh.last_of;
-        __syncthreads();
-        if (!mine) continue;
+        sh.last_of[tid] = last;
+    }
+    __syncthreads();
+    for (int part = 0; part < 2; ++part) {
+        if (!sh.last_of[part]) continue;
         __threadfence();
-        const Request rq = request_of(a, sh.part_b[part]);
-        const int rt = sh.part_rt[part], h = sh.part_h[part];
-        const int rows = min(kRowsItem, rq.rows - rt * kRowsItem);
+        const uint32_t u0 = sh.part_u0[part], c0 = u0 / per, c1 = (sh.part_u1[part] - 1) / per;
+        const int q0 = sh.part_q0[part], h = sh.part_h[part], row0 = sh.part_row0[part];
+        const int rows = sh.part_rows[part];
         const int odd = u0 > c0 * per ? 1 : 0;  // in its first CTA the item is the last one
         constexpr int kGroup = 2 * (32 / (D / 4));
         for (int row = w * kGroup; row < rows; row += kThreads / 32 * kGroup)
@@ -998,8 +1000,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnAr
                 [&](int i) { return a.cta_slots + ((size_t)2 * (c0 + i) + (i ? 0 : odd)) * C::kSlot; },
                 [&](int r, int d4, float mm, float ll, float4 s) {
                     if (r >= rows) return;
-                    const int rr = rt * kRowsItem + r, i = div_group(rr, a.gdiv), hh = rr - i * a.group;
-                    const size_t o = (size_t)(rq.q0 + i) * a.q_heads + h * a.group + hh;
+                    const int rr = row0 + r, i = div_group(rr, a.gdiv), hh = rr - i * a.group;
+                    const size_t o = (size_t)(q0 + i) * a.q_heads + h * a.group + hh;
                     const float inv = ll > 0.0f ? 1.0f / ll : 0.0f;
                     const __nv_bfloat162 x = __floats2bfloat162_rn(s.x * inv, s.y * inv);
                     const __nv_bfloat162 y = __floats2bfloat162_rn(s.z * inv, s.w * inv);
