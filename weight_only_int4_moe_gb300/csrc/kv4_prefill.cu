@@ -47,6 +47,7 @@ constexpr int kTok = 128;        // tokens of a unit
 constexpr int kPad = 4;
 constexpr int kRowsItem = 256;
 constexpr int kChunks = 1024;
+constexpr uint32_t kRuns = 8;    // of the CTA's list, in shared memory at a time
 constexpr int kThreads = 896;
 constexpr uint32_t kTmemCols = 512;
 // Registers a thread of each role (multiples of 8).  The seven warpgroups' shares add
@@ -74,20 +75,7 @@ struct Cfg {
 };
 
 // S and P: by row tile and half tile (2 m + sub); kPv: by row tile, after every P V.
-enum Bar { kKFull = 0, kKEmpty = 2, kVFull = 4, kVEmpty = 6, kQFull = 8, kPv = 10, kSFull = 12, kPFull = 16, kQEmpty = 20, kOFull = 22, kBars = 24 };
-
-struct Shared {
-    uint64_t bar[kBars];
-    uint32_t tmem, warp_tot[kThreads / 32];
-    int abort_flag, last_of[2];
-    uint32_t ok[8];              // runs of 16 tokens that have a page, by tile
-    uint32_t prefix[kChunks + 1];
-    int4 see[2][2][128];         // by row tile, half and row: lo, hi, first new token
-    uint64_t word[2][2][128];    // and the row's word of the tree
-    float top[2][2][2][128];     // a tile's row maxima: by parity, row tile, half
-    uint32_t part_u0[2], part_u1[2];
-    int part_q0[2], part_h[2], part_row0[2], part_rows[2];
-};
+enum Bar { kKFull = 0, kKEmpty = 2, kVFull = 4, kVEmpty = 6, kQFull = 8, kPv = 10, kSFull = 12, kPFull = 16, kQEmpty = 20, kOFull = 22, kRunFull = 24, kRunEmpty = 32, kBars = 40 };
 
 struct Request {
     int q0, m, first, end, rows, row_tiles;
@@ -125,14 +113,30 @@ MOE_DEV uint32_t request_units(const KvAttnArgs &a, const Request &r) {
     return __reduce_add_sync(0xffffffffu, n) * a.pool.hkv;
 }
 
-// A run of one item's tiles that a CTA works on.  Every warp of every role walks
-// the same list (whole-warp calls).
+// A run of one item's tiles that a CTA works on.
 struct Segment {
     Request r;
     int b, rt, h, tile0, n;       // tile0: the first token tile of the run
     uint32_t i_u0, i_u1;          // the item's tiles as units
     int rows;                     // of the item
     bool whole;
+};
+
+struct Shared {
+    uint64_t bar[kBars];
+    uint32_t tmem, warp_tot[kThreads / 32];
+    int abort_flag, last_of[2];
+    // The CTA's runs, a few ahead: one warp finds them, the others read them here.  stop:
+    // the number of the run at which the list breaks off (a wait gave up).
+    Segment run[kRuns];
+    volatile uint32_t stop;
+    uint32_t ok[8];              // runs of 16 tokens that have a page, by tile
+    uint32_t prefix[kChunks + 1];
+    int4 see[2][2][128];         // by row tile, half and row: lo, hi, first new token
+    uint64_t word[2][2][128];    // and the row's word of the tree
+    float top[2][2][2][128];     // a tile's row maxima: by parity, row tile, half
+    uint32_t part_u0[2], part_u1[2];
+    int part_q0[2], part_h[2], part_row0[2], part_rows[2];
 };
 
 struct Walk {
@@ -211,6 +215,45 @@ struct Walk {
         return false;
     }
 };
+
+// Run number idx of the CTA's list, or null at its end.  The warp that writes the list
+// either publishes a run or stops at it, so that all warps see the same list.
+MOE_DEV const Segment *run_at(Shared &sh, uint32_t idx) {
+    const uint32_t bar = smem_u32(&sh.bar[kRunFull + idx % kRuns]), ph = (idx / kRuns) & 1u;
+    for (uint32_t it = 0; it < (1u << 30); ++it) {
+        if (__any_sync(0xffffffffu, mbar_try_wait(bar, ph))) {
+            const Segment *r = &sh.run[idx % kRuns];
+            return r->n ? r : nullptr;
+        }
+        if (__any_sync(0xffffffffu, sh.stop == idx)) return nullptr;
+    }
+    return nullptr;
+}
+// A warp needs run idx no more.
+MOE_DEV void run_done(Shared &sh, uint32_t idx) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&sh.bar[kRunEmpty + idx % kRuns]));
+}
+// The warp that finds the runs.
+MOE_DEV void write_runs(const KvAttnArgs &a, Shared &sh, Walk walk) {
+    for (uint32_t idx = 0;; ++idx) {
+        Segment sg;
+        const bool more = walk.next(a, sg);
+        if (!more) sg.n = 0;
+        if (idx >= kRuns &&
+            __any_sync(0xffffffffu, !mbar_wait(smem_u32(&sh.bar[kRunEmpty + idx % kRuns]),
+                                               (idx / kRuns - 1) & 1u, &sh.abort_flag, a.err, 200))) {
+            if ((threadIdx.x & 31) == 0) sh.stop = idx;
+            return;
+        }
+        if ((threadIdx.x & 31) == 0) {
+            sh.run[idx % kRuns] = sg;
+            mbar_arrive(smem_u32(&sh.bar[kRunFull + idx % kRuns]));
+        }
+        __syncwarp();
+        if (!more) return;
+    }
+}
 
 MOE_DEV void fence_proxy_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
@@ -394,7 +437,7 @@ MOE_DEV int row_of_lane(int dt) {
 
 // The warpgroup that turns one side's codes (part 0: K, 1: V) into operand tiles.
 template <int D, int part>
-MOE_DEV void unpack_role(const KvAttnArgs &a, Shared &sh, uint32_t smem, Walk walk) {
+MOE_DEV void unpack_role(const KvAttnArgs &a, Shared &sh, uint32_t smem) {
     using C = Cfg<D>;
     constexpr int kLanesRow = D == 128 ? 4 : 2;  // 16-byte chunks of a row
     constexpr int kStep = 128 / kLanesRow;       // rows of one load of the group
@@ -414,6 +457,7 @@ MOE_DEV void unpack_role(const KvAttnArgs &a, Shared &sh, uint32_t smem, Walk wa
     const int32_t *table = nullptr;
     int tiles_left = 0, left = 0, id_at = 0, entry = 0, entries = 0, ids = -1, ids_next = -1;
     bool reports = false;
+    uint32_t run_idx = 0;
     // page ids: lane l holds the tile's and the following ones, 32 in all, then 32 more
     auto next_ids = [&] {
         ids = ids_next;
@@ -428,8 +472,9 @@ MOE_DEV void unpack_role(const KvAttnArgs &a, Shared &sh, uint32_t smem, Walk wa
     uint32_t ok_next = 0;
     auto advance = [&]() -> bool {
         if (tiles_left == 0) {
-            Segment sg;
-            if (!walk.next(a, sg)) return false;
+            const Segment *run = run_at(sh, run_idx);
+            if (!run) return false;
+            const Segment &sg = *run;
             table = a.batch.tables + (size_t)sg.b * a.batch.stride;
             head = a.pool.base + (size_t)sg.h * a.pool.block;
             reports = part == 0 && sg.h == 0 && dt < 32;
@@ -437,6 +482,7 @@ MOE_DEV void unpack_role(const KvAttnArgs &a, Shared &sh, uint32_t smem, Walk wa
             left = sg.r.end - sg.tile0 * kTok;
             entry = sg.tile0 * ppt;
             entries = min((sg.tile0 + sg.n) * ppt, (sg.r.end + ps - 1) >> ps_log);
+            run_done(sh, run_idx++);
             ids_next = entry + lane < entries ? table[entry + lane] : -1;
             next_ids();
         } else {
@@ -569,7 +615,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnAr
     if (a.beside) pdl_launch_dependents();
     if (tid == 0) {
         sh.abort_flag = 0;
-        const int counts[12] = {128, 2, 128, 2, 256, 1, 1, 1, 256, 256, 2, 1};
+        const int counts[20] = {128, 2, 128, 2, 256, 1, 1, 1, 256, 256, 2, 1, 1, 1, 1, 1, 26, 26, 26, 26};
+        sh.stop = 0xffffffffu;
         for (int i = 0; i < kBars; ++i) mbar_init(smem_u32(&sh.bar[i]), counts[i / 2]);
         mbar_fence_init();
         sh.part_u0[0] = sh.part_u1[0] = sh.part_u0[1] = sh.part_u1[1] = 0;
@@ -638,9 +685,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnAr
     int *abort_flag = &sh.abort_flag;
 
     if (c_lo < c_hi) {
-        Walk walk;
-        walk.start(a, sh.prefix, chunks, per_chunk, c_lo, c_hi);
-        Segment sg;
         if (w < 16) {
             // ------------------------------------------- softmax of a tile of rows --
             more_regs<kRegsSoftmax>();
@@ -659,9 +703,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnAr
                           min(128, x.rows - m * 128), tid & 255);
                 mbar_arrive(bar(kQFull + m));
             };
-            bool more = walk.next(a, sg);
-            if (more && m * 128 < sg.rows) queries(sg);
-            while (more) {
+            uint32_t run_idx = 0;
+            const Segment *run = run_at(sh, 0);
+            if (run && m * 128 < run->rows) queries(*run);
+            while (run) {
+                const Segment &sg = *run;
                 // up to 128 rows: both pairs take them, every other tile of tokens each
                 const bool narrow = sg.rows <= 128;
                 const int first = narrow ? m : 0, step = narrow ? 2 : 1;
@@ -767,13 +813,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnAr
                 // the next run's queries, once the products of this one have read theirs:
                 // its first scores are then on their way while this one's output is written
                 t0 += sg.n;
-                Segment nx;
-                const bool another = walk.next(a, nx);
-                if (another && m * 128 < nx.rows) {
+                const Segment *next = run_at(sh, run_idx + 1);
+                if (next && m * 128 < next->rows) {
                     // (only a pair that loads may wait here: without its load the barrier
                     // cannot run a phase ahead of the one it waits for)
                     if (!dead) dead = __any_sync(0xffffffffu, !mbar_wait(bar(kQEmpty), e_ph, abort_flag, a.err));
-                    queries(nx);
+                    queries(*next);
                 }
                 e_ph ^= 1;
                 // O of the run
@@ -884,8 +929,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnAr
                 }
                 tc_fence_before();  // the reads of O before the next run's first product
                 if (narrow) named_bar_sync(kBarBoth, 512);
-                sg = nx;
-                more = another;
+                run_done(sh, run_idx++);
+                run = next;
             }
             fewer_regs<kRegsLaunch>();
             named_bar_sync(kBarRegs, kThreads);
@@ -893,9 +938,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnAr
             // ----------------------------------------------- codes to operand tiles --
             fewer_regs<kRegsCodes>();
             if (w < 20)
-                unpack_role<D, 0>(a, sh, smem, walk);
+                unpack_role<D, 0>(a, sh, smem);
             else
-                unpack_role<D, 1>(a, sh, smem, walk);
+                unpack_role<D, 1>(a, sh, smem);
             named_bar_sync(kBarRegs, kThreads);
             more_regs<kRegsLaunch>();
         } else {
@@ -916,10 +961,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnAr
             // a tile's slot in the rings of two, and its phase
             auto slot = [&](int k) { return (t0 + k) & 1u; };
             auto phase = [&](int k) { return ((t0 + k) >> 1) & 1u; };
-            while (m < 2 && ok && walk.next(a, sg)) {
+            if (m == 2) {
+                Walk walk;
+                walk.start(a, sh.prefix, chunks, per_chunk, c_lo, c_hi);
+                write_runs(a, sh, walk);
+            }
+            for (uint32_t run_idx = 0; m < 2 && ok; ++run_idx) {
+                const Segment *run = run_at(sh, run_idx);
+                if (!run) break;
+                const int n = run->n;
                 // narrow: warp m takes every other tile, for the same rows, and lets go
                 // of a tile for both
-                const bool narrow = sg.rows <= 128;
+                const bool narrow = run->rows <= 128;
+                run_done(sh, run_idx);
                 const int first = narrow ? m : 0, step = narrow ? 2 : 1;
                 const uint32_t q_at = smem + C::kQ + (narrow ? 0u : (uint32_t)m * C::kTileBytes);
                 if (!wait(kQFull, q_ph[0])) break;
@@ -936,9 +990,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnAr
                     const uint32_t done = sub ? bar(kKEmpty + slot(k)) : 0u;
                     tc_commit2_elect(bar(kSFull + 2 * m + sub), done);
                     if (sub)
-                        tc_commit2_elect(narrow ? done : 0u, k + step >= sg.n ? bar(kQEmpty) : 0u);
+                        tc_commit2_elect(narrow ? done : 0u, k + step >= n ? bar(kQEmpty) : 0u);
                 };
-                if (first < sg.n) {
+                if (first < n) {
                     if (!wait(kKFull + slot(first), phase(first))) break;
                     tc_fence_after();
                     scores(first, 0);
@@ -946,8 +1000,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnAr
                 } else if (lane == 0) {
                     mbar_arrive(bar(kQEmpty));
                 }
-                for (int k = first; ok && k < sg.n; k += step) {
-                    const bool again = k + step < sg.n;
+                for (int k = first; ok && k < n; k += step) {
+                    const bool again = k + step < n;
                     if (!wait(kVFull + slot(k), phase(k))) break;
                     if (again && !wait(kKFull + slot(k + step), phase(k + step))) break;
                     const uint32_t v_at = smem + C::kV + slot(k) * C::kTileBytes, done = bar(kVEmpty + slot(k));
@@ -962,7 +1016,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnAr
                     tc_commit2_elect(narrow ? done : 0u, again ? 0u : bar(kOFull + m));
                     p_ph ^= 1;
                 }
-                t0 += sg.n;
+                t0 += n;
             }
             named_bar_sync(kBarRegs, kThreads);
             more_regs<kRegsLaunch>();
