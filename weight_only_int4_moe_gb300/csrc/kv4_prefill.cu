@@ -500,31 +500,40 @@ MOE_DEV void unpack_role(const KvAttnArgs &a, Shared &sh, uint32_t smem) {
         return true;
     };
     Packed<D> pk;
-    pk.live = 0;
     // (nothing waits for a load here: rows without a token load page 0 and are zeroed when
-    // they are unpacked)
-    auto request = [&](int i) {
-        const int row = i * kStep + row_l, slot = row & (ps - 1);
-        const int id = __shfl_sync(0xffffffffu, ids, id_at + (row >> ps_log));
-        pk.live = (pk.live & ~(1u << i)) | (id >= 0 && row < left ? 1u : 0u) << i;
-        const uint8_t *blk = head + (size_t)(uint32_t)max(id, 0) * page_bytes;
-        pk.c[i] = *reinterpret_cast<const uint4 *>(blk + (part * ps + slot) * (D / 2) + 16 * ch);
-        const uint8_t *sc = blk + ps * D + (part * ps + slot) * (NG * 2);
-        if constexpr (D == 128) {
-            const uint2 v = *reinterpret_cast<const uint2 *>(sc);
-            pk.z[i][0] = v.x;
-            pk.z[i][1] = v.y;
-        } else {
-            pk.z[i][0] = *reinterpret_cast<const uint32_t *>(sc);
+    // they are unpacked).  All page ids come first: a warp has six scoreboards, and a
+    // shuffle that shared one with a load would wait for the load.
+    auto request = [&] {
+        int id[C::kLoads];
+#pragma unroll
+        for (int i = 0; i < C::kLoads; ++i)
+            id[i] = __shfl_sync(0xffffffffu, ids, id_at + ((i * kStep + row_l) >> ps_log));
+        pk.live = 0;
+#pragma unroll
+        for (int i = 0; i < C::kLoads; ++i) {
+            pk.live |= (id[i] >= 0 && i * kStep + row_l < left ? 1u : 0u) << i;
+            id[i] = max(id[i], 0);
+            asm volatile("" : "+r"(id[i])::"memory");
+        }
+#pragma unroll
+        for (int i = 0; i < C::kLoads; ++i) {
+            const int slot = (i * kStep + row_l) & (ps - 1);
+            const uint8_t *blk = head + (size_t)(uint32_t)id[i] * page_bytes;
+            pk.c[i] = *reinterpret_cast<const uint4 *>(blk + (part * ps + slot) * (D / 2) + 16 * ch);
+            const uint8_t *sc = blk + ps * D + (part * ps + slot) * (NG * 2);
+            if constexpr (D == 128) {
+                const uint2 v = *reinterpret_cast<const uint2 *>(sc);
+                pk.z[i][0] = v.x;
+                pk.z[i][1] = v.y;
+            } else {
+                pk.z[i][0] = *reinterpret_cast<const uint32_t *>(sc);
+            }
         }
     };
     Ring ring(2);
     uint32_t tiles = 0;
     bool more = advance();
-    if (more) {
-#pragma unroll
-        for (int i = 0; i < C::kLoads; ++i) request(i);
-    }
+    if (more) request();
     while (more) {
         const uint32_t ok = ok_next;
         more = advance();
@@ -560,8 +569,7 @@ MOE_DEV void unpack_role(const KvAttnArgs &a, Shared &sh, uint32_t smem) {
         }
         fence_proxy_async_shared();
         mbar_arrive(full + 8 * ring.idx);
-#pragma unroll
-        for (int i = 0; i < C::kLoads; ++i) request(i);
+        request();  // (past the last tile: that one again)
         ring.next();
     }
 }
