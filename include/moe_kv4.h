@@ -151,7 +151,8 @@ size_t moe_kv4_workspace_bytes(const moe_kv4_shape *shape, int q_heads);
  * workspace: >= moe_kv4_workspace_bytes, 16-byte aligned; its first
  *   MOE_KV4_WS_HEADER bytes are zeroed once when it is allocated (the first two
  *   words are the error words, which accumulate; the rest returns to zero after
- *   every call).  Calls in flight at once must not share it.
+ *   every call, but for one that reports MOE_DEVERR_TIMEOUT: zero it again).  Calls
+ *   in flight at once must not share it.
  * The softmax statistics, scores and sums are fp32; q is converted to fp16 (exact
  * for magnitudes in [2^-14, 65504]) and the unnormalised probabilities to fp16
  * (11 significant bits) for the tensor cores.  How a sequence is split over the

@@ -12,6 +12,12 @@
 // order does not depend on the lane) and the group maximum (four lanes) do.  A warp
 // stays with one token and walks its heads, so that the token's place, its rotation
 // and the weights are read once; where there are few tokens several warps share one.
+//
+// Measured: 6800 tokens of 56 + 8 + 8 heads of 128: 54 us for the 236 MB that append
+// itself touches, 4.4 TB/s of the 6.8 that a copy reaches; with the read of what it wrote
+// 67 us.  One token of 32 + 8 + 8 heads: 6 us for both, two launches.  The issue slots
+// are 56 % busy with the 21 warps that 80 registers a thread allow, the rest waits for
+// loads; two heads of a warp are in flight at a time.
 #include "kv4.cuh"
 #include "kv4_launch.cuh"
 

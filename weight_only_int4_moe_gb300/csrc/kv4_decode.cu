@@ -24,6 +24,15 @@
 // size of 64 is one contiguous block).  Warps of a CTA join their parts of an item
 // through shared memory, CTAs through the workspace, the last one to arrive adding
 // them up in list order.
+//
+// Measured: 90 streams of up to 8192 tokens, 56 heads over 8 kv heads of 128: 89 us,
+// 4.6 TB/s of the 6.8 that a copy reaches; two of 131071 tokens, 64 heads: 66 us, the same
+// rate; one of 777, 32 heads: 12 us.  Bound by instructions, not bytes: a tile of 64
+// tokens is some 1000 instructions of a warp, most of them the unpacking, and the ALU
+// pipe, which takes two cycles for one, is 45 % busy, the issue slots 58 %, with the three
+// warps a scheduler that the registers allow.  Joining the parts is a tenth of the time
+// on the ragged batch.  Half tiles (half the code and the score registers) were slower:
+// 95 and 71 us.  12 warps for 8 rows, 8 for 16: what the registers allow.
 #include <atomic>
 
 #include "dequant.cuh"

