@@ -36,8 +36,8 @@
 // CTA to arrive, in list order.
 //
 // Measured: 4096 new tokens behind 4096 cached ones, 32 heads over 8 kv heads of 128:
-// 424 us, 973 TFLOP/s of the 1901 that a large bf16 product reaches; 10 verify streams of
-// up to 5000 tokens, up to 63 rows each: 51 us.  A tile of 256 rows and 128 tokens takes about
+// 423 us, 975 TFLOP/s of the 1901 that a large bf16 product reaches; 10 verify streams of
+// up to 5000 tokens, up to 63 rows each: 50 us.  A tile of 256 rows and 128 tokens takes about
 // 4900 cycles, its MMAs alone 2520.  With the softmax's arithmetic, or the unpacking,
 // taken out the first fell from 447 to 414 and to 383 us, without either to 350: what
 // remains is the round trip between the products and the softmax.  A whole tile's more
@@ -459,7 +459,9 @@ MOE_DEV void unpack_role(const KvAttnArgs &a, Shared &sh, uint32_t smem) {
     const int ps = a.pool.ps, ppt = kTok >> (31 - __clz(ps)), hkv = a.pool.hkv;
     const uint32_t full = smem_u32(&sh.bar[part ? kVFull : kKFull]);
     const uint32_t empty = smem_u32(&sh.bar[part ? kVEmpty : kKEmpty]);
-    const uint32_t buf = smem + (part ? C::kV : C::kK);
+    // where the thread's first chunk goes (tile_at is the same for rows kStep apart)
+    const int first = part == 0 ? (D == 128 ? ch : 2 * ch) : (D == 128 ? 2 * ch : 4 * ch);
+    const uint32_t at0 = smem + (part ? C::kV : C::kK) + tile_at(row_l, first);
     // The tile whose loads are requested.  Each of them goes out as soon as the tile
     // before has left its registers.  Kept from the run: the head's blocks (from the
     // thread's chunk on), the tiles left, the tokens left, the table's next entry and end.
@@ -553,30 +555,27 @@ MOE_DEV void unpack_role(const KvAttnArgs &a, Shared &sh, uint32_t smem) {
             return;
         if (part == 0 && dt == 0) sh.ok[tiles & 7] = ok;
         ++tiles;
-        const uint32_t dst = buf + ring.idx * C::kTileBytes;
+        const uint32_t dst = at0 + ring.idx * C::kTileBytes;
 #pragma unroll
         for (int i = 0; i < C::kLoads; ++i) {
-            const int row = i * kStep + row_l;
             const uint32_t words[4] = {pk.c[i].x, pk.c[i].y, pk.c[i].z, pk.c[i].w};
-            const bool live = (pk.live >> i) & 1u;
+            uint32_t z[D / 64];
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c) z[c] = (pk.live >> i) & 1u ? pk.z[i][c] : 0u;
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                uint32_t s;
-                int chunk;
-                if (part == 0) {
-                    // word (t, G): dimensions 32G + 8t.., the row's chunk 4G + t
-                    const int G = D == 128 ? u : u & 1, t = D == 128 ? ch : 2 * ch + (u >> 1);
-                    s = __byte_perm(pk.z[i][G / 2], 0, G & 1 ? 0x3232 : 0x1010);
-                    chunk = 4 * G + t;
-                } else {
-                    // piece g of groups 2p and 2p + 1: column chunk 8p + g
-                    const int pp = D == 128 ? u & 1 : 0, g = D == 128 ? 2 * ch + (u >> 1) : 4 * ch + u;
-                    s = pk.z[i][pp];
-                    chunk = 8 * pp + g;
-                }
+                // K's word (t, G) holds dimensions 32G + 8t.., the row's chunk 4G + t; V's
+                // piece g of groups 2p and 2p + 1 is the column chunk 8p + g.  Seen from the
+                // thread's first chunk: a change of chunk bits, which the swizzle keeps, and
+                // a column block.
+                const int G = D == 128 ? u : u & 1, pp = D == 128 ? u & 1 : 0;
+                const uint32_t flip = part == 0 ? (G & 1) * 64u + (D == 128 ? 0u : (u >> 1) * 16u)
+                                                : (D == 128 ? (u >> 1) * 16u : u * 16u);
+                const uint32_t block = part == 0 ? G >> 1 : pp;
+                const uint32_t s = part == 0 ? as_u32(G & 1 ? __high2half2(as_h2(z[G / 2])) : __low2half2(as_h2(z[G / 2]))) : z[pp];
                 uint32_t x[4];
-                scaled_codes(words[u], a.k, live ? s : 0u, x);
-                sts128(dst + tile_at(row, chunk), x[0], x[1], x[2], x[3]);
+                scaled_codes(words[u], a.k, s, x);
+                sts128((dst ^ flip) + block * (kTok * 128) + i * (kStep * 128), x[0], x[1], x[2], x[3]);
             }
         }
         fence_proxy_async_shared();
