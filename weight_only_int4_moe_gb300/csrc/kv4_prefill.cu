@@ -87,6 +87,17 @@ struct Cfg {
 };
 
 // S and P: by row tile and half tile (2 m + sub); kPv: by row tile, after every P V.
+// A wait names a phase by its parity, so it is only sound while the barrier is at most
+// one lap away from the phase waited for.  The rings of two (K, V) and Q hold that for a
+// MMA warp because
+//  - within a run it waits for its own tiles in order, and a tile that it has to consume
+//    cannot be overwritten, so no ring runs ahead of it;
+//  - in a narrow run it skips the other warp's tiles.  K and Q: the next run's kQFull
+//    follows kQEmpty, so all scores of the old run, and with them all its K, are done.
+//    V: the old run's last tile may still be on its way to the slot of this warp's first
+//    tile of the new run, whose wait would pass a lap early and multiply stale values.  The
+//    first tile's P comes after kBarBoth of the old run, so after its last product with
+//    V: a run's first kVFull is waited for behind that P.
 enum Bar { kKFull = 0, kKEmpty = 2, kVFull = 4, kVEmpty = 6, kQFull = 8, kPv = 10, kSFull = 12, kPFull = 16, kQEmpty = 20, kOFull = 22, kRunFull = 24, kRunEmpty = 32, kBars = 40 };
 
 struct Request {
@@ -1016,6 +1027,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnAr
                     tc_fence_after();
                     scores(first, 0);
                     scores(first, 1);
+                    // before the run's first wait for V (the rings' invariant at Bar)
+                    if (!wait(kPFull + 2 * m, p_ph)) break;
                 } else if (lane == 0) {
                     mbar_arrive(bar(kQEmpty));
                 }
