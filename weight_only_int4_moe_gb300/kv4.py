@@ -7,6 +7,10 @@ A program keeps three kinds of objects, all over its own device tensors: a
 ``Cache`` (the page pool of all layers), a ``Batch`` for each shape of step (whose
 tensors it may update in place between calls), and ``Sequences`` for page
 management.
+
+Calls run on `stream`, or on the current one.  What a call makes for itself (outputs
+that are not given, a workspace, scratch) is made on that stream; the caller orders its
+own tensors, and reads of the results, with it.
 """
 from __future__ import annotations
 
@@ -107,6 +111,18 @@ def _raw_stream(stream, index):
     return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
 
+def _empty(shape, dtype, device, stream):
+    """Uninitialised memory for a call on `stream` (None: the device's current one).
+    It comes from that stream's memory, so that nothing still running elsewhere uses it,
+    and the current stream, where the caller goes on with it, is recorded."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 # The checks below run before every launch and are kept short: a single-token step
 # is bound by what the host does per call (a tensor's get_device() costs a third
 # of comparing its .device).
@@ -183,20 +199,21 @@ class Cache:
         return cls(pages, kv_heads, head_dim, page_size)
 
     def errors(self):
-        """(flags, count) accumulated so far; waits for the device."""
+        """(flags, count) accumulated so far; waits for the device (all its streams)."""
+        torch.cuda.synchronize(self.device)
         flags, count = self.err.tolist()
         return flags & 0xFFFFFFFF, count
 
     def clear_errors(self):
         self.err.zero_()
 
-    def scratch(self):
+    def scratch(self, stream=None):
         """(pointer, bytes) of the device scratch of page calls, for any number of
-        requests: taken once and kept (calls that share it run one after the other
-        on one stream)."""
+        requests: taken by the first call, on its stream, and kept (calls that share it
+        run one after the other)."""
         if self._scratch is None:
             n = load_library().moe_kv4_scratch_bytes(self.ref, MAX_REQUESTS)
-            self._scratch = torch.empty(n, dtype=torch.uint8, device=self.device)
+            self._scratch = _empty(n, torch.uint8, self.device, stream)
         return self._scratch.data_ptr(), self._scratch.numel()
 
 
@@ -272,7 +289,7 @@ def moe_kv4_append(cache: Cache, batch: Batch, q, k, v, q_weight=None, k_weight=
     else:
         qp, qs, hq = _rows(q, "q", dev, t, d)
         if q_out is None:
-            q_out = torch.empty((t, hq, d), dtype=_BF16, device=cache.device)
+            q_out = _empty((t, hq, d), _BF16, cache.device, stream)
             op = q_out.data_ptr()
         else:
             op = _like(q_out, "q_out", dev, _BF16, (t, hq, d))
@@ -303,9 +320,9 @@ def moe_kv4_read(cache: Cache, batch: Batch, layer: int = 0, k_out=None, v_out=N
     shape = (batch.tokens, cache.shape.kv_heads, cache.shape.head_dim)
     dev = cache.index
     if k_out is None:
-        k_out = torch.empty(shape, dtype=torch.float16, device=cache.device)
+        k_out = _empty(shape, torch.float16, cache.device, stream)
     if v_out is None:
-        v_out = torch.empty(shape, dtype=torch.float16, device=cache.device)
+        v_out = _empty(shape, torch.float16, cache.device, stream)
     kp = _like(k_out, "k_out", dev, torch.float16, shape)
     vp = _like(v_out, "v_out", dev, torch.float16, shape)
     with _on(dev):
@@ -316,15 +333,20 @@ def moe_kv4_read(cache: Cache, batch: Batch, layer: int = 0, k_out=None, v_out=N
     return k_out, v_out
 
 
-def alloc_workspace(cache: Cache, batch: Batch | None, q_heads: int) -> torch.Tensor:
+def alloc_workspace(cache: Cache, batch: Batch | None, q_heads: int, stream=None) -> torch.Tensor:
     """A workspace for attention with this cache and number of query heads (any
-    batch), its header zeroed."""
+    batch), its header zeroed on `stream` (None: the current one), on which, or after
+    which, its calls run."""
     n = load_library().moe_kv4_workspace_bytes(cache.ref, q_heads)
     if n == 0:
         raise ValueError(f"{q_heads} query heads over {cache.shape.kv_heads} kv heads are not "
                          "supported")
-    ws = torch.empty(n, dtype=torch.uint8, device=cache.device)
-    ws[:MOE_KV4_WS_HEADER].zero_()
+    ws = _empty(n, torch.uint8, cache.device, stream)
+    if stream is None:
+        ws[:MOE_KV4_WS_HEADER].zero_()
+    else:
+        with torch.cuda.stream(stream):
+            ws[:MOE_KV4_WS_HEADER].zero_()
     return ws
 
 
@@ -335,21 +357,22 @@ def moe_kv4_attention(q, cache: Cache, batch: Batch, scale: float | None = None,
     their sequences: out bf16 [tokens, q_heads, D], with return_lse (or an lse
     tensor) also the fp32 log-sum-exp [tokens, q_heads].  window: only the last
     tokens (0: all).  tree: int64 [tokens], bit i set where the i-th new token of
-    the request is seen.  scale defaults to 1 / sqrt(D)."""
+    the request is seen.  scale defaults to 1 / sqrt(D).  Without a workspace the call
+    takes one for itself (its error words are lost with it)."""
     _same(cache, batch)
     dev, d, t = cache.index, cache.shape.head_dim, batch.tokens
     qp, qs, hq = _rows(q, "q", dev, t, d)
     if out is None:
-        out = torch.empty((t, hq, d), dtype=_BF16, device=cache.device)
+        out = _empty((t, hq, d), _BF16, cache.device, stream)
         op = out.data_ptr()
     else:
         op = _like(out, "out", dev, _BF16, (t, hq, d))
     if lse is None and return_lse:
-        lse = torch.empty((t, hq), dtype=_F32, device=cache.device)
+        lse = _empty((t, hq), _F32, cache.device, stream)
     lp = None if lse is None else _like(lse, "lse", dev, _F32, (t, hq))
     tp = None if tree is None else _like(tree, "tree", dev, torch.int64, (t,))
     if workspace is None:
-        workspace = alloc_workspace(cache, batch, hq)
+        workspace = alloc_workspace(cache, batch, hq, stream)
     elif workspace.get_device() != dev or workspace.dtype is not torch.uint8 or \
             not workspace.is_contiguous():
         raise ValueError(f"workspace: expected a contiguous uint8 tensor on cuda:{dev}")
@@ -383,7 +406,7 @@ def moe_kv4_reserve(cache: Cache, seqs: Sequences, ids, new_lens, stream=None):
     _pool_of(cache, seqs)
     n = ids.numel()
     ip, lp = _ids(ids, "ids", cache), _ids(new_lens, "new_lens", cache, n)
-    sp, sb = cache.scratch()
+    sp, sb = cache.scratch(stream)
     with _on(cache.index):
         rc = (_lib or load_library()).moe_kv4_reserve(
             cache.ref, seqs.ref, ip, lp, n, sp, sb, cache.err_ptr,
@@ -398,7 +421,7 @@ def moe_kv4_fork(cache: Cache, seqs: Sequences, parents, children, stream=None):
     _pool_of(cache, seqs)
     n = parents.numel()
     pp, cp = _ids(parents, "parents", cache), _ids(children, "children", cache, n)
-    sp, sb = cache.scratch()
+    sp, sb = cache.scratch(stream)
     with _on(cache.index):
         rc = (_lib or load_library()).moe_kv4_fork(
             cache.pages_ptr, cache.ref, seqs.ref, pp, cp, n, sp, sb, cache.err_ptr,
@@ -431,10 +454,10 @@ def moe_kv4_compact(cache: Cache, seqs: Sequences, tables_out=None, refs_out=Non
     refs_out = seqs.refs if refs_out is None else \
         _ints(refs_out, "refs_out", dev, seqs.refs.shape)
     if n_used is None:
-        n_used = torch.empty(1, dtype=_I32, device=cache.device)
+        n_used = _empty(1, _I32, cache.device, stream)
     else:
         _ints(n_used, "n_used", dev, (1,))
-    sp, sb = cache.scratch()
+    sp, sb = cache.scratch(stream)
     with _on(dev):
         rc = (_lib or load_library()).moe_kv4_compact(
             cache.pages_ptr, cache.ref, seqs.ref, tables_out.data_ptr(), refs_out.data_ptr(),
