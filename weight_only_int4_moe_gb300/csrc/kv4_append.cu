@@ -25,8 +25,10 @@ namespace moe {
 
 namespace {
 
-// Two floats in one register pair; every operation rounds each on its own, as the
-// scalar ones do, in half the instructions.
+// Two floats in one register pair: each is rounded on its own, as by the scalar
+// operations, in half the instructions.  A product that is added up next is made by
+// prod2: the compiler fuses a packed product with the sum behind it (the scalar
+// intrinsics are never fused), and the sum would then see it unrounded.
 MOE_DEV uint64_t pair(float a, float b) {
     uint64_t r;
     asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
@@ -41,6 +43,10 @@ MOE_DEV uint64_t mul2(uint64_t a, uint64_t b) {
     uint64_t r;
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
+}
+MOE_DEV uint64_t prod2(uint64_t a, uint64_t b) {
+    const float2 x = both(a), y = both(b);
+    return pair(__fmul_rn(x.x, y.x), __fmul_rn(x.y, y.y));
 }
 MOE_DEV uint64_t add2(uint64_t a, uint64_t b) {
     uint64_t r;
@@ -77,8 +83,8 @@ MOE_DEV void load8(const float *p, uint64_t (&x)[4]) {
 
 // Pairs (a, b) -> (a c - b s, b c + a s), two at a time.
 MOE_DEV void turn2(uint64_t &a, uint64_t &b, uint64_t c, uint64_t s, uint64_t minus1) {
-    const uint64_t x = sub2(mul2(a, c), mul2(b, s), minus1);
-    b = add2(mul2(b, c), mul2(a, s));
+    const uint64_t x = sub2(prod2(a, c), prod2(b, s), minus1);
+    b = add2(prod2(b, c), prod2(a, s));
     a = x;
 }
 // One pair whose members are the two halves of v.
@@ -178,7 +184,7 @@ MOE_DEV void append_heads(const KvAppendArgs &a, int t, int from, int to, const 
             // sum of squares of the row, in the documented order
             uint64_t s[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) s[j] = add2(mul2(x2[j], x2[j]), mul2(y2[j], y2[j]));
+            for (int j = 0; j < 4; ++j) s[j] = add2(prod2(x2[j], x2[j]), prod2(y2[j], y2[j]));
             const float2 f = both(add2(add2(s[0], s[2]), add2(s[1], s[3])));
             float sum = __fadd_rn(f.x, f.y);
 #pragma unroll
