@@ -128,6 +128,10 @@ def test_attention_refusals():
     assert _attend(batch=none, q=None, out=None) == 0
 
 
+def test_scales_whose_power_of_two_overflows():
+    assert _attend(scale=3e38) == -2 and _attend(scale=-3e38) == -2
+
+
 def test_page_refusals():
     lib = kv4.load_library()
     sh = ctypes.byref(kv4.Shape(1, 100, 2, 64, 16))

@@ -119,14 +119,14 @@ MOE_DEV void add_parts(int n, int row0, float sl2, At at, Done done) {
             float nm = m[r];
 #pragma unroll
             for (int u = 0; u < U; ++u) nm = fmaxf(nm, ml[u][r].x);  // a part twice: no harm
-            const float base = nm > -INFINITY ? nm * sl2 : 0.0f;
-            const float x = kv_ex2(m[r] * sl2 - base);
+            const float base = nm > -INFINITY ? nm : 0.0f;
+            const float x = kv_ex2((m[r] - base) * sl2);
             m[r] = nm;
             l[r] *= x;
             s[r].x *= x, s[r].y *= x, s[r].z *= x, s[r].w *= x;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const float y = i0 + u < n ? kv_ex2(ml[u][r].x * sl2 - base) : 0.0f;
+                const float y = i0 + u < n ? kv_ex2((ml[u][r].x - base) * sl2) : 0.0f;
                 l[r] = fmaf(ml[u][r].y, y, l[r]);
                 s[r].x = fmaf(v[u][r].x, y, s[r].x);
                 s[r].y = fmaf(v[u][r].y, y, s[r].y);

@@ -196,7 +196,8 @@ int moe_kv4_attention(const uint16_t *q, int64_t q_stride, int q_heads, const vo
     int rc = check_batch(pages, layer, shape, batch, &empty);
     if (rc != MOE_OK) return rc;
     if (!moe_kv4_workspace_bytes(shape, q_heads)) return MOE_ERR_SHAPE;
-    if (window < 0 || std::isnan(scale) || std::isinf(scale)) return MOE_ERR_SHAPE;
+    const float scale_log2 = scale * 1.4426950408889634f;
+    if (window < 0 || !std::isfinite(scale_log2)) return MOE_ERR_SHAPE;
     if (tree && batch->max_q > 64) return MOE_ERR_SHAPE;
     if (empty) return MOE_OK;
     if (!q || !out || !workspace) return MOE_ERR_NULL;
@@ -216,7 +217,10 @@ int moe_kv4_attention(const uint16_t *q, int64_t q_stride, int q_heads, const vo
     a.tree = tree;
     a.out = out;
     a.lse = lse;
-    a.scale_log2 = scale * 1.4426950408889634f;
+    a.scale_log2 = scale_log2;
+    a.sl2 = std::fmax(std::fabs(a.scale_log2), 1e-30f);
+    a.lag = 8.0f / a.sl2;
+    a.far = 1048576.0f / a.sl2;
     a.q_heads = q_heads;
     a.group = q_heads / shape->kv_heads;
     a.gdiv.group = a.group;

@@ -44,7 +44,6 @@ namespace {
 
 constexpr int kTile = 64;       // tokens of a unit of work
 constexpr int kChunks = 1024;   // entries of the prefix table over requests
-constexpr float kSlack = 8.0f;
 // Units before an item's first tile that hold no work: what a warp spends on a new
 // item (its queries, the first copies' latency), in tiles.
 constexpr int kPad = 1;
@@ -185,7 +184,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
     const int hkv = a.pool.hkv, G = a.group;
     constexpr int ps = PS, ppt = kTile / PS;          // pages of a tile
     constexpr uint32_t kBlock = PS * (D + D / 8);     // bytes of a page of a head
-    const float sl2 = fmaxf(fabsf(a.scale_log2), 1e-30f);
+    const float sl2 = a.sl2;
     if (tid == 0) abort_flag = 0;
     if (lane == 0)
         for (int s = 0; s < S; ++s) mbar_init(smem_u32(&bars[w * S + s]), 1);
@@ -522,7 +521,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
                     }
             }
             // Maximum and sum of each row (a column here: over the lanes g).  The maximum
-            // moves only when some score exceeds it by more than 2^kSlack: the
+            // moves only when some score exceeds it by more than 2^8: the
             // probabilities then stay below that, far inside fp16, and neither the
             // exchange between the lanes nor the rescaling is paid for every tile.
             uint32_t pb[4][NT][2];
@@ -546,7 +545,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
                         v = fmaxf(v, m[n][e]);
                         const float r = v > m[n][e] ? kv_ex2((m[n][e] - v) * sl2) : 1.0f;
                         m[n][e] = v;
-                        lim[n][e] = v + kSlack / sl2;
+                        lim[n][e] = fabsf(v) > a.far ? v : v + a.lag;
                         l[n][e] *= r;
 #pragma unroll
                         for (int G4 = 0; G4 < NG; ++G4)
@@ -554,8 +553,20 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
                             for (int c = 0; c < 2; ++c) acc[G4][c][n][e] *= r, acc[G4][c][n][2 + e] *= r;
                     }
                 }
-                const float o0 = m[n][0] == -INFINITY ? 0.0f : -m[n][0] * sl2;
-                const float o1 = m[n][1] == -INFINITY ? 0.0f : -m[n][1] * sl2;
+                float o0 = m[n][0] == -INFINITY ? 0.0f : -m[n][0] * sl2;
+                float o1 = m[n][1] == -INFINITY ? 0.0f : -m[n][1] * sl2;
+                if (fmaxf(fabsf(m[n][0]), fabsf(m[n][1])) > a.far) {
+                    // the rounding of m * sl2 would be a power of two of its own: such rows
+                    // subtract before the scale, and their maximum does not lag
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const bool far = fabsf(m[n][e]) > a.far && m[n][e] > -INFINITY;
+                        const float base = far ? m[n][e] : 0.0f;
+                        if (far) (e ? o1 : o0) = 0.0f;
+#pragma unroll
+                        for (int s = 0; s < 4; ++s) x[s][n][e] -= base, x[s][n][2 + e] -= base;
+                    }
+                }
 #pragma unroll
                 for (int s = 0; s < 4; ++s) {
                     float p[4];

@@ -58,6 +58,10 @@ struct KvAttnArgs {
     float *warp_slots, *cta_slots;
     uint32_t *err;
     bool beside;           // both kernels take part: the decode kernel runs beside the other
+    // scale_log2's magnitude (no less than 1e-30).  In units of q . k: how far a score may
+    // exceed the maximum that its row's probabilities are relative to (2^8), and from which
+    // magnitude on fp32 holds a score's power of two in steps of an eighth or more.
+    float sl2, lag, far;
 };
 
 constexpr int kKvMaxCtas = 160;     // slots of the workspace (a GB300 has 152 SMs)

@@ -51,6 +51,8 @@ namespace moe {
 
 namespace {
 
+// A row's maximum before any score: finite, so that differences from it are numbers.
+constexpr float kLow = -3e38f;
 constexpr int kTok = 128;        // tokens of a unit
 // Units before an item's first tile that hold no work: what a new item costs (its
 // queries, filling the pipeline, its output) in tiles.  Without them a CTA whose run
@@ -706,7 +708,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnAr
     const uint32_t per = max((uint32_t)a.min_units, (total + gridDim.x - 1) / gridDim.x);
     const uint32_t c_lo = min(total, blockIdx.x * per), c_hi = min(total, c_lo + per);
     const uint32_t tmem = sh.tmem;
-    const float sl2 = fmaxf(fabsf(a.scale_log2), 1e-30f);
+    const float sl2 = a.sl2;
     auto bar = [&](int i) { return smem_u32(&sh.bar[i]); };
     // S of the row tiles' half tiles, then their O; P lies over the first half of either
     // 32 columns of S
@@ -755,7 +757,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnAr
                 const int open = __reduce_min_sync(0xffffffffu, live ? (a.tree ? min(hi + 1, sg.r.first) : hi + 1)
                                                                      : INT32_MAX);
                 const int shut = __reduce_max_sync(0xffffffffu, live ? lo + 1 : 0);
-                float top = -INFINITY, sum = 0.0f;
+                float top = kLow, sum = 0.0f;
                 int j0 = (sg.tile0 + first) * kTok + 32 * half;
                 uint32_t at = t0 + first;  // the tile among all of the CTA's
                 const int mine = sg.n > first ? (sg.n - first + step - 1) / step : 0;
@@ -795,9 +797,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnAr
                     swap[128 * half] = now;
                     named_bar_sync(pair_bar, 64);
                     now = fmaxf(now, swap[128 * (half ^ 1)]);
-                    // the first maximum of a run is taken as it is; later ones only when
-                    // they have grown by more than 2^8
-                    const bool grow = now > top && (top == -INFINITY || (now - top) * sl2 > 8.0f);
+                    // the maximum moves when it has grown by more than 2^8; a run's first one
+                    // is taken as it is
+                    const bool grow = now - top > a.lag;
                     if (__any_sync(0xffffffffu, grow)) {
                         const float f = grow ? kv_ex2((top - now) * sl2) : 1.0f;
                         if (grow) top = now;
@@ -811,14 +813,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnAr
                         }
                     }
                     ++pv;
-                    const float off = top == -INFINITY ? 0.0f : -top * sl2;
-                    const uint64_t sc2 = pack2(sl2, sl2), off2 = pack2(off, off);
+                    // the difference first: the rounding of top * sl2, which one FMA behind the
+                    // scale would need, is a power of two of its own for large scores
+                    // (424 -> 434 us on the prompt above)
+                    const uint64_t sc2 = pack2(sl2, sl2), top2 = pack2(-top, -top);
                     uint64_t sum2[2] = {pack2(sum, 0.0f), 0};
                     uint32_t p[16];
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {
                         float x, y;
-                        unpack2(fma2(pack2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), sc2, off2), x, y);
+                        unpack2(fma2(add2(pack2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), top2), sc2, 0), x, y);
                         x = kv_ex2(x);
                         y = kv_ex2(y);
                         sum2[(e >> 1) & 1] = add2(sum2[(e >> 1) & 1], pack2(x, y));
@@ -875,8 +879,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnAr
                         if (m == 0) {
                             const float top1 = sh.top[0][1][0][r], sum1 = sh.top[0][1][1][r];
                             const float both = fmaxf(top, top1);
-                            mix = top > -INFINITY ? kv_ex2((top - both) * sl2) : 0.0f;
-                            mix1 = top1 > -INFINITY ? kv_ex2((top1 - both) * sl2) : 0.0f;
+                            mix = kv_ex2((top - both) * sl2);
+                            mix1 = kv_ex2((top1 - both) * sl2);
                             top = both;
                             sum = sum * mix + sum1 * mix1;
                         }
