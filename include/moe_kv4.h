@@ -154,9 +154,10 @@ size_t moe_kv4_workspace_bytes(const moe_kv4_shape *shape, int q_heads);
  *   every call, but for one that reports MOE_DEVERR_TIMEOUT: zero it again).  Calls
  *   in flight at once must not share it.
  * The softmax statistics, scores and sums are fp32; q is converted to fp16 (exact
- * for magnitudes in [2^-14, 65504]) and the unnormalised probabilities to fp16
- * (11 significant bits) for the tensor cores.  How a sequence is split over the
- * GPU depends on the batch; for equal arguments results are equal bit for bit.
+ * for magnitudes in [2^-14, 65504], in steps of 2^-24 below) and the unnormalised
+ * probabilities to fp16 (11 significant bits down to 2^-21 of the row's maximum, steps
+ * of 2^-31 below) for the tensor cores.  How a sequence is split over the GPU depends on
+ * the batch; for equal arguments results are equal bit for bit.
  * Errors: MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_ALIGN, MOE_ERR_WORKSPACE,
  *   MOE_ERR_UNSUPPORTED, MOE_ERR_CUDA.
  */

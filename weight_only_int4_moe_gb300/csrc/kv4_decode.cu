@@ -522,7 +522,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
             }
             // Maximum and sum of each row (a column here: over the lanes g).  The maximum
             // moves only when some score exceeds it by more than 2^8: the
-            // probabilities then stay below that, far inside fp16, and neither the
+            // probabilities then stay below 2^15, inside fp16, and neither the
             // exchange between the lanes nor the rescaling is paid for every tile.
             uint32_t pb[4][NT][2];
 #pragma unroll
@@ -553,8 +553,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
                             for (int c = 0; c < 2; ++c) acc[G4][c][n][e] *= r, acc[G4][c][n][2 + e] *= r;
                     }
                 }
-                float o0 = m[n][0] == -INFINITY ? 0.0f : -m[n][0] * sl2;
-                float o1 = m[n][1] == -INFINITY ? 0.0f : -m[n][1] * sl2;
+                float o0 = m[n][0] == -INFINITY ? 0.0f : fmaf(-m[n][0], sl2, kKvRaise);
+                float o1 = m[n][1] == -INFINITY ? 0.0f : fmaf(-m[n][1], sl2, kKvRaise);
                 if (fmaxf(fabsf(m[n][0]), fabsf(m[n][1])) > a.far) {
                     // the rounding of m * sl2 would be a power of two of its own: such rows
                     // subtract before the scale, and their maximum does not lag
@@ -562,7 +562,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
                     for (int e = 0; e < 2; ++e) {
                         const bool far = fabsf(m[n][e]) > a.far && m[n][e] > -INFINITY;
                         const float base = far ? m[n][e] : 0.0f;
-                        if (far) (e ? o1 : o0) = 0.0f;
+                        if (far) (e ? o1 : o0) = kKvRaise;
 #pragma unroll
                         for (int s = 0; s < 4; ++s) x[s][n][e] -= base, x[s][n][2 + e] -= base;
                     }
@@ -661,7 +661,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
                     }
                     if (a.lse && g == 0)
                         a.lse[o] = l[n][e] > 0.0f
-                                       ? (m[n][e] * sl2 + log2f(l[n][e])) * 0.6931471805599453f
+                                       ? (m[n][e] * sl2 + (log2f(l[n][e]) - kKvRaise)) * 0.6931471805599453f
                                        : -INFINITY;
                 }
         } else {
@@ -714,7 +714,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
         *reinterpret_cast<uint2 *>(a.out + o * D + 4 * d4) = make_uint2(
             *reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
         if (a.lse && d4 == 0)
-            a.lse[o] = ll > 0.0f ? (mm * sl2 + log2f(ll)) * 0.6931471805599453f : -INFINITY;
+            a.lse[o] = ll > 0.0f ? (mm * sl2 + (log2f(ll) - kKvRaise)) * 0.6931471805599453f : -INFINITY;
     };
     const int runs = n_runs;
     // a warp's share: two rows (D = 64: four) of one item at a time

@@ -40,6 +40,13 @@ struct alignas(16) KvConsts {
     uint32_t cm24 = 0xCE00CE00u;                          // fp16 pair (-24, -24)
 };
 
+// The probabilities are held as 2^7 times their value relative to the row's maximum, which
+// lags by up to 2^8: 2^15 at most, inside fp16.  Without the factor what lies 2^14 below
+// the maximum would lose bits and what lies 2^25 below would be lost, while the sum counts
+// it: in a long context with one strong token percents of the output.  It costs nothing
+// (it is the addend of the exponent's FMA) and cancels in the output; the lse takes it off.
+constexpr float kKvRaise = 7.0f;
+
 struct KvAttnArgs {
     const uint16_t *q;
     int64_t q_stride;

@@ -5,12 +5,12 @@
 // consecutive tokens), two tiles of 128 for tcgen05.mma, against tiles of 128
 // tokens.  Per tile of tokens and rows,
 //   S = Q K^T   (128 x 128 x D, both operands fp16 in shared memory)
-//   P = 2^(S - m) in fp16, written over S in tensor memory
+//   P = 2^(S - m + 7) in fp16, written over S in tensor memory
 //   O += P V    (128 x D x 128, P from tensor memory, V from shared memory)
 // with the running maximum m and the sum of a row in the one thread that owns the
 // row.  O is rescaled only when a row's maximum has grown by more than 2^8 since
-// its last rescale (the probabilities then stay below 2^8, far inside fp16, and
-// the quotient O / l does not depend on m).
+// its last rescale (P then stays below 2^15, inside fp16, and the quotient O / l does
+// not depend on m).
 //
 // Roles of the 28 warps: two pairs of warpgroups each own one tile of rows, a thread
 // half of a row's columns (they load its Q, do the softmax, write the output; the
@@ -816,13 +816,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnAr
                     // the difference first: the rounding of top * sl2, which one FMA behind the
                     // scale would need, is a power of two of its own for large scores
                     // (424 -> 434 us on the prompt above)
-                    const uint64_t sc2 = pack2(sl2, sl2), top2 = pack2(-top, -top);
+                    const uint64_t sc2 = pack2(sl2, sl2), top2 = pack2(-top, -top), raise2 = pack2(kKvRaise, kKvRaise);
                     uint64_t sum2[2] = {pack2(sum, 0.0f), 0};
                     uint32_t p[16];
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {
                         float x, y;
-                        unpack2(fma2(add2(pack2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), top2), sc2, 0), x, y);
+                        unpack2(fma2(add2(pack2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), top2), sc2, raise2), x, y);
                         x = kv_ex2(x);
                         y = kv_ex2(y);
                         sum2[(e >> 1) & 1] = add2(sum2[(e >> 1) & 1], pack2(x, y));
@@ -947,7 +947,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnAr
                             slot[D] = top;
                             slot[D + 1] = sum;
                         } else if (a.lse) {
-                            a.lse[o_row] = sum > 0.0f ? (top * sl2 + log2f(sum)) * 0.6931471805599453f
+                            a.lse[o_row] = sum > 0.0f ? (top * sl2 + (log2f(sum) - kKvRaise)) * 0.6931471805599453f
                                                       : -INFINITY;
                         }
                     }
@@ -1099,7 +1099,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnAr
                         make_uint2(*reinterpret_cast<const uint32_t *>(&x),
                                    *reinterpret_cast<const uint32_t *>(&y));
                     if (a.lse && d4 == 0)
-                        a.lse[o] = ll > 0.0f ? (mm * sl2 + log2f(ll)) * 0.6931471805599453f : -INFINITY;
+                        a.lse[o] = ll > 0.0f ? (mm * sl2 + (log2f(ll) - kKvRaise)) * 0.6931471805599453f : -INFINITY;
                 });
     }
 }
