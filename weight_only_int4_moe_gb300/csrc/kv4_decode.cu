@@ -15,7 +15,10 @@
 // multiplies the group's fp32 partial score (four FMAs per 16 tokens and group
 // instead of eight fp16 ones), the operands are 64 + q and the accumulator starts
 // at -72 sum(q); with two the operands are (q - 8) scale, exact in fp16, as for the
-// expert weights.  V pieces of two tokens are interleaved by one byte permute into
+// expert weights.  What cancels against the -72 sum(q) costs the fp32 scores about three
+// bits, which leaves them inside the bound of a sum of D fp32 terms (D 2^-23 of their
+// magnitudes, tested with keys of few large codes); operands q - 8, a subtraction more
+// each, would keep the bits at 93 and 69 us below.  V pieces of two tokens are interleaved by one byte permute into
 // (token, token + 1) pairs and take their two scales by the same exact FMA.
 //
 // Work is cut by tokens: all (request, row tile, kv head) items' tiles in one
