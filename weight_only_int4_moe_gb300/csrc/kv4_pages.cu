@@ -65,6 +65,12 @@ struct TakeArgs {
     uint32_t *err;
 };
 
+// Pages of len tokens (any len up to the largest int).
+MOE_DEV int pages_for(int len, int ps) { return len / ps + (len % ps > 0); }
+
+// Requests may ask for more pages than an int counts.  What the pool cannot hold fails
+// whatever its exact size, so a request's need and the running total are cut off at one
+// page more than there are, and the sum of a turn's kScan needs stays below 2^31.
 __global__ void __launch_bounds__(kScan) kv4_take_kernel(const TakeArgs t) {
     __shared__ int warp_sums[32];
     pdl_wait();
@@ -87,7 +93,7 @@ __global__ void __launch_bounds__(kScan) kv4_take_kernel(const TakeArgs t) {
             } else {
                 const int to = t.b[i];
                 ok = ok && len >= 0 && to >= len && to <= t.q.table_stride * (long long)ps;
-                need = ok ? (to + ps - 1) / ps - (len + ps - 1) / ps : 0;
+                need = ok ? min(pages_for(to, ps) - pages_for(len, ps), t.p.n_pages + 1) : 0;
             }
             if (!ok) kv_report(t.err, MOE_KV4_DEVERR_SEQ);
         }
@@ -97,7 +103,7 @@ __global__ void __launch_bounds__(kScan) kv4_take_kernel(const TakeArgs t) {
             first[i] = ok ? at : -1;
             need_of[i] = need;
         }
-        total += sum;
+        total = min(total + sum, t.p.n_pages + 1);
     }
     // the lowest free pages
     int found = 0;
@@ -132,7 +138,7 @@ __global__ void __launch_bounds__(kScan) kv4_take_kernel(const TakeArgs t) {
             continue;
         }
         const int x = t.a[i], to = t.b[i];
-        int32_t *row = t.q.tables + (size_t)x * t.q.table_stride + (to + ps - 1) / ps - need;
+        int32_t *row = t.q.tables + (size_t)x * t.q.table_stride + pages_for(to, ps) - need;
         for (int j = lane; j < need; j += 32) {
             const int page = page_of[r + j];
             row[j] = page;
@@ -227,7 +233,7 @@ __global__ void __launch_bounds__(128) kv4_free_kernel(const KvPages p, const mo
         if (threadIdx.x == 0) kv_report(err, MOE_KV4_DEVERR_SEQ);
         return;
     }
-    const int n = min((q.lens[x] + p.ps - 1) / p.ps, q.table_stride);
+    const int n = min(pages_for(q.lens[x], p.ps), q.table_stride);
     int32_t *row = q.tables + (size_t)x * q.table_stride;
     for (int j = threadIdx.x; j < n; j += blockDim.x) {
         const int page = row[j];
