@@ -73,7 +73,7 @@ typedef struct {
     int32_t max_kv;         /* largest kv_len (an upper bound) */
     int32_t table_stride;   /* entries from one row of tables to the next (its capacity) */
     const int32_t *cu_q;    /* [requests + 1] */
-    const int32_t *kv_len;  /* [requests] */
+    const int32_t *kv_len;  /* [requests]; attention cuts lengths at 2^31 - 2^22 */
     const int32_t *tables;  /* [requests][table_stride] */
 } moe_kv4_batch;
 

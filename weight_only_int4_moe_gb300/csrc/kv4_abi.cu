@@ -225,7 +225,7 @@ int moe_kv4_attention(const uint16_t *q, int64_t q_stride, int q_heads, const vo
     a.group = q_heads / shape->kv_heads;
     a.gdiv.group = a.group;
     a.gdiv.magic = a.group == 1 ? 0u : (uint32_t)((1ull << 32) / a.group + 1);
-    a.window = window;
+    a.window = window > kKvMaxLen ? 0 : window;  // no sequence is longer
     uint8_t *ws = reinterpret_cast<uint8_t *>(workspace);
     a.err = reinterpret_cast<uint32_t *>(ws);
     a.max_kv = batch->max_kv;

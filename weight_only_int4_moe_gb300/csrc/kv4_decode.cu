@@ -152,7 +152,7 @@ MOE_DEV Request request_of(const KvAttnArgs &a, int q0, int q1, int len, int row
     r.q0 = q0;
     r.m = q1 - q0;
     r.first = len - r.m;
-    r.end = (int)min((long long)len, (long long)a.batch.stride * a.pool.ps);
+    r.end = (int)min((long long)min(len, kKvMaxLen), (long long)a.batch.stride * a.pool.ps);
     const int start = a.window > 0 ? max(0, r.first - a.window + 1) : 0;
     r.tile0 = start / kTile;
     r.tiles = max(1, (r.end + kTile - 1) / kTile - r.tile0);

@@ -47,6 +47,10 @@ struct alignas(16) KvConsts {
 // (it is the addend of the exponent's FMA) and cancels in the output; the lse takes it off.
 constexpr float kKvRaise = 7.0f;
 
+// The longest sequence that attention works on, in tokens: what it adds to and takes from
+// a token's index (tiles, windows, new tokens) then stays inside an int.
+constexpr int kKvMaxLen = INT32_MAX - (1 << 22);
+
 struct KvAttnArgs {
     const uint16_t *q;
     int64_t q_stride;

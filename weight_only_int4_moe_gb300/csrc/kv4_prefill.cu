@@ -112,7 +112,7 @@ MOE_DEV Request request_of(const KvAttnArgs &a, int b) {
     r.m = a.batch.cu_q[b + 1] - r.q0;
     const int len = a.batch.kv_len[b];
     r.first = len - r.m;
-    r.end = (int)min((long long)len, (long long)a.batch.stride * a.pool.ps);
+    r.end = (int)min((long long)min(len, kKvMaxLen), (long long)a.batch.stride * a.pool.ps);
     r.rows = r.m * a.group;
     // (a row range outside the batch's tokens is no request)
     const bool mine = r.m > 0 && r.q0 >= 0 && r.q0 + r.m <= a.batch.tokens && r.rows >= a.rows_lo &&

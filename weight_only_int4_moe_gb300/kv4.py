@@ -99,6 +99,7 @@ class _Here:
 
 _HERE = _Here()
 _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+_INT_MAX = 2 ** 31 - 1  # (ctypes would wrap what lies beyond)
 
 
 def _on(index):
@@ -379,7 +380,8 @@ def moe_kv4_attention(q, cache: Cache, batch: Batch, scale: float | None = None,
     with _on(dev):
         rc = (_lib or load_library()).moe_kv4_attention(
             qp, qs, hq, cache.pages_ptr, layer, cache.ref, batch.ref,
-            d ** -0.5 if scale is None else scale, window, tp, op, lp, workspace.data_ptr(),
+            d ** -0.5 if scale is None else scale, min(max(window, -1), _INT_MAX), tp, op, lp,
+            workspace.data_ptr(),
             workspace.numel(), _raw_stream(stream, dev))
     if rc:
         ops._check(rc, "moe_kv4_attention")
