@@ -65,10 +65,13 @@ typedef struct {
 /* A batch of requests: request b has new tokens cu_q[b]..cu_q[b+1]-1 of the call
  * (any number, zero included), which are the last ones of its kv_len[b] tokens.
  * A request with more new tokens than kv_len is a contract violation whose
- * surplus first tokens see nothing and are not stored. */
+ * surplus first tokens see nothing and are not stored.  tokens may exceed
+ * cu_q[requests] (a batch padded to a captured step's size): rows of the call that no
+ * request owns are not stored, read as 0 and get no attention output. */
 typedef struct {
     int32_t requests;       /* 0..65536 */
-    int32_t tokens;         /* cu_q[requests]: rows of q, k, v and the outputs; 0..1<<20 */
+    int32_t tokens;         /* rows of q, k, v and the outputs, cu_q[requests] of them in use;
+                               0..1<<20 */
     int32_t max_q;          /* largest number of new tokens of a request (an upper bound) */
     int32_t max_kv;         /* largest kv_len (an upper bound) */
     int32_t table_stride;   /* entries from one row of tables to the next (its capacity) */

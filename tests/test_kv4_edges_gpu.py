@@ -1,10 +1,11 @@
 """Attention and append at the edges of their arguments: windows up to the largest int
-and beyond."""
+and beyond, rows that no request owns."""
 import numpy as np
 import pytest
 import torch
 
 import kv4_gpu_reference as gref
+import kv4_reference as ref
 
 pytestmark = pytest.mark.gpu
 
@@ -18,6 +19,12 @@ def kv4():
 
 def ints(v):
     return torch.from_numpy(np.ascontiguousarray(v, np.int32)).cuda()
+
+
+def close(out, want, spread, size):
+    """The bound of test_kv4_gpu, for lengths of a few hundred."""
+    tol = 2.0 ** -8 * want.abs() + (2.0 ** -11 + 2.0 ** -12 + 2e-5 * size[..., None]) * spread + 1e-4
+    return bool(((out.double() - want).abs() <= tol).all())
 
 
 # ------------------------------------------------------------------ windows --
@@ -45,3 +52,47 @@ def test_windows_below_the_ints_are_refused(kv4):
     for window in (-1, -2 ** 31, -2 ** 32 + 5):
         with pytest.raises(RuntimeError):
             kv4.moe_kv4_attention(q, cache, batch, window=window)
+
+
+# ---------------------------------------------------- rows without a request --
+@pytest.mark.parametrize("rotate", [False, True])
+def test_rows_of_no_request(kv4, rotate):
+    """A batch padded to a captured step's number of tokens: rows past cu_q's last entry
+    (and before its first) are not stored, read as zeros and report nothing."""
+    hkv, d, ps = 2, 128, 16
+    g = torch.Generator(device="cuda").manual_seed(1)
+    pool = torch.randint(0, 64, (1, 8, hkv, kv4.block_bytes(d, ps)), dtype=torch.uint8, device="cuda",
+                         generator=g)
+    cache = kv4.Cache(pool, hkv, d, ps)
+    before = pool.clone()
+    tables = ints([[0, 1], [2, 3], [4, 5]])
+    # two single tokens of sequences of 16 and 20 tokens; the row behind the first one's
+    # last full page would land in its next page
+    t = 6
+    batch = kv4.Batch(ints([1, 2, 2, 3]), ints([16, 7, 20]), tables, t, 2, 32)
+    x = torch.randn(t, hkv, d, device="cuda", generator=g).to(torch.bfloat16)
+    c, s = torch.rand(32, d // 2, device="cuda"), torch.rand(32, d // 2, device="cuda")
+    q = kv4.moe_kv4_append(cache, batch, x, x, x, cos=c if rotate else None, sin=s if rotate else None)
+    assert cache.errors() == (0, 0)
+    k, _ = kv4.moe_kv4_read(cache, batch)
+    assert cache.errors() == (0, 0)
+    changed = (cache.pages != before).any(-1).any(-1)[0].nonzero().flatten().tolist()
+    assert changed == [0, 5]
+    own = torch.tensor([1, 2], device="cuda")
+    rest = torch.tensor([0, 3, 4, 5], device="cuda")
+    assert not k[rest].any() and k[own].any(-1).all()
+    if not rotate:
+        assert torch.equal(q, x)
+    assert torch.isfinite(q).all()
+
+
+def test_attention_leaves_rows_of_no_request(kv4):
+    hkv, group, d, ps = 2, 4, 128, 64
+    pool, tables, cu, q = gref.make_case(5, [300, 90], [1, 1], hkv, group, d, ps)
+    cache = kv4.Cache(pool[None], hkv, d, ps)
+    q6 = torch.cat([q, torch.ones(4, hkv * group, d, dtype=torch.bfloat16, device="cuda")])
+    batch = kv4.Batch(ints([0, 1, 2]), ints([300, 90]), ints(tables), 6, 3, 300)
+    out = torch.full_like(q6, 7.0)
+    kv4.moe_kv4_attention(q6, cache, batch, out=out)
+    want, _, spread, size = gref.attention(q, pool, tables, [300, 90], cu, ps, ref.default_scale(d))
+    assert close(out[:2], want, spread, size) and (out[2:] == 7).all()

@@ -53,6 +53,15 @@ MOE_DEV int kv_request_of(const int32_t *cu_q, int requests, int t) {
     return lo;
 }
 
+// The index in its sequence of token t, which kv_request_of found in request b.  Negative:
+// it has no place there, being before the sequence's first token or, with owned false, a
+// row outside every request's range.
+MOE_DEV int kv_index_of(const KvBatch &b, int request, int t, bool &owned) {
+    const int q1 = b.cu_q[request + 1];
+    owned = t >= b.cu_q[request] && t < q1;
+    return owned ? b.kv_len[request] - (q1 - t) : -1;
+}
+
 // The page of token j of a sequence, or -1 (and a report) where its table has
 // none.
 MOE_DEV int kv_page_of(const KvBatch &b, const KvPool &p, int request, int j, uint32_t *err) {

@@ -306,10 +306,11 @@ __global__ void __launch_bounds__(256, 3) kv4_append_kernel(const KvAppendArgs a
     const int from = steps * share / a.split, to = steps * (share + 1) / a.split;
     Place place{nullptr, 0};
     int at = 0;
+    bool owned = true;  // by a request
     if (to > nq || (a.cos && !a.positions)) {
         const int b = kv_request_of(a.batch.cu_q, a.batch.requests, t);
-        at = a.batch.kv_len[b] - (a.batch.cu_q[b + 1] - t);
-        // more new tokens than the sequence's length: not stored
+        at = kv_index_of(a.batch, b, t, owned);
+        // of no request, or more new tokens than the sequence's length: not stored
         if (to > nq && at >= 0) {
             const int page =
                 kv_page_of(a.batch, a.pool, b, at, lane == 0 && to == steps ? a.err : nullptr);
@@ -320,7 +321,8 @@ __global__ void __launch_bounds__(256, 3) kv4_append_kernel(const KvAppendArgs a
     if (a.cos && from < nq + nk) {
         int pos = a.positions ? a.positions[t] : at;
         if (pos < 0 || pos >= a.max_pos) {
-            if (lane == 0 && share == 0) kv_report(a.err, MOE_KV4_DEVERR_POSITION);
+            if (lane == 0 && share == 0 && (owned || a.positions))
+                kv_report(a.err, MOE_KV4_DEVERR_POSITION);
             pos = min(max(pos, 0), a.max_pos - 1);
         }
         const float *cs = a.cos + (size_t)pos * (D / 2), *sn = a.sin + (size_t)pos * (D / 2);
@@ -355,7 +357,8 @@ __global__ void __launch_bounds__(256) kv4_read_kernel(const KvReadArgs a) {
     if (!dst) return;
     const int t = row / hkv, h = row - t * hkv;
     const int b = kv_request_of(a.batch.cu_q, a.batch.requests, t);
-    const int at = a.batch.kv_len[b] - (a.batch.cu_q[b + 1] - t);
+    bool owned;
+    const int at = kv_index_of(a.batch, b, t, owned);
     const int page = at < 0 ? -1 : kv_page_of(a.batch, a.pool, b, at, l == 0 ? a.err : nullptr);
     dst += (size_t)row * D + 8 * l;
     if (page < 0) {
