@@ -39,8 +39,8 @@
 extern "C" {
 #endif
 
-#define MOE_KV4_DEVERR_PAGE 0x10u      /* a page id outside [0, n_pages), or a length beyond its
-                                          table: those tokens are skipped */
+#define MOE_KV4_DEVERR_PAGE 0x10u      /* a page id outside [0, n_pages) that a token needs, or a
+                                          length beyond its table: those tokens are skipped */
 #define MOE_KV4_DEVERR_POSITION 0x20u  /* a rotary position outside [0, max_pos): the nearest
                                           one is used */
 #define MOE_KV4_DEVERR_RANGE 0x40u     /* a key or value beyond +-19040 or not finite was
@@ -141,7 +141,8 @@ size_t moe_kv4_workspace_bytes(const moe_kv4_shape *shape, int q_heads);
  * moe_kv4_attention: out[t, h] = sum_j softmax_j(scale * q[t,h] . k[j]) v[j] over
  * the tokens j of t's sequence that t sees, with kv head h / (q_heads / kv_heads).
  * With p = t's index in its sequence, t sees j <= p; of these
- *   window > 0: only j > p - window (0: all);
+ *   window > 0: only j > p - window (0: all); pages wholly before every row's window
+ *     are not read, and their table entries may be anything;
  *   tree (uint64 [tokens], NULL: none): of the request's new tokens only those
  *     whose bit is set, bit i for its i-th new token (requests of at most 64 new
  *     tokens): a tree of drafts, each seeing its ancestors and itself.

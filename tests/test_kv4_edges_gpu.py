@@ -1,5 +1,5 @@
 """Attention and append at the edges of their arguments: windows up to the largest int
-and beyond, rows that no request owns."""
+and beyond, rows that no request owns, pages that a window has left behind."""
 import numpy as np
 import pytest
 import torch
@@ -96,3 +96,25 @@ def test_attention_leaves_rows_of_no_request(kv4):
     kv4.moe_kv4_attention(q6, cache, batch, out=out)
     want, _, spread, size = gref.attention(q, pool, tables, [300, 90], cu, ps, ref.default_scale(d))
     assert close(out[:2], want, spread, size) and (out[2:] == 7).all()
+
+
+# ------------------------------------------------ pages a window has left behind --
+@pytest.mark.parametrize("ps", [16, 32])
+@pytest.mark.parametrize("m,group", [(1, 4), (1, 16), (5, 4), (150, 4)])
+@pytest.mark.parametrize("window", [1, 37, 64, 100, 130])
+def test_pages_before_the_window_are_not_needed(kv4, ps, m, group, window):
+    """Their entries may be anything, also pages of NaN: nothing read there reaches a result
+    and nothing is reported."""
+    hkv, d, kv = 2, 128, [517, 333, 1024]
+    pool, tables, cu, q = gref.make_case(window, kv, [m] * 3, hkv, group, d, ps)
+    cache = kv4.Cache(pool[None], hkv, d, ps)
+    want, _, spread, size = gref.attention(q, pool, tables, kv, cu, ps, ref.default_scale(d), window)
+    other = min(set(range(pool.shape[0])) - set(tables.flatten().tolist()))  # all its scales are NaN
+    for b, n in enumerate(kv):
+        gone = tables[b, :max(0, n - m - window + 1) // ps]
+        gone[:] = np.where(np.arange(len(gone)) % 3 == 2, -1, other)
+    batch = kv4.Batch(ints(cu), ints(kv), ints(tables), int(cu[-1]), m, max(kv))
+    ws = kv4.alloc_workspace(cache, batch, hkv * group)
+    out = kv4.moe_kv4_attention(q, cache, batch, window=window, workspace=ws)
+    assert close(out, want, spread, size)
+    assert ws[:8].view(torch.int32).tolist() == [0, 0]

@@ -346,7 +346,11 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
             e_base = from;
             const int e = from + lane;
             ids = -1;
-            if (e < (tile_lo + n_tiles) * ppt && (long long)e * ps < rq.end) {
+            // (not the pages that the window of the item's first row has left behind: they
+            // may be gone, or hold anything)
+            const int seen = a.window > 0 ? rq.first + div_group(row0, a.gdiv) - a.window + 1 : 0;
+            if (e < (tile_lo + n_tiles) * ppt && (long long)e * ps < rq.end &&
+                (long long)(e + 1) * ps > seen) {
                 ids = table[e];
                 if ((unsigned)ids >= (unsigned)a.pool.n_pages) {
                     ids = -1;

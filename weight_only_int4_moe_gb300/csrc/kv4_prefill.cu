@@ -477,19 +477,22 @@ MOE_DEV void unpack_role(const KvAttnArgs &a, Shared &sh, uint32_t smem) {
     const uint32_t at0 = smem + (part ? C::kV : C::kK) + tile_at(row_l, first);
     // The tile whose loads are requested.  Each of them goes out as soon as the tile
     // before has left its registers.  Kept from the run: the head's blocks (from the
-    // thread's chunk on), the tiles left, the tokens left, the table's next entry and end.
+    // thread's chunk on), the tiles left, the tokens left, the table's first,
+    // next and last entry.
     const int ps_log = 31 - __clz(ps);
     const uint32_t page_bytes = a.pool.block * hkv;
     const uint8_t *head = nullptr;
     const int32_t *table = nullptr;
-    int tiles_left = 0, left = 0, id_at = 0, entry = 0, entries = 0, ids = -1, ids_next = -1;
+    int tiles_left = 0, left = 0, id_at = 0, entry = 0, entries = 0, ids = -1, ids_next = -1, from = 0;
     bool reports = false;
     uint32_t run_idx = 0;
     // page ids: lane l holds the tile's and the following ones, 32 in all, then 32 more
     auto next_ids = [&] {
         ids = ids_next;
+        if (entry + lane < from) ids = -1;
         if ((unsigned)ids >= (unsigned)a.pool.n_pages) {
-            if (reports && entry + lane < entries) kv_report(a.err, MOE_KV4_DEVERR_PAGE);
+            if (reports && entry + lane >= from && entry + lane < entries)
+                kv_report(a.err, MOE_KV4_DEVERR_PAGE);
             ids = -1;
         }
         entry += 32;
@@ -505,6 +508,11 @@ MOE_DEV void unpack_role(const KvAttnArgs &a, Shared &sh, uint32_t smem) {
             table = a.batch.tables + (size_t)sg.b * a.batch.stride;
             head = a.pool.base + (size_t)sg.h * a.pool.block;
             reports = part == 0 && sg.h == 0 && dt < 32;
+            // (not the pages that the window of the run's first row has left behind: they may
+            // be gone, or hold anything)
+            from = a.window > 0
+                       ? max(0, sg.r.first + div_group(sg.rt * kRowsItem, a.gdiv) - a.window + 1) >> ps_log
+                       : 0;
             tiles_left = sg.n;
             left = sg.r.end - sg.tile0 * kTok;
             entry = sg.tile0 * ppt;
