@@ -4,6 +4,7 @@
 
 #include <atomic>
 #include <cmath>
+#include <cstdlib>
 
 #include "kv4_launch.cuh"
 
@@ -229,6 +230,10 @@ int moe_kv4_attention(const uint16_t *q, int64_t q_stride, int q_heads, const vo
     uint8_t *ws = reinterpret_cast<uint8_t *>(workspace);
     a.err = reinterpret_cast<uint32_t *>(ws);
     a.max_kv = batch->max_kv;
+    a.skip_tile = -1;
+#ifdef MOE_DEBUG_BOUNDS
+    if (const char *v = getenv("MOE_KV4_DEBUG_SKIP_TILE")) a.skip_tile = atoi(v);
+#endif
     // Requests of up to kKvFewRows rows go to the decode kernel, others to the
     // prefill kernel; where all have the same number of new tokens one is enough.
     const int ctas = sms < kKvMaxCtas ? sms : kKvMaxCtas;

@@ -377,6 +377,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
             }
             if (lane == 0) mbar_arrive_expect_tx(my_bar + 8 * slot, have * kBlock);
             if (ppt > 1) __syncwarp();
+            if (kDebugBounds && k == a.skip_tile && blockIdx.x == 0 && w == 0) mine = -1;
             if (mine >= 0)
                 bulk_copy(my_ring + slot * C::kTileBytes + lane * kBlock,
                           head_base + (size_t)mine * page_bytes, kBlock, my_bar + 8 * slot);
@@ -438,7 +439,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
 #pragma unroll
         for (int x = 0; x < NG * 2 * NT * 4; ++x) (&acc[0][0][0][0])[x] = 0.0f;
 
-        for (int k = 0; k < n_tiles; ++k) {
+        int k = 0;
+        for (; k < n_tiles; ++k) {
             const uint32_t slot = cons.idx;
             if (__any_sync(0xffffffffu, !mbar_wait(my_bar + 8 * slot, cons.ph, &abort_flag, a.err))) {
                 aborted = true;
@@ -632,6 +634,16 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
             if (k + S < n_tiles)
                 ok_ring = (ok_ring & ~(15u << (4 * slot))) | fetch(k + S, slot) << (4 * slot);
             cons.next();
+        }
+
+        if (aborted) {
+            // the copies in flight land before the ring is used otherwise or the CTA ends
+            // (waits that the abort does not cut short, limited as any other)
+            volatile int none = 0;
+            Ring left = cons;
+            for (int i = k; i < min(n_tiles, k + S); ++i, left.next())
+                mbar_wait(my_bar + 8 * left.idx, left.ph, &none, a.err);
+            __syncwarp();
         }
 
         // the segment's result

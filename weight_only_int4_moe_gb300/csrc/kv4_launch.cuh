@@ -73,6 +73,9 @@ struct KvAttnArgs {
     // exceed the maximum that its row's probabilities are relative to (2^8), and from which
     // magnitude on fp32 holds a score's power of two in steps of an eighth or more.
     float sl2, lag, far;
+    // Debug-bounds builds: CTA 0 leaves a tile's copy out (decode kernel, its first warp), or
+    // does not say that V's is unpacked (prefill kernel), so that a wait runs out.  -1: none.
+    int skip_tile;
 };
 
 constexpr int kKvMaxCtas = 160;     // slots of the workspace (a GB300 has 152 SMs)

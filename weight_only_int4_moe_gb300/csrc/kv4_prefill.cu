@@ -100,7 +100,7 @@ struct Cfg {
 //    tile of the new run, whose wait would pass a lap early and multiply stale values.  The
 //    first tile's P comes after kBarBoth of the old run, so after its last product with
 //    V: a run's first kVFull is waited for behind that P.
-enum Bar { kKFull = 0, kKEmpty = 2, kVFull = 4, kVEmpty = 6, kQFull = 8, kPv = 10, kSFull = 12, kPFull = 16, kQEmpty = 20, kOFull = 22, kRunFull = 24, kRunEmpty = 32, kBars = 40 };
+enum Bar { kKFull = 0, kKEmpty = 2, kVFull = 4, kVEmpty = 6, kQFull = 8, kPv = 10, kSFull = 12, kPFull = 16, kQEmpty = 20, kOFull = 22, kRunFull = 24, kRunEmpty = 32, kDrain = 40, kBars = 42 };
 
 struct Request {
     int q0, m, first, end, rows, row_tiles;
@@ -242,10 +242,11 @@ struct Walk {
 };
 
 // Run number idx of the CTA's list, or null at its end.  The warp that writes the list
-// either publishes a run or stops at it, so that all warps see the same list.
+// either publishes a run or stops at it, within the limit of its own waits, so that all
+// warps see the same list.  (The limit here only guards that: 2^22 polls of up to 20 us.)
 MOE_DEV const Segment *run_at(Shared &sh, uint32_t idx) {
     const uint32_t bar = smem_u32(&sh.bar[kRunFull + idx % kRuns]), ph = (idx / kRuns) & 1u;
-    for (uint32_t it = 0; it < (1u << 30); ++it) {
+    for (uint32_t it = 0; it < (1u << 22); ++it) {
         if (__any_sync(0xffffffffu, mbar_try_wait(bar, ph))) {
             const Segment *r = &sh.run[idx % kRuns];
             return r->n ? r : nullptr;
@@ -600,7 +601,8 @@ MOE_DEV void unpack_role(const KvAttnArgs &a, Shared &sh, uint32_t smem) {
             }
         }
         fence_proxy_async_shared();
-        mbar_arrive(full + 8 * ring.idx);
+        if (!(kDebugBounds && part == 1 && blockIdx.x == 0 && (int)tiles - 1 == a.skip_tile))
+            mbar_arrive(full + 8 * ring.idx);
         request();  // (past the last tile: that one again)
         ring.next();
     }
@@ -655,7 +657,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnAr
     if (a.beside) pdl_launch_dependents();
     if (tid == 0) {
         sh.abort_flag = 0;
-        const int counts[20] = {128, 2, 128, 2, 256, 1, 1, 1, 256, 256, 2, 1, 1, 1, 1, 1, 26, 26, 26, 26};
+        const int counts[21] = {128, 2, 128, 2, 256, 1, 1, 1, 256, 256, 2, 1, 1, 1, 1, 1, 26, 26, 26, 26, 1};
         sh.stop = 0xffffffffu;
         for (int i = 0; i < kBars; ++i) mbar_init(smem_u32(&sh.bar[i]), counts[i / 2]);
         mbar_fence_init();
@@ -1065,6 +1067,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnAr
             named_bar_sync(kBarRegs, kThreads);
             more_regs<kRegsLaunch>();
         }
+    }
+    if ((w == 24 || w == 25) && __any_sync(0xffffffffu, *(volatile int *)abort_flag)) {
+        // products in flight end before the tensor memory is given back
+        volatile int none = 0;
+        tc_commit_elect(bar(kDrain + w - 24));
+        mbar_wait(bar(kDrain + w - 24), 0, &none, a.err);
+        __syncwarp();
     }
     tc_fence_before();
     __threadfence();
