@@ -287,8 +287,8 @@ static int take(void *pages, const moe_kv4_shape *shape, const moe_kv4_seqs *seq
     int sms;
     rc = device_info(&sms);
     if (rc != MOE_OK) return rc;
-    return done(launch_kv4_take(pages_of(pages, shape), *seqs, a, b, fork, n, scratch, err, sms,
-                                str(stream)));
+    return done(
+        launch_kv4_take(pages_of(pages, shape), *seqs, a, b, fork, n, scratch, err, str(stream)));
 }
 
 int moe_kv4_reserve(const moe_kv4_shape *shape, const moe_kv4_seqs *seqs, const int32_t *ids,
@@ -312,7 +312,7 @@ int moe_kv4_free(const moe_kv4_shape *shape, const moe_kv4_seqs *seqs, const int
     int sms;
     rc = device_info(&sms);
     if (rc != MOE_OK) return rc;
-    return done(launch_kv4_free(pages_of(nullptr, shape), *seqs, ids, n, err, sms, str(stream)));
+    return done(launch_kv4_free(pages_of(nullptr, shape), *seqs, ids, n, err, str(stream)));
 }
 
 int moe_kv4_compact(void *pages, const moe_kv4_shape *shape, const moe_kv4_seqs *seqs,

@@ -104,12 +104,13 @@ cudaError_t launch_kv4_decode(KvAttnArgs a, int D, int max_rows, void *slots, in
 // Attention of the requests with many rows (a.rows_lo and up).
 size_t kv4_prefill_slot_bytes(int D, int ctas);
 cudaError_t launch_kv4_prefill(KvAttnArgs a, int D, void *slots, int ctas, cudaStream_t s);
-// new_lens null: fork (one page for each parent with a begun page), else reserve.
+// fork: a are parents, b children (one page for each parent with a begun page); else
+// reserve: a are sequences, b their new lengths.
 cudaError_t launch_kv4_take(const KvPages &p, const moe_kv4_seqs &q, const int32_t *a,
                             const int32_t *b, bool fork, int n, void *scratch, uint32_t *err,
-                            int sms, cudaStream_t s);
+                            cudaStream_t s);
 cudaError_t launch_kv4_free(const KvPages &p, const moe_kv4_seqs &q, const int32_t *ids, int n,
-                            uint32_t *err, int sms, cudaStream_t s);
+                            uint32_t *err, cudaStream_t s);
 cudaError_t launch_kv4_compact(const KvPages &p, const moe_kv4_seqs &q, int32_t *tables_out,
                                int32_t *refs_out, int32_t *n_used, void *scratch, uint32_t *err,
                                int sms, cudaStream_t s);

@@ -391,7 +391,7 @@ cudaLaunchConfig_t config(long long grid, unsigned block, cudaStream_t s, cudaLa
 
 cudaError_t launch_kv4_take(const KvPages &p, const moe_kv4_seqs &q, const int32_t *a,
                             const int32_t *b, bool fork, int n, void *scratch, uint32_t *err,
-                            int sms, cudaStream_t s) {
+                            cudaStream_t s) {
     TakeArgs t{p, q, a, b, fork, n, reinterpret_cast<int32_t *>(scratch), err};
     cudaLaunchAttribute at{};
     auto c = config(1, kScan, s, at);
@@ -402,7 +402,7 @@ cudaError_t launch_kv4_take(const KvPages &p, const moe_kv4_seqs &q, const int32
 }
 
 cudaError_t launch_kv4_free(const KvPages &p, const moe_kv4_seqs &q, const int32_t *ids, int n,
-                            uint32_t *err, int sms, cudaStream_t s) {
+                            uint32_t *err, cudaStream_t s) {
     cudaLaunchAttribute at{};
     auto c = config(n, 128, s, at);
     return cudaLaunchKernelEx(&c, kv4_free_kernel, p, q, ids, err);
