@@ -13,10 +13,10 @@
 // stays with one token and walks its heads, so that the token's place, its rotation
 // and the weights are read once; where there are few tokens several warps share one.
 //
-// Measured: 6800 tokens of 56 + 8 + 8 heads of 128: 54 us for the 236 MB that append
-// itself touches, 4.4 TB/s of the 6.8 that a copy reaches; with the read of what it wrote
+// Measured: 6800 tokens of 56 + 8 + 8 heads of 128: 56 us for the 236 MB that append
+// itself touches, 4.2 TB/s of the 6.8 that a copy reaches; with the read of what it wrote
 // 67 us.  One token of 32 + 8 + 8 heads: 6 us for both, two launches.  The issue slots
-// are 56 % busy with the 21 warps that 80 registers a thread allow, the rest waits for
+// are 61 % busy with the 21 warps that 80 registers a thread allow, the rest waits for
 // loads; two heads of a warp are in flight at a time.
 #include "kv4.cuh"
 #include "kv4_launch.cuh"
@@ -344,7 +344,9 @@ __global__ void __launch_bounds__(256, 3) kv4_append_kernel(const KvAppendArgs a
     append_heads<D, 2>(a, t, max(from, nq + nk) - nq - nk, to - nq - nk, c, z, place);
 }
 
-// One row (token, head, K or V) per D/16 lanes, as in the append.
+// One row (token, head, K or V) per D/16 lanes, as in the append.  6800 tokens of 8 heads
+// of 128: 10.4 us for 36 MB, half the copy's rate: a lane has one row, so one dependent
+// round trip (lengths, page id, codes) and, for V, loads of two bytes.
 template <int D>
 __global__ void __launch_bounds__(256) kv4_read_kernel(const KvReadArgs a) {
     constexpr int kLanes = D / 16, NG = D / 32;

@@ -18,8 +18,9 @@
 // expert weights.  What cancels against the -72 sum(q) costs the fp32 scores about three
 // bits, which leaves them inside the bound of a sum of D fp32 terms (D 2^-23 of their
 // magnitudes, tested with keys of few large codes); operands q - 8, a subtraction more
-// each, would keep the bits at 93 and 69 us below.  V pieces of two tokens are interleaved by one byte permute into
-// (token, token + 1) pairs and take their two scales by the same exact FMA.
+// each, would keep the bits at 93 and 69 us below.  V pieces of two tokens are
+// interleaved by one byte permute into (token, token + 1) pairs and take their two scales
+// by the same exact FMA.
 //
 // Work is cut by tokens: all (request, row tile, kv head) items' tiles in one
 // list, every CTA an equal run of it, every warp of the CTA an equal part of the
@@ -30,11 +31,11 @@
 //
 // Measured: 90 streams of up to 8192 tokens, 56 heads over 8 kv heads of 128: 89 us,
 // 4.6 TB/s of the 6.8 that a copy reaches; two of 131071 tokens, 64 heads: 66 us, the same
-// rate; one of 777, 32 heads: 12 us.  Bound by instructions, not bytes: a tile of 64
-// tokens is some 1000 instructions of a warp, most of them the unpacking, and the ALU
-// pipe, which takes two cycles for one, is 45 % busy, the issue slots 58 %, with the three
-// warps a scheduler that the registers allow.  Joining the parts is a tenth of the time
-// on the ragged batch.  Half tiles (half the code and the score registers) were slower:
+// rate; one of 777, 32 heads: 12 us.  Bound by latency, not bytes and not yet by a pipe: a
+// tile of 64 tokens is some 1000 instructions of a warp, most of them the unpacking, in
+// one chain of products, softmax and products, and with the three warps a scheduler that
+// the registers allow the issue slots are 58 % busy, the ALU pipe 45 %, FMA 33 %, tensor
+// 23 %.  Joining the parts is a tenth of the time on the ragged batch.  Half tiles (half the code and the score registers) were slower:
 // 95 and 71 us.  12 warps for 8 rows, 8 for 16: what the registers allow.
 #include <atomic>
 

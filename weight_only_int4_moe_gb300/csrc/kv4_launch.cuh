@@ -81,10 +81,10 @@ struct KvAttnArgs {
 constexpr int kKvMaxCtas = 160;     // slots of the workspace (a GB300 has 152 SMs)
 // Rows of a request (new tokens x group) up to which the decode kernel takes it, which
 // works on 16 of them at a time.  Measured, decode against prefill kernel: 10 streams of
-// 4000 tokens, 8 kv heads of 128 dimensions, 16, 32, 64 and 128 rows: 29, 40, 64 and
-// 114 us against 49, 49, 51 and 55; 32 such streams, 32, 64 and 128 rows: 95, 176 and
-// 332 us against 129, 132 and 139; 24 of 2000 tokens, 16 heads of 64, the same rows: 53,
-// 96 and 180 us against 70, 71 and 75.
+// 4000 tokens, 8 kv heads of 128 dimensions, 16, 32, 64 and 128 rows: 29, 41, 66 and
+// 118 us against 50, 51, 53 and 57; 32 such streams, 32, 64 and 128 rows: 99, 182 and
+// 344 us against 131, 136 and 142; 24 of 2000 tokens, 16 heads of 64, the same rows: 54,
+// 98 and 187 us against 68, 70 and 73.
 constexpr int kKvFewRows = 48;
 constexpr int kKvCounterByte = 256; // the counters' place in the workspace header
 

@@ -11,7 +11,12 @@
 // Measured: 200 sequences of up to 4000 tokens in a fragmented pool of 4 layers made
 // dense: 210 us for 1.32 GB, 6.3 TB/s (a copy reaches 6.8); 256 branches of 64 sequences
 // in 8 layers: 34 us for 144 MB, 4.2 TB/s.  Small pools are
-// launches: 10 us for 8 branches (free, take and fork), 6 us for a compaction.
+// launches: 10 us for 8 branches (free, take and fork), 6 us for a compaction.  A reserve
+// of 256 streams that grow by a token, 16 of them into a new page: 6 us where free pages
+// are spread over the pool, of any size; one block scans 4096 pages a turn, so where only
+// the last pages are free 27, 101 and 204 us in pools of 100000, 500000 and 2^20 pages.
+// Each block of a compaction counts the whole pool: with nothing to move 10, 28 and 93 us.
+// Copied pages of 4.6 KB: 6.2 to 6.4 TB/s.
 #include "kv4_launch.cuh"
 
 namespace moe {

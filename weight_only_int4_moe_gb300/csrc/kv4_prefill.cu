@@ -9,8 +9,8 @@
 //   O += P V    (128 x D x 128, P from tensor memory, V from shared memory)
 // with the running maximum m and the sum of a row in the one thread that owns the
 // row.  O is rescaled only when a row's maximum has grown by more than 2^8 since
-// its last rescale (P then stays below 2^15, inside fp16, and the quotient O / l does
-// not depend on m).
+// its last rescale, a method known from published attention kernels (P then stays below
+// 2^15, inside fp16, and the quotient O / l does not depend on m).
 //
 // Roles of the 28 warps: two pairs of warpgroups each own one tile of rows, a thread
 // half of a row's columns (they load its Q, do the softmax, write the output; the
@@ -36,12 +36,14 @@
 // CTA to arrive, in list order.
 //
 // Measured: 4096 new tokens behind 4096 cached ones, 32 heads over 8 kv heads of 128:
-// 423 us, 975 TFLOP/s of the 1901 that a large bf16 product reaches; 10 verify streams of
-// up to 5000 tokens, up to 63 rows each: 50 us.  A tile of 256 rows and 128 tokens takes about
-// 4900 cycles, its MMAs alone 2520.  With the softmax's arithmetic, or the unpacking,
-// taken out the first fell from 447 to 414 and to 383 us, without either to 350: what
+// 441 us, 935 TFLOP/s of the 1901 that a large bf16 product reaches; 10 verify streams of
+// up to 5000 tokens, up to 63 rows each: 51 us.  A tile of 256 rows and 128 tokens takes about
+// 5000 cycles, its MMAs alone 2520.  With the softmax's arithmetic, or the unpacking,
+// taken out the first, then at 447 us, fell to 414 and to 383, without either to 350: what
 // remains is the round trip between the products and the softmax.  A whole tile's more
 // scores in flight would need tensor memory that is all in use (O 256 columns, S 256).
+// The verify streams' items are bound by the two warpgroups that unpack, about 4000 cycles
+// a tile; their loads go through registers one tile ahead.
 #include <atomic>
 
 #include "dequant.cuh"
@@ -825,7 +827,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnAr
                     ++pv;
                     // the difference first: the rounding of top * sl2, which one FMA behind the
                     // scale would need, is a power of two of its own for large scores
-                    // (424 -> 434 us on the prompt above)
+                    // (ten of the prompt's 441 us)
                     const uint64_t sc2 = pack2(sl2, sl2), top2 = pack2(-top, -top), raise2 = pack2(kKvRaise, kKvRaise);
                     uint64_t sum2[2] = {pack2(sum, 0.0f), 0};
                     uint32_t p[16];
