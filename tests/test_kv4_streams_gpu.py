@@ -51,6 +51,7 @@ def test_attention_makes_its_workspace_on_the_given_stream(kv4):
     side = torch.cuda.Stream()
     torch.cuda.synchronize()
     kv4.moe_kv4_attention(q, cache, batch, return_lse=True, stream=side)  # its memory is there now
+    shown = False
     for _ in range(3):
         used_memory(ws.numel(), q.numel() * 2, 4 * lse.numel())
         torch.cuda.synchronize()
@@ -59,12 +60,14 @@ def test_attention_makes_its_workspace_on_the_given_stream(kv4):
         done.record()
         out, out_lse = kv4.moe_kv4_attention(q, cache, batch, return_lse=True, stream=side)
         side.synchronize()
-        assert not done.query(), "the current stream was not busy: nothing is shown"
+        shown |= not done.query()
         with torch.cuda.stream(side):
             same = torch.equal(out, want) and torch.equal(out_lse, lse)
         assert same
         torch.cuda.synchronize()
         del busy
+    if not shown:
+        pytest.skip("the current stream was never busy while the call ran: nothing is shown")
 
 
 def test_workspace_of_a_stream(kv4):
