@@ -65,7 +65,8 @@ typedef struct {
 /* A batch of requests: request b has new tokens cu_q[b]..cu_q[b+1]-1 of the call
  * (any number, zero included), which are the last ones of its kv_len[b] tokens.
  * A request with more new tokens than kv_len is a contract violation whose
- * surplus first tokens see nothing and are not stored.  tokens may exceed
+ * surplus first tokens see nothing and are not stored.  A request whose rows are not
+ * 0 <= cu_q[b] <= cu_q[b+1] <= tokens is left out.  tokens may exceed
  * cu_q[requests] (a batch padded to a captured step's size): rows of the call that no
  * request owns are not stored, read as 0 and get no attention output. */
 typedef struct {

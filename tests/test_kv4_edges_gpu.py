@@ -98,6 +98,31 @@ def test_attention_leaves_rows_of_no_request(kv4):
     assert close(out[:2], want, spread, size) and (out[2:] == 7).all()
 
 
+@pytest.mark.parametrize("big", [False, True])
+def test_row_ranges_that_are_none(kv4, big):
+    """cu_q that decreases, lies outside the rows or wraps in a difference: such requests
+    are left out, the others are computed."""
+    hkv, group, d, ps = 2, 4, 128, 64
+    m = 40 if big else 1
+    kv, ql = [300, 500, 90], [m, m, m]
+    pool, tables, cu, q = gref.make_case(6, kv, ql, hkv, group, d, ps)
+    cache = kv4.Cache(pool[None], hkv, d, ps)
+    far = 0x70000000
+    # requests 1 and 3 are rows [0, m) and [m, 2 m); around them [far, -far), [m, m) after a
+    # decrease, [2 m, far) and [far, wrapped)
+    bounds = [far, 0, m, m, 2 * m, far, -2 ** 31 + 16]
+    lens = [300, 300, 77, 500, 90, 90]
+    t6 = ints(np.stack([tables[0], tables[0], tables[1], tables[1], tables[2], tables[2]]))
+    batch = kv4.Batch(ints(bounds), ints(lens), t6, 3 * m, m, 500)
+    out = torch.full_like(q, 7.0)
+    ws = kv4.alloc_workspace(cache, batch, hkv * group)
+    kv4.moe_kv4_attention(q, cache, batch, out=out, workspace=ws)
+    want, _, spread, size = gref.attention(q, pool, tables, kv, cu, ps, ref.default_scale(d), only=[0, 1])
+    assert close(out[:2 * m], want[:2 * m], spread[:2 * m], size[:2 * m])
+    assert (out[2 * m:] == 7).all()
+    assert not ws[:kv4.MOE_KV4_WS_HEADER].any()
+
+
 # ------------------------------------------------ pages a window has left behind --
 @pytest.mark.parametrize("ps", [16, 32])
 @pytest.mark.parametrize("m,group", [(1, 4), (1, 16), (5, 4), (150, 4)])

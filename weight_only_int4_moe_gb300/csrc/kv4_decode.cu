@@ -157,8 +157,9 @@ MOE_DEV Request request_of(const KvAttnArgs &a, int q0, int q1, int len, int row
     const int start = a.window > 0 ? max(0, r.first - a.window + 1) : 0;
     r.tile0 = start / kTile;
     r.tiles = max(1, (r.end + kTile - 1) / kTile - r.tile0);
-    // (a row range outside the batch's tokens is no request)
-    const bool mine = r.m > 0 && q0 >= 0 && q1 <= a.batch.tokens && r.m * a.group >= a.rows_lo &&
+    // (a row range outside the batch's tokens is no request; compared before r.m is used,
+    // as the difference of two ints may wrap)
+    const bool mine = q0 >= 0 && q1 > q0 && q1 <= a.batch.tokens && r.m * a.group >= a.rows_lo &&
                       r.m * a.group <= a.rows_hi;
     r.row_tiles = mine ? (r.m * a.group + rows - 1) / rows : 0;
     return r;

@@ -111,13 +111,15 @@ struct Request {
 MOE_DEV Request request_of(const KvAttnArgs &a, int b) {
     Request r;
     r.q0 = a.batch.cu_q[b];
-    r.m = a.batch.cu_q[b + 1] - r.q0;
+    const int q1 = a.batch.cu_q[b + 1];
+    r.m = q1 - r.q0;
     const int len = a.batch.kv_len[b];
     r.first = len - r.m;
     r.end = (int)min((long long)min(len, kKvMaxLen), (long long)a.batch.stride * a.pool.ps);
     r.rows = r.m * a.group;
-    // (a row range outside the batch's tokens is no request)
-    const bool mine = r.m > 0 && r.q0 >= 0 && r.q0 + r.m <= a.batch.tokens && r.rows >= a.rows_lo &&
+    // (a row range outside the batch's tokens is no request; compared before r.m is used,
+    // as the difference of two ints may wrap)
+    const bool mine = r.q0 >= 0 && q1 > r.q0 && q1 <= a.batch.tokens && r.rows >= a.rows_lo &&
                       r.rows <= a.rows_hi;
     r.row_tiles = mine ? (r.rows + kRowsItem - 1) / kRowsItem : 0;
     return r;
