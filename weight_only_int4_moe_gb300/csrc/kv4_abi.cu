@@ -222,6 +222,8 @@ int moe_kv4_attention(const uint16_t *q, int64_t q_stride, int q_heads, const vo
     a.sl2 = std::fmax(std::fabs(a.scale_log2), 1e-30f);
     a.lag = 8.0f / a.sl2;
     a.far = 1048576.0f / a.sl2;
+    a.raise = 7.0f / a.sl2;
+    a.reach = 15.0f / a.sl2;
     a.q_heads = q_heads;
     a.group = q_heads / shape->kv_heads;
     a.gdiv.group = a.group;

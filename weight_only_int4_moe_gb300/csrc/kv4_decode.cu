@@ -431,7 +431,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
         const int open = min(rq.end, a.tree ? rq.first : rq.first + i_lo + 1);
         const int shut = a.window > 0 ? rq.first + i_hi - a.window + 1 : 0;
 
-        // lim: the score from which a row's maximum moves
+        // m: what a row's probabilities are relative to (see KvAttnArgs); lim: the score from
+        // which it moves
         float m[NT][2], lim[NT][2], l[NT][2], acc[NG][2][NT][4];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -532,8 +533,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
                     }
             }
             // Maximum and sum of each row (a column here: over the lanes g).  The maximum
-            // moves only when some score exceeds it by more than 2^8: the
-            // probabilities then stay below 2^15, inside fp16, and neither the
+            // moves only when some score exceeds it by more than 2^8: the probabilities,
+            // relative to m, 2^7 below it, then stay below 2^15, inside fp16, and neither the
             // exchange between the lanes nor the rescaling is paid for every tile.
             uint32_t pb[4][NT][2];
 #pragma unroll
@@ -553,10 +554,11 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
                         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
                         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
                         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-                        v = fmaxf(v, m[n][e]);
-                        const float r = v > m[n][e] ? kv_ex2((m[n][e] - v) * sl2) : 1.0f;
-                        m[n][e] = v;
-                        lim[n][e] = fabsf(v) > a.far ? v : v + a.lag;
+                        const bool up = v > lim[n][e], far = fabsf(v) > a.far;
+                        const float base = up ? (far ? v : v - a.raise) : m[n][e];
+                        const float r = up ? kv_ex2((m[n][e] - base) * sl2) : 1.0f;
+                        if (up) lim[n][e] = far ? v : v + a.lag;
+                        m[n][e] = base;
                         l[n][e] *= r;
 #pragma unroll
                         for (int G4 = 0; G4 < NG; ++G4)
@@ -564,8 +566,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
                             for (int c = 0; c < 2; ++c) acc[G4][c][n][e] *= r, acc[G4][c][n][2 + e] *= r;
                     }
                 }
-                float o0 = m[n][0] == -INFINITY ? 0.0f : fmaf(-m[n][0], sl2, kKvRaise);
-                float o1 = m[n][1] == -INFINITY ? 0.0f : fmaf(-m[n][1], sl2, kKvRaise);
+                float o0 = m[n][0] == -INFINITY ? 0.0f : -m[n][0] * sl2;
+                float o1 = m[n][1] == -INFINITY ? 0.0f : -m[n][1] * sl2;
                 if (fmaxf(fabsf(m[n][0]), fabsf(m[n][1])) > a.far) {
                     // the rounding of m * sl2 would be a power of two of its own: such rows
                     // subtract before the scale, and their maximum does not lag
@@ -573,7 +575,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
                     for (int e = 0; e < 2; ++e) {
                         const bool far = fabsf(m[n][e]) > a.far && m[n][e] > -INFINITY;
                         const float base = far ? m[n][e] : 0.0f;
-                        if (far) (e ? o1 : o0) = kKvRaise;
+                        if (far) (e ? o1 : o0) = 0.0f;
 #pragma unroll
                         for (int s = 0; s < 4; ++s) x[s][n][e] -= base, x[s][n][2 + e] -= base;
                     }
@@ -682,7 +684,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
                     }
                     if (a.lse && g == 0)
                         a.lse[o] = l[n][e] > 0.0f
-                                       ? (m[n][e] * sl2 + (log2f(l[n][e]) - kKvRaise)) * 0.6931471805599453f
+                                       ? (m[n][e] * sl2 + log2f(l[n][e])) * 0.6931471805599453f
                                        : -INFINITY;
                 }
         } else {
@@ -735,7 +737,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, 1)
         *reinterpret_cast<uint2 *>(a.out + o * D + 4 * d4) = make_uint2(
             *reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
         if (a.lse && d4 == 0)
-            a.lse[o] = ll > 0.0f ? (mm * sl2 + (log2f(ll) - kKvRaise)) * 0.6931471805599453f : -INFINITY;
+            a.lse[o] = ll > 0.0f ? (mm * sl2 + log2f(ll)) * 0.6931471805599453f : -INFINITY;
     };
     const int runs = n_runs;
     // a warp's share: two rows (D = 64: four) of one item at a time

@@ -40,13 +40,6 @@ struct alignas(16) KvConsts {
     uint32_t cm24 = 0xCE00CE00u;                          // fp16 pair (-24, -24)
 };
 
-// The probabilities are held as 2^7 times their value relative to the row's maximum, which
-// lags by up to 2^8: 2^15 at most, inside fp16.  Without the factor what lies 2^14 below
-// the maximum would lose bits and what lies 2^25 below would be lost, while the sum counts
-// it: in a long context with one strong token percents of the output.  It costs nothing
-// (it is the addend of the exponent's FMA) and cancels in the output; the lse takes it off.
-constexpr float kKvRaise = 7.0f;
-
 // The longest sequence that attention works on, in tokens: what it adds to and takes from
 // a token's index (tiles, windows, new tokens) then stays inside an int.
 constexpr int kKvMaxLen = INT32_MAX - (1 << 22);
@@ -69,10 +62,16 @@ struct KvAttnArgs {
     float *warp_slots, *cta_slots;
     uint32_t *err;
     bool beside;           // both kernels take part: the decode kernel runs beside the other
-    // scale_log2's magnitude (no less than 1e-30).  In units of q . k: how far a score may
-    // exceed the maximum that its row's probabilities are relative to (2^8), and from which
-    // magnitude on fp32 holds a score's power of two in steps of an eighth or more.
-    float sl2, lag, far;
+    // scale_log2's magnitude (no less than 1e-30), and in units of q . k:
+    //  raise: probabilities are relative to a number that lies 2^7 below the row's maximum
+    //    (where that was found; it may grow by up to `lag`, 2^8, before they are related to a
+    //    new one), so that they fill fp16 up to 2^15.  Relative to the maximum itself, what
+    //    lies 2^14 below would lose bits and what lies 2^25 below would be lost, while the
+    //    sum counts it: in a long context with one strong token percents of the output.
+    //  far: from this magnitude on fp32 holds a score's power of two in steps of an eighth
+    //    or more; such rows are related to the maximum itself.
+    //  reach: raise + lag.
+    float sl2, lag, far, raise, reach;
     // Debug-bounds builds: CTA 0 leaves a tile's copy out (decode kernel, its first warp), or
     // does not say that V's is unpacked (prefill kernel), so that a wait runs out.  -1: none.
     int skip_tile;

@@ -5,12 +5,12 @@
 // consecutive tokens), two tiles of 128 for tcgen05.mma, against tiles of 128
 // tokens.  Per tile of tokens and rows,
 //   S = Q K^T   (128 x 128 x D, both operands fp16 in shared memory)
-//   P = 2^(S - m + 7) in fp16, written over S in tensor memory
+//   P = 2^(S - m) in fp16, written over S in tensor memory
 //   O += P V    (128 x D x 128, P from tensor memory, V from shared memory)
-// with the running maximum m and the sum of a row in the one thread that owns the
-// row.  O is rescaled only when a row's maximum has grown by more than 2^8 since
-// its last rescale, a method known from published attention kernels (P then stays below
-// 2^15, inside fp16, and the quotient O / l does not depend on m).
+// with m, 2^7 below the row's running maximum, and the sum of a row in the two threads
+// that own the row.  O is rescaled only when a row's maximum has grown by more than 2^8
+// since its last rescale, a method known from published attention kernels (P then stays
+// below 2^15, inside fp16, and the quotient O / l does not depend on m).
 //
 // Roles of the 28 warps: two pairs of warpgroups each own one tile of rows, a thread
 // half of a row's columns (they load its Q, do the softmax, write the output; the
@@ -36,9 +36,9 @@
 // CTA to arrive, in list order.
 //
 // Measured: 4096 new tokens behind 4096 cached ones, 32 heads over 8 kv heads of 128:
-// 441 us, 935 TFLOP/s of the 1901 that a large bf16 product reaches; 10 verify streams of
-// up to 5000 tokens, up to 63 rows each: 51 us.  A tile of 256 rows and 128 tokens takes about
-// 5000 cycles, its MMAs alone 2520.  With the softmax's arithmetic, or the unpacking,
+// 428 us, 962 TFLOP/s of the 1901 that a large bf16 product reaches; 10 verify streams of
+// up to 5000 tokens, up to 63 rows each: 50 us.  A tile of 256 rows and 128 tokens takes about
+// 4900 cycles, its MMAs alone 2520.  With the softmax's arithmetic, or the unpacking,
 // taken out the first, then at 447 us, fell to 414 and to 383, without either to 350: what
 // remains is the round trip between the products and the softmax.  A whole tile's more
 // scores in flight would need tensor memory that is all in use (O 256 columns, S 256).
@@ -53,7 +53,7 @@ namespace moe {
 
 namespace {
 
-// A row's maximum before any score: finite, so that differences from it are numbers.
+// What a row is relative to before any score: finite, so that differences are numbers.
 constexpr float kLow = -3e38f;
 constexpr int kTok = 128;        // tokens of a unit
 // Units before an item's first tile that hold no work: what a new item costs (its
@@ -811,10 +811,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnAr
                     swap[128 * half] = now;
                     named_bar_sync(pair_bar, 64);
                     now = fmaxf(now, swap[128 * (half ^ 1)]);
-                    // the maximum moves when it has grown by more than 2^8; a run's first one
-                    // is taken as it is
-                    const bool grow = now - top > a.lag;
+                    // top: what the row's probabilities are relative to (see KvAttnArgs); it
+                    // moves when the maximum has grown by more than 2^8, and with a run's first
+                    const bool grow = now - top > a.reach;
                     if (__any_sync(0xffffffffu, grow)) {
+                        if (fabsf(now) <= a.far) now -= a.raise;
                         const float f = grow ? kv_ex2((top - now) * sl2) : 1.0f;
                         if (grow) top = now;
                         sum *= f;
@@ -829,14 +830,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnAr
                     ++pv;
                     // the difference first: the rounding of top * sl2, which one FMA behind the
                     // scale would need, is a power of two of its own for large scores
-                    // (ten of the prompt's 441 us)
-                    const uint64_t sc2 = pack2(sl2, sl2), top2 = pack2(-top, -top), raise2 = pack2(kKvRaise, kKvRaise);
+                    const uint64_t sc2 = pack2(sl2, sl2), top2 = pack2(-top, -top);
                     uint64_t sum2[2] = {pack2(sum, 0.0f), 0};
                     uint32_t p[16];
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {
                         float x, y;
-                        unpack2(fma2(add2(pack2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), top2), sc2, raise2), x, y);
+                        unpack2(fma2(add2(pack2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), top2), sc2, 0), x, y);
                         x = kv_ex2(x);
                         y = kv_ex2(y);
                         sum2[(e >> 1) & 1] = add2(sum2[(e >> 1) & 1], pack2(x, y));
@@ -961,7 +961,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnAr
                             slot[D] = top;
                             slot[D + 1] = sum;
                         } else if (a.lse) {
-                            a.lse[o_row] = sum > 0.0f ? (top * sl2 + (log2f(sum) - kKvRaise)) * 0.6931471805599453f
+                            a.lse[o_row] = sum > 0.0f ? (top * sl2 + log2f(sum)) * 0.6931471805599453f
                                                       : -INFINITY;
                         }
                     }
@@ -1120,7 +1120,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const KvAttnAr
                         make_uint2(*reinterpret_cast<const uint32_t *>(&x),
                                    *reinterpret_cast<const uint32_t *>(&y));
                     if (a.lse && d4 == 0)
-                        a.lse[o] = ll > 0.0f ? (mm * sl2 + (log2f(ll) - kKvRaise)) * 0.6931471805599453f : -INFINITY;
+                        a.lse[o] = ll > 0.0f ? (mm * sl2 + log2f(ll)) * 0.6931471805599453f : -INFINITY;
                 });
     }
 }
