@@ -622,7 +622,9 @@ MOE_DEV void fewer_regs() {
 }
 
 // A tile of up to 128 query rows, from row_base of the request on: 16-byte chunks,
-// converted to fp16 and swizzled, by 256 threads (id).
+// converted to fp16 and swizzled, by 256 threads (id).  (fp16, as both operands of a
+// product have one type and K's values are exact there: bf16's eight bits fit from 2^-14
+// up, smaller queries keep steps of 2^-24, larger ones than 65504 are reported.)
 template <int D>
 MOE_DEV void load_q(const KvAttnArgs &a, const Segment &sg, uint32_t dst, int row_base, int n_rows, int id) {
     bool bad = false;
