@@ -10,12 +10,10 @@
 
 using namespace moe;
 
-namespace {
-
-inline bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
+namespace moe {
 
 // SM count of the current device, MOE_ERR_UNSUPPORTED unless it is sm_103.
-int device_info(int *sms) {
+int device_sms(int *sms) {
     static std::atomic<int> known[64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
@@ -32,6 +30,12 @@ int device_info(int *sms) {
     if (dev >= 0 && dev < 64) known[dev].store(*sms, std::memory_order_relaxed);
     return MOE_OK;
 }
+
+}  // namespace moe
+
+namespace {
+
+inline bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
 
 bool shape_ok(const moe_kv4_shape *s) {
     return s->layers >= 1 && s->layers <= 1024 && s->n_pages >= 1 && s->n_pages <= (1 << 20) &&
@@ -134,7 +138,7 @@ int moe_kv4_append(const uint16_t *q, int64_t q_stride, const uint16_t *k, int64
         !aligned16(k_weight) || !aligned16(cos) || !aligned16(sin) || !aligned16(q_out))
         return MOE_ERR_ALIGN;
     int sms;
-    rc = device_info(&sms);
+    rc = device_sms(&sms);
     if (rc != MOE_OK) return rc;
     KvAppendArgs a{};
     a.q = q;
@@ -169,7 +173,7 @@ int moe_kv4_read(const void *pages, int layer, const moe_kv4_shape *shape,
     if (!k_out && !v_out) return MOE_OK;
     if (!aligned16(k_out) || !aligned16(v_out)) return MOE_ERR_ALIGN;
     int sms;
-    rc = device_info(&sms);
+    rc = device_sms(&sms);
     if (rc != MOE_OK) return rc;
     KvReadArgs a{};
     a.pool = pool_of(pages, layer, shape);
@@ -208,7 +212,7 @@ int moe_kv4_attention(const uint16_t *q, int64_t q_stride, int q_heads, const vo
         ((uintptr_t)tree & 7u))
         return MOE_ERR_ALIGN;
     int sms;
-    rc = device_info(&sms);
+    rc = device_sms(&sms);
     if (rc != MOE_OK) return rc;
     KvAttnArgs a{};
     a.q = q;
@@ -287,7 +291,7 @@ static int take(void *pages, const moe_kv4_shape *shape, const moe_kv4_seqs *seq
     if (scratch_bytes < moe_kv4_scratch_bytes(shape, n)) return MOE_ERR_WORKSPACE;
     if (!aligned16(pages) || !aligned16(scratch)) return MOE_ERR_ALIGN;
     int sms;
-    rc = device_info(&sms);
+    rc = device_sms(&sms);
     if (rc != MOE_OK) return rc;
     return done(
         launch_kv4_take(pages_of(pages, shape), *seqs, a, b, fork, n, scratch, err, str(stream)));
@@ -312,7 +316,7 @@ int moe_kv4_free(const moe_kv4_shape *shape, const moe_kv4_seqs *seqs, const int
     if (n == 0) return MOE_OK;
     if (!ids) return MOE_ERR_NULL;
     int sms;
-    rc = device_info(&sms);
+    rc = device_sms(&sms);
     if (rc != MOE_OK) return rc;
     return done(launch_kv4_free(pages_of(nullptr, shape), *seqs, ids, n, err, str(stream)));
 }
@@ -326,7 +330,7 @@ int moe_kv4_compact(void *pages, const moe_kv4_shape *shape, const moe_kv4_seqs 
     if (scratch_bytes < moe_kv4_scratch_bytes(shape, 0)) return MOE_ERR_WORKSPACE;
     if (!aligned16(pages) || !aligned16(scratch)) return MOE_ERR_ALIGN;
     int sms;
-    rc = device_info(&sms);
+    rc = device_sms(&sms);
     if (rc != MOE_OK) return rc;
     return done(launch_kv4_compact(pages_of(pages, shape), *seqs, tables_out, refs_out, n_used,
                                    scratch, err, sms, str(stream)));
@@ -340,7 +344,7 @@ int moe_kv4_copy_pages(void *pages, const moe_kv4_shape *shape, const int32_t *s
     if (!pages || !src || !dst) return MOE_ERR_NULL;
     if (!aligned16(pages)) return MOE_ERR_ALIGN;
     int sms;
-    const int rc = device_info(&sms);
+    const int rc = device_sms(&sms);
     if (rc != MOE_OK) return rc;
     return done(launch_kv4_copy(pages_of(pages, shape), src, dst, n, err, sms, str(stream)));
 }

@@ -1,0 +1,258 @@
+"""Thin Python binding of the operators between attention and experts
+(``include/moe_layer.h``): the residual's addition with the norm, matrix products with
+their epilogue, and the routing to experts.  Argument checks and marshalling only; the
+work is done by the CUDA library that ``ops`` loads, and calls raise where that is
+missing.
+
+Calls run on `stream`, or on the current one.  Outputs that are not given are made on
+that stream; the caller orders its own tensors, and reads of the results, with it.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import NamedTuple
+
+import torch
+
+from . import ops
+from .kv4 import _empty, _on, _raw_stream
+
+MOE_T_BF16 = 0
+MOE_T_F32 = 1
+MOE_T_F16 = 2
+MOE_T_E4M3 = 3
+ACTIVATIONS = {"none": 0, None: 0, "relu": 1, "silu": 2, "gelu": 3}
+SCORES = {"softmax": 0, "sigmoid": 1}
+
+EXPORTED = ["moe_add_norm", "moe_linear", "moe_route_experts"]
+
+_TYPES = {torch.bfloat16: MOE_T_BF16, torch.float32: MOE_T_F32, torch.float16: MOE_T_F16}
+_OPERANDS = {torch.bfloat16: MOE_T_BF16, torch.float16: MOE_T_F16,
+             torch.float8_e4m3fn: MOE_T_E4M3}
+_F32, _I32, _E4M3 = torch.float32, torch.int32, torch.float8_e4m3fn
+_lib = None
+
+
+def load_library():
+    """The CUDA library with this module's signatures declared."""
+    global _lib
+    if _lib is None:
+        lib = ops.load_library()
+        p, i, i64, f = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float
+        sig = {
+            "moe_add_norm": ([p, i, i64, p, i, i64, p, i, f, i, i, p, i64, p, i, i64, p, i64, p, p], i),
+            "moe_linear": ([p, i64, p, p, i64, p, i, p, i, p, i, i64, p, i, i64, p, i, i64, i, i, i, p,
+                            p], i),
+            "moe_route_experts": ([p, i, i64, p, i, i, i, i, i, i, i, i, f, p, p, p], i),
+        }
+        for name, (args, res) in sig.items():
+            fn = getattr(lib, name)
+            fn.argtypes = args
+            fn.restype = res
+        _lib = lib
+    return _lib
+
+
+# The checks below run before every launch and are kept short: a single-token step is
+# bound by what the host does per call.
+def _device_of(t, what):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{what}: expected a CUDA tensor")
+    return t.get_device()
+
+
+def _matrix(t, what, index, shape, types):
+    """(pointer, type, row stride) of a matrix whose rows are contiguous."""
+    kind = types.get(t.dtype)
+    if kind is None:
+        raise TypeError(f"{what}: {t.dtype} is not supported")
+    if t.get_device() != index:
+        raise ValueError(f"{what}: expected a tensor on cuda:{index}")
+    if t.shape != shape:
+        raise ValueError(f"{what}: expected {tuple(shape)}, got {tuple(t.shape)}")
+    rows, cols = t.stride()
+    if cols != 1 and shape[1] > 1 and shape[0]:
+        raise ValueError(f"{what}: the elements of a row must be contiguous")
+    # (torch may say any stride for a single row; empty matrices have no rows to step)
+    return t.data_ptr(), kind, rows if shape[0] > 1 else shape[1]
+
+
+def _vector(t, what, index, n, dtype=_F32):
+    if t.dtype is not dtype or t.shape != (n,):
+        raise ValueError(f"{what}: expected {dtype} [{n}], got {t.dtype} {tuple(t.shape)}")
+    if t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{what}: expected a contiguous tensor on cuda:{index}")
+    return t.data_ptr()
+
+
+class Normed(NamedTuple):
+    """What moe_add_norm returns; None for what was not asked for."""
+    out: torch.Tensor | None
+    residual: torch.Tensor | None
+    codes: torch.Tensor | None
+    scales: torch.Tensor | None
+
+
+def moe_add_norm(x, weight=None, residual=None, eps: float = 1e-6, out_dtype=torch.bfloat16,
+                 codes: bool | torch.Tensor = False, out=None, residual_out=None, scales=None,
+                 stream=None) -> Normed:
+    """The root-mean-square norm of h = x + residual over the last axis of x [rows,
+    hidden] (bf16, fp16 or fp32), times weight [hidden].  h is rounded to the residual's
+    type and returned as `residual` (residual_out may be the residual itself).  `out` is
+    of out_dtype (None, with no out given: not wanted).  codes=True (or an e4m3 tensor):
+    also e4m3 `codes` with a scale for each row, `scales` fp32 [rows]."""
+    dev = _device_of(x, "x")
+    if x.dim() != 2:
+        raise ValueError(f"x: expected [rows, hidden], got {tuple(x.shape)}")
+    shape = x.shape
+    rows, hidden = shape
+    xp, xt, xs = _matrix(x, "x", dev, shape, _TYPES)
+    rp, rt, rs, np_, ns = None, 0, 0, None, 0
+    if residual is not None:
+        rp, rt, rs = _matrix(residual, "residual", dev, shape, _TYPES)
+        if residual_out is None:
+            residual_out = _empty(shape, residual.dtype, residual.device, stream)
+        elif residual_out.dtype is not residual.dtype:
+            raise TypeError(f"residual_out: expected {residual.dtype}, got {residual_out.dtype}")
+        np_, _, ns = _matrix(residual_out, "residual_out", dev, shape, _TYPES)
+    elif residual_out is not None:
+        raise ValueError("residual_out: there is no residual")
+    wp, wt = None, 0
+    if weight is not None:
+        wt = _TYPES.get(weight.dtype)
+        if wt is None:
+            raise TypeError(f"weight: {weight.dtype} is not supported")
+        wp = _vector(weight, "weight", dev, hidden, weight.dtype)
+    op, ot, os = None, 0, 0
+    if out is None and out_dtype is not None:
+        if out_dtype not in _TYPES:
+            raise TypeError(f"out_dtype: {out_dtype} is not supported")
+        out = _empty(shape, out_dtype, x.device, stream)
+    if out is not None:
+        op, ot, os = _matrix(out, "out", dev, shape, _TYPES)
+    cp, cs, sp = None, 0, None
+    if codes is not False and codes is not None:
+        if codes is True:
+            codes = _empty(shape, _E4M3, x.device, stream)
+        cp, _, cs = _matrix(codes, "codes", dev, shape, {_E4M3: 0})
+        if scales is None:
+            scales = _empty((rows,), _F32, x.device, stream)
+        sp = _vector(scales, "scales", dev, rows)
+    elif scales is not None:
+        raise ValueError("scales: there are no codes")
+    else:
+        codes = None
+    with _on(dev):
+        rc = (_lib or load_library()).moe_add_norm(
+            xp, xt, xs, rp, rt, rs, wp, wt, eps, rows, hidden, np_, ns, op, ot, os, cp, cs, sp,
+            _raw_stream(stream, dev))
+    if rc:
+        ops._check(rc, "moe_add_norm")
+    return Normed(out, residual_out, codes, scales)
+
+
+class Linear:
+    """The weights of a product, built once: weight [N, K] in bf16, fp16 or e4m3 codes
+    (rows contiguous, beginning at multiples of 16 bytes), bias [N] (kept in fp32) and, for
+    codes, scale fp32 [N].  ``errors`` reads the device error word of its calls."""
+
+    def __init__(self, weight: torch.Tensor, bias=None, scale=None):
+        dev = _device_of(weight, "weight")
+        if weight.dim() != 2:
+            raise ValueError(f"weight: expected [N, K], got {tuple(weight.shape)}")
+        self.weight, self.index, self.device = weight, dev, weight.device
+        self.N, self.K = weight.shape
+        self.ptr, self.type, self.stride = _matrix(weight, "weight", dev, weight.shape, _OPERANDS)
+        self.dtype = weight.dtype
+        self.scale, self.scale_ptr, self.bias, self.bias_ptr = scale, None, None, None
+        if scale is not None:
+            self.scale_ptr = _vector(scale, "scale", dev, self.N)
+        if bias is not None:
+            if bias.dtype not in _TYPES:
+                raise TypeError(f"bias: {bias.dtype} is not supported")
+            self.bias = bias.float().contiguous()
+            self.bias_ptr = _vector(self.bias, "bias", dev, self.N)
+        if self.ptr % 16 or (self.N > 1 and self.stride * weight.element_size() % 16):
+            raise ValueError("weight: rows must begin at multiples of 16 bytes")
+        self.err = torch.zeros(1, dtype=_I32, device=weight.device)
+        self.err_ptr = self.err.data_ptr()
+
+    def errors(self) -> int:
+        """The device error flags accumulated so far; waits for the device."""
+        torch.cuda.synchronize(self.device)
+        return int(self.err.item()) & 0xFFFFFFFF
+
+    def clear_errors(self):
+        self.err.zero_()
+
+
+def moe_linear(x, linear: Linear, activation=None, gate=None, residual=None, x_scale=None,
+               out=None, out_dtype=torch.bfloat16, stream=None) -> torch.Tensor:
+    """activation(x weight^T [* x_scale * scale] + bias) * gate + residual, [M, N] of
+    out's type or out_dtype (bf16, fp16 or fp32), summed in fp32 and rounded once.  x
+    [M, K] has the weight's type; x_scale fp32 [M] (for codes).  gate and residual
+    [M, N] are bf16, fp16 or fp32; out may be either of them.  activation: "relu",
+    "silu", "gelu" or None."""
+    dev = linear.index
+    if x.dim() != 2:
+        raise ValueError(f"x: expected [M, {linear.K}], got {tuple(x.shape)}")
+    if x.dtype is not linear.dtype:
+        raise TypeError(f"x: expected {linear.dtype}, got {x.dtype}")
+    m = x.shape[0]
+    act = ACTIVATIONS.get(activation)
+    if act is None:
+        raise ValueError(f"activation: {activation!r} is not one of {list(ACTIVATIONS)}")
+    xp, _, xs = _matrix(x, "x", dev, (m, linear.K), _OPERANDS)
+    shape = (m, linear.N)
+    sp = None if x_scale is None else _vector(x_scale, "x_scale", dev, m)
+    gp, gt, gs = (None, 0, 0) if gate is None else _matrix(gate, "gate", dev, shape, _TYPES)
+    rp, rt, rs = (None, 0, 0) if residual is None else \
+        _matrix(residual, "residual", dev, shape, _TYPES)
+    if out is None:
+        if out_dtype not in _TYPES:
+            raise TypeError(f"out_dtype: {out_dtype} is not supported")
+        out = _empty(shape, out_dtype, linear.device, stream)
+    op, ot, os = _matrix(out, "out", dev, shape, _TYPES)
+    with _on(dev):
+        rc = (_lib or load_library()).moe_linear(
+            xp, xs, sp, linear.ptr, linear.stride, linear.scale_ptr, linear.type, linear.bias_ptr,
+            act, gp, gt, gs, rp, rt, rs, op, ot, os, m, linear.N, linear.K, linear.err_ptr,
+            _raw_stream(stream, dev))
+    if rc:
+        ops._check(rc, "moe_linear")
+    return out
+
+
+def moe_route_experts(logits, top_k: int, scoring: str = "softmax", bias=None, groups: int = 1,
+                      top_groups: int | None = None, group_best: int = 2, renormalize: bool = True,
+                      scale: float = 1.0, topk_ids=None, topk_weights=None, stream=None):
+    """(topk_ids int32 [M, top_k], topk_weights fp32 [M, top_k]) from router logits
+    [M, E] (fp32, bf16 or fp16): the experts with the largest score + bias among the
+    top_groups best groups (all by default), and their scores, renormalised to their sum,
+    times scale.  scoring: "softmax" or "sigmoid".  group_best: groups compare by their
+    best expert (1) or the sum of their two best (2)."""
+    dev = _device_of(logits, "logits")
+    if logits.dim() != 2:
+        raise ValueError(f"logits: expected [M, E], got {tuple(logits.shape)}")
+    m, e = shape = logits.shape
+    kind = SCORES.get(scoring)
+    if kind is None:
+        raise ValueError(f"scoring: {scoring!r} is not one of {list(SCORES)}")
+    lp, lt, ls = _matrix(logits, "logits", dev, shape, _TYPES)
+    bp = None if bias is None else _vector(bias, "bias", dev, e)
+    if topk_ids is None:
+        topk_ids = _empty((m, top_k), _I32, logits.device, stream)
+    if topk_weights is None:
+        topk_weights = _empty((m, top_k), _F32, logits.device, stream)
+    for t, what, dtype in ((topk_ids, "topk_ids", _I32), (topk_weights, "topk_weights", _F32)):
+        if t.dtype is not dtype or t.shape != (m, top_k) or t.get_device() != dev or \
+                not t.is_contiguous():
+            raise ValueError(f"{what}: expected a contiguous {dtype} [{m}, {top_k}] on cuda:{dev}")
+    with _on(dev):
+        rc = (_lib or load_library()).moe_route_experts(
+            lp, lt, ls, bp, m, e, top_k, kind, groups, groups if top_groups is None else top_groups,
+            group_best, 1 if renormalize else 0, scale, topk_ids.data_ptr(),
+            topk_weights.data_ptr(), _raw_stream(stream, dev))
+    if rc:
+        ops._check(rc, "moe_route_experts")
+    return topk_ids, topk_weights
