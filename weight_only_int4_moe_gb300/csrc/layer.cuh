@@ -51,6 +51,7 @@ struct LinearArgs {
     MatIn gate, residual;
     MatOut out;
     uint32_t *err;
+    bool vec_gate, vec_residual, vec_out;  // four neighbours of a row may be one access
 };
 
 struct RouteExpertsArgs {
@@ -66,7 +67,7 @@ struct RouteExpertsArgs {
 
 cudaError_t launch_add_norm(const AddNormArgs &a, cudaStream_t s);
 // cudaErrorNotSupported: the operands' tensor maps could not be made.
-cudaError_t launch_linear(const LinearArgs &a, const void *x, int64_t x_stride, const void *w,
+cudaError_t launch_linear(LinearArgs a, const void *x, int64_t x_stride, const void *w,
                           int64_t w_stride, int sms, cudaStream_t s);
 cudaError_t launch_route_experts(const RouteExpertsArgs &a, int sms, cudaStream_t s);
 

@@ -1,15 +1,18 @@
 // Matrix products with an epilogue (moe_linear):
 //   out[m][n] = act(sum_k x[m][k] w[n][k] * sx[m] * sw[n] + bias[n]) * gate[m][n] + residual[m][n]
 //
-// The tensor cores' M side (128 lanes of tensor memory) takes 128 rows of w, their N side TN
+// The tensor cores' M side (the 128 lanes of tensor memory) takes rows of w, their N side TN
 // rows of x: a few tokens then waste little, and a warp's 32 lanes hold 32 neighbouring
 // columns of one output row, so that the epilogue reads and writes whole sectors without a
 // detour through shared memory, whatever the matrices' strides.  Both operands come by TMA in
 // stages of 128 bytes of k (64 two-byte elements or 128 codes); what lies outside a matrix is
 // filled with zeros.
 //
-// One tile a cluster.  Where there are too few tiles for the GPU, the blocks of a cluster share
-// a tile's k and add their parts up through distributed shared memory, in the order of the
+// Two kernels.  Where the tiles fill the GPU, linear_pair_kernel: two blocks work on one tile
+// of 256 rows of w by TN of x, each holding its half of either operand, and walk over tiles
+// with the sums in two buffers, so that the epilogue of a tile runs under the products of the
+// next.  Otherwise linear_split_kernel: one tile of 128 by TN a cluster, whose blocks share the
+// tile's k and add their parts up through distributed shared memory, in the order of the
 // blocks: no workspace, and the same bits every time.
 #include <atomic>
 
@@ -19,19 +22,11 @@ namespace moe {
 
 namespace {
 
-constexpr int kRowsW = 128;                 // rows of w of a tile
+constexpr int kRowsW = 128;                 // rows of w of a block's tile
 constexpr int kLine = 128;                  // bytes of k of a stage
 constexpr int kBytesW = kRowsW * kLine;
-constexpr int kThreads = 192;               // warps 0-3 epilogue, 4 copies, 5 products
-
-template <int TN>
-struct Tile {
-    static constexpr int kStage = kBytesW + TN * kLine;
-    static constexpr int kStages = TN >= 128 ? 4 : 5;
-    static constexpr int kSmem = kStages * kStage + 1024;  // (stages begin at multiples of 1024)
-    static constexpr uint32_t kCols = TN < 32 ? 32 : TN;   // of tensor memory
-    static_assert(TN * kRowsW * 4 <= kStages * kStage, "the parts lie where the stages were");
-};
+constexpr int kThreads = 320;               // warps 0-7 epilogue, 8 copies, 9 products
+constexpr int kEpilogue = 8;                // warps
 
 MOE_DEV uint32_t cluster_rank() {
     uint32_t r;
@@ -53,72 +48,178 @@ MOE_DEV uint32_t map_to(uint32_t addr, uint32_t rank) {
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
     return r;
 }
-MOE_DEV float ld_cluster(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+MOE_DEV float4 ld_cluster4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
     return v;
 }
+MOE_DEV void arrive_at(uint32_t addr) {  // (an address of map_to)
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
 
-// Instruction descriptor: fp32 sums, both operands K-major, 128 rows by n.
-MOE_DEV uint32_t idesc_of(int type, uint32_t n) {
+// Instruction descriptor: fp32 sums, both operands K-major, m rows by n.
+MOE_DEV uint32_t idesc_of(int type, uint32_t m, uint32_t n) {
     const uint32_t f = type == MOE_T_BF16 ? 1u : 0u;  // kind::f16: 1 bf16, 0 f16; f8f6f4: 0 e4m3
-    return (1u << 4) | (f << 7) | (f << 10) | ((n >> 3) << 17) | ((128u >> 4) << 24);
+    return (1u << 4) | (f << 7) | (f << 10) | ((n >> 3) << 17) | ((m >> 4) << 24);
 }
 
 // The four products of a stage (32 bytes of k each) from one elected thread, then the commit
-// that hands the stage back.
-template <bool CODES>
-MOE_DEV void mma_stage(uint32_t d, uint64_t wd, uint64_t xd, uint32_t idesc, uint32_t accumulate,
-                       uint32_t bar) {
-#define MOE_MMA4(KIND)                                                                     \
+// that hands the stage back: to this block, or for a pair to both.
+#define MOE_MMA4(GROUP, KIND, COMMIT)                                                      \
     asm volatile(                                                                          \
-        "{\n\t.reg .pred p, t, e;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"                \
+        "{\n\t.reg .pred p, t, e;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t.reg .b16 both;\n\t" \
         "setp.ne.b32 p, %4, 0;\n\t"                                                        \
         "setp.eq.b32 t, %4, %4;\n\t"                                                       \
+        "mov.b16 both, 3;\n\t"                                                             \
         "add.u64 a1, %1, 2;\n\tadd.u64 a2, %1, 4;\n\tadd.u64 a3, %1, 6;\n\t"               \
         "add.u64 b1, %2, 2;\n\tadd.u64 b2, %2, 4;\n\tadd.u64 b3, %2, 6;\n\t"               \
         "elect.sync _|e, 0xffffffff;\n\t"                                                  \
-        "@e tcgen05.mma.cta_group::1.kind::" KIND " [%0], %1, %2, %3, p;\n\t"              \
-        "@e tcgen05.mma.cta_group::1.kind::" KIND " [%0], a1, b1, %3, t;\n\t"              \
-        "@e tcgen05.mma.cta_group::1.kind::" KIND " [%0], a2, b2, %3, t;\n\t"              \
-        "@e tcgen05.mma.cta_group::1.kind::" KIND " [%0], a3, b3, %3, t;\n\t"              \
-        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5];\n\t}" ::"r"( \
-            d),                                                                            \
+        "@e tcgen05.mma.cta_group::" GROUP ".kind::" KIND " [%0], %1, %2, %3, p;\n\t"      \
+        "@e tcgen05.mma.cta_group::" GROUP ".kind::" KIND " [%0], a1, b1, %3, t;\n\t"      \
+        "@e tcgen05.mma.cta_group::" GROUP ".kind::" KIND " [%0], a2, b2, %3, t;\n\t"      \
+        "@e tcgen05.mma.cta_group::" GROUP ".kind::" KIND " [%0], a3, b3, %3, t;\n\t"      \
+        "@e tcgen05.commit.cta_group::" GROUP COMMIT ";\n\t}" ::"r"(d),                    \
         "l"(wd), "l"(xd), "r"(idesc), "r"(accumulate), "r"(bar)                            \
         : "memory")
-    if constexpr (CODES)
-        MOE_MMA4("f8f6f4");
+#define MOE_COMMIT_ONE ".mbarrier::arrive::one.shared::cluster.b64 [%5]"
+#define MOE_COMMIT_BOTH ".mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%5], both"
+template <bool CODES, bool PAIR>
+MOE_DEV void mma_stage(uint32_t d, uint64_t wd, uint64_t xd, uint32_t idesc, uint32_t accumulate,
+                       uint32_t bar) {
+    if constexpr (PAIR && CODES)
+        MOE_MMA4("2", "f8f6f4", MOE_COMMIT_BOTH);
+    else if constexpr (PAIR)
+        MOE_MMA4("2", "f16", MOE_COMMIT_BOTH);
+    else if constexpr (CODES)
+        MOE_MMA4("1", "f8f6f4", MOE_COMMIT_ONE);
     else
-        MOE_MMA4("f16");
+        MOE_MMA4("1", "f16", MOE_COMMIT_ONE);
+}
 #undef MOE_MMA4
+#undef MOE_COMMIT_ONE
+#undef MOE_COMMIT_BOTH
+// Arrives on both blocks' barrier once the products issued so far are done.
+MOE_DEV void commit_both(uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t.reg .b16 both;\n\tmov.b16 both, 3;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+        "[%0], both;\n\t}" ::"r"(bar)
+        : "memory");
+}
+
+// Tensor memory -> registers: issued, and waited for with the registers as operands, so that
+// no use of them moves ahead of the wait.
+template <int C>
+struct Cols {
+    uint32_t r[C];
+    MOE_DEV void issue(uint32_t taddr) {
+        static_assert(C == 16 || C == 32, "");
+        if constexpr (C == 16)
+            asm volatile(
+                "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+                "%11, %12, %13, %14, %15}, [%16];"
+                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+                  "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+                  "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                : "r"(taddr)
+                : "memory");
+        else
+            asm volatile(
+                "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+                "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
+                "%28, %29, %30, %31}, [%32];"
+                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+                  "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+                  "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+                  "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+                  "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
+                  "=r"(r[31])
+                : "r"(taddr)
+                : "memory");
+    }
+    MOE_DEV void wait() {
+        asm volatile("tcgen05.wait::ld.sync.aligned;"
+                     : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                       "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                       "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                     :
+                     : "memory");
+        if constexpr (C == 32)
+            asm volatile(""
+                         : "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]),
+                           "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]),
+                           "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]),
+                           "+r"(r[31])
+                         :
+                         : "memory");
+    }
+};
+
+// --------------------------------------------------------------- epilogue --
+MOE_DEV float from_bits16(uint32_t v, int type) {
+    return type == MOE_T_BF16 ? __uint_as_float(v << 16) : __half2float(__ushort_as_half((uint16_t)v));
 }
 
 template <int C>
-MOE_DEV void load_column(const MatIn &s, int m, int n, int cols, float (&f)[C]) {
-    const int64_t at = (int64_t)m * s.stride + n;
-    if (s.type == MOE_T_F32) {
-        const float *p = reinterpret_cast<const float *>(s.p) + at;
+MOE_DEV void activate(int act, float (&v)[C]) {
+    if (act == MOE_ACT_RELU) {
 #pragma unroll
-        for (int j = 0; j < C; ++j) f[j] = j < cols ? p[j * s.stride] : 0.0f;
-    } else {
-        const uint16_t *p = reinterpret_cast<const uint16_t *>(s.p) + at;
-        uint16_t v[C];
+        for (int j = 0; j < C; ++j) v[j] = v[j] < 0.0f ? 0.0f : v[j];
+    } else if (act == MOE_ACT_SILU) {
 #pragma unroll
-        for (int j = 0; j < C; ++j) v[j] = j < cols ? p[j * s.stride] : (uint16_t)0;
-        if (s.type == MOE_T_BF16) {
+        for (int j = 0; j < C; ++j) v[j] = v[j] / (1.0f + expf(-v[j]));
+    } else if (act == MOE_ACT_GELU) {
 #pragma unroll
-            for (int j = 0; j < C; ++j) f[j] = __uint_as_float((uint32_t)v[j] << 16);
-        } else {
-#pragma unroll
-            for (int j = 0; j < C; ++j) f[j] = __half2float(__ushort_as_half(v[j]));
-        }
+        for (int j = 0; j < C; ++j) v[j] = 0.5f * v[j] * (1.0f + erff(v[j] * 0.7071067811865476f));
     }
 }
 
-// The epilogue of C neighbouring output rows m.. (cols of them exist) in column n.
+// C elements of a column of a matrix, as they lie in memory (`cols` of them exist).
 template <int C>
-MOE_DEV void finish(const LinearArgs &a, int m, int n, int cols, float (&v)[C], float sw,
-                    float bias) {
+struct Column {
+    uint32_t r[C];
+    MOE_DEV void load(const MatIn &s, int m, int n, int cols) {
+        const int64_t at = (int64_t)m * s.stride + n;
+        if (s.type == MOE_T_F32) {
+            const uint32_t *p = reinterpret_cast<const uint32_t *>(s.p) + at;
+#pragma unroll
+            for (int j = 0; j < C; ++j) r[j] = j < cols ? p[j * s.stride] : 0u;
+        } else {
+            const uint16_t *p = reinterpret_cast<const uint16_t *>(s.p) + at;
+#pragma unroll
+            for (int j = 0; j < C; ++j) r[j] = j < cols ? p[j * s.stride] : 0u;
+        }
+    }
+    MOE_DEV void get(int type, float (&f)[C]) const {
+        if (type == MOE_T_F32) {
+#pragma unroll
+            for (int j = 0; j < C; ++j) f[j] = __uint_as_float(r[j]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < C; ++j) f[j] = from_bits16(r[j], type);
+        }
+    }
+};
+
+// Column n of C output rows m.. (cols of them exist), from this thread's lane of tensor memory.
+// The other operands are asked for before the sums are waited for.
+template <int C>
+MOE_DEV void column_out(const LinearArgs &a, uint32_t taddr, int m, int n, int cols, bool mine,
+                        float sw, float bias) {
+    Cols<C> acc;
+    acc.issue(taddr);
+    Column<C> gate, residual;
+    if (a.gate.p && mine) gate.load(a.gate, m, n, cols);
+    if (a.residual.p && mine) residual.load(a.residual, m, n, cols);
+    acc.wait();
+    if (!mine) return;
+    float v[C], f[C];
+#pragma unroll
+    for (int j = 0; j < C; ++j) v[j] = __uint_as_float(acc.r[j]);
     if (a.x_scale) {
 #pragma unroll
         for (int j = 0; j < C; ++j)
@@ -126,24 +227,14 @@ MOE_DEV void finish(const LinearArgs &a, int m, int n, int cols, float (&v)[C], 
     }
 #pragma unroll
     for (int j = 0; j < C; ++j) v[j] = v[j] * sw + bias;
-    if (a.activation == MOE_ACT_RELU) {
-#pragma unroll
-        for (int j = 0; j < C; ++j) v[j] = v[j] < 0.0f ? 0.0f : v[j];
-    } else if (a.activation == MOE_ACT_SILU) {
-#pragma unroll
-        for (int j = 0; j < C; ++j) v[j] = v[j] / (1.0f + expf(-v[j]));
-    } else if (a.activation == MOE_ACT_GELU) {
-#pragma unroll
-        for (int j = 0; j < C; ++j) v[j] = 0.5f * v[j] * (1.0f + erff(v[j] * 0.7071067811865476f));
-    }
-    float f[C];
+    activate<C>(a.activation, v);
     if (a.gate.p) {
-        load_column<C>(a.gate, m, n, cols, f);
+        gate.get(a.gate.type, f);
 #pragma unroll
         for (int j = 0; j < C; ++j) v[j] *= f[j];
     }
     if (a.residual.p) {
-        load_column<C>(a.residual, m, n, cols, f);
+        residual.get(a.residual.type, f);
 #pragma unroll
         for (int j = 0; j < C; ++j) v[j] += f[j];
     }
@@ -161,11 +252,109 @@ MOE_DEV void finish(const LinearArgs &a, int m, int n, int cols, float (&v)[C], 
     }
 }
 
+// A block's whole tile, 128 columns from n0 by `rows` output rows from m0: each warp the lanes
+// it can reach and every other run of C rows.
+template <int TN>
+MOE_DEV void tile_out(const LinearArgs &a, uint32_t tmem, int m0, int n0, int rows, int w, int lane) {
+    constexpr int C = TN >= 64 ? 32 : 16;
+    const int n = n0 + (w & 3) * 32 + lane;
+    const bool mine = n < a.N;
+    const float sw = mine && a.w_scale ? a.w_scale[n] : 1.0f;
+    const float bias = mine && a.bias ? a.bias[n] : 0.0f;
+    const uint32_t lanes = tmem + ((uint32_t)(w & 3) << 21);
+#pragma unroll 1
+    for (int c = (w >> 2) * C; c < rows; c += 2 * C)
+        column_out<C>(a, lanes + c, m0 + c, n, min(C, rows - c), mine, sw, bias);
+}
+
+// Four neighbours of a row, n..n+3 (those below N exist).
+struct Quad {
+    uint32_t r[4];
+    MOE_DEV void load(const MatIn &s, bool vec, int m, int n, int N) {
+        const int64_t at = (int64_t)m * s.stride + n;
+        if (s.type == MOE_T_F32) {
+            const uint32_t *p = reinterpret_cast<const uint32_t *>(s.p) + at;
+            if (vec && n + 3 < N) {
+                const uint4 v = *reinterpret_cast<const uint4 *>(p);
+                r[0] = v.x, r[1] = v.y, r[2] = v.z, r[3] = v.w;
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) r[j] = n + j < N ? p[j] : 0u;
+            }
+        } else {
+            const uint16_t *p = reinterpret_cast<const uint16_t *>(s.p) + at;
+            if (vec && n + 3 < N) {
+                const uint2 v = *reinterpret_cast<const uint2 *>(p);
+                r[0] = v.x & 0xFFFFu, r[1] = v.x >> 16, r[2] = v.y & 0xFFFFu, r[3] = v.y >> 16;
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) r[j] = n + j < N ? p[j] : 0u;
+            }
+        }
+    }
+    MOE_DEV void get(int type, float (&f)[4]) const {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            f[j] = type == MOE_T_F32 ? __uint_as_float(r[j]) : from_bits16(r[j], type);
+    }
+};
+
+MOE_DEV void quad_out(const LinearArgs &a, int m, int n, float (&v)[4], const float (&sw)[4],
+                      const float (&bias)[4], const Quad &gate, const Quad &residual, float sx) {
+    float f[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = v[j] * sx * sw[j] + bias[j];
+    activate<4>(a.activation, v);
+    if (a.gate.p) {
+        gate.get(a.gate.type, f);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] *= f[j];
+    }
+    if (a.residual.p) {
+        residual.get(a.residual.type, f);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] += f[j];
+    }
+    const int64_t at = (int64_t)m * a.out.stride + n;
+    if (a.out.type == MOE_T_F32) {
+        float *p = reinterpret_cast<float *>(a.out.p) + at;
+        if (a.vec_out && n + 3 < a.N) {
+            *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (n + j < a.N) p[j] = v[j];
+        }
+    } else {
+        uint16_t *p = reinterpret_cast<uint16_t *>(a.out.p) + at;
+        uint32_t b[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) b[j] = to_bits16(v[j], a.out.type);
+        if (a.vec_out && n + 3 < a.N) {
+            *reinterpret_cast<uint2 *>(p) = make_uint2(b[0] | b[1] << 16, b[2] | b[3] << 16);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (n + j < a.N) p[j] = (uint16_t)b[j];
+        }
+    }
+}
+
+// ----------------------------------------------------- one tile a cluster --
+template <int TN>
+struct Split {
+    static constexpr int kStage = kBytesW + TN * kLine;
+    static constexpr int kStages = TN >= 128 ? 4 : 5;
+    static constexpr int kSmem = kStages * kStage + 1024;  // (stages begin at multiples of 1024)
+    static constexpr uint32_t kCols = TN < 32 ? 32 : TN;   // of tensor memory
+    static_assert(TN * kRowsW * 4 <= kStages * kStage, "the parts lie where the stages were");
+};
+
 template <int TN, bool CODES>
 __global__ void __launch_bounds__(kThreads)
-    linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
-                  const LinearArgs a) {
-    using T = Tile<TN>;
+    linear_split_kernel(const __grid_constant__ CUtensorMap wmap,
+                        const __grid_constant__ CUtensorMap xmap, const LinearArgs a) {
+    using T = Split<TN>;
     extern __shared__ uint8_t dyn[];
     __shared__ alignas(8) uint64_t bars[2 * T::kStages + 1];
     __shared__ uint32_t tmem_slot;
@@ -184,7 +373,10 @@ __global__ void __launch_bounds__(kThreads)
         for (int i = 0; i < 2 * T::kStages + 1; ++i) mbar_init(full + 8 * i, 1);
         mbar_fence_init();
     }
-    if (w == 5) {
+    // Tensor memory is taken behind the previous kernel, whose blocks may still want theirs, and
+    // before the next one may start.
+    pdl_wait();
+    if (w == 9) {
         tmem_alloc(smem_u32(&tmem_slot), T::kCols);
         tmem_relinquish();
     }
@@ -192,8 +384,9 @@ __global__ void __launch_bounds__(kThreads)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
+    pdl_launch_dependents();
 
-    if (w == 4) {
+    if (w == 8) {
         if (lane == 0) {
             Ring r(T::kStages);
             int issued = 0;
@@ -214,71 +407,72 @@ __global__ void __launch_bounds__(kThreads)
             }
         }
         __syncwarp();
-    } else if (w == 5) {
-        const uint32_t idesc = idesc_of(a.type, TN);
+    } else if (w == 9) {
+        const uint32_t idesc = idesc_of(a.type, 128, TN);
         Ring r(T::kStages);
         for (int k = kb0; k < kb1; ++k, r.next()) {
             if (__any_sync(0xffffffffu, !mbar_wait(full + 8 * r.idx, r.ph, &abort_flag, a.err))) break;
             tc_fence_after();
             const uint32_t s = stages + r.idx * T::kStage;
-            mma_stage<CODES>(tmem, smem_desc_sw128(s), smem_desc_sw128(s + kBytesW), idesc,
-                             k > kb0, empty + 8 * r.idx);
+            mma_stage<CODES, false>(tmem, smem_desc_sw128(s), smem_desc_sw128(s + kBytesW), idesc,
+                                    k > kb0, empty + 8 * r.idx);
         }
         tc_commit_elect(done);  // also after giving up: products in flight end first
     }
     // The sums are complete, and with them every copy has been used.
     __syncwarp();
-    if (w < 4) {
+    if (w < kEpilogue) {
         mbar_wait(done, 0, &abort_flag, a.err);
         __syncwarp();
         tc_fence_after();
     }
-    const int n = n0 + (w & 3) * 32 + lane;
-    const bool mine = w < 4 && n < a.N;
-    const float sw = mine && a.w_scale ? a.w_scale[n] : 1.0f;
-    const float bias = mine && a.bias ? a.bias[n] : 0.0f;
     const int rows = min(TN, a.M - m0);  // output rows of the tile
-    const uint32_t quarter = tmem + ((uint32_t)(w & 3) << 21);
     if (S == 1) {
-        if (w < 4) {
-#pragma unroll 1
-            for (int c = 0; c < rows; c += 16) {
-                float v[16];
-                tmem_ld_32x32b_x16_wait(quarter + c, v);
-                if (mine) finish<16>(a, m0 + c, n, min(16, rows - c), v, sw, bias);
-            }
-        }
+        if (w < kEpilogue) tile_out<TN>(a, tmem, m0, n0, rows, w, lane);
     } else {
         // parts[m][n]: 128 fp32 numbers for each output row
-        if (w < 4) {
-            const uint32_t at = stages + 4 * (uint32_t)(w * 32 + lane);
+        if (w < kEpilogue) {
+            const uint32_t at = stages + 4 * (uint32_t)((w & 3) * 32 + lane);
+            const uint32_t lanes = tmem + ((uint32_t)(w & 3) << 21);
 #pragma unroll 1
-            for (int c = 0; c < rows; c += 16) {
-                float v[16];
-                tmem_ld_32x32b_x16_wait(quarter + c, v);
+            for (int c = (w >> 2) * 16; c < rows; c += 32) {
+                Cols<16> v;
+                v.issue(lanes + c);
+                v.wait();
 #pragma unroll
                 for (int j = 0; j < 16; ++j)
-                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + (c + j) * 512), "f"(v[j]) : "memory");
+                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + (c + j) * 512), "r"(v.r[j]) : "memory");
             }
         }
         __syncwarp();
         cluster_sync();
-        if (w < 4) {
+        // a warp takes a row of its block's share, a lane four columns
+        if (w < kEpilogue) {
             const int c0 = rows * (int)rank / (int)S, c1 = rows * (int)(rank + 1) / (int)S;
+            const int n = n0 + 4 * lane;
+            float sw[4], bias[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                sw[j] = a.w_scale && n + j < a.N ? a.w_scale[n + j] : 1.0f;
+                bias[j] = a.bias && n + j < a.N ? a.bias[n + j] : 0.0f;
+            }
 #pragma unroll 1
-            for (int c = c0; c < c1; c += 8) {
-                float v[8];
+            for (int c = c0 + w; c < c1; c += kEpilogue) {
+                const int m = m0 + c;
+                Quad gate, residual;
+                if (a.gate.p) gate.load(a.gate, a.vec_gate, m, n, a.N);
+                if (a.residual.p) residual.load(a.residual, a.vec_residual, m, n, a.N);
+                const float sx = a.x_scale ? a.x_scale[m] : 1.0f;
+                const uint32_t at = stages + c * 512 + 16 * lane;
+                float4 p[8];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] = 0.0f;
-                for (uint32_t q = 0; q < S; ++q) {
-                    const uint32_t at = map_to(stages + 4 * (uint32_t)(w * 32 + lane), q);
-                    float p[8];
+                for (int q = 0; q < 8; ++q)
+                    if (q < S) p[q] = ld_cluster4(map_to(at, q));
+                float v[4] = {p[0].x, p[0].y, p[0].z, p[0].w};
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) p[j] = c + j < c1 ? ld_cluster(at + (c + j) * 512) : 0.0f;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) v[j] += p[j];
-                }
-                if (mine) finish<8>(a, m0 + c, n, min(8, c1 - c), v, sw, bias);
+                for (int q = 1; q < 8; ++q)
+                    if (q < S) v[0] += p[q].x, v[1] += p[q].y, v[2] += p[q].z, v[3] += p[q].w;
+                quad_out(a, m, n, v, sw, bias, gate, residual, sx);
             }
         }
         __syncwarp();
@@ -287,9 +481,161 @@ __global__ void __launch_bounds__(kThreads)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (w == 5) tmem_dealloc(tmem, T::kCols);
+    if (w == 9) tmem_dealloc(tmem, T::kCols);
 }
 
+// ------------------------------------------------ two blocks, many tiles --
+template <int TN>
+struct Pair {
+    static constexpr int kStage = kBytesW + TN / 2 * kLine;  // of one block
+    static constexpr int kStages = TN == 256 ? 6 : 8;
+    static constexpr int kSmem = kStages * kStage + 1024;
+    static constexpr uint32_t kCols = 2 * TN;
+    static constexpr int kBars = 2 * kStages + 5;  // full, empty, sums full, sums empty, end
+};
+
+// A pair's copy: its bytes are counted by the first block's barrier (an address of map_to).
+MOE_DEV void tma_load_pair(uint32_t dst, const void *tmap, int32_t c0, int32_t c1, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(tmap), "r"(c0), "r"(c1), "r"(bar)
+        : "memory");
+}
+
+// Tiles are taken in bands of kBand along x's rows, so that what runs at the same time shares
+// rows of both operands in L2.
+constexpr int kBand = 8;
+MOE_DEV void tile_at(int t, int tiles_m, int tiles_n, int &tm, int &tn) {
+    const int band = t / (kBand * tiles_n), r = t - band * kBand * tiles_n;
+    const int high = min(kBand, tiles_m - band * kBand);
+    tn = r / high;
+    tm = band * kBand + r - tn * high;
+}
+
+template <int TN, bool CODES>
+__global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
+    linear_pair_kernel(const __grid_constant__ CUtensorMap wmap,
+                       const __grid_constant__ CUtensorMap xmap, const LinearArgs a) {
+    using T = Pair<TN>;
+    extern __shared__ uint8_t dyn[];
+    __shared__ alignas(8) uint64_t bars[T::kBars];
+    __shared__ uint32_t tmem_slot;
+    __shared__ int abort_flag;
+    const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+    const uint32_t rank = cluster_rank();
+    const int first = (int)blockIdx.x >> 1, step = (int)gridDim.x >> 1;
+    const int tiles_n = (a.N + 2 * kRowsW - 1) / (2 * kRowsW), tiles_m = (a.M + TN - 1) / TN;
+    const int tiles = tiles_m * tiles_n;
+    const uint32_t stages = (smem_u32(dyn) + 1023u) & ~1023u;
+    const uint32_t full = smem_u32(bars), empty = full + 8 * T::kStages;
+    const uint32_t sums_full = full + 16 * T::kStages, sums_empty = sums_full + 16;
+    const uint32_t end = sums_empty + 16;
+    constexpr int kElems = CODES ? kLine : kLine / 2;
+    const int kb = (a.K + kElems - 1) / kElems;
+
+    if (tid == 0) {
+        abort_flag = 0;
+        for (int i = 0; i < T::kBars; ++i)
+            mbar_init(full + 8 * i, i == 2 * T::kStages + 2 || i == 2 * T::kStages + 3 ? 2 * kEpilogue : 1);
+        mbar_fence_init();
+    }
+    pdl_wait();
+    if (w == 9) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_u32(&tmem_slot)),
+                     "r"(T::kCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // the other block's barriers are there
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+    pdl_launch_dependents();
+
+    if (w == 8) {
+        if (lane == 0) {
+            const uint32_t full0 = map_to(full, 0);
+            Ring r(T::kStages);
+            int issued = 0;
+            bool ok = true;
+            for (int t = first; t < tiles && ok; t += step) {
+                int tm, tn;
+                tile_at(t, tiles_m, tiles_n, tm, tn);
+                const int n0 = tn * 2 * kRowsW + (int)rank * kRowsW, m0 = tm * TN + (int)rank * (TN / 2);
+                for (int k = 0; k < kb; ++k, r.next()) {
+                    ok = mbar_wait(empty + 8 * r.idx, r.ph ^ 1, &abort_flag, a.err);
+                    if (!ok) break;
+                    const uint32_t s = stages + r.idx * T::kStage;
+                    if (rank == 0) mbar_arrive_expect_tx(full + 8 * r.idx, 2 * T::kStage);
+                    tma_load_pair(s, &wmap, k * kElems, n0, full0 + 8 * r.idx);
+                    tma_load_pair(s + kBytesW, &xmap, k * kElems, m0, full0 + 8 * r.idx);
+                    ++issued;
+                }
+            }
+            if (rank == 0 && *(volatile int *)&abort_flag) {
+                // the copies in flight, of both blocks, end before the blocks do
+                volatile int none = 0;
+                Ring q(T::kStages);
+                for (int i = 0; i < issued; ++i, q.next())
+                    if (i >= issued - T::kStages) mbar_wait(full + 8 * q.idx, q.ph, &none, a.err);
+            }
+        }
+        __syncwarp();
+    } else if (w == 9) {
+        if (rank == 0) {
+            const uint32_t idesc = idesc_of(a.type, 256, TN);
+            Ring r(T::kStages), acc(2);
+            bool ok = true;
+            for (int t = first; t < tiles && ok; t += step, acc.next()) {
+                ok = __all_sync(0xffffffffu, mbar_wait(sums_empty + 8 * acc.idx, acc.ph ^ 1, &abort_flag, a.err));
+                tc_fence_after();
+                for (int k = 0; k < kb && ok; ++k, r.next()) {
+                    ok = __all_sync(0xffffffffu, mbar_wait(full + 8 * r.idx, r.ph, &abort_flag, a.err));
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t s = stages + r.idx * T::kStage;
+                    mma_stage<CODES, true>(tmem + acc.idx * TN, smem_desc_sw128(s),
+                                           smem_desc_sw128(s + kBytesW), idesc, k > 0, empty + 8 * r.idx);
+                }
+                if (ok) commit_both(sums_full + 8 * acc.idx);
+            }
+            if (!ok) {
+                // products in flight end before the tensor memory is given back
+                volatile int none = 0;
+                commit_both(end);
+                mbar_wait(end, 0, &none, a.err);
+                __syncwarp();
+            }
+        }
+    } else {
+        const uint32_t empty0 = map_to(sums_empty, 0);
+        Ring acc(2);
+        for (int t = first; t < tiles; t += step, acc.next()) {
+            int tm, tn;
+            tile_at(t, tiles_m, tiles_n, tm, tn);
+            if (!__all_sync(0xffffffffu, mbar_wait(sums_full + 8 * acc.idx, acc.ph, &abort_flag, a.err))) break;
+            tc_fence_after();
+            tile_out<TN>(a, tmem + acc.idx * TN, tm * TN, tn * 2 * kRowsW + (int)rank * kRowsW,
+                         min(TN, a.M - tm * TN), w, lane);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_at(empty0 + 8 * acc.idx);
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after();
+    if (w == 9)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(T::kCols)
+                     : "memory");
+}
+
+// ------------------------------------------------------------------- host --
 // Tensor map over rows of k, one 128-byte line of a row wide, box_rows high.
 bool rows_map(CUtensorMap *m, const void *p, int64_t stride, int rows, int K, int type, int box_rows) {
     EncodeTiledFn fn = encode_fn();
@@ -308,60 +654,123 @@ bool rows_map(CUtensorMap *m, const void *p, int64_t stride, int rows, int K, in
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int TN, bool CODES>
-cudaError_t launch(const LinearArgs &a, const void *x, int64_t x_stride, const void *w,
-                   int64_t w_stride, int sms, cudaStream_t s) {
-    using T = Tile<TN>;
-    static std::atomic<bool> set[64];
+// What a launch needs to know of the operands.
+struct Operands {
+    const void *x, *w;
+    int64_t x_stride, w_stride;
+    int sms;
+};
+
+// Allows a kernel its shared memory, once a device; *n: clusters that fit on it at once (for
+// a kernel of pairs).
+template <typename K>
+cudaError_t prepare(K kernel, int smem, std::atomic<int> *known, int *n, int pair_grid) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    if (dev < 0 || dev >= 64 || !set[dev]) {
-        e = cudaFuncSetAttribute(linear_kernel<TN, CODES>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 T::kSmem);
-        if (e != cudaSuccess) return e;
-        if (dev >= 0 && dev < 64) set[dev] = true;
+    if (dev >= 0 && dev < 64 && known[dev] > 0) {
+        *n = known[dev];
+        return cudaSuccess;
     }
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    *n = 1;
+    if (pair_grid) {
+        cudaLaunchConfig_t c{};
+        c.gridDim = dim3((unsigned)pair_grid);
+        c.blockDim = dim3(kThreads);
+        c.dynamicSmemBytes = smem;
+        cudaLaunchAttribute at{};
+        at.id = cudaLaunchAttributeClusterDimension;
+        at.val.clusterDim.x = 2;
+        at.val.clusterDim.y = at.val.clusterDim.z = 1;
+        c.numAttrs = 1;
+        c.attrs = &at;
+        e = cudaOccupancyMaxActiveClusters(n, kernel, &c);
+        if (e != cudaSuccess) return e;
+        if (*n < 1) return cudaErrorLaunchOutOfResources;
+    }
+    if (dev >= 0 && dev < 64) known[dev] = *n;
+    return cudaSuccess;
+}
+
+template <int TN, bool CODES>
+cudaError_t launch_pair(const LinearArgs &a, const Operands &o, cudaStream_t s) {
+    using T = Pair<TN>;
+    static std::atomic<int> known[64];
+    int pairs;
+    cudaError_t e = prepare(linear_pair_kernel<TN, CODES>, T::kSmem, known, &pairs, o.sms / 2 * 2);
+    if (e != cudaSuccess) return e;
     CUtensorMap wmap, xmap;
-    if (!rows_map(&wmap, w, w_stride, a.N, a.K, a.type, kRowsW) ||
-        !rows_map(&xmap, x, x_stride, a.M, a.K, a.type, TN))
+    if (!rows_map(&wmap, o.w, o.w_stride, a.N, a.K, a.type, kRowsW) ||
+        !rows_map(&xmap, o.x, o.x_stride, a.M, a.K, a.type, TN / 2))
+        return cudaErrorNotSupported;
+    const int64_t tiles = (int64_t)((a.N + 2 * kRowsW - 1) / (2 * kRowsW)) * ((a.M + TN - 1) / TN);
+    auto c = pdl_config((unsigned)(2 * (tiles < pairs ? tiles : pairs)), kThreads, T::kSmem, s);
+    cudaLaunchAttribute at{};
+    c.numAttrs = pdl_attr(at);
+    c.attrs = &at;
+    return cudaLaunchKernelEx(&c, linear_pair_kernel<TN, CODES>, wmap, xmap, a);
+}
+
+template <int TN, bool CODES>
+cudaError_t launch_split(const LinearArgs &a, const Operands &o, cudaStream_t s) {
+    using T = Split<TN>;
+    static std::atomic<int> known[64];
+    int one;
+    cudaError_t e = prepare(linear_split_kernel<TN, CODES>, T::kSmem, known, &one, 0);
+    if (e != cudaSuccess) return e;
+    CUtensorMap wmap, xmap;
+    if (!rows_map(&wmap, o.w, o.w_stride, a.N, a.K, a.type, kRowsW) ||
+        !rows_map(&xmap, o.x, o.x_stride, a.M, a.K, a.type, TN))
         return cudaErrorNotSupported;
     const int tiles_n = (a.N + kRowsW - 1) / kRowsW, tiles_m = (a.M + TN - 1) / TN;
     const int kb = (a.K * (CODES ? 1 : 2) + kLine - 1) / kLine;
     // Blocks that share a tile: as many as fill the GPU about twice over (two blocks of a few
     // tokens lie on an SM), each with a few stages at least.
     int S = 1;
-    while (S < 8 && (int64_t)tiles_n * tiles_m * S * 2 <= 2 * sms && kb >= 8 * S) S *= 2;
-    cudaLaunchConfig_t c{};
+    while (S < 8 && (int64_t)tiles_n * tiles_m * S * 2 <= 2 * o.sms && kb >= 8 * S) S *= 2;
+    auto c = pdl_config(1, kThreads, T::kSmem, s);
     c.gridDim = dim3((unsigned)(tiles_n * S), (unsigned)tiles_m);
-    c.blockDim = dim3(kThreads);
-    c.dynamicSmemBytes = T::kSmem;
-    c.stream = s;
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = (unsigned)S;
-    at.val.clusterDim.y = at.val.clusterDim.z = 1;
-    c.numAttrs = 1;
-    c.attrs = &at;
-    return cudaLaunchKernelEx(&c, linear_kernel<TN, CODES>, wmap, xmap, a);
+    cudaLaunchAttribute at[2] = {};
+    c.numAttrs = 1 + pdl_attr(at[0]);
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = (unsigned)S;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    c.attrs = at;
+    return cudaLaunchKernelEx(&c, linear_split_kernel<TN, CODES>, wmap, xmap, a);
 }
 
 template <bool CODES>
-cudaError_t by_rows(const LinearArgs &a, const void *x, int64_t xs, const void *w, int64_t ws, int sms,
-                    cudaStream_t s) {
-    if (a.M <= 16) return launch<16, CODES>(a, x, xs, w, ws, sms, s);
-    if (a.M <= 32) return launch<32, CODES>(a, x, xs, w, ws, sms, s);
-    if (a.M <= 64) return launch<64, CODES>(a, x, xs, w, ws, sms, s);
-    if (a.M <= 128) return launch<128, CODES>(a, x, xs, w, ws, sms, s);
-    return launch<256, CODES>(a, x, xs, w, ws, sms, s);
+cudaError_t by_size(const LinearArgs &a, const Operands &o, cudaStream_t s) {
+    const int64_t half_tiles = (int64_t)((a.N + 255) / 256) * ((a.M + 127) / 128);
+    if (a.M > 128 && half_tiles >= o.sms / 2) {
+        if ((int64_t)((a.N + 255) / 256) * ((a.M + 255) / 256) >= o.sms / 2)
+            return launch_pair<256, CODES>(a, o, s);
+        return launch_pair<128, CODES>(a, o, s);
+    }
+    if (a.M <= 16) return launch_split<16, CODES>(a, o, s);
+    if (a.M <= 32) return launch_split<32, CODES>(a, o, s);
+    if (a.M <= 64) return launch_split<64, CODES>(a, o, s);
+    if (a.M <= 128) return launch_split<128, CODES>(a, o, s);
+    return launch_split<256, CODES>(a, o, s);
+}
+
+// Four neighbours of a row may be one access.
+bool quads(const void *p, int64_t stride, int type, int rows) {
+    const int bytes = type == MOE_T_F32 ? 16 : 8;
+    return ((uintptr_t)p % bytes) == 0 && (rows == 1 || stride % 4 == 0);
 }
 
 }  // namespace
 
-cudaError_t launch_linear(const LinearArgs &a, const void *x, int64_t x_stride, const void *w,
+cudaError_t launch_linear(LinearArgs a, const void *x, int64_t x_stride, const void *w,
                           int64_t w_stride, int sms, cudaStream_t s) {
-    return a.type == MOE_T_E4M3 ? by_rows<true>(a, x, x_stride, w, w_stride, sms, s)
-                                : by_rows<false>(a, x, x_stride, w, w_stride, sms, s);
+    a.vec_gate = quads(a.gate.p, a.gate.stride, a.gate.type, a.M);
+    a.vec_residual = quads(a.residual.p, a.residual.stride, a.residual.type, a.M);
+    a.vec_out = quads(a.out.p, a.out.stride, a.out.type, a.M);
+    const Operands o{x, w, x_stride, w_stride, sms};
+    return a.type == MOE_T_E4M3 ? by_size<true>(a, o, s) : by_size<false>(a, o, s);
 }
 
 }  // namespace moe
