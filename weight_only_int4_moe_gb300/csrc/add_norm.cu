@@ -83,6 +83,10 @@ struct Elems {
                 q[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
         }
     }
+    MOE_DEV void zero() {
+#pragma unroll
+        for (int k = 0; k < (kWords ? kWords : 1); ++k) w[k] = 0u;
+    }
     MOE_DEV float get(int j) const {
         if constexpr (TYPE == MOE_T_F32) return __uint_as_float(w[j]);
         const uint32_t v = (j & 1) ? w[j / 2] >> 16 : w[j / 2] & 0xFFFFu;
@@ -160,56 +164,62 @@ MOE_DEV uint16_t e4m3x2(float lo, float hi) {
 
 constexpr int kNone = -1;  // no residual
 
-// TX, TS: types of x and of the residual; VEC: elements of a load; NV: loads of a thread.
-template <int TX, int TS, int VEC, int NV>
-__global__ void __launch_bounds__(1024) add_norm_kernel(const AddNormArgs a) {
+// TX, TS: types of x and of the residual; VEC: elements of a load; NV: loads of a thread;
+// MAX: threads of a block at most.
+template <int TX, int TS, int VEC, int NV, int MAX>
+__global__ void __launch_bounds__(MAX, 1024 / MAX) add_norm_kernel(const AddNormArgs a) {
     __shared__ float part_hi[32], part_lo[32], part_max[32];
     __shared__ double part_d[32];
     const int row = blockIdx.x, tid = threadIdx.x, T = blockDim.x, lane = tid & 31;
     const int warps = T >> 5, H = a.hidden;
     constexpr bool kAdd = TS != kNone;
-    constexpr int kTS = kAdd ? TS : MOE_T_F32;
+    constexpr int kHeld = kAdd ? TS : TX;  // h has this type exactly: it is kept as it lies in memory
+    pdl_wait();
+    pdl_launch_dependents();
 
-    float h[NV][VEC], w[NV][VEC];
-    {
+    Elems<kHeld, VEC> h[NV];
+    float w[NV == 1 ? VEC : 1];
+    if constexpr (kAdd) {
         Elems<TX, VEC> x[NV];
-        Elems<kTS, VEC> r[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int p = (i * T + tid) * VEC;
             if (p < H) {
                 x[i].load(a.x.p, row * a.x.stride + p);
-                if constexpr (kAdd) r[i].load(a.residual.p, row * a.residual.stride + p);
+                h[i].load(a.residual.p, row * a.residual.stride + p);
             }
         }
+        if constexpr (NV == 1)
+            if (tid * VEC < H) load_weight<VEC>(a, tid * VEC, w);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int p = (i * T + tid) * VEC;
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) h[i][j] = w[i][j] = 0.0f;
             if (p < H) {
-                load_weight<VEC>(a, p, w[i]);
+                float f[VEC];
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) {
-                    h[i][j] = x[i].get(j);
-                    if constexpr (kAdd) h[i][j] = __fadd_rn(h[i][j], r[i].get(j));
-                }
-                if constexpr (kAdd) {
-                    r[i].set(h[i]);
-#pragma unroll
-                    for (int j = 0; j < VEC; ++j) h[i][j] = r[i].get(j);
-                    if (a.residual_out.p)
-                        r[i].store(a.residual_out.p, row * a.residual_out.stride + p);
-                }
+                for (int j = 0; j < VEC; ++j) f[j] = __fadd_rn(x[i].get(j), h[i].get(j));
+                h[i].set(f);
+                if (a.residual_out.p) h[i].store(a.residual_out.p, row * a.residual_out.stride + p);
+            } else {
+                h[i].zero();
             }
         }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int p = (i * T + tid) * VEC;
+            h[i].zero();
+            if (p < H) h[i].load(a.x.p, row * a.x.stride + p);
+        }
+        if constexpr (NV == 1)
+            if (tid * VEC < H) load_weight<VEC>(a, tid * VEC, w);
     }
 
     Sum2 t{0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) add_square(t, h[i][j]);
+        for (int j = 0; j < VEC; ++j) add_square(t, h[i].get(j));
 #pragma unroll
     for (int o = 16; o; o >>= 1)
         t = join(t, Sum2{__shfl_xor_sync(0xffffffffu, t.hi, o), __shfl_xor_sync(0xffffffffu, t.lo, o)});
@@ -234,7 +244,7 @@ __global__ void __launch_bounds__(1024) add_norm_kernel(const AddNormArgs a) {
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) d += (double)h[i][j] * (double)h[i][j];
+            for (int j = 0; j < VEC; ++j) d += (double)h[i].get(j) * (double)h[i].get(j);
 #pragma unroll
         for (int o = 16; o; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
         if (warps > 1) {
@@ -249,17 +259,19 @@ __global__ void __launch_bounds__(1024) add_norm_kernel(const AddNormArgs a) {
         q = __frcp_rn(__fsqrt_rn(__fadd_rn(__fmul_rn(total, a.inv_hidden), a.eps)));
     }
 
-    float top = 0.0f;
+    float top = 0.0f, y[NV][VEC];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int p = (i * T + tid) * VEC;
         if (p < H) {
+            float f[VEC];
+            if constexpr (NV > 1) load_weight<VEC>(a, p, f);
 #pragma unroll
             for (int j = 0; j < VEC; ++j) {
-                h[i][j] = __fmul_rn(__fmul_rn(h[i][j], q), w[i][j]);
-                top = fmaxf(top, fabsf(h[i][j]));  // (NaN is not counted)
+                y[i][j] = __fmul_rn(__fmul_rn(h[i].get(j), q), NV == 1 ? w[j] : f[j]);
+                top = fmaxf(top, fabsf(y[i][j]));  // (NaN is not counted)
             }
-            if (a.out.p) store_as<VEC>(a.out, row * a.out.stride + p, h[i]);
+            if (a.out.p) store_as<VEC>(a.out, row * a.out.stride + p, y[i]);
         }
     }
     if (!a.codes) return;
@@ -281,44 +293,49 @@ __global__ void __launch_bounds__(1024) add_norm_kernel(const AddNormArgs a) {
         if (p >= H) continue;
         uint8_t *c = a.codes + row * a.codes_stride + p;
         if constexpr (VEC == 1) {
-            *c = (uint8_t)e4m3x2(__fmul_rn(h[i][0], inv), 0.0f);
+            *c = (uint8_t)e4m3x2(__fmul_rn(y[i][0], inv), 0.0f);
         } else {
             uint32_t v[2];
 #pragma unroll
             for (int k = 0; k < 2; ++k)
-                v[k] = e4m3x2(__fmul_rn(h[i][4 * k], inv), __fmul_rn(h[i][4 * k + 1], inv)) |
-                       (uint32_t)e4m3x2(__fmul_rn(h[i][4 * k + 2], inv),
-                                        __fmul_rn(h[i][4 * k + 3], inv))
+                v[k] = e4m3x2(__fmul_rn(y[i][4 * k], inv), __fmul_rn(y[i][4 * k + 1], inv)) |
+                       (uint32_t)e4m3x2(__fmul_rn(y[i][4 * k + 2], inv),
+                                        __fmul_rn(y[i][4 * k + 3], inv))
                            << 16;
             *reinterpret_cast<uint2 *>(c) = make_uint2(v[0], v[1]);
         }
     }
 }
 
-template <int TX, int TS, int VEC, int NV>
+template <int TX, int TS, int VEC, int NV, int MAX>
 cudaError_t launch(const AddNormArgs &a, cudaStream_t s) {
     const int per = VEC * NV, T = ((a.hidden + per - 1) / per + 31) / 32 * 32;
-    add_norm_kernel<TX, TS, VEC, NV><<<a.rows, T, 0, s>>>(a);
-    return cudaGetLastError();
+    auto c = pdl_config((unsigned)a.rows, (unsigned)T, 0, s);
+    cudaLaunchAttribute at{};
+    c.numAttrs = pdl_attr(at);
+    c.attrs = &at;
+    return cudaLaunchKernelEx(&c, add_norm_kernel<TX, TS, VEC, NV, MAX>, a);
 }
 
 template <int TX, int TS>
-cudaError_t by_size(const AddNormArgs &a, bool vec, cudaStream_t s) {
+cudaError_t by_size(const AddNormArgs &a, bool vec, int sms, cudaStream_t s) {
     if (vec) {
-        if (a.hidden <= 8 * 1024) return launch<TX, TS, 8, 1>(a, s);
-        if (a.hidden <= 16 * 1024) return launch<TX, TS, 8, 2>(a, s);
-        return launch<TX, TS, 8, 4>(a, s);
+        if (a.hidden <= 8192) {
+            if (a.hidden <= 1024 || a.rows <= 2 * sms) return launch<TX, TS, 8, 1, 1024>(a, s);
+            return launch<TX, TS, 8, 4, 256>(a, s);
+        }
+        return launch<TX, TS, 8, 4, 1024>(a, s);
     }
-    if (a.hidden <= 8 * 1024) return launch<TX, TS, 1, 8>(a, s);
-    return launch<TX, TS, 1, 32>(a, s);
+    if (a.hidden <= 4096) return launch<TX, TS, 1, 8, 512>(a, s);
+    return launch<TX, TS, 1, 32, 1024>(a, s);
 }
 
 template <int TX>
-cudaError_t by_stream(const AddNormArgs &a, bool vec, cudaStream_t s) {
-    if (!a.residual.p) return by_size<TX, kNone>(a, vec, s);
-    if (a.residual.type == MOE_T_BF16) return by_size<TX, MOE_T_BF16>(a, vec, s);
-    if (a.residual.type == MOE_T_F16) return by_size<TX, MOE_T_F16>(a, vec, s);
-    return by_size<TX, MOE_T_F32>(a, vec, s);
+cudaError_t by_stream(const AddNormArgs &a, bool vec, int sms, cudaStream_t s) {
+    if (!a.residual.p) return by_size<TX, kNone>(a, vec, sms, s);
+    if (a.residual.type == MOE_T_BF16) return by_size<TX, MOE_T_BF16>(a, vec, sms, s);
+    if (a.residual.type == MOE_T_F16) return by_size<TX, MOE_T_F16>(a, vec, sms, s);
+    return by_size<TX, MOE_T_F32>(a, vec, sms, s);
 }
 
 // Every row of a matrix begins at a multiple of `to` bytes.
@@ -329,16 +346,16 @@ int size_of(int type) { return type == MOE_T_F32 ? 4 : 2; }
 
 }  // namespace
 
-cudaError_t launch_add_norm(const AddNormArgs &a, cudaStream_t s) {
+cudaError_t launch_add_norm(const AddNormArgs &a, int sms, cudaStream_t s) {
     const int n = a.rows;
     const bool vec = a.hidden % 8 == 0 && rows_at(a.x.p, a.x.stride, size_of(a.x.type), n, 16) &&
                      rows_at(a.residual.p, a.residual.stride, size_of(a.residual.type), n, 16) &&
                      rows_at(a.residual_out.p, a.residual_out.stride, size_of(a.residual.type), n, 16) &&
                      rows_at(a.out.p, a.out.stride, size_of(a.out.type), n, 16) &&
                      rows_at(a.weight, 0, 2, 1, 16) && rows_at(a.codes, a.codes_stride, 1, n, 8);
-    if (a.x.type == MOE_T_BF16) return by_stream<MOE_T_BF16>(a, vec, s);
-    if (a.x.type == MOE_T_F16) return by_stream<MOE_T_F16>(a, vec, s);
-    return by_stream<MOE_T_F32>(a, vec, s);
+    if (a.x.type == MOE_T_BF16) return by_stream<MOE_T_BF16>(a, vec, sms, s);
+    if (a.x.type == MOE_T_F16) return by_stream<MOE_T_F16>(a, vec, sms, s);
+    return by_stream<MOE_T_F32>(a, vec, sms, s);
 }
 
 }  // namespace moe

@@ -65,7 +65,7 @@ struct RouteExpertsArgs {
     float *weights;
 };
 
-cudaError_t launch_add_norm(const AddNormArgs &a, cudaStream_t s);
+cudaError_t launch_add_norm(const AddNormArgs &a, int sms, cudaStream_t s);
 // cudaErrorNotSupported: the operands' tensor maps could not be made.
 cudaError_t launch_linear(LinearArgs a, const void *x, int64_t x_stride, const void *w,
                           int64_t w_stride, int sms, cudaStream_t s);

@@ -69,7 +69,7 @@ int moe_add_norm(const void *x, int x_type, int64_t x_stride, const void *residu
     a.codes = codes;
     a.codes_stride = codes_stride;
     a.scales = scales;
-    return done(launch_add_norm(a, str(stream)));
+    return done(launch_add_norm(a, sms, str(stream)));
 }
 
 int moe_linear(const void *x, int64_t x_stride, const float *x_scale, const void *w,

@@ -2,14 +2,16 @@
 // renormalised weights.
 //
 // A warp has a token; lane l holds experts l, l + 32, ...  The kernel reads M E logits and
-// writes 8 M top_k bytes; what costs is choosing: each of the top_k rounds takes the warp's
-// largest remaining key and, among equal ones, the lowest index (two warp reductions).
+// writes 8 M top_k bytes; what costs is choosing.  The lanes' largest keys are sorted across
+// the warp: the top_k experts lie at or above the top_k-th of them, and seldom more than half
+// as many again do.  These candidates move to a lane each (in index order) and count who is
+// before them.
 //
 // Which experts are chosen must not depend on how an exponential was rounded.  Without a bias
 // the scores order as the logits do, and the logits are the keys.  With one, c = s + bias is
 // formed in fp32, whose error against the real number is bounded (`unsure`); where two
-// neighbours in the order are nearer to each other than that, the token is done again in 64
-// bits.  That is seldom: the 9 gaps of a top-8 choice are some 1e-2 wide.
+// neighbours in the order are nearer to each other than that, the candidates are compared
+// again in 64 bits.  That is seldom: the 9 gaps of a top-8 choice are some 1e-2 wide.
 #include <cfloat>
 
 #include "layer.cuh"
@@ -35,8 +37,20 @@ MOE_DEV float logit_of(const RouteExpertsArgs &a, int64_t row, int e) {
     const float x = load_as_float(a.logits, a.type, row * a.stride + e);
     return isnan(x) ? -INFINITY : fminf(x, FLT_MAX);
 }
-MOE_DEV float sigmoid(float x) { return expf(fminf(x, 0.0f)) / (1.0f + expf(-fabsf(x))); }
-MOE_DEV double sigmoid(double x) { return exp(fmin(x, 0.0)) / (1.0 + exp(-fabs(x))); }
+MOE_DEV float sigmoid(float x) {
+    const float t = expf(-fabsf(x));
+    return (x < 0.0f ? t : 1.0f) / (1.0f + t);
+}
+MOE_DEV double sigmoid(double x) {
+    const double t = exp(-fabs(x));
+    return (x < 0.0 ? t : 1.0) / (1.0 + t);
+}
+// With the hardware's exponential (2^-22 relative; its argument's rounding adds |x| 2^-24) and
+// quotient (2 steps): within 3.7e-7.
+MOE_DEV float sigmoid_fast(float x) {
+    const float t = __expf(-fabsf(x));
+    return __fdividef(x < 0.0f ? t : 1.0f, 1.0f + t);
+}
 
 MOE_DEV float warp_max(float v) {
 #pragma unroll
@@ -67,25 +81,52 @@ MOE_DEV uint32_t choose_groups(const RouteExpertsArgs &a, F value, int lane, F &
     return __ballot_sync(0xffffffffu, in && before < a.top_groups);
 }
 
+// The softmax's top and 1 / sum in 64 bits (0 and 1 for the sigmoid).
+MOE_DEV void softmax_exactly(const RouteExpertsArgs &a, int64_t row, int lane, double &top, double &inv) {
+    top = 0.0;
+    inv = 1.0;
+    if (a.scoring != MOE_SCORE_SOFTMAX) return;
+    float m = -INFINITY;
+    for (int e = lane; e < a.E; e += 32) m = fmaxf(m, logit_of(a, row, e));
+    m = warp_max(m);
+    top = m == -INFINITY ? 0.0 : (double)m;
+    double sum = 0.0;
+#pragma unroll 4
+    for (int e = lane; e < a.E; e += 32) sum += exp((double)logit_of(a, row, e) - top);
+    sum = warp_sum(sum);
+    inv = sum > 0.0 ? 1.0 / sum : 0.0;
+}
+// An expert's c in 64 bits, -inf where it is not available.
+MOE_DEV double score_exactly(const RouteExpertsArgs &a, int64_t row, int e, double top, double inv) {
+    const float l = logit_of(a, row, e), b = a.bias ? a.bias[e] : 0.0f;
+    const double s = a.scoring == MOE_SCORE_SOFTMAX ? exp((double)l - top) * inv : sigmoid((double)l);
+    return l > -INFINITY && b > -INFINITY ? s + (double)b : -INFINITY;
+}
+
+// The candidates of a token in 64 bits: lane j < n has expert e (ascending in j).  -> the
+// lane's expert in the order of choice; list: room for 32.
+__device__ __noinline__ int order_exactly(const RouteExpertsArgs &a, int64_t row, int lane, int n, int e,
+                                          int *list) {
+    double top, inv;
+    softmax_exactly(a, row, lane, top, inv);
+    const double c = lane < n ? score_exactly(a, row, e, top, inv) : -INFINITY;
+    int before = 0;
+    for (int j = 0; j < n; ++j) {
+        const double o = __shfl_sync(0xffffffffu, c, j);
+        before += o > c || (o == c && j < lane);
+    }
+    __syncwarp();
+    if (lane < n) list[before] = e;
+    __syncwarp();
+    return list[lane];
+}
+
 // The whole choice in 64 bits; c: room for E numbers.  -> the lane's expert.
 __device__ __noinline__ int choose_exactly(const RouteExpertsArgs &a, int64_t row, int lane, double *c) {
-    double top = -INFINITY, inv = 0.0;
-    if (a.scoring == MOE_SCORE_SOFTMAX) {
-        float m = -INFINITY;
-        for (int e = lane; e < a.E; e += 32) m = fmaxf(m, logit_of(a, row, e));
-        m = warp_max(m);
-        top = m == -INFINITY ? 0.0 : (double)m;
-        double sum = 0.0;
-        for (int e = lane; e < a.E; e += 32) sum += exp((double)logit_of(a, row, e) - top);
-        sum = warp_sum(sum);
-        inv = sum > 0.0 ? 1.0 / sum : 0.0;
-    }
-    for (int e = lane; e < a.E; e += 32) {
-        const float l = logit_of(a, row, e), b = a.bias ? a.bias[e] : 0.0f;
-        const double s = a.scoring == MOE_SCORE_SOFTMAX ? exp((double)l - top) * inv : sigmoid((double)l);
-        const bool here = l > -INFINITY && b > -INFINITY;
-        c[e] = here ? s + (double)b : -INFINITY;
-    }
+    double top, inv;
+    softmax_exactly(a, row, lane, top, inv);
+#pragma unroll 4
+    for (int e = lane; e < a.E; e += 32) c[e] = score_exactly(a, row, e, top, inv);
     __syncwarp();
     uint32_t open = 0xffffffffu;
     const int size = a.E / a.groups;
@@ -147,23 +188,52 @@ __device__ __noinline__ int choose_exactly(const RouteExpertsArgs &a, int64_t ro
     return chosen;
 }
 
+// Descending order of a value a lane across the warp.
+MOE_DEV uint32_t sort_lanes(uint32_t v, int lane) {
+#pragma unroll
+    for (int k = 2; k <= 32; k *= 2)
+#pragma unroll
+        for (int j = k / 2; j; j /= 2) {
+            const uint32_t o = __shfl_xor_sync(0xffffffffu, v, j);
+            const bool larger = ((lane & j) == 0) == ((lane & k) == 0);
+            v = larger ? max(v, o) : min(v, o);
+        }
+    return v;
+}
+
 // V: experts of a lane.
 template <int V>
 __global__ void __launch_bounds__(32 * kWarps) route_experts_kernel(const RouteExpertsArgs a) {
     extern __shared__ double exact[];
+    __shared__ uint32_t list_key[kWarps][32];
+    __shared__ int list_e[kWarps][32];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int size = a.E / a.groups;
+    const float per_group = 1.0f / (float)size;
     const bool soft = a.scoring == MOE_SCORE_SOFTMAX;
+    const bool sums = a.groups > 1 && a.group_best == 2 && size > 1;
+    const bool scored = a.bias || sums;  // some keys are scores, not logits
+    pdl_wait();
+    pdl_launch_dependents();
     for (int64_t t = (int64_t)blockIdx.x * kWarps + w; t < a.M; t += (int64_t)gridDim.x * kWarps) {
-        float l[V];
+        float l[V], b[V];
         uint32_t key[V];
+        if (a.type == MOE_T_F32) {
+            const float *p = reinterpret_cast<const float *>(a.logits) + t * a.stride + lane;
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int e = lane + 32 * i;
-            l[i] = e < a.E ? logit_of(a, t, e) : -INFINITY;
+            for (int i = 0; i < V; ++i) l[i] = lane + 32 * i < a.E ? p[32 * i] : -INFINITY;
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                l[i] = lane + 32 * i < a.E ? load_as_float(a.logits, a.type, t * a.stride + lane + 32 * i)
+                                           : -INFINITY;
         }
+#pragma unroll
+        for (int i = 0; i < V; ++i) b[i] = a.bias && lane + 32 * i < a.E ? a.bias[lane + 32 * i] : 0.0f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) l[i] = isnan(l[i]) ? -INFINITY : fminf(l[i], FLT_MAX);
         float top = 0.0f, inv = 1.0f;
-        if (soft) {
+        if (soft && (scored || !a.renormalize)) {
             top = l[0];
 #pragma unroll
             for (int i = 1; i < V; ++i) top = fmaxf(top, l[i]);
@@ -171,73 +241,149 @@ __global__ void __launch_bounds__(32 * kWarps) route_experts_kernel(const RouteE
             if (top == -INFINITY) top = 0.0f;
             float sum = 0.0f;
 #pragma unroll
-            for (int i = 0; i < V; ++i) sum += expf(l[i] - top);
+            for (int i = 0; i < V; ++i) sum += __expf(l[i] - top);
             sum = warp_sum(sum);
             inv = sum > 0.0f ? 1.0f / sum : 0.0f;
         }
-        // the largest score bounds every score's error; c adds its own rounding
+        // bounds the error of the difference of two scores (the softmax's by its largest, and
+        // by the sum's 37 additions at most); c adds its own rounding
         const float unsure = soft ? 4e-6f * inv : 1e-6f;
         bool sure = true;
-        uint32_t open = 0xffffffffu;
-        const bool sums = a.groups > 1 && a.group_best == 2 && size > 1;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const int e = lane + 32 * i;
-            key[i] = kGone;
-            if (e < a.E) {
-                const float b = a.bias ? a.bias[e] : 0.0f;
-                const bool here = l[i] > -INFINITY && b > -INFINITY;
-                float c = l[i];
-                if (a.bias || sums) c = (soft ? expf(l[i] - top) * inv : sigmoid(l[i])) + b;
-                key[i] = here ? key_of(c) : kMasked;
-            }
+            const bool here = l[i] > -INFINITY && b[i] > -INFINITY;
+            float c = l[i];
+            if (scored) c = (soft ? __expf(l[i] - top) * inv : sigmoid_fast(l[i])) + b[i];
+            key[i] = lane + 32 * i < a.E ? here ? key_of(c) : kMasked : kGone;
         }
         if (a.groups > 1) {
             float mine = -INFINITY;
-            for (int g = 0; g < a.groups; ++g) {
-                uint32_t x = 0, y = 0;
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const int e = lane + 32 * i;
-                    const uint32_t k = e >= g * size && e < (g + 1) * size ? key[i] : 0u;
-                    y = max(y, min(x, k));
-                    x = max(x, k);
-                }
+            // the warp's two best of a group -> its value, in lane g
+            auto value = [&](int g, uint32_t x, uint32_t y) {
                 const uint32_t best = __reduce_max_sync(0xffffffffu, x);
-                const uint32_t who = __ballot_sync(0xffffffffu, x == best);
                 uint32_t second = 0;
-                if (sums)
+                if (sums) {
+                    const uint32_t who = __ballot_sync(0xffffffffu, x == best);
                     second = __popc(who) > 1 ? best : __reduce_max_sync(0xffffffffu, x == best ? y : x);
+                }
                 if (lane == g && best > kMasked)
                     mine = second > kMasked ? value_of(best) + value_of(second) : value_of(best);
+            };
+            if (size % 32 == 0) {
+                // a group is some of every lane's registers
+                uint32_t x = 0, y = 0;
+                int g = 0, left = size / 32;
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    y = max(y, min(x, key[i]));
+                    x = max(x, key[i]);
+                    if (--left == 0 && g < a.groups) {
+                        value(g++, x, y);
+                        x = y = 0;
+                        left = size / 32;
+                    }
+                }
+            } else {
+                for (int g = 0; g < a.groups; ++g) {
+                    uint32_t x = 0, y = 0;
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        const uint32_t k = (uint32_t)(lane + 32 * i - g * size) < (uint32_t)size ? key[i] : 0u;
+                        y = max(y, min(x, k));
+                        x = max(x, k);
+                    }
+                    value(g, x, y);
+                }
             }
             float gap, edge;
-            open = choose_groups(a, mine, lane, gap, edge);
-            if ((a.bias || sums) && !(gap > 2.0f * unsure + 2.5e-7f * fabsf(edge))) sure = edge == -INFINITY;
+            const uint32_t open = choose_groups(a, mine, lane, gap, edge);
+            if (scored && !(gap > 2.0f * unsure + 2.5e-7f * fabsf(edge))) sure = edge == -INFINITY;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const int e = lane + 32 * i;
                 if (e < a.E) {
                     if (!a.bias && sums) key[i] = l[i] > -INFINITY ? key_of(l[i]) : kMasked;
-                    if (!((open >> (e / size)) & 1u)) key[i] = kGone;
+                    // e / size: E is at most 1024, so the product is off by less than 1 / (2 size)
+                    if (!((open >> (int)(((float)e + 0.5f) * per_group)) & 1u)) key[i] = kGone;
                 }
             }
         }
-        // top_k rounds, and one more to see how far the next expert is
-        uint32_t best = 0;
-        int at = 0;
-        int chosen = 0;
-        float last = 0.0f;
-        const int rounds = a.bias ? a.top_k + 1 : a.top_k;
+
+        // the next expert behind the chosen ones counts too, where keys are scores
+        const int want = a.bias ? a.top_k + 1 : a.top_k;
+        uint32_t floor_key = 0;
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (key[i] > best) {
-                best = key[i];
-                at = lane + 32 * i;
+        for (int i = 0; i < V; ++i) floor_key = max(floor_key, key[i]);
+        floor_key = want <= 32 ? __shfl_sync(0xffffffffu, sort_lanes(floor_key, lane), want - 1) : 0u;
+        floor_key = max(floor_key, kMasked);
+        int chosen = 0, n = 0;
+        // -> how many keys are no smaller than floor_key; the first 32 move to the list
+        auto gather = [&]() {
+            int m = 0;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const bool in = key[i] >= floor_key;
+                const uint32_t who = __ballot_sync(0xffffffffu, in);
+                const int at = m + __popc(who & ((1u << lane) - 1u));
+                if (in && at < 32) {
+                    list_key[w][at] = key[i];
+                    list_e[w][at] = lane + 32 * i;
+                }
+                m += __popc(who);
             }
-        for (int j = 0; j < rounds; ++j) {
-            const uint32_t k = __reduce_max_sync(0xffffffffu, best);
-            if (j < a.top_k) {
+            __syncwarp();
+            return m;
+        };
+        if (sure) {
+            n = gather();
+            if (n <= 32) {
+                const uint32_t k = lane < n ? list_key[w][lane] : kGone;
+                int e = lane < n ? list_e[w][lane] : 0, before = 0;
+                for (int j = 0; j < n; ++j) {
+                    const uint32_t o = __shfl_sync(0xffffffffu, k, j);
+                    before += o > k || (o == k && j < lane);
+                }
+                __syncwarp();
+                if (lane < n) {
+                    list_key[w][before] = k;
+                    list_e[w][before] = e;
+                }
+                __syncwarp();
+                chosen = list_e[w][lane < n ? lane : 0];
+                if (a.bias) {
+                    const uint32_t sorted = lane < n ? list_key[w][lane] : kGone;
+                    const float c = value_of(sorted), prev = __shfl_up_sync(0xffffffffu, c, 1);
+                    const bool close = lane > 0 && lane < want && lane < n && sorted > kMasked &&
+                                       !(prev - c > unsure + 2.5e-7f * fabsf(prev));
+                    if (__any_sync(0xffffffffu, close)) {
+                        // all that may belong to the chosen ones: whatever is not surely less
+                        // than the last of them
+                        const float last = __shfl_sync(0xffffffffu, c, a.top_k - 1);
+                        const uint32_t least = __shfl_sync(0xffffffffu, sorted, a.top_k - 1);
+                        __syncwarp();
+                        if (least > kMasked)
+                            floor_key = min(floor_key, key_of(last - (unsure + 2.5e-7f * fabsf(last))));
+                        n = gather();
+                        if (n <= 32) chosen = order_exactly(a, t, lane, n, list_e[w][lane < n ? lane : 0], list_e[w]);
+                    }
+                }
+            }
+            // many equal ones, or more than 31 of them wanted
+            if (n > 32 && a.bias) sure = false;
+        }
+        if (!sure) {
+            chosen = choose_exactly(a, t, lane, exact + (size_t)w * a.E);
+        } else if (n > 32) {
+            uint32_t best = 0;
+            int at = 0;
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (key[i] > best) {
+                    best = key[i];
+                    at = lane + 32 * i;
+                }
+            for (int j = 0; j < a.top_k; ++j) {
+                const uint32_t k = __reduce_max_sync(0xffffffffu, best);
                 const int e = (int)__reduce_min_sync(0xffffffffu, best == k ? (uint32_t)at : 0xffffffffu);
                 if (lane == j) chosen = e;
                 if (best == k && at == e) {
@@ -252,13 +398,7 @@ __global__ void __launch_bounds__(32 * kWarps) route_experts_kernel(const RouteE
                     }
                 }
             }
-            if (a.bias && k > kMasked) {
-                const float c = value_of(k);
-                if (j > 0 && !(last - c > unsure + 2.5e-7f * fabsf(last))) sure = false;
-                last = c;
-            }
         }
-        if (!sure) chosen = choose_exactly(a, t, lane, exact + (size_t)w * a.E);
 
         const bool has = lane < a.top_k;
         const float x = has ? logit_of(a, t, chosen) : -INFINITY;
@@ -284,15 +424,18 @@ __global__ void __launch_bounds__(32 * kWarps) route_experts_kernel(const RouteE
             a.ids[t * a.top_k + lane] = chosen;
             a.weights[t * a.top_k + lane] = v * a.scale;
         }
+        __syncwarp();
     }
 }
 
 template <int V>
 cudaError_t launch(const RouteExpertsArgs &a, int sms, cudaStream_t s) {
     const int64_t blocks = ((int64_t)a.M + kWarps - 1) / kWarps, most = (int64_t)sms * 16;
-    route_experts_kernel<V><<<(unsigned)(blocks < most ? blocks : most), 32 * kWarps,
-                              (size_t)kWarps * a.E * 8, s>>>(a);
-    return cudaGetLastError();
+    auto c = pdl_config((unsigned)(blocks < most ? blocks : most), 32 * kWarps, (size_t)kWarps * a.E * 8, s);
+    cudaLaunchAttribute at{};
+    c.numAttrs = pdl_attr(at);
+    c.attrs = &at;
+    return cudaLaunchKernelEx(&c, route_experts_kernel<V>, a);
 }
 
 }  // namespace
