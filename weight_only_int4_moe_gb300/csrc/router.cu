@@ -21,12 +21,13 @@ namespace moe {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr uint32_t kGone = 0, kMasked = 1;  // keys of what is taken or not open, and not available
+constexpr uint32_t kGone = 0;              // the key of what is taken or not open
+constexpr uint32_t kMasked = 0x007FFFFFu;  // of -inf: what is not available
 
-// A key that orders as the float does (numbers only), above kMasked.
+// A key that orders as the float does (no NaN; -0 is below +0).
 MOE_DEV uint32_t key_of(float x) {
-    const uint32_t u = __float_as_uint(x + 0.0f);  // (-0 and +0 are equal)
-    return (u >> 31) ? ~u : u | 0x80000000u;
+    const uint32_t u = __float_as_uint(x);
+    return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
 MOE_DEV float value_of(uint32_t k) {
     return __uint_as_float((k >> 31) ? k & 0x7FFFFFFFu : ~k);
@@ -45,11 +46,19 @@ MOE_DEV double sigmoid(double x) {
     const double t = exp(-fabs(x));
     return (x < 0.0 ? t : 1.0) / (1.0 + t);
 }
-// With the hardware's exponential (2^-22 relative; its argument's rounding adds |x| 2^-24) and
-// quotient (2 steps): within 3.7e-7.
+// With the hardware's exponential (2^-22 relative, and its argument's rounding, |x| 2^-23) and
+// reciprocal (one step): s (1 - s) (2^-22 + |x| 2^-23) + 3 2^-24, within 3e-7.  Far below 0 the
+// exponential is infinite and the score 0.
 MOE_DEV float sigmoid_fast(float x) {
-    const float t = __expf(-fabsf(x));
-    return __fdividef(x < 0.0f ? t : 1.0f, 1.0f + t);
+    float t, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(x * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + t));
+    return r;
+}
+MOE_DEV float exp_fast(float x) {
+    float t;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(x * 1.4426950408889634f));
+    return t;
 }
 
 MOE_DEV float warp_max(float v) {
@@ -201,18 +210,21 @@ MOE_DEV uint32_t sort_lanes(uint32_t v, int lane) {
     return v;
 }
 
+// What the keys are made of.
+constexpr int kLogits = 0, kSigmoid = 1, kSoftmax = 2;
+
 // V: experts of a lane.
-template <int V>
-__global__ void __launch_bounds__(32 * kWarps) route_experts_kernel(const RouteExpertsArgs a) {
-    extern __shared__ double exact[];
-    __shared__ uint32_t list_key[kWarps][32];
-    __shared__ int list_e[kWarps][32];
+template <int V, int KEYS>
+__global__ void __launch_bounds__(32 * kWarps, V <= 12 ? 6 : V <= 16 ? 4 : 2)
+    route_experts_kernel(const RouteExpertsArgs a) {
+    extern __shared__ uint2 room[];  // of a warp: E pairs (key, expert), or E 64-bit numbers
+    __shared__ int order[kWarps][32];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    uint2 *const list = room + (size_t)w * a.E;
     const int size = a.E / a.groups;
     const float per_group = 1.0f / (float)size;
-    const bool soft = a.scoring == MOE_SCORE_SOFTMAX;
-    const bool sums = a.groups > 1 && a.group_best == 2 && size > 1;
-    const bool scored = a.bias || sums;  // some keys are scores, not logits
+    const bool soft = KEYS == kSoftmax || (KEYS == kLogits && a.scoring == MOE_SCORE_SOFTMAX);
+    const bool sums = KEYS != kLogits && a.groups > 1 && a.group_best == 2 && size > 1;
     pdl_wait();
     pdl_launch_dependents();
     for (int64_t t = (int64_t)blockIdx.x * kWarps + w; t < a.M; t += (int64_t)gridDim.x * kWarps) {
@@ -223,17 +235,29 @@ __global__ void __launch_bounds__(32 * kWarps) route_experts_kernel(const RouteE
 #pragma unroll
             for (int i = 0; i < V; ++i) l[i] = lane + 32 * i < a.E ? p[32 * i] : -INFINITY;
         } else {
+            const uint16_t *p = reinterpret_cast<const uint16_t *>(a.logits) + t * a.stride + lane;
+            uint16_t r[V];
 #pragma unroll
-            for (int i = 0; i < V; ++i)
-                l[i] = lane + 32 * i < a.E ? load_as_float(a.logits, a.type, t * a.stride + lane + 32 * i)
-                                           : -INFINITY;
+            for (int i = 0; i < V; ++i) r[i] = lane + 32 * i < a.E ? p[32 * i] : (uint16_t)0xFFFFu;
+            // (all ones are NaN in either type)
+            if (a.type == MOE_T_BF16) {
+#pragma unroll
+                for (int i = 0; i < V; ++i) l[i] = __uint_as_float((uint32_t)r[i] << 16);
+            } else {
+#pragma unroll
+                for (int i = 0; i < V; ++i) l[i] = __half2float(__ushort_as_half(r[i]));
+            }
         }
+        if (KEYS != kLogits) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) b[i] = a.bias && lane + 32 * i < a.E ? a.bias[lane + 32 * i] : 0.0f;
+            for (int i = 0; i < V; ++i) b[i] = a.bias && lane + 32 * i < a.E ? a.bias[lane + 32 * i] : 0.0f;
+        }
+        if (KEYS != kSigmoid) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) l[i] = isnan(l[i]) ? -INFINITY : fminf(l[i], FLT_MAX);
+            for (int i = 0; i < V; ++i) l[i] = l[i] > -INFINITY ? fminf(l[i], FLT_MAX) : -INFINITY;
+        }
         float top = 0.0f, inv = 1.0f;
-        if (soft && (scored || !a.renormalize)) {
+        if (KEYS == kSoftmax || (soft && !a.renormalize)) {
             top = l[0];
 #pragma unroll
             for (int i = 1; i < V; ++i) top = fmaxf(top, l[i]);
@@ -241,20 +265,21 @@ __global__ void __launch_bounds__(32 * kWarps) route_experts_kernel(const RouteE
             if (top == -INFINITY) top = 0.0f;
             float sum = 0.0f;
 #pragma unroll
-            for (int i = 0; i < V; ++i) sum += __expf(l[i] - top);
+            for (int i = 0; i < V; ++i) sum += exp_fast(l[i] - top);
             sum = warp_sum(sum);
             inv = sum > 0.0f ? 1.0f / sum : 0.0f;
         }
         // bounds the error of the difference of two scores (the softmax's by its largest, and
         // by the sum's 37 additions at most); c adds its own rounding
-        const float unsure = soft ? 4e-6f * inv : 1e-6f;
+        const float unsure = KEYS == kSoftmax ? 4e-6f * inv : 1e-6f;
         bool sure = true;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const bool here = l[i] > -INFINITY && b[i] > -INFINITY;
-            float c = l[i];
-            if (scored) c = (soft ? __expf(l[i] - top) * inv : sigmoid_fast(l[i])) + b[i];
-            key[i] = lane + 32 * i < a.E ? here ? key_of(c) : kMasked : kGone;
+            float c = l[i] + 0.0f;  // (-0 and +0 are equal)
+            if (KEYS == kSigmoid) c = sigmoid_fast(l[i]) + b[i];
+            if (KEYS == kSoftmax) c = exp_fast(l[i] - top) * inv + b[i];
+            if (KEYS != kLogits) c = l[i] > -INFINITY && c > -INFINITY ? c : -INFINITY;
+            key[i] = lane + 32 * i < a.E ? key_of(c) : kGone;
         }
         if (a.groups > 1) {
             float mine = -INFINITY;
@@ -297,38 +322,37 @@ __global__ void __launch_bounds__(32 * kWarps) route_experts_kernel(const RouteE
             }
             float gap, edge;
             const uint32_t open = choose_groups(a, mine, lane, gap, edge);
-            if (scored && !(gap > 2.0f * unsure + 2.5e-7f * fabsf(edge))) sure = edge == -INFINITY;
+            if (KEYS != kLogits && !(gap > 2.0f * unsure + 2.5e-7f * fabsf(edge))) sure = edge == -INFINITY;
+            if (KEYS != kLogits && !a.bias) {
+                // inside the groups the logits decide
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const int e = lane + 32 * i;
-                if (e < a.E) {
-                    if (!a.bias && sums) key[i] = l[i] > -INFINITY ? key_of(l[i]) : kMasked;
-                    // e / size: E is at most 1024, so the product is off by less than 1 / (2 size)
-                    if (!((open >> (int)(((float)e + 0.5f) * per_group)) & 1u)) key[i] = kGone;
-                }
+                for (int i = 0; i < V; ++i)
+                    key[i] = lane + 32 * i < a.E ? key_of(logit_of(a, t, lane + 32 * i) + 0.0f) : kGone;
             }
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                // e / size: E is at most 1024, so the product is off by less than 1 / (2 size)
+                if (!((open >> (int)(((float)(lane + 32 * i) + 0.5f) * per_group)) & 1u)) key[i] = kGone;
         }
 
         // the next expert behind the chosen ones counts too, where keys are scores
-        const int want = a.bias ? a.top_k + 1 : a.top_k;
+        const bool scored = KEYS != kLogits && a.bias;
+        const int want = scored ? a.top_k + 1 : a.top_k;
         uint32_t floor_key = 0;
 #pragma unroll
         for (int i = 0; i < V; ++i) floor_key = max(floor_key, key[i]);
         floor_key = want <= 32 ? __shfl_sync(0xffffffffu, sort_lanes(floor_key, lane), want - 1) : 0u;
         floor_key = max(floor_key, kMasked);
         int chosen = 0, n = 0;
-        // -> how many keys are no smaller than floor_key; the first 32 move to the list
+        // lists the keys that are no smaller than floor_key, in index order -> how many
+        const uint32_t below = (1u << lane) - 1u;
         auto gather = [&]() {
             int m = 0;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const bool in = key[i] >= floor_key;
                 const uint32_t who = __ballot_sync(0xffffffffu, in);
-                const int at = m + __popc(who & ((1u << lane) - 1u));
-                if (in && at < 32) {
-                    list_key[w][at] = key[i];
-                    list_e[w][at] = lane + 32 * i;
-                }
+                if (in) list[m + __popc(who & below)] = make_uint2(key[i], (uint32_t)(lane + 32 * i));
                 m += __popc(who);
             }
             __syncwarp();
@@ -337,42 +361,37 @@ __global__ void __launch_bounds__(32 * kWarps) route_experts_kernel(const RouteE
         if (sure) {
             n = gather();
             if (n <= 32) {
-                const uint32_t k = lane < n ? list_key[w][lane] : kGone;
-                int e = lane < n ? list_e[w][lane] : 0, before = 0;
-                for (int j = 0; j < n; ++j) {
-                    const uint32_t o = __shfl_sync(0xffffffffu, k, j);
-                    before += o > k || (o == k && j < lane);
-                }
+                const uint2 own = lane < n ? list[lane] : make_uint2(kGone, 0u);
+                int before = 0;
+                for (int j = 0; j < n; ++j)  // (keys end below the largest number)
+                    before += __shfl_sync(0xffffffffu, own.x, j) + (j < lane) > own.x;
                 __syncwarp();
-                if (lane < n) {
-                    list_key[w][before] = k;
-                    list_e[w][before] = e;
-                }
+                if (lane < n) list[before] = own;
                 __syncwarp();
-                chosen = list_e[w][lane < n ? lane : 0];
-                if (a.bias) {
-                    const uint32_t sorted = lane < n ? list_key[w][lane] : kGone;
-                    const float c = value_of(sorted), prev = __shfl_up_sync(0xffffffffu, c, 1);
-                    const bool close = lane > 0 && lane < want && lane < n && sorted > kMasked &&
+                const uint2 sorted = lane < n ? list[lane] : make_uint2(kGone, 0u);
+                chosen = (int)sorted.y;
+                if (scored) {
+                    const float c = value_of(sorted.x), prev = __shfl_up_sync(0xffffffffu, c, 1);
+                    const bool close = lane > 0 && lane < want && lane < n && sorted.x > kMasked &&
                                        !(prev - c > unsure + 2.5e-7f * fabsf(prev));
                     if (__any_sync(0xffffffffu, close)) {
                         // all that may belong to the chosen ones: whatever is not surely less
                         // than the last of them
                         const float last = __shfl_sync(0xffffffffu, c, a.top_k - 1);
-                        const uint32_t least = __shfl_sync(0xffffffffu, sorted, a.top_k - 1);
-                        __syncwarp();
-                        if (least > kMasked)
+                        if (last > -INFINITY)  // (NaN: fewer than top_k are available)
                             floor_key = min(floor_key, key_of(last - (unsure + 2.5e-7f * fabsf(last))));
+                        __syncwarp();
                         n = gather();
-                        if (n <= 32) chosen = order_exactly(a, t, lane, n, list_e[w][lane < n ? lane : 0], list_e[w]);
+                        if (n <= 32)
+                            chosen = order_exactly(a, t, lane, n, lane < n ? (int)list[lane].y : 0, order[w]);
                     }
                 }
             }
             // many equal ones, or more than 31 of them wanted
-            if (n > 32 && a.bias) sure = false;
+            if (n > 32 && scored) sure = false;
         }
         if (!sure) {
-            chosen = choose_exactly(a, t, lane, exact + (size_t)w * a.E);
+            chosen = choose_exactly(a, t, lane, reinterpret_cast<double *>(list));
         } else if (n > 32) {
             uint32_t best = 0;
             int at = 0;
@@ -428,25 +447,32 @@ __global__ void __launch_bounds__(32 * kWarps) route_experts_kernel(const RouteE
     }
 }
 
-template <int V>
+template <int V, int KEYS>
 cudaError_t launch(const RouteExpertsArgs &a, int sms, cudaStream_t s) {
     const int64_t blocks = ((int64_t)a.M + kWarps - 1) / kWarps, most = (int64_t)sms * 16;
     auto c = pdl_config((unsigned)(blocks < most ? blocks : most), 32 * kWarps, (size_t)kWarps * a.E * 8, s);
     cudaLaunchAttribute at{};
     c.numAttrs = pdl_attr(at);
     c.attrs = &at;
-    return cudaLaunchKernelEx(&c, route_experts_kernel<V>, a);
+    return cudaLaunchKernelEx(&c, route_experts_kernel<V, KEYS>, a);
+}
+
+template <int V>
+cudaError_t by_keys(const RouteExpertsArgs &a, int sms, cudaStream_t s) {
+    const bool sums = a.groups > 1 && a.group_best == 2 && a.groups < a.E;
+    if (!a.bias && !sums) return launch<V, kLogits>(a, sms, s);
+    return a.scoring == MOE_SCORE_SOFTMAX ? launch<V, kSoftmax>(a, sms, s) : launch<V, kSigmoid>(a, sms, s);
 }
 
 }  // namespace
 
 cudaError_t launch_route_experts(const RouteExpertsArgs &a, int sms, cudaStream_t s) {
-    if (a.E <= 64) return launch<2>(a, sms, s);
-    if (a.E <= 128) return launch<4>(a, sms, s);
-    if (a.E <= 256) return launch<8>(a, sms, s);
-    if (a.E <= 384) return launch<12>(a, sms, s);
-    if (a.E <= 512) return launch<16>(a, sms, s);
-    return launch<32>(a, sms, s);
+    if (a.E <= 64) return by_keys<2>(a, sms, s);
+    if (a.E <= 128) return by_keys<4>(a, sms, s);
+    if (a.E <= 256) return by_keys<8>(a, sms, s);
+    if (a.E <= 384) return by_keys<12>(a, sms, s);
+    if (a.E <= 512) return by_keys<16>(a, sms, s);
+    return by_keys<32>(a, sms, s);
 }
 
 }  // namespace moe
