@@ -130,6 +130,32 @@ __device__ __noinline__ int order_exactly(const RouteExpertsArgs &a, int64_t row
     return list[lane];
 }
 
+// The groups of a token where some lie too near to the border for fp32: lane g has group g's
+// value, and for the groups in `close` the best experts' c are formed in 64 bits: lane j < n
+// has one, expert e.  -> the chosen groups.
+__device__ __noinline__ uint32_t groups_exactly(const RouteExpertsArgs &a, int64_t row, int lane, int n,
+                                                int e, float value, uint32_t close) {
+    double top, inv;
+    softmax_exactly(a, row, lane, top, inv);
+    const double c = lane < n ? score_exactly(a, row, e, top, inv) : -INFINITY;
+    const int mine = lane < n ? e / (a.E / a.groups) : -1;
+    double of_group = (double)value;
+    for (; close; close &= close - 1) {
+        const int g = __ffs(close) - 1;
+        double x = mine == g ? c : -INFINITY, y = -INFINITY;  // the two best
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+            const double x2 = __shfl_xor_sync(0xffffffffu, x, o);
+            const double y2 = __shfl_xor_sync(0xffffffffu, y, o);
+            y = fmax(fmin(x, x2), fmax(y, y2));
+            x = fmax(x, x2);
+        }
+        if (lane == g) of_group = a.group_best == 2 && y > -INFINITY ? x + y : x;
+    }
+    double gap, edge;
+    return choose_groups(a, of_group, lane, gap, edge);
+}
+
 // The whole choice in 64 bits; c: room for E numbers.  -> the lane's expert.
 __device__ __noinline__ int choose_exactly(const RouteExpertsArgs &a, int64_t row, int lane, double *c) {
     double top, inv;
@@ -221,6 +247,7 @@ __global__ void __launch_bounds__(32 * kWarps, V <= 12 ? 6 : V <= 16 ? 4 : 2)
     __shared__ int order[kWarps][32];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     uint2 *const list = room + (size_t)w * a.E;
+    const uint32_t below = (1u << lane) - 1u;
     const int size = a.E / a.groups;
     const float per_group = 1.0f / (float)size;
     const bool soft = KEYS == kSoftmax || (KEYS == kLogits && a.scoring == MOE_SCORE_SOFTMAX);
@@ -283,6 +310,7 @@ __global__ void __launch_bounds__(32 * kWarps, V <= 12 ? 6 : V <= 16 ? 4 : 2)
         }
         if (a.groups > 1) {
             float mine = -INFINITY;
+            uint32_t least = kMasked;  // the last of the group's experts that count
             // the warp's two best of a group -> its value, in lane g
             auto value = [&](int g, uint32_t x, uint32_t y) {
                 const uint32_t best = __reduce_max_sync(0xffffffffu, x);
@@ -291,6 +319,7 @@ __global__ void __launch_bounds__(32 * kWarps, V <= 12 ? 6 : V <= 16 ? 4 : 2)
                     const uint32_t who = __ballot_sync(0xffffffffu, x == best);
                     second = __popc(who) > 1 ? best : __reduce_max_sync(0xffffffffu, x == best ? y : x);
                 }
+                if (lane == g) least = sums ? second : best;
                 if (lane == g && best > kMasked)
                     mine = second > kMasked ? value_of(best) + value_of(second) : value_of(best);
             };
@@ -321,8 +350,35 @@ __global__ void __launch_bounds__(32 * kWarps, V <= 12 ? 6 : V <= 16 ? 4 : 2)
                 }
             }
             float gap, edge;
-            const uint32_t open = choose_groups(a, mine, lane, gap, edge);
-            if (KEYS != kLogits && !(gap > 2.0f * unsure + 2.5e-7f * fabsf(edge))) sure = edge == -INFINITY;
+            uint32_t open = choose_groups(a, mine, lane, gap, edge);
+            if (KEYS != kLogits) {
+                // (-inf: fewer groups than that have an expert left)
+                const float near = 2.0f * unsure + 2.5e-7f * fabsf(edge);
+                if (!(gap > near) && edge > -INFINITY) {
+                    const uint32_t close =
+                        __ballot_sync(0xffffffffu, lane < a.groups && !(fabsf(mine - edge) > 2.0f * near));
+                    if (least > kMasked) {
+                        const float v = value_of(least);
+                        least = key_of(v - (unsure + 2.5e-7f * fabsf(v)));
+                    }
+                    least = max(least, kMasked + 1u);
+                    int m = 0;
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        const int g = (int)(((float)(lane + 32 * i) + 0.5f) * per_group) & 31;
+                        const bool in = key[i] >= __shfl_sync(0xffffffffu, least, g) && ((close >> g) & 1u);
+                        const uint32_t who = __ballot_sync(0xffffffffu, in);
+                        if (in) list[m + __popc(who & below)] = make_uint2(0u, (uint32_t)(lane + 32 * i));
+                        m += __popc(who);
+                    }
+                    __syncwarp();
+                    if (m <= 32)
+                        open = groups_exactly(a, t, lane, m, lane < m ? (int)list[lane].y : 0, mine, close);
+                    else
+                        sure = false;
+                    __syncwarp();
+                }
+            }
             if (KEYS != kLogits && !a.bias) {
                 // inside the groups the logits decide
 #pragma unroll
@@ -345,7 +401,6 @@ __global__ void __launch_bounds__(32 * kWarps, V <= 12 ? 6 : V <= 16 ? 4 : 2)
         floor_key = max(floor_key, kMasked);
         int chosen = 0, n = 0;
         // lists the keys that are no smaller than floor_key, in index order -> how many
-        const uint32_t below = (1u << lane) - 1u;
         auto gather = [&]() {
             int m = 0;
 #pragma unroll
