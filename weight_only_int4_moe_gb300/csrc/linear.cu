@@ -27,6 +27,7 @@ constexpr int kLine = 128;                  // bytes of k of a stage
 constexpr int kBytesW = kRowsW * kLine;
 constexpr int kThreads = 320;               // warps 0-7 epilogue, 8 copies, 9 products
 constexpr int kEpilogue = 8;                // warps
+constexpr int kMaxSmem = 227 * 1024 - 1024; // of a block, beside its few static bytes
 
 MOE_DEV uint32_t cluster_rank() {
     uint32_t r;
@@ -55,6 +56,10 @@ MOE_DEV float4 ld_cluster4(uint32_t addr) {
                  : "r"(addr)
                  : "memory");
     return v;
+}
+MOE_DEV void prefetch_2d(const void *tmap, int32_t c0, int32_t c1) {
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(tmap), "r"(c0), "r"(c1)
+                 : "memory");
 }
 MOE_DEV void arrive_at(uint32_t addr) {  // (an address of map_to)
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
@@ -254,9 +259,8 @@ MOE_DEV void column_out(const LinearArgs &a, uint32_t taddr, int m, int n, int c
 
 // A block's whole tile, 128 columns from n0 by `rows` output rows from m0: each warp the lanes
 // it can reach and every other run of C rows.
-template <int TN>
+template <int C>
 MOE_DEV void tile_out(const LinearArgs &a, uint32_t tmem, int m0, int n0, int rows, int w, int lane) {
-    constexpr int C = TN >= 64 ? 32 : 16;
     const int n = n0 + (w & 3) * 32 + lane;
     const bool mine = n < a.N;
     const float sw = mine && a.w_scale ? a.w_scale[n] : 1.0f;
@@ -341,43 +345,47 @@ MOE_DEV void quad_out(const LinearArgs &a, int m, int n, float (&v)[4], const fl
 }
 
 // ----------------------------------------------------- one tile a cluster --
-template <int TN>
-struct Split {
-    static constexpr int kStage = kBytesW + TN * kLine;
-    static constexpr int kStages = TN >= 128 ? 4 : 5;
-    static constexpr int kSmem = kStages * kStage + 1024;  // (stages begin at multiples of 1024)
-    static constexpr uint32_t kCols = TN < 32 ? 32 : TN;   // of tensor memory
-    static_assert(TN * kRowsW * 4 <= kStages * kStage, "the parts lie where the stages were");
+// How a product is cut: rows of x of a tile (a multiple of 16 up to 256), blocks that share a
+// tile's k, and stages of a block.
+struct Cut {
+    int tn, split, stages;
+    int stage_bytes() const { return kBytesW + tn * kLine; }
+    int smem() const { return stages * stage_bytes() + 1024; }  // (stages begin at multiples of 1024)
 };
+constexpr int kMaxStages = 12, kMaxSplit = 8;
 
-template <int TN, bool CODES>
-__global__ void __launch_bounds__(kThreads)
+template <bool CODES>
+__global__ void __launch_bounds__(kThreads, 2)
     linear_split_kernel(const __grid_constant__ CUtensorMap wmap,
-                        const __grid_constant__ CUtensorMap xmap, const LinearArgs a) {
-    using T = Split<TN>;
+                        const __grid_constant__ CUtensorMap xmap, const LinearArgs a, const int tn,
+                        const int n_stages) {
     extern __shared__ uint8_t dyn[];
-    __shared__ alignas(8) uint64_t bars[2 * T::kStages + 1];
+    __shared__ alignas(8) uint64_t bars[2 * kMaxStages + 1];
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
     const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
     const uint32_t rank = cluster_rank(), S = cluster_size();
-    const int n0 = (int)(blockIdx.x / S) * kRowsW, m0 = (int)blockIdx.y * TN;
+    const int n0 = (int)(blockIdx.x / S) * kRowsW, m0 = (int)blockIdx.y * tn;
+    const uint32_t stage_bytes = kBytesW + tn * kLine;
     const uint32_t stages = (smem_u32(dyn) + 1023u) & ~1023u;
-    const uint32_t full = smem_u32(bars), empty = full + 8 * T::kStages, done = full + 16 * T::kStages;
+    const uint32_t full = smem_u32(bars), empty = full + 8 * kMaxStages, done = full + 16 * kMaxStages;
+    const uint32_t cols = tn <= 32 ? 32 : tn <= 64 ? 64 : tn <= 128 ? 128 : 256;  // of tensor memory
     constexpr int kElems = CODES ? kLine : kLine / 2;
     const int kb = (a.K + kElems - 1) / kElems;
     const int kb0 = (int)((int64_t)kb * rank / S), kb1 = (int)((int64_t)kb * (rank + 1) / S);
 
     if (tid == 0) {
         abort_flag = 0;
-        for (int i = 0; i < 2 * T::kStages + 1; ++i) mbar_init(full + 8 * i, 1);
+        for (int i = 0; i < 2 * kMaxStages + 1; ++i) mbar_init(full + 8 * i, 1);
         mbar_fence_init();
     }
+    // The first lines of w come to L2 while the previous kernel ends.
+    if (w == 8 && lane < n_stages && kb0 + lane < kb1) prefetch_2d(&wmap, (kb0 + lane) * kElems, n0);
     // Tensor memory is taken behind the previous kernel, whose blocks may still want theirs, and
     // before the next one may start.
     pdl_wait();
     if (w == 9) {
-        tmem_alloc(smem_u32(&tmem_slot), T::kCols);
+        tmem_alloc(smem_u32(&tmem_slot), cols);
         tmem_relinquish();
     }
     tc_fence_before();
@@ -388,12 +396,12 @@ __global__ void __launch_bounds__(kThreads)
 
     if (w == 8) {
         if (lane == 0) {
-            Ring r(T::kStages);
+            Ring r(n_stages);
             int issued = 0;
             for (int k = kb0; k < kb1; ++k, r.next()) {
                 if (!mbar_wait(empty + 8 * r.idx, r.ph ^ 1, &abort_flag, a.err)) break;
-                const uint32_t bar = full + 8 * r.idx, s = stages + r.idx * T::kStage;
-                mbar_arrive_expect_tx(bar, T::kStage);
+                const uint32_t bar = full + 8 * r.idx, s = stages + r.idx * stage_bytes;
+                mbar_arrive_expect_tx(bar, stage_bytes);
                 tma_load_2d(s, &wmap, k * kElems, n0, bar);
                 tma_load_2d(s + kBytesW, &xmap, k * kElems, m0, bar);
                 ++issued;
@@ -401,19 +409,19 @@ __global__ void __launch_bounds__(kThreads)
             if (*(volatile int *)&abort_flag) {
                 // the copies in flight end before the block does
                 volatile int none = 0;
-                Ring q(T::kStages);
+                Ring q(n_stages);
                 for (int i = 0; i < issued; ++i, q.next())
-                    if (i >= issued - T::kStages) mbar_wait(full + 8 * q.idx, q.ph, &none, a.err);
+                    if (i >= issued - n_stages) mbar_wait(full + 8 * q.idx, q.ph, &none, a.err);
             }
         }
         __syncwarp();
     } else if (w == 9) {
-        const uint32_t idesc = idesc_of(a.type, 128, TN);
-        Ring r(T::kStages);
+        const uint32_t idesc = idesc_of(a.type, 128, tn);
+        Ring r(n_stages);
         for (int k = kb0; k < kb1; ++k, r.next()) {
             if (__any_sync(0xffffffffu, !mbar_wait(full + 8 * r.idx, r.ph, &abort_flag, a.err))) break;
             tc_fence_after();
-            const uint32_t s = stages + r.idx * T::kStage;
+            const uint32_t s = stages + r.idx * stage_bytes;
             mma_stage<CODES, false>(tmem, smem_desc_sw128(s), smem_desc_sw128(s + kBytesW), idesc,
                                     k > kb0, empty + 8 * r.idx);
         }
@@ -426,9 +434,9 @@ __global__ void __launch_bounds__(kThreads)
         __syncwarp();
         tc_fence_after();
     }
-    const int rows = min(TN, a.M - m0);  // output rows of the tile
+    const int rows = min(tn, a.M - m0);  // output rows of the tile
     if (S == 1) {
-        if (w < kEpilogue) tile_out<TN>(a, tmem, m0, n0, rows, w, lane);
+        if (w < kEpilogue) tile_out<16>(a, tmem, m0, n0, rows, w, lane);
     } else {
         // parts[m][n]: 128 fp32 numbers for each output row
         if (w < kEpilogue) {
@@ -481,7 +489,7 @@ __global__ void __launch_bounds__(kThreads)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (w == 9) tmem_dealloc(tmem, T::kCols);
+    if (w == 9) tmem_dealloc(tmem, cols);
 }
 
 // ------------------------------------------------ two blocks, many tiles --
@@ -618,7 +626,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             tile_at(t, tiles_m, tiles_n, tm, tn);
             if (!__all_sync(0xffffffffu, mbar_wait(sums_full + 8 * acc.idx, acc.ph, &abort_flag, a.err))) break;
             tc_fence_after();
-            tile_out<TN>(a, tmem + acc.idx * TN, tm * TN, tn * 2 * kRowsW + (int)rank * kRowsW,
+            tile_out<32>(a, tmem + acc.idx * TN, tm * TN, tn * 2 * kRowsW + (int)rank * kRowsW,
                          min(TN, a.M - tm * TN), w, lane);
             tc_fence_before();
             __syncwarp();
@@ -713,32 +721,35 @@ cudaError_t launch_pair(const LinearArgs &a, const Operands &o, cudaStream_t s) 
     return cudaLaunchKernelEx(&c, linear_pair_kernel<TN, CODES>, wmap, xmap, a);
 }
 
-template <int TN, bool CODES>
-cudaError_t launch_split(const LinearArgs &a, const Operands &o, cudaStream_t s) {
-    using T = Split<TN>;
+template <bool CODES>
+cudaError_t launch_split(const LinearArgs &a, const Operands &o, const Cut &cut, cudaStream_t s) {
+    // (the parts lie where the stages were)
+    if (cut.stages < 2 || cut.tn * kRowsW * 4 > cut.stages * cut.stage_bytes()) return cudaErrorInvalidValue;
     static std::atomic<int> known[64];
     int one;
-    cudaError_t e = prepare(linear_split_kernel<TN, CODES>, T::kSmem, known, &one, 0);
+    cudaError_t e = prepare(linear_split_kernel<CODES>, kMaxSmem, known, &one, 0);
     if (e != cudaSuccess) return e;
     CUtensorMap wmap, xmap;
     if (!rows_map(&wmap, o.w, o.w_stride, a.N, a.K, a.type, kRowsW) ||
-        !rows_map(&xmap, o.x, o.x_stride, a.M, a.K, a.type, TN))
+        !rows_map(&xmap, o.x, o.x_stride, a.M, a.K, a.type, cut.tn))
         return cudaErrorNotSupported;
-    const int tiles_n = (a.N + kRowsW - 1) / kRowsW, tiles_m = (a.M + TN - 1) / TN;
-    const int kb = (a.K * (CODES ? 1 : 2) + kLine - 1) / kLine;
-    // Blocks that share a tile: as many as fill the GPU about twice over (two blocks of a few
-    // tokens lie on an SM), each with a few stages at least.
-    int S = 1;
-    while (S < 8 && (int64_t)tiles_n * tiles_m * S * 2 <= 2 * o.sms && kb >= 8 * S) S *= 2;
-    auto c = pdl_config(1, kThreads, T::kSmem, s);
-    c.gridDim = dim3((unsigned)(tiles_n * S), (unsigned)tiles_m);
+    auto c = pdl_config(1, kThreads, (size_t)cut.smem(), s);
+    c.gridDim = dim3((unsigned)((a.N + kRowsW - 1) / kRowsW * cut.split),
+                     (unsigned)((a.M + cut.tn - 1) / cut.tn));
     cudaLaunchAttribute at[2] = {};
     c.numAttrs = 1 + pdl_attr(at[0]);
     at[1].id = cudaLaunchAttributeClusterDimension;
-    at[1].val.clusterDim.x = (unsigned)S;
+    at[1].val.clusterDim.x = (unsigned)cut.split;
     at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     c.attrs = at;
-    return cudaLaunchKernelEx(&c, linear_split_kernel<TN, CODES>, wmap, xmap, a);
+    return cudaLaunchKernelEx(&c, linear_split_kernel<CODES>, wmap, xmap, a, cut.tn, cut.stages);
+}
+
+Cut make_cut(int tn, int split, int per_sm) {
+    Cut c{tn, split, 0};
+    c.stages = (kMaxSmem / per_sm - 1024 * per_sm) / c.stage_bytes();
+    if (c.stages > kMaxStages) c.stages = kMaxStages;
+    return c;
 }
 
 template <bool CODES>
@@ -749,11 +760,12 @@ cudaError_t by_size(const LinearArgs &a, const Operands &o, cudaStream_t s) {
             return launch_pair<256, CODES>(a, o, s);
         return launch_pair<128, CODES>(a, o, s);
     }
-    if (a.M <= 16) return launch_split<16, CODES>(a, o, s);
-    if (a.M <= 32) return launch_split<32, CODES>(a, o, s);
-    if (a.M <= 64) return launch_split<64, CODES>(a, o, s);
-    if (a.M <= 128) return launch_split<128, CODES>(a, o, s);
-    return launch_split<256, CODES>(a, o, s);
+    const int tn = a.M >= 128 ? 128 : (a.M + 15) / 16 * 16;
+    const int64_t tiles = (int64_t)((a.N + kRowsW - 1) / kRowsW) * ((a.M + tn - 1) / tn);
+    const int kb = (a.K * (CODES ? 1 : 2) + kLine - 1) / kLine;
+    int S = 1;
+    while (S < kMaxSplit && tiles * S * 2 <= 2 * o.sms && kb >= 8 * S) S *= 2;
+    return launch_split<CODES>(a, o, make_cut(tn, S, tiles * S > o.sms ? 2 : 1), s);
 }
 
 // Four neighbours of a row may be one access.

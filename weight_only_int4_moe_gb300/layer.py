@@ -15,7 +15,7 @@ from typing import NamedTuple
 import torch
 
 from . import ops
-from .kv4 import _empty, _on, _raw_stream
+from .kv4 import _empty, _like, _raw_stream
 
 MOE_T_BF16 = 0
 MOE_T_F32 = 1
@@ -55,6 +55,9 @@ def load_library():
 
 # The checks below run before every launch and are kept short: a single-token step is
 # bound by what the host does per call.
+_here = torch._C._cuda_getDevice
+
+
 def _device_of(t, what):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{what}: expected a CUDA tensor")
@@ -85,6 +88,17 @@ def _vector(t, what, index, n, dtype=_F32):
     return t.data_ptr()
 
 
+def _call(fn, name, index, args):
+    """fn(*args) with the tensors' device as the current one."""
+    if _here() == index:
+        rc = fn(*args)
+    else:
+        with torch.cuda.device(index):
+            rc = fn(*args)
+    if rc:
+        ops._check(rc, name)
+
+
 class Normed(NamedTuple):
     """What moe_add_norm returns; None for what was not asked for."""
     out: torch.Tensor | None
@@ -107,14 +121,16 @@ def moe_add_norm(x, weight=None, residual=None, eps: float = 1e-6, out_dtype=tor
     shape = x.shape
     rows, hidden = shape
     xp, xt, xs = _matrix(x, "x", dev, shape, _TYPES)
-    rp, rt, rs, np_, ns = None, 0, 0, None, 0
+    rp, rt, rs, np_, ns = None, 0, 0, None, hidden
     if residual is not None:
         rp, rt, rs = _matrix(residual, "residual", dev, shape, _TYPES)
         if residual_out is None:
             residual_out = _empty(shape, residual.dtype, residual.device, stream)
-        elif residual_out.dtype is not residual.dtype:
-            raise TypeError(f"residual_out: expected {residual.dtype}, got {residual_out.dtype}")
-        np_, _, ns = _matrix(residual_out, "residual_out", dev, shape, _TYPES)
+            np_ = residual_out.data_ptr()
+        else:
+            if residual_out.dtype is not residual.dtype:
+                raise TypeError(f"residual_out: expected {residual.dtype}, got {residual_out.dtype}")
+            np_, _, ns = _matrix(residual_out, "residual_out", dev, shape, _TYPES)
     elif residual_out is not None:
         raise ValueError("residual_out: there is no residual")
     wp, wt = None, 0
@@ -123,13 +139,15 @@ def moe_add_norm(x, weight=None, residual=None, eps: float = 1e-6, out_dtype=tor
         if wt is None:
             raise TypeError(f"weight: {weight.dtype} is not supported")
         wp = _vector(weight, "weight", dev, hidden, weight.dtype)
-    op, ot, os = None, 0, 0
-    if out is None and out_dtype is not None:
-        if out_dtype not in _TYPES:
-            raise TypeError(f"out_dtype: {out_dtype} is not supported")
-        out = _empty(shape, out_dtype, x.device, stream)
+    op, ot, os = None, 0, hidden
     if out is not None:
         op, ot, os = _matrix(out, "out", dev, shape, _TYPES)
+    elif out_dtype is not None:
+        ot = _TYPES.get(out_dtype)
+        if ot is None:
+            raise TypeError(f"out_dtype: {out_dtype} is not supported")
+        out = _empty(shape, out_dtype, x.device, stream)
+        op = out.data_ptr()
     cp, cs, sp = None, 0, None
     if codes is not False and codes is not None:
         if codes is True:
@@ -142,12 +160,9 @@ def moe_add_norm(x, weight=None, residual=None, eps: float = 1e-6, out_dtype=tor
         raise ValueError("scales: there are no codes")
     else:
         codes = None
-    with _on(dev):
-        rc = (_lib or load_library()).moe_add_norm(
-            xp, xt, xs, rp, rt, rs, wp, wt, eps, rows, hidden, np_, ns, op, ot, os, cp, cs, sp,
+    args = (xp, xt, xs, rp, rt, rs, wp, wt, eps, rows, hidden, np_, ns, op, ot, os, cp, cs, sp,
             _raw_stream(stream, dev))
-    if rc:
-        ops._check(rc, "moe_add_norm")
+    _call((_lib or load_library()).moe_add_norm, "moe_add_norm", dev, args)
     return Normed(out, residual_out, codes, scales)
 
 
@@ -209,17 +224,17 @@ def moe_linear(x, linear: Linear, activation=None, gate=None, residual=None, x_s
     rp, rt, rs = (None, 0, 0) if residual is None else \
         _matrix(residual, "residual", dev, shape, _TYPES)
     if out is None:
-        if out_dtype not in _TYPES:
+        ot, os = _TYPES.get(out_dtype), linear.N
+        if ot is None:
             raise TypeError(f"out_dtype: {out_dtype} is not supported")
         out = _empty(shape, out_dtype, linear.device, stream)
-    op, ot, os = _matrix(out, "out", dev, shape, _TYPES)
-    with _on(dev):
-        rc = (_lib or load_library()).moe_linear(
-            xp, xs, sp, linear.ptr, linear.stride, linear.scale_ptr, linear.type, linear.bias_ptr,
+        op = out.data_ptr()
+    else:
+        op, ot, os = _matrix(out, "out", dev, shape, _TYPES)
+    args = (xp, xs, sp, linear.ptr, linear.stride, linear.scale_ptr, linear.type, linear.bias_ptr,
             act, gp, gt, gs, rp, rt, rs, op, ot, os, m, linear.N, linear.K, linear.err_ptr,
             _raw_stream(stream, dev))
-    if rc:
-        ops._check(rc, "moe_linear")
+    _call((_lib or load_library()).moe_linear, "moe_linear", dev, args)
     return out
 
 
@@ -240,19 +255,17 @@ def moe_route_experts(logits, top_k: int, scoring: str = "softmax", bias=None, g
         raise ValueError(f"scoring: {scoring!r} is not one of {list(SCORES)}")
     lp, lt, ls = _matrix(logits, "logits", dev, shape, _TYPES)
     bp = None if bias is None else _vector(bias, "bias", dev, e)
+    size = (m, top_k)
     if topk_ids is None:
-        topk_ids = _empty((m, top_k), _I32, logits.device, stream)
+        topk_ids = _empty(size, _I32, logits.device, stream)
+    else:
+        _like(topk_ids, "topk_ids", dev, _I32, size)
     if topk_weights is None:
-        topk_weights = _empty((m, top_k), _F32, logits.device, stream)
-    for t, what, dtype in ((topk_ids, "topk_ids", _I32), (topk_weights, "topk_weights", _F32)):
-        if t.dtype is not dtype or t.shape != (m, top_k) or t.get_device() != dev or \
-                not t.is_contiguous():
-            raise ValueError(f"{what}: expected a contiguous {dtype} [{m}, {top_k}] on cuda:{dev}")
-    with _on(dev):
-        rc = (_lib or load_library()).moe_route_experts(
-            lp, lt, ls, bp, m, e, top_k, kind, groups, groups if top_groups is None else top_groups,
+        topk_weights = _empty(size, _F32, logits.device, stream)
+    else:
+        _like(topk_weights, "topk_weights", dev, _F32, size)
+    args = (lp, lt, ls, bp, m, e, top_k, kind, groups, groups if top_groups is None else top_groups,
             group_best, 1 if renormalize else 0, scale, topk_ids.data_ptr(),
             topk_weights.data_ptr(), _raw_stream(stream, dev))
-    if rc:
-        ops._check(rc, "moe_route_experts")
+    _call((_lib or load_library()).moe_route_experts, "moe_route_experts", dev, args)
     return topk_ids, topk_weights
