@@ -52,6 +52,7 @@ struct LinearArgs {
     MatOut out;
     uint32_t *err;
     bool vec_gate, vec_residual, vec_out;  // four neighbours of a row may be one access
+    bool vec2;  // two may, in each of the three
 };
 
 struct RouteExpertsArgs {

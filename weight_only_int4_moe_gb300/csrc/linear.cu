@@ -14,7 +14,9 @@
 // next.  Otherwise linear_split_kernel: one tile of 128 by TN a cluster, whose blocks share the
 // tile's k and add their parts up through distributed shared memory, in the order of the
 // blocks: no workspace, and the same bits every time.
+#include <algorithm>
 #include <atomic>
+#include <cmath>
 
 #include "layer.cuh"
 
@@ -120,31 +122,17 @@ MOE_DEV void commit_both(uint32_t bar) {
 // no use of them moves ahead of the wait.
 template <int C>
 struct Cols {
+    static_assert(C == 16, "columns of a load");
     uint32_t r[C];
     MOE_DEV void issue(uint32_t taddr) {
-        static_assert(C == 16 || C == 32, "");
-        if constexpr (C == 16)
-            asm volatile(
-                "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
-                "%11, %12, %13, %14, %15}, [%16];"
-                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-                  "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
-                  "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-                : "r"(taddr)
-                : "memory");
-        else
-            asm volatile(
-                "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
-                "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
-                "%28, %29, %30, %31}, [%32];"
-                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-                  "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
-                  "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
-                  "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-                  "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
-                  "=r"(r[31])
-                : "r"(taddr)
-                : "memory");
+        asm volatile(
+            "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+            "%11, %12, %13, %14, %15}, [%16];"
+            : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+              "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+              "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+            : "r"(taddr)
+            : "memory");
     }
     MOE_DEV void wait() {
         asm volatile("tcgen05.wait::ld.sync.aligned;"
@@ -153,14 +141,6 @@ struct Cols {
                        "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
                      :
                      : "memory");
-        if constexpr (C == 32)
-            asm volatile(""
-                         : "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]),
-                           "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]),
-                           "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]),
-                           "+r"(r[31])
-                         :
-                         : "memory");
     }
 };
 
@@ -183,92 +163,185 @@ MOE_DEV void activate(int act, float (&v)[C]) {
     }
 }
 
-// C elements of a column of a matrix, as they lie in memory (`cols` of them exist).
-template <int C>
-struct Column {
-    uint32_t r[C];
+// Two neighbouring columns of a matrix in eight rows two apart, as they lie in memory.
+struct Pairs {
+    uint32_t r[16];
     MOE_DEV void load(const MatIn &s, int m, int n, int cols) {
         const int64_t at = (int64_t)m * s.stride + n;
         if (s.type == MOE_T_F32) {
-            const uint32_t *p = reinterpret_cast<const uint32_t *>(s.p) + at;
+            const float *p = reinterpret_cast<const float *>(s.p) + at;
 #pragma unroll
-            for (int j = 0; j < C; ++j) r[j] = j < cols ? p[j * s.stride] : 0u;
+            for (int q = 0; q < 8; ++q) {
+                const uint2 v = 2 * q < cols ? *reinterpret_cast<const uint2 *>(p + 2 * q * s.stride)
+                                             : make_uint2(0u, 0u);
+                r[2 * q] = v.x, r[2 * q + 1] = v.y;
+            }
         } else {
             const uint16_t *p = reinterpret_cast<const uint16_t *>(s.p) + at;
 #pragma unroll
-            for (int j = 0; j < C; ++j) r[j] = j < cols ? p[j * s.stride] : 0u;
+            for (int q = 0; q < 8; ++q)
+                r[q] = 2 * q < cols ? *reinterpret_cast<const uint32_t *>(p + 2 * q * s.stride) : 0u;
         }
     }
-    MOE_DEV void get(int type, float (&f)[C]) const {
+    MOE_DEV void get(int type, float (&f)[16]) const {
         if (type == MOE_T_F32) {
 #pragma unroll
-            for (int j = 0; j < C; ++j) f[j] = __uint_as_float(r[j]);
+            for (int i = 0; i < 16; ++i) f[i] = __uint_as_float(r[i]);
+        } else if (type == MOE_T_BF16) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                f[2 * q] = __uint_as_float(r[q] << 16);
+                f[2 * q + 1] = __uint_as_float(r[q] & 0xFFFF0000u);
+            }
         } else {
 #pragma unroll
-            for (int j = 0; j < C; ++j) f[j] = from_bits16(r[j], type);
+            for (int q = 0; q < 8; ++q) {
+                const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&r[q]));
+                f[2 * q] = v.x;
+                f[2 * q + 1] = v.y;
+            }
         }
     }
 };
 
-// Column n of C output rows m.. (cols of them exist), from this thread's lane of tensor memory.
-// The other operands are asked for before the sums are waited for.
-template <int C>
-MOE_DEV void column_out(const LinearArgs &a, uint32_t taddr, int m, int n, int cols, bool mine,
-                        float sw, float bias) {
-    Cols<C> acc;
-    acc.issue(taddr);
-    Column<C> gate, residual;
-    if (a.gate.p && mine) gate.load(a.gate, m, n, cols);
-    if (a.residual.p && mine) residual.load(a.residual, m, n, cols);
-    acc.wait();
-    if (!mine) return;
-    float v[C], f[C];
-#pragma unroll
-    for (int j = 0; j < C; ++j) v[j] = __uint_as_float(acc.r[j]);
-    if (a.x_scale) {
-#pragma unroll
-        for (int j = 0; j < C; ++j)
-            if (j < cols) v[j] *= a.x_scale[m + j];
-    }
-#pragma unroll
-    for (int j = 0; j < C; ++j) v[j] = v[j] * sw + bias;
-    activate<C>(a.activation, v);
-    if (a.gate.p) {
-        gate.get(a.gate.type, f);
-#pragma unroll
-        for (int j = 0; j < C; ++j) v[j] *= f[j];
-    }
-    if (a.residual.p) {
-        residual.get(a.residual.type, f);
-#pragma unroll
-        for (int j = 0; j < C; ++j) v[j] += f[j];
-    }
-    const int64_t at = (int64_t)m * a.out.stride + n;
-    if (a.out.type == MOE_T_F32) {
-        float *p = reinterpret_cast<float *>(a.out.p) + at;
-#pragma unroll
-        for (int j = 0; j < C; ++j)
-            if (j < cols) p[j * a.out.stride] = v[j];
-    } else {
-        uint16_t *p = reinterpret_cast<uint16_t *>(a.out.p) + at;
-#pragma unroll
-        for (int j = 0; j < C; ++j)
-            if (j < cols) p[j * a.out.stride] = to_bits16(v[j], a.out.type);
-    }
-}
+// The block's part of a tile: 128 columns from n0 by `rows` output rows from m0, in the sums at
+// `tmem`.  A warp takes the lanes it can reach and every other run of 16 rows.  A lane has one
+// column of the sums; lanes 2i and 2i + 1 trade, so that either has both columns of every other
+// row, and a row takes half the accesses.  (Each lane with its own column, two bytes an access,
+// 34 instructions an element made the epilogue the bound: 8192 x 7168 from K = 512 with a
+// residual 143 us.)  The gate and the residual of a run are asked for DEPTH runs ahead, the
+// first ones before the sums are complete (begin).
+template <int DEPTH>
+struct TileOut {
+    static constexpr int C = 16;
+    Pairs gate[DEPTH], residual[DEPTH];
+    int m0, rows, n, c;
+    float sw, bias;
 
-// A block's whole tile, 128 columns from n0 by `rows` output rows from m0: each warp the lanes
-// it can reach and every other run of C rows.
-template <int C>
-MOE_DEV void tile_out(const LinearArgs &a, uint32_t tmem, int m0, int n0, int rows, int w, int lane) {
-    const int n = n0 + (w & 3) * 32 + lane;
-    const bool mine = n < a.N;
-    const float sw = mine && a.w_scale ? a.w_scale[n] : 1.0f;
-    const float bias = mine && a.bias ? a.bias[n] : 0.0f;
-    const uint32_t lanes = tmem + ((uint32_t)(w & 3) << 21);
+    // the rows of run `at` that this lane has after the trade: at + odd, at + odd + 2, ...
+    MOE_DEV void load(const LinearArgs &a, int at, Pairs &g, Pairs &r) {
+        const int odd = n & 1, cols = rows - at - odd;
+        if (!a.vec2 || n >= a.N || cols <= 0) return;
+        if (a.gate.p) g.load(a.gate, m0 + at + odd, n - odd, cols);
+        if (a.residual.p) r.load(a.residual, m0 + at + odd, n - odd, cols);
+    }
+    MOE_DEV void begin(const LinearArgs &a, int m0_, int n0, int rows_, int w, int lane) {
+        m0 = m0_, rows = rows_, n = n0 + (w & 3) * 32 + lane, c = (w >> 2) * C;
+        sw = n < a.N && a.w_scale ? a.w_scale[n] : 1.0f;
+        bias = n < a.N && a.bias ? a.bias[n] : 0.0f;
+#pragma unroll
+        for (int d = 0; d < DEPTH; ++d) load(a, c + 2 * C * d, gate[d], residual[d]);
+    }
+    MOE_DEV void run(const LinearArgs &a, uint32_t tmem, int w) {
+        const uint32_t lanes = tmem + ((uint32_t)(w & 3) << 21);
 #pragma unroll 1
-    for (int c = (w >> 2) * C; c < rows; c += 2 * C)
-        column_out<C>(a, lanes + c, m0 + c, n, min(C, rows - c), mine, sw, bias);
+        while (c < rows) {
+#pragma unroll
+            for (int d = 0; d < DEPTH; ++d, c += 2 * C) {
+                if (c >= rows) break;
+                Cols<C> acc;
+                acc.issue(lanes + c);
+                acc.wait();
+                float v[C];
+#pragma unroll
+                for (int j = 0; j < C; ++j) v[j] = __uint_as_float(acc.r[j]);
+                if (a.x_scale) {
+#pragma unroll
+                    for (int j = 0; j < C; ++j)
+                        if (c + j < rows) v[j] *= a.x_scale[m0 + c + j];
+                }
+#pragma unroll
+                for (int j = 0; j < C; ++j) v[j] = v[j] * sw + bias;
+                activate<C>(a.activation, v);
+                if (a.vec2)
+                    pairs(a, v, gate[d], residual[d]);
+                else if (n < a.N)
+                    singles(a, v);
+                load(a, c + 2 * C * DEPTH, gate[d], residual[d]);
+            }
+        }
+    }
+    MOE_DEV void pairs(const LinearArgs &a, float (&v)[C], const Pairs &g, const Pairs &r) {
+        const int odd = n & 1, cols = rows - c - odd;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            const float other = __shfl_xor_sync(0xffffffffu, odd ? v[2 * q] : v[2 * q + 1], 1);
+            v[2 * q] = odd ? other : v[2 * q];
+            v[2 * q + 1] = odd ? v[2 * q + 1] : other;
+        }
+        if (n >= a.N) return;
+        float f[C];
+        if (a.gate.p) {
+            g.get(a.gate.type, f);
+#pragma unroll
+            for (int j = 0; j < C; ++j) v[j] *= f[j];
+        }
+        if (a.residual.p) {
+            r.get(a.residual.type, f);
+#pragma unroll
+            for (int j = 0; j < C; ++j) v[j] += f[j];
+        }
+        const int64_t at = (int64_t)(m0 + c + odd) * a.out.stride + (n - odd);
+        if (a.out.type == MOE_T_F32) {
+            float *p = reinterpret_cast<float *>(a.out.p) + at;
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                if (2 * q < cols)
+                    *reinterpret_cast<float2 *>(p + 2 * q * a.out.stride) = make_float2(v[2 * q], v[2 * q + 1]);
+        } else {
+            uint16_t *p = reinterpret_cast<uint16_t *>(a.out.p) + at;
+            uint32_t b[8];
+            if (a.out.type == MOE_T_BF16) {
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(b[q]) : "f"(v[2 * q + 1]), "f"(v[2 * q]));
+            } else {
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(b[q]) : "f"(v[2 * q + 1]), "f"(v[2 * q]));
+            }
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                if (2 * q < cols) *reinterpret_cast<uint32_t *>(p + 2 * q * a.out.stride) = b[q];
+        }
+    }
+    // Matrices whose neighbours are not one access: the lane's own column.
+    MOE_DEV void singles(const LinearArgs &a, float (&v)[C]) {
+        const int m = m0 + c, cols = rows - c;
+        if (a.gate.p) {
+#pragma unroll
+            for (int j = 0; j < C; ++j)
+                if (j < cols) v[j] *= load_as_float(a.gate.p, a.gate.type, (m + j) * a.gate.stride + n);
+        }
+        if (a.residual.p) {
+#pragma unroll
+            for (int j = 0; j < C; ++j)
+                if (j < cols) v[j] += load_as_float(a.residual.p, a.residual.type, (m + j) * a.residual.stride + n);
+        }
+        const int64_t at = (int64_t)m * a.out.stride + n;
+#pragma unroll
+        for (int j = 0; j < C; ++j)
+            if (j < cols) {
+                if (a.out.type == MOE_T_F32)
+                    reinterpret_cast<float *>(a.out.p)[at + j * a.out.stride] = v[j];
+                else
+                    reinterpret_cast<uint16_t *>(a.out.p)[at + j * a.out.stride] = to_bits16(v[j], a.out.type);
+            }
+    }
+};
+
+// Asks for a tile's gate and residual in L2 (of the epilogue's 256 threads, one a row).
+MOE_DEV void row_lines(const MatIn &s, int m, int n0, int N) {
+    const int size = s.type == MOE_T_F32 ? 4 : 2;
+    const char *p = reinterpret_cast<const char *>(s.p) + ((int64_t)m * s.stride + n0) * size;
+    for (int i = 0; i < min(kRowsW, N - n0) * size; i += 128)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(p + i));
+}
+MOE_DEV void tile_lines(const LinearArgs &a, int m0, int n0, int rows, int tid) {
+    const int m = m0 + tid;
+    if (tid >= rows || m >= a.M || n0 >= a.N) return;
+    if (a.gate.p) row_lines(a.gate, m, n0, a.N);
+    if (a.residual.p) row_lines(a.residual, m, n0, a.N);
 }
 
 // Four neighbours of a row, n..n+3 (those below N exist).
@@ -429,15 +502,22 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     // The sums are complete, and with them every copy has been used.
     __syncwarp();
-    if (w < kEpilogue) {
-        mbar_wait(done, 0, &abort_flag, a.err);
-        __syncwarp();
-        tc_fence_after();
-    }
     const int rows = min(tn, a.M - m0);  // output rows of the tile
     if (S == 1) {
-        if (w < kEpilogue) tile_out<16>(a, tmem, m0, n0, rows, w, lane);
+        if (w < kEpilogue) {
+            TileOut<1> out;
+            out.begin(a, m0, n0, rows, w, lane);
+            mbar_wait(done, 0, &abort_flag, a.err);
+            __syncwarp();
+            tc_fence_after();
+            out.run(a, tmem, w);
+        }
     } else {
+        if (w < kEpilogue) {
+            mbar_wait(done, 0, &abort_flag, a.err);
+            __syncwarp();
+            tc_fence_after();
+        }
         // parts[m][n]: 128 fp32 numbers for each output row
         if (w < kEpilogue) {
             const uint32_t at = stages + 4 * (uint32_t)((w & 3) * 32 + lane);
@@ -624,10 +704,17 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         for (int t = first; t < tiles; t += step, acc.next()) {
             int tm, tn;
             tile_at(t, tiles_m, tiles_n, tm, tn);
+            TileOut<2> out;
+            if (t == first) tile_lines(a, tm * TN, tn * 2 * kRowsW + (int)rank * kRowsW, TN, tid);
+            out.begin(a, tm * TN, tn * 2 * kRowsW + (int)rank * kRowsW, min(TN, a.M - tm * TN), w, lane);
+            if (t + step < tiles) {
+                int next_m, next_n;
+                tile_at(t + step, tiles_m, tiles_n, next_m, next_n);
+                tile_lines(a, next_m * TN, next_n * 2 * kRowsW + (int)rank * kRowsW, TN, tid);
+            }
             if (!__all_sync(0xffffffffu, mbar_wait(sums_full + 8 * acc.idx, acc.ph, &abort_flag, a.err))) break;
             tc_fence_after();
-            tile_out<32>(a, tmem + acc.idx * TN, tm * TN, tn * 2 * kRowsW + (int)rank * kRowsW,
-                         min(TN, a.M - tm * TN), w, lane);
+            out.run(a, tmem + acc.idx * TN, w);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) arrive_at(empty0 + 8 * acc.idx);
@@ -752,6 +839,61 @@ Cut make_cut(int tn, int split, int per_sm) {
     return c;
 }
 
+// The time of linear_split_kernel in us, from what was measured of its parts:
+//  - A block takes a line of k in 170 ns and 0.65 ns for each of its tn rows of x (its waits,
+//    and the copies' requests, one a row); two blocks of an SM, or the copies of one, get a
+//    row in 0.95 ns.
+//  - w comes from HBM once, at 6.6 TB/s.
+//  - An epilogue of two warps a quarter of the lanes takes 0.55 us for 32 rows; parts cost
+//    1.2 us for the two cluster barriers, 0.12 us for 32 rows to write them and 0.35 us for
+//    8 rows of a block's share to add them up.
+//  - 3 us for the launch and the first lines; every further block of an SM adds 1.5 us for
+//    its own and its epilogue.
+double split_time(int M, int N, int kb, int sms, const Cut &c, int per_sm) {
+    const double tiles = (double)((N + kRowsW - 1) / kRowsW) * ((M + c.tn - 1) / c.tn);
+    const double blocks = tiles * c.split, lines = (double)kb / c.split;
+    double line = 170 + 0.65 * c.tn;
+    if (per_sm == 1) {
+        line *= std::ceil(blocks / sms);
+    } else {
+        const double waves = std::ceil(blocks / (2.0 * sms)), share = blocks / (sms * waves);
+        line = waves * std::max(line, 0.95 * (kRowsW + c.tn) * std::max(1.0, share));
+    }
+    const double hbm = ((double)N + M) * kb * kLine / 6.6e6;
+    const double rows = std::min(c.tn, M);
+    const double out = c.split == 1 ? 0.55 * std::ceil(rows / 32)
+                                    : 1.2 + 0.12 * std::ceil(rows / 32) +
+                                          0.35 * std::ceil(rows / c.split / 8);
+    const double waves = std::ceil(blocks / ((double)sms * per_sm));
+    return 3 + std::max(hbm, lines * line / 1000) + out + (waves - 1) * (1.5 + out);
+}
+
+// Blocks that run at the same time: clusters lie inside a group of 19 SMs of 8.
+int room(int split, int per_sm, int sms) { return split == 1 ? sms * per_sm : 19 * per_sm / split * split * 8; }
+
+Cut best_cut(int M, int N, int kb, int sms) {
+    Cut best{};
+    double least = 1e30;
+    const int whole = (M + 15) / 16 * 16;
+    for (int tn : {16, 32, 48, 64, 96, 128, whole}) {
+        if (tn > whole || tn > 128) continue;
+        for (int split = 1; split <= kMaxSplit && split * 3 <= std::max(kb, 3); ++split)
+            for (int per_sm = 1; per_sm <= 2; ++per_sm) {
+                const Cut c = make_cut(tn, split, per_sm);
+                if (c.stages < 3) continue;
+                if (split > 1 && (int64_t)((N + kRowsW - 1) / kRowsW) * ((M + tn - 1) / tn) * split >
+                                     room(split, per_sm, sms))
+                    continue;
+                const double t = split_time(M, N, kb, sms, c, per_sm);
+                if (t < least) {
+                    least = t;
+                    best = c;
+                }
+            }
+    }
+    return best;
+}
+
 template <bool CODES>
 cudaError_t by_size(const LinearArgs &a, const Operands &o, cudaStream_t s) {
     const int64_t half_tiles = (int64_t)((a.N + 255) / 256) * ((a.M + 127) / 128);
@@ -760,27 +902,27 @@ cudaError_t by_size(const LinearArgs &a, const Operands &o, cudaStream_t s) {
             return launch_pair<256, CODES>(a, o, s);
         return launch_pair<128, CODES>(a, o, s);
     }
-    const int tn = a.M >= 128 ? 128 : (a.M + 15) / 16 * 16;
-    const int64_t tiles = (int64_t)((a.N + kRowsW - 1) / kRowsW) * ((a.M + tn - 1) / tn);
-    const int kb = (a.K * (CODES ? 1 : 2) + kLine - 1) / kLine;
-    int S = 1;
-    while (S < kMaxSplit && tiles * S * 2 <= 2 * o.sms && kb >= 8 * S) S *= 2;
-    return launch_split<CODES>(a, o, make_cut(tn, S, tiles * S > o.sms ? 2 : 1), s);
+    return launch_split<CODES>(a, o, best_cut(a.M, a.N, (a.K * (CODES ? 1 : 2) + kLine - 1) / kLine,
+                                              o.sms),
+                               s);
 }
 
-// Four neighbours of a row may be one access.
-bool quads(const void *p, int64_t stride, int type, int rows) {
-    const int bytes = type == MOE_T_F32 ? 16 : 8;
-    return ((uintptr_t)p % bytes) == 0 && (rows == 1 || stride % 4 == 0);
+// `count` neighbours of a row may be one access.
+bool together(const void *p, int64_t stride, int type, int rows, int count) {
+    const int bytes = (type == MOE_T_F32 ? 4 : 2) * count;
+    return !p || (((uintptr_t)p % bytes) == 0 && (rows == 1 || stride % count == 0));
 }
 
 }  // namespace
 
 cudaError_t launch_linear(LinearArgs a, const void *x, int64_t x_stride, const void *w,
                           int64_t w_stride, int sms, cudaStream_t s) {
-    a.vec_gate = quads(a.gate.p, a.gate.stride, a.gate.type, a.M);
-    a.vec_residual = quads(a.residual.p, a.residual.stride, a.residual.type, a.M);
-    a.vec_out = quads(a.out.p, a.out.stride, a.out.type, a.M);
+    a.vec_gate = together(a.gate.p, a.gate.stride, a.gate.type, a.M, 4);
+    a.vec_residual = together(a.residual.p, a.residual.stride, a.residual.type, a.M, 4);
+    a.vec_out = together(a.out.p, a.out.stride, a.out.type, a.M, 4);
+    a.vec2 = a.N % 2 == 0 && together(a.gate.p, a.gate.stride, a.gate.type, a.M, 2) &&
+             together(a.residual.p, a.residual.stride, a.residual.type, a.M, 2) &&
+             together(a.out.p, a.out.stride, a.out.type, a.M, 2);
     const Operands o{x, w, x_stride, w_stride, sms};
     return a.type == MOE_T_E4M3 ? by_size<true>(a, o, s) : by_size<false>(a, o, s);
 }
