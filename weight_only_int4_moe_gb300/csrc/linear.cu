@@ -29,6 +29,8 @@ constexpr int kLine = 128;                  // bytes of k of a stage
 constexpr int kBytesW = kRowsW * kLine;
 constexpr int kThreads = 320;               // warps 0-7 epilogue, 8 copies, 9 products
 constexpr int kEpilogue = 8;                // warps
+constexpr int kPairThreads = 576;           // of a pair's block: warps 0-15 epilogue, 16 copies, 17 products
+constexpr int kPairEpilogue = 16;
 constexpr int kMaxSmem = 227 * 1024 - 1024; // of a block, beside its few static bytes
 
 MOE_DEV uint32_t cluster_rank() {
@@ -205,15 +207,15 @@ struct Pairs {
 };
 
 // The block's part of a tile: 128 columns from n0 by `rows` output rows from m0, in the sums at
-// `tmem`.  A warp takes the lanes it can reach and every other run of 16 rows.  A lane has one
+// `tmem`.  A warp takes the lanes it can reach and every WARPS / 4-th run of 16 rows.  A lane has one
 // column of the sums; lanes 2i and 2i + 1 trade, so that either has both columns of every other
 // row, and a row takes half the accesses.  (Each lane with its own column, two bytes an access,
 // 34 instructions an element made the epilogue the bound: 8192 x 7168 from K = 512 with a
 // residual 143 us.)  The gate and the residual of a run are asked for DEPTH runs ahead, the
 // first ones before the sums are complete (begin).
-template <int DEPTH>
+template <int DEPTH, int WARPS>
 struct TileOut {
-    static constexpr int C = 16;
+    static constexpr int C = 16, kStep = WARPS / 4 * C;
     Pairs gate[DEPTH], residual[DEPTH];
     int m0, rows, n, c;
     float sw, bias;
@@ -230,14 +232,14 @@ struct TileOut {
         sw = n < a.N && a.w_scale ? a.w_scale[n] : 1.0f;
         bias = n < a.N && a.bias ? a.bias[n] : 0.0f;
 #pragma unroll
-        for (int d = 0; d < DEPTH; ++d) load(a, c + 2 * C * d, gate[d], residual[d]);
+        for (int d = 0; d < DEPTH; ++d) load(a, c + kStep * d, gate[d], residual[d]);
     }
     MOE_DEV void run(const LinearArgs &a, uint32_t tmem, int w) {
         const uint32_t lanes = tmem + ((uint32_t)(w & 3) << 21);
 #pragma unroll 1
         while (c < rows) {
 #pragma unroll
-            for (int d = 0; d < DEPTH; ++d, c += 2 * C) {
+            for (int d = 0; d < DEPTH; ++d, c += kStep) {
                 if (c >= rows) break;
                 Cols<C> acc;
                 acc.issue(lanes + c);
@@ -257,7 +259,7 @@ struct TileOut {
                     pairs(a, v, gate[d], residual[d]);
                 else if (n < a.N)
                     singles(a, v);
-                load(a, c + 2 * C * DEPTH, gate[d], residual[d]);
+                load(a, c + kStep * DEPTH, gate[d], residual[d]);
             }
         }
     }
@@ -330,7 +332,7 @@ struct TileOut {
     }
 };
 
-// Asks for a tile's gate and residual in L2 (of the epilogue's 256 threads, one a row).
+// Asks for a tile's gate and residual in L2 (one thread a row).
 MOE_DEV void row_lines(const MatIn &s, int m, int n0, int N) {
     const int size = s.type == MOE_T_F32 ? 4 : 2;
     const char *p = reinterpret_cast<const char *>(s.p) + ((int64_t)m * s.stride + n0) * size;
@@ -505,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int rows = min(tn, a.M - m0);  // output rows of the tile
     if (S == 1) {
         if (w < kEpilogue) {
-            TileOut<1> out;
+            TileOut<1, kEpilogue> out;
             out.begin(a, m0, n0, rows, w, lane);
             mbar_wait(done, 0, &abort_flag, a.err);
             __syncwarp();
@@ -602,7 +604,7 @@ MOE_DEV void tile_at(int t, int tiles_m, int tiles_n, int &tm, int &tn) {
 }
 
 template <int TN, bool CODES>
-__global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
+__global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap wmap,
                        const __grid_constant__ CUtensorMap xmap, const LinearArgs a) {
     using T = Pair<TN>;
@@ -625,11 +627,11 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     if (tid == 0) {
         abort_flag = 0;
         for (int i = 0; i < T::kBars; ++i)
-            mbar_init(full + 8 * i, i == 2 * T::kStages + 2 || i == 2 * T::kStages + 3 ? 2 * kEpilogue : 1);
+            mbar_init(full + 8 * i, i == 2 * T::kStages + 2 || i == 2 * T::kStages + 3 ? 2 * kPairEpilogue : 1);
         mbar_fence_init();
     }
     pdl_wait();
-    if (w == 9) {
+    if (w == kPairEpilogue + 1) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          smem_u32(&tmem_slot)),
                      "r"(T::kCols)
@@ -643,7 +645,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     const uint32_t tmem = tmem_slot;
     pdl_launch_dependents();
 
-    if (w == 8) {
+    if (w == kPairEpilogue) {
         if (lane == 0) {
             const uint32_t full0 = map_to(full, 0);
             Ring r(T::kStages);
@@ -672,7 +674,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             }
         }
         __syncwarp();
-    } else if (w == 9) {
+    } else if (w == kPairEpilogue + 1) {
         if (rank == 0) {
             const uint32_t idesc = idesc_of(a.type, 256, TN);
             Ring r(T::kStages), acc(2);
@@ -704,7 +706,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         for (int t = first; t < tiles; t += step, acc.next()) {
             int tm, tn;
             tile_at(t, tiles_m, tiles_n, tm, tn);
-            TileOut<2> out;
+            TileOut<1, kPairEpilogue> out;
             if (t == first) tile_lines(a, tm * TN, tn * 2 * kRowsW + (int)rank * kRowsW, TN, tid);
             out.begin(a, tm * TN, tn * 2 * kRowsW + (int)rank * kRowsW, min(TN, a.M - tm * TN), w, lane);
             if (t + step < tiles) {
@@ -725,7 +727,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     __syncthreads();
     cluster_sync();
     tc_fence_after();
-    if (w == 9)
+    if (w == kPairEpilogue + 1)
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(T::kCols)
                      : "memory");
 }
@@ -773,7 +775,7 @@ cudaError_t prepare(K kernel, int smem, std::atomic<int> *known, int *n, int pai
     if (pair_grid) {
         cudaLaunchConfig_t c{};
         c.gridDim = dim3((unsigned)pair_grid);
-        c.blockDim = dim3(kThreads);
+        c.blockDim = dim3(kPairThreads);
         c.dynamicSmemBytes = smem;
         cudaLaunchAttribute at{};
         at.id = cudaLaunchAttributeClusterDimension;
@@ -801,7 +803,7 @@ cudaError_t launch_pair(const LinearArgs &a, const Operands &o, cudaStream_t s) 
         !rows_map(&xmap, o.x, o.x_stride, a.M, a.K, a.type, TN / 2))
         return cudaErrorNotSupported;
     const int64_t tiles = (int64_t)((a.N + 2 * kRowsW - 1) / (2 * kRowsW)) * ((a.M + TN - 1) / TN);
-    auto c = pdl_config((unsigned)(2 * (tiles < pairs ? tiles : pairs)), kThreads, T::kSmem, s);
+    auto c = pdl_config((unsigned)(2 * (tiles < pairs ? tiles : pairs)), kPairThreads, T::kSmem, s);
     cudaLaunchAttribute at{};
     c.numAttrs = pdl_attr(at);
     c.attrs = &at;
@@ -839,54 +841,58 @@ Cut make_cut(int tn, int split, int per_sm) {
     return c;
 }
 
-// The time of linear_split_kernel in us, from what was measured of its parts:
+// Times in us, from what was measured of the kernels' parts:
 //  - A block takes a line of k in 170 ns and 0.65 ns for each of its tn rows of x (its waits,
-//    and the copies' requests, one a row); two blocks of an SM, or the copies of one, get a
-//    row in 0.95 ns.
+//    and the copies' requests, one a row); two blocks on an SM get a row in 0.93 ns.
 //  - w comes from HBM once, at 6.6 TB/s.
 //  - An epilogue of two warps a quarter of the lanes takes 0.55 us for 32 rows; parts cost
 //    1.2 us for the two cluster barriers, 0.12 us for 32 rows to write them and 0.35 us for
 //    8 rows of a block's share to add them up.
-//  - 3 us for the launch and the first lines; every further block of an SM adds 1.5 us for
-//    its own and its epilogue.
+//  - 3 us for the launch and the first lines, 1 us more where blocks share an SM; every further
+//    block of an SM adds 1.5 us for its own and its epilogue.
+//  - A pair takes a line in 0.33 us (256 rows of x) or 0.22 us (128), under which runs the
+//    epilogue of the tile before, 5 and 2.5 us; 4.5 us for its start.
+// They chose within 10 % of the best cut at all but 2 of 21 sizes from 1 x 7168 x 7168 to
+// 4096 x 4096 x 4096 that were timed with every cut.
+double hbm_time(int M, int N, int kb) { return ((double)N + M) * kb * kLine / 6.6e6; }
+
 double split_time(int M, int N, int kb, int sms, const Cut &c, int per_sm) {
-    const double tiles = (double)((N + kRowsW - 1) / kRowsW) * ((M + c.tn - 1) / c.tn);
-    const double blocks = tiles * c.split, lines = (double)kb / c.split;
+    const double blocks = (double)((N + kRowsW - 1) / kRowsW) * ((M + c.tn - 1) / c.tn) * c.split;
+    const double waves = std::ceil(blocks / ((double)sms * per_sm));
     double line = 170 + 0.65 * c.tn;
-    if (per_sm == 1) {
-        line *= std::ceil(blocks / sms);
-    } else {
-        const double waves = std::ceil(blocks / (2.0 * sms)), share = blocks / (sms * waves);
-        line = waves * std::max(line, 0.95 * (kRowsW + c.tn) * std::max(1.0, share));
-    }
-    const double hbm = ((double)N + M) * kb * kLine / 6.6e6;
+    if (per_sm == 2) line = std::max(line, 0.93 * (kRowsW + c.tn) * std::min(2.0, std::ceil(blocks / sms)));
     const double rows = std::min(c.tn, M);
     const double out = c.split == 1 ? 0.55 * std::ceil(rows / 32)
                                     : 1.2 + 0.12 * std::ceil(rows / 32) +
                                           0.35 * std::ceil(rows / c.split / 8);
-    const double waves = std::ceil(blocks / ((double)sms * per_sm));
-    return 3 + std::max(hbm, lines * line / 1000) + out + (waves - 1) * (1.5 + out);
+    return 2 + per_sm + std::max(hbm_time(M, N, kb), waves * line * kb / c.split / 1000) + out +
+           (waves - 1) * (1.5 + out);
+}
+
+double pair_time(int M, int N, int kb, int sms, int tn) {
+    const double tiles = (double)((N + 2 * kRowsW - 1) / (2 * kRowsW)) * ((M + tn - 1) / tn);
+    const double work = kb * (tn == 256 ? 0.33 : 0.22), out = tn == 256 ? 5 : 2.5;
+    return 4.5 + std::max(hbm_time(M, N, kb), std::ceil(tiles / (sms / 2)) * std::max(work, out)) +
+           std::min(work, out);
 }
 
 // Blocks that run at the same time: clusters lie inside a group of 19 SMs of 8.
 int room(int split, int per_sm, int sms) { return split == 1 ? sms * per_sm : 19 * per_sm / split * split * 8; }
 
-Cut best_cut(int M, int N, int kb, int sms) {
+Cut best_cut(int M, int N, int kb, int sms, double *time) {
     Cut best{};
-    double least = 1e30;
+    *time = 1e30;
     const int whole = (M + 15) / 16 * 16;
     for (int tn : {16, 32, 48, 64, 96, 128, whole}) {
         if (tn > whole || tn > 128) continue;
+        const int64_t tiles = (int64_t)((N + kRowsW - 1) / kRowsW) * ((M + tn - 1) / tn);
         for (int split = 1; split <= kMaxSplit && split * 3 <= std::max(kb, 3); ++split)
             for (int per_sm = 1; per_sm <= 2; ++per_sm) {
                 const Cut c = make_cut(tn, split, per_sm);
-                if (c.stages < 3) continue;
-                if (split > 1 && (int64_t)((N + kRowsW - 1) / kRowsW) * ((M + tn - 1) / tn) * split >
-                                     room(split, per_sm, sms))
-                    continue;
+                if (c.stages < 3 || (split > 1 && tiles * split > room(split, per_sm, sms))) continue;
                 const double t = split_time(M, N, kb, sms, c, per_sm);
-                if (t < least) {
-                    least = t;
+                if (t < *time) {
+                    *time = t;
                     best = c;
                 }
             }
@@ -896,15 +902,12 @@ Cut best_cut(int M, int N, int kb, int sms) {
 
 template <bool CODES>
 cudaError_t by_size(const LinearArgs &a, const Operands &o, cudaStream_t s) {
-    const int64_t half_tiles = (int64_t)((a.N + 255) / 256) * ((a.M + 127) / 128);
-    if (a.M > 128 && half_tiles >= o.sms / 2) {
-        if ((int64_t)((a.N + 255) / 256) * ((a.M + 255) / 256) >= o.sms / 2)
-            return launch_pair<256, CODES>(a, o, s);
-        return launch_pair<128, CODES>(a, o, s);
-    }
-    return launch_split<CODES>(a, o, best_cut(a.M, a.N, (a.K * (CODES ? 1 : 2) + kLine - 1) / kLine,
-                                              o.sms),
-                               s);
+    const int kb = (a.K * (CODES ? 1 : 2) + kLine - 1) / kLine;
+    double split;
+    const Cut cut = best_cut(a.M, a.N, kb, o.sms, &split);
+    const double wide = pair_time(a.M, a.N, kb, o.sms, 256), half = pair_time(a.M, a.N, kb, o.sms, 128);
+    if (split <= wide && split <= half) return launch_split<CODES>(a, o, cut, s);
+    return half < wide ? launch_pair<128, CODES>(a, o, s) : launch_pair<256, CODES>(a, o, s);
 }
 
 // `count` neighbours of a row may be one access.
