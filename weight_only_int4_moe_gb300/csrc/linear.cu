@@ -308,27 +308,46 @@ struct TileOut {
         }
     }
     // Matrices whose neighbours are not one access: the lane's own column.
+    static MOE_DEV void own(const MatIn &s, int m, int n, int cols, float (&f)[C]) {
+        const int64_t at = (int64_t)m * s.stride + n;
+        if (s.type == MOE_T_F32) {
+            const float *p = reinterpret_cast<const float *>(s.p) + at;
+#pragma unroll
+            for (int j = 0; j < C; ++j) f[j] = j < cols ? p[j * s.stride] : 0.0f;
+        } else {
+            const uint16_t *p = reinterpret_cast<const uint16_t *>(s.p) + at;
+            uint16_t b[C];
+#pragma unroll
+            for (int j = 0; j < C; ++j) b[j] = j < cols ? p[j * s.stride] : (uint16_t)0;
+#pragma unroll
+            for (int j = 0; j < C; ++j) f[j] = from_bits16(b[j], s.type);
+        }
+    }
     MOE_DEV void singles(const LinearArgs &a, float (&v)[C]) {
         const int m = m0 + c, cols = rows - c;
+        float f[C];
         if (a.gate.p) {
+            own(a.gate, m, n, cols, f);
 #pragma unroll
-            for (int j = 0; j < C; ++j)
-                if (j < cols) v[j] *= load_as_float(a.gate.p, a.gate.type, (m + j) * a.gate.stride + n);
+            for (int j = 0; j < C; ++j) v[j] *= f[j];
         }
         if (a.residual.p) {
+            own(a.residual, m, n, cols, f);
 #pragma unroll
-            for (int j = 0; j < C; ++j)
-                if (j < cols) v[j] += load_as_float(a.residual.p, a.residual.type, (m + j) * a.residual.stride + n);
+            for (int j = 0; j < C; ++j) v[j] += f[j];
         }
         const int64_t at = (int64_t)m * a.out.stride + n;
+        if (a.out.type == MOE_T_F32) {
+            float *p = reinterpret_cast<float *>(a.out.p) + at;
 #pragma unroll
-        for (int j = 0; j < C; ++j)
-            if (j < cols) {
-                if (a.out.type == MOE_T_F32)
-                    reinterpret_cast<float *>(a.out.p)[at + j * a.out.stride] = v[j];
-                else
-                    reinterpret_cast<uint16_t *>(a.out.p)[at + j * a.out.stride] = to_bits16(v[j], a.out.type);
-            }
+            for (int j = 0; j < C; ++j)
+                if (j < cols) p[j * a.out.stride] = v[j];
+        } else {
+            uint16_t *p = reinterpret_cast<uint16_t *>(a.out.p) + at;
+#pragma unroll
+            for (int j = 0; j < C; ++j)
+                if (j < cols) p[j * a.out.stride] = to_bits16(v[j], a.out.type);
+        }
     }
 };
 
@@ -843,54 +862,57 @@ Cut make_cut(int tn, int split, int per_sm) {
 
 // Times in us, from what was measured of the kernels' parts:
 //  - A block takes a line of k in 170 ns and 0.65 ns for each of its tn rows of x (its waits,
-//    and the copies' requests, one a row); two blocks on an SM get a row in 0.93 ns.
+//    and the copies' requests, one a row); two blocks on an SM get a row in 0.93 ns.  Rows that
+//    do not begin at multiples of 128 bytes take two requests a line: 1.4 times that.
 //  - w comes from HBM once, at 6.6 TB/s.
-//  - An epilogue of two warps a quarter of the lanes takes 0.55 us for 32 rows; parts cost
-//    1.2 us for the two cluster barriers, 0.12 us for 32 rows to write them and 0.35 us for
-//    8 rows of a block's share to add them up.
-//  - 3 us for the launch and the first lines, 1 us more where blocks share an SM; every further
+//  - An epilogue of two warps a quarter of the lanes takes 0.55 us for 32 rows (twice that where
+//    columns do not go in pairs); parts cost 1.2 us for the two cluster barriers, 0.12 us for
+//    32 rows to write them and 0.35 us for 8 rows of a block's share to add them up.
+//  - 2 us for the launch and the first lines, 1 us more where blocks share an SM; every further
 //    block of an SM adds 1.5 us for its own and its epilogue.
 //  - A pair takes a line in 0.33 us (256 rows of x) or 0.22 us (128), under which runs the
-//    epilogue of the tile before, 5 and 2.5 us; 4.5 us for its start.
-// They chose within 10 % of the best cut at all but 2 of 21 sizes from 1 x 7168 x 7168 to
-// 4096 x 4096 x 4096 that were timed with every cut.
-double hbm_time(int M, int N, int kb) { return ((double)N + M) * kb * kLine / 6.6e6; }
+//    epilogue of the tile before, 6.2 and 3.7 us; 3 us for its start.
+struct Size {
+    int M, N, kb, sms;
+    bool even, lined;  // columns go in pairs; rows begin at multiples of 128 bytes
+    double hbm() const { return ((double)N + M) * kb * kLine / 6.6e6; }
+};
 
-double split_time(int M, int N, int kb, int sms, const Cut &c, int per_sm) {
-    const double blocks = (double)((N + kRowsW - 1) / kRowsW) * ((M + c.tn - 1) / c.tn) * c.split;
-    const double waves = std::ceil(blocks / ((double)sms * per_sm));
+double split_time(const Size &z, const Cut &c, int per_sm) {
+    const double blocks = (double)((z.N + kRowsW - 1) / kRowsW) * ((z.M + c.tn - 1) / c.tn) * c.split;
+    const double waves = std::ceil(blocks / ((double)z.sms * per_sm));
     double line = 170 + 0.65 * c.tn;
-    if (per_sm == 2) line = std::max(line, 0.93 * (kRowsW + c.tn) * std::min(2.0, std::ceil(blocks / sms)));
-    const double rows = std::min(c.tn, M);
-    const double out = c.split == 1 ? 0.55 * std::ceil(rows / 32)
+    if (per_sm == 2) line = std::max(line, 0.93 * (kRowsW + c.tn) * std::min(2.0, std::ceil(blocks / z.sms)));
+    if (!z.lined) line *= 1.4;
+    const double rows = std::min(c.tn, z.M);
+    const double out = c.split == 1 ? (z.even ? 0.55 : 1.1) * std::ceil(rows / 32)
                                     : 1.2 + 0.12 * std::ceil(rows / 32) +
                                           0.35 * std::ceil(rows / c.split / 8);
-    return 2 + per_sm + std::max(hbm_time(M, N, kb), waves * line * kb / c.split / 1000) + out +
+    return 1 + per_sm + std::max(z.hbm(), waves * line * z.kb / c.split / 1000) + out +
            (waves - 1) * (1.5 + out);
 }
 
-double pair_time(int M, int N, int kb, int sms, int tn) {
-    const double tiles = (double)((N + 2 * kRowsW - 1) / (2 * kRowsW)) * ((M + tn - 1) / tn);
-    const double work = kb * (tn == 256 ? 0.33 : 0.22), out = tn == 256 ? 5 : 2.5;
-    return 4.5 + std::max(hbm_time(M, N, kb), std::ceil(tiles / (sms / 2)) * std::max(work, out)) +
+double pair_time(const Size &z, int tn) {
+    const double tiles = (double)((z.N + 2 * kRowsW - 1) / (2 * kRowsW)) * ((z.M + tn - 1) / tn);
+    const double work = z.kb * (tn == 256 ? 0.33 : 0.22), out = (tn == 256 ? 6.2 : 3.7) * (z.even ? 1 : 2);
+    return 3 + std::max(z.hbm(), std::ceil(tiles / (z.sms / 2)) * std::max(work, out)) +
            std::min(work, out);
 }
 
-// Blocks that run at the same time: clusters lie inside a group of 19 SMs of 8.
-int room(int split, int per_sm, int sms) { return split == 1 ? sms * per_sm : 19 * per_sm / split * split * 8; }
-
-Cut best_cut(int M, int N, int kb, int sms, double *time) {
+// The fastest cut by that; fits[per_sm - 1][split]: blocks that run at the same time (clusters
+// lie inside a group of SMs, so not all of them can be used).
+Cut best_cut(const Size &z, const int (&fits)[2][kMaxSplit + 1], double *time) {
     Cut best{};
     *time = 1e30;
-    const int whole = (M + 15) / 16 * 16;
+    const int whole = (z.M + 15) / 16 * 16;
     for (int tn : {16, 32, 48, 64, 96, 128, whole}) {
         if (tn > whole || tn > 128) continue;
-        const int64_t tiles = (int64_t)((N + kRowsW - 1) / kRowsW) * ((M + tn - 1) / tn);
-        for (int split = 1; split <= kMaxSplit && split * 3 <= std::max(kb, 3); ++split)
+        const int64_t tiles = (int64_t)((z.N + kRowsW - 1) / kRowsW) * ((z.M + tn - 1) / tn);
+        for (int split = 1; split <= kMaxSplit && split * 3 <= std::max(z.kb, 3); ++split)
             for (int per_sm = 1; per_sm <= 2; ++per_sm) {
                 const Cut c = make_cut(tn, split, per_sm);
-                if (c.stages < 3 || (split > 1 && tiles * split > room(split, per_sm, sms))) continue;
-                const double t = split_time(M, N, kb, sms, c, per_sm);
+                if (c.stages < 3 || (split > 1 && tiles * split > fits[per_sm - 1][split])) continue;
+                const double t = split_time(z, c, per_sm);
                 if (t < *time) {
                     *time = t;
                     best = c;
@@ -900,12 +922,55 @@ Cut best_cut(int M, int N, int kb, int sms, double *time) {
     return best;
 }
 
+// fits of best_cut on the current device, asked once.
+template <bool CODES>
+cudaError_t cluster_room(int (&fits)[2][kMaxSplit + 1]) {
+    static std::atomic<int> known[64][2][kMaxSplit + 1];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const bool keep = dev >= 0 && dev < 64;
+    for (int p = 0; p < 2; ++p)
+        for (int split = 1; split <= kMaxSplit; ++split) {
+            if (keep && known[dev][p][split] > 0) {
+                fits[p][split] = known[dev][p][split];
+                continue;
+            }
+            cudaLaunchConfig_t c{};
+            c.gridDim = dim3((unsigned)split);
+            c.blockDim = dim3(kThreads);
+            c.dynamicSmemBytes = (size_t)(kMaxSmem / (p + 1) - 1024 * p);
+            cudaLaunchAttribute at{};
+            at.id = cudaLaunchAttributeClusterDimension;
+            at.val.clusterDim.x = (unsigned)split;
+            at.val.clusterDim.y = at.val.clusterDim.z = 1;
+            c.numAttrs = 1;
+            c.attrs = &at;
+            int n = 0;
+            e = cudaFuncSetAttribute(linear_split_kernel<CODES>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     kMaxSmem);
+            if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&n, linear_split_kernel<CODES>, &c);
+            if (e != cudaSuccess) return e;
+            fits[p][split] = n * split;
+            if (keep) known[dev][p][split] = n * split;
+        }
+    return cudaSuccess;
+}
+
 template <bool CODES>
 cudaError_t by_size(const LinearArgs &a, const Operands &o, cudaStream_t s) {
-    const int kb = (a.K * (CODES ? 1 : 2) + kLine - 1) / kLine;
+    const int size = CODES ? 1 : 2;
+    const auto at_lines = [&](const void *p, int64_t stride, int rows) {
+        return (uintptr_t)p % kLine == 0 && (rows == 1 || stride * size % kLine == 0);
+    };
+    const Size z{a.M, a.N, (a.K * size + kLine - 1) / kLine, o.sms, a.vec2,
+                 at_lines(o.x, o.x_stride, a.M) && at_lines(o.w, o.w_stride, a.N)};
+    int fits[2][kMaxSplit + 1];
+    cudaError_t e = cluster_room<CODES>(fits);
+    if (e != cudaSuccess) return e;
     double split;
-    const Cut cut = best_cut(a.M, a.N, kb, o.sms, &split);
-    const double wide = pair_time(a.M, a.N, kb, o.sms, 256), half = pair_time(a.M, a.N, kb, o.sms, 128);
+    const Cut cut = best_cut(z, fits, &split);
+    const double wide = pair_time(z, 256), half = pair_time(z, 128);
     if (split <= wide && split <= half) return launch_split<CODES>(a, o, cut, s);
     return half < wide ? launch_pair<128, CODES>(a, o, s) : launch_pair<256, CODES>(a, o, s);
 }
