@@ -206,6 +206,34 @@ def test_linear_odd_sums(layer, k):
     check_linear(layer, 20, 150, k, E4M3, seed=k, wide=True)
 
 
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("m,n,k", [(1, 130, 9000), (90, 384, 7168), (200, 700, 5000), (2500, 520, 3000),
+                                   (1300, 3001, 1700), (700, 5000, 800)])
+def test_linear_long_sums_of_fp32_results(layer, dtype, m, n, k):
+    """What a long product's single sum would lose shows in a result that stays fp32: no sum
+    takes more than 12 stages (48 instructions, each cuts a step at most), and the sums are
+    added up in fp32 (K / 384 of them at most, 64 elements a stage at least)."""
+    x, w, sx, sw = operands(m, n, k, dtype, k)
+    pad = -k % 16
+    put = (lambda t: strided(t, 16 + pad)) if pad else gpu
+    r = torch.randn(m, n, generator=rng(1))
+    lin = layer.Linear(put(w), None, gpu(sw))
+    got = layer.moe_linear(put(x), lin, None, None, r.cuda(), gpu(sx), out_dtype=FP32)
+    assert lin.errors() == 0
+    xd, wd = x.double().cuda(), w.double().cuda()
+    y, size = xd @ wd.T, xd.abs() @ wd.abs().T
+    if sx is not None:
+        scale = sx.double().cuda()[:, None] * sw.double().cuda()
+        y, size = y * scale, size * scale
+    # a sum's share of the products, and 32 steps inside an instruction
+    bound = size * 2 * ref.U * (48 + 32 + k / 384) + 4 * ref.U * y.abs()
+    worst = ((got.double() - y - r.double().cuda()).abs() / (bound + ref.U * (y.abs() + r.abs().cuda()))).max()
+    assert worst.item() <= 1.0
+    # and over all elements: truncations of random sums are far below their bound
+    rms = ((got.double() - y - r.double().cuda()).pow(2).mean() / y.pow(2).mean()).sqrt().item()
+    assert rms <= 48 * 2 * ref.U
+
+
 @pytest.mark.parametrize("act", [None, "relu", "silu", "gelu"])
 @pytest.mark.parametrize("m,n,k", [(3, 200, 520), (90, 130, 2000), (300, 260, 130)])
 @pytest.mark.parametrize("bias,gate,residual,out", [

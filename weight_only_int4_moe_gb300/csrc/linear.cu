@@ -146,6 +146,22 @@ struct Cols {
     }
 };
 
+// 16 columns of n sums that lie `apart` columns from each other, added up.
+MOE_DEV void add_sums(uint32_t taddr, int n, int apart, float (&v)[16]) {
+    Cols<16> acc;
+    acc.issue(taddr);
+    acc.wait();
+#pragma unroll
+    for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(acc.r[j]);
+#pragma unroll 1
+    for (int i = 1; i < n; ++i) {
+        acc.issue(taddr + i * apart);
+        acc.wait();
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[j] += __uint_as_float(acc.r[j]);
+    }
+}
+
 // --------------------------------------------------------------- epilogue --
 MOE_DEV float from_bits16(uint32_t v, int type) {
     return type == MOE_T_BF16 ? __uint_as_float(v << 16) : __half2float(__ushort_as_half((uint16_t)v));
@@ -234,34 +250,36 @@ struct TileOut {
 #pragma unroll
         for (int d = 0; d < DEPTH; ++d) load(a, c + kStep * d, gate[d], residual[d]);
     }
-    MOE_DEV void run(const LinearArgs &a, uint32_t tmem, int w) {
+    // From n sums, `apart` columns from each other.
+    MOE_DEV void run(const LinearArgs &a, uint32_t tmem, int w, int n_sums, int apart) {
         const uint32_t lanes = tmem + ((uint32_t)(w & 3) << 21);
 #pragma unroll 1
         while (c < rows) {
 #pragma unroll
-            for (int d = 0; d < DEPTH; ++d, c += kStep) {
+            for (int d = 0; d < DEPTH; ++d) {
                 if (c >= rows) break;
-                Cols<C> acc;
-                acc.issue(lanes + c);
-                acc.wait();
                 float v[C];
-#pragma unroll
-                for (int j = 0; j < C; ++j) v[j] = __uint_as_float(acc.r[j]);
-                if (a.x_scale) {
-#pragma unroll
-                    for (int j = 0; j < C; ++j)
-                        if (c + j < rows) v[j] *= a.x_scale[m0 + c + j];
-                }
-#pragma unroll
-                for (int j = 0; j < C; ++j) v[j] = v[j] * sw + bias;
-                activate<C>(a.activation, v);
-                if (a.vec2)
-                    pairs(a, v, gate[d], residual[d]);
-                else if (n < a.N)
-                    singles(a, v);
-                load(a, c + kStep * DEPTH, gate[d], residual[d]);
+                add_sums(lanes + c, n_sums, apart, v);
+                emit(a, v, gate[d], residual[d]);
             }
         }
+    }
+    // The next run, from its sums.
+    MOE_DEV void emit(const LinearArgs &a, float (&v)[C], Pairs &g, Pairs &r) {
+        if (a.x_scale) {
+#pragma unroll
+            for (int j = 0; j < C; ++j)
+                if (c + j < rows) v[j] *= a.x_scale[m0 + c + j];
+        }
+#pragma unroll
+        for (int j = 0; j < C; ++j) v[j] = v[j] * sw + bias;
+        activate<C>(a.activation, v);
+        if (a.vec2)
+            pairs(a, v, g, r);
+        else if (n < a.N)
+            singles(a, v);
+        load(a, c + kStep * DEPTH, g, r);
+        c += kStep;
     }
     MOE_DEV void pairs(const LinearArgs &a, float (&v)[C], const Pairs &g, const Pairs &r) {
         const int odd = n & 1, cols = rows - c - odd;
@@ -439,20 +457,26 @@ MOE_DEV void quad_out(const LinearArgs &a, int m, int n, float (&v)[4], const fl
 }
 
 // ----------------------------------------------------- one tile a cluster --
-// How a product is cut: rows of x of a tile (a multiple of 16 up to 256), blocks that share a
-// tile's k, and stages of a block.
+// How a product is cut: rows of x of a tile (a multiple of 16), blocks that share a tile's k,
+// stages of a block, and sums that the lines of k go to in turn.
 struct Cut {
-    int tn, split, stages;
+    int tn, split, stages, sums;
     int stage_bytes() const { return kBytesW + tn * kLine; }
     int smem() const { return stages * stage_bytes() + 1024; }  // (stages begin at multiples of 1024)
 };
 constexpr int kMaxStages = 12, kMaxSplit = 8;
 
+// Lines of k that one sum in tensor memory takes where the result stays fp32.  The tensor cores
+// cut a sum's last place with every instruction, 4 a line: the error of a random product,
+// relative to it, measured 1.6e-8 an instruction (K = 7168 in one sum 7e-6; 16-bit results do
+// not show it).  So longer products go to several sums, which are added up in fp32.
+constexpr int kExactLines = 12;
+
 template <bool CODES>
 __global__ void __launch_bounds__(kThreads, 2)
     linear_split_kernel(const __grid_constant__ CUtensorMap wmap,
                         const __grid_constant__ CUtensorMap xmap, const LinearArgs a, const int tn,
-                        const int n_stages) {
+                        const int n_stages, const int n_sums) {
     extern __shared__ uint8_t dyn[];
     __shared__ alignas(8) uint64_t bars[2 * kMaxStages + 1];
     __shared__ uint32_t tmem_slot;
@@ -463,7 +487,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     const uint32_t stage_bytes = kBytesW + tn * kLine;
     const uint32_t stages = (smem_u32(dyn) + 1023u) & ~1023u;
     const uint32_t full = smem_u32(bars), empty = full + 8 * kMaxStages, done = full + 16 * kMaxStages;
-    const uint32_t cols = tn <= 32 ? 32 : tn <= 64 ? 64 : tn <= 128 ? 128 : 256;  // of tensor memory
+    const int all = tn * n_sums;
+    const uint32_t cols = all <= 32 ? 32 : all <= 64 ? 64 : all <= 128 ? 128 : all <= 256 ? 256 : 512;
     constexpr int kElems = CODES ? kLine : kLine / 2;
     const int kb = (a.K + kElems - 1) / kElems;
     const int kb0 = (int)((int64_t)kb * rank / S), kb1 = (int)((int64_t)kb * (rank + 1) / S);
@@ -512,12 +537,13 @@ __global__ void __launch_bounds__(kThreads, 2)
     } else if (w == 9) {
         const uint32_t idesc = idesc_of(a.type, 128, tn);
         Ring r(n_stages);
-        for (int k = kb0; k < kb1; ++k, r.next()) {
+        int sum = 0;
+        for (int k = kb0; k < kb1; ++k, r.next(), sum = sum + 1 == n_sums ? 0 : sum + 1) {
             if (__any_sync(0xffffffffu, !mbar_wait(full + 8 * r.idx, r.ph, &abort_flag, a.err))) break;
             tc_fence_after();
             const uint32_t s = stages + r.idx * stage_bytes;
-            mma_stage<CODES, false>(tmem, smem_desc_sw128(s), smem_desc_sw128(s + kBytesW), idesc,
-                                    k > kb0, empty + 8 * r.idx);
+            mma_stage<CODES, false>(tmem + sum * tn, smem_desc_sw128(s), smem_desc_sw128(s + kBytesW),
+                                    idesc, k >= kb0 + n_sums, empty + 8 * r.idx);
         }
         tc_commit_elect(done);  // also after giving up: products in flight end first
     }
@@ -531,7 +557,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             mbar_wait(done, 0, &abort_flag, a.err);
             __syncwarp();
             tc_fence_after();
-            out.run(a, tmem, w);
+            out.run(a, tmem, w, n_sums, tn);
         }
     } else {
         if (w < kEpilogue) {
@@ -545,12 +571,11 @@ __global__ void __launch_bounds__(kThreads, 2)
             const uint32_t lanes = tmem + ((uint32_t)(w & 3) << 21);
 #pragma unroll 1
             for (int c = (w >> 2) * 16; c < rows; c += 32) {
-                Cols<16> v;
-                v.issue(lanes + c);
-                v.wait();
+                float v[16];
+                add_sums(lanes + c, n_sums, tn, v);
 #pragma unroll
                 for (int j = 0; j < 16; ++j)
-                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + (c + j) * 512), "r"(v.r[j]) : "memory");
+                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + (c + j) * 512), "f"(v[j]) : "memory");
             }
         }
         __syncwarp();
@@ -622,7 +647,9 @@ MOE_DEV void tile_at(int t, int tiles_m, int tiles_n, int &tm, int &tn) {
     tm = band * kBand + r - tn * high;
 }
 
-template <int TN, bool CODES>
+// LONG: a tile's k in parts of kExactLines, each a sum of its own in one of the two buffers, that
+// the epilogue adds up in registers.
+template <int TN, bool CODES, bool LONG>
 __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap wmap,
                        const __grid_constant__ CUtensorMap xmap, const LinearArgs a) {
@@ -641,7 +668,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
     const uint32_t sums_full = full + 16 * T::kStages, sums_empty = sums_full + 16;
     const uint32_t end = sums_empty + 16;
     constexpr int kElems = CODES ? kLine : kLine / 2;
-    const int kb = (a.K + kElems - 1) / kElems;
+    const int kb = (a.K + kElems - 1) / kElems, part = LONG ? kExactLines : kb;
 
     if (tid == 0) {
         abort_flag = 0;
@@ -698,19 +725,22 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
             const uint32_t idesc = idesc_of(a.type, 256, TN);
             Ring r(T::kStages), acc(2);
             bool ok = true;
-            for (int t = first; t < tiles && ok; t += step, acc.next()) {
-                ok = __all_sync(0xffffffffu, mbar_wait(sums_empty + 8 * acc.idx, acc.ph ^ 1, &abort_flag, a.err));
-                tc_fence_after();
-                for (int k = 0; k < kb && ok; ++k, r.next()) {
-                    ok = __all_sync(0xffffffffu, mbar_wait(full + 8 * r.idx, r.ph, &abort_flag, a.err));
-                    if (!ok) break;
+            for (int t = first; t < tiles && ok; t += step)
+                for (int k0 = 0; k0 < kb && ok; k0 += part, acc.next()) {
+                    ok = __all_sync(0xffffffffu,
+                                    mbar_wait(sums_empty + 8 * acc.idx, acc.ph ^ 1, &abort_flag, a.err));
                     tc_fence_after();
-                    const uint32_t s = stages + r.idx * T::kStage;
-                    mma_stage<CODES, true>(tmem + acc.idx * TN, smem_desc_sw128(s),
-                                           smem_desc_sw128(s + kBytesW), idesc, k > 0, empty + 8 * r.idx);
+                    for (int k = k0; k < min(kb, k0 + part) && ok; ++k, r.next()) {
+                        ok = __all_sync(0xffffffffu, mbar_wait(full + 8 * r.idx, r.ph, &abort_flag, a.err));
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint32_t s = stages + r.idx * T::kStage;
+                        mma_stage<CODES, true>(tmem + acc.idx * TN, smem_desc_sw128(s),
+                                               smem_desc_sw128(s + kBytesW), idesc, k > k0,
+                                               empty + 8 * r.idx);
+                    }
+                    if (ok) commit_both(sums_full + 8 * acc.idx);
                 }
-                if (ok) commit_both(sums_full + 8 * acc.idx);
-            }
             if (!ok) {
                 // products in flight end before the tensor memory is given back
                 volatile int none = 0;
@@ -722,7 +752,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
     } else {
         const uint32_t empty0 = map_to(sums_empty, 0);
         Ring acc(2);
-        for (int t = first; t < tiles; t += step, acc.next()) {
+        bool ok = true;
+        for (int t = first; t < tiles && ok; t += step) {
             int tm, tn;
             tile_at(t, tiles_m, tiles_n, tm, tn);
             TileOut<1, kPairEpilogue> out;
@@ -733,12 +764,36 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
                 tile_at(t + step, tiles_m, tiles_n, next_m, next_n);
                 tile_lines(a, next_m * TN, next_n * 2 * kRowsW + (int)rank * kRowsW, TN, tid);
             }
-            if (!__all_sync(0xffffffffu, mbar_wait(sums_full + 8 * acc.idx, acc.ph, &abort_flag, a.err))) break;
-            tc_fence_after();
-            out.run(a, tmem + acc.idx * TN, w);
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) arrive_at(empty0 + 8 * acc.idx);
+            constexpr int kRuns = LONG ? TN / (kPairEpilogue * 4) : 1;  // of 16 rows, of a warp
+            float total[kRuns][16];
+            for (int k0 = 0; k0 < kb && ok; k0 += part, acc.next()) {
+                ok = __all_sync(0xffffffffu, mbar_wait(sums_full + 8 * acc.idx, acc.ph, &abort_flag, a.err));
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t sums = tmem + acc.idx * TN;
+                if constexpr (LONG) {
+                    const uint32_t lanes = sums + ((uint32_t)(w & 3) << 21) + (w >> 2) * 16;
+#pragma unroll
+                    for (int i = 0; i < kRuns; ++i) {
+                        Cols<16> v;
+                        v.issue(lanes + i * kPairEpilogue * 4);
+                        v.wait();
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            total[i][j] = (k0 ? total[i][j] : 0.0f) + __uint_as_float(v.r[j]);
+                    }
+                } else {
+                    out.run(a, sums, w, 1, 0);
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_at(empty0 + 8 * acc.idx);
+            }
+            if constexpr (LONG) {
+#pragma unroll
+                for (int i = 0; i < kRuns; ++i)
+                    if (ok && out.c < out.rows) out.emit(a, total[i], out.gate[0], out.residual[0]);
+            }
         }
     }
     __syncwarp();
@@ -810,12 +865,12 @@ cudaError_t prepare(K kernel, int smem, std::atomic<int> *known, int *n, int pai
     return cudaSuccess;
 }
 
-template <int TN, bool CODES>
+template <int TN, bool CODES, bool LONG>
 cudaError_t launch_pair(const LinearArgs &a, const Operands &o, cudaStream_t s) {
     using T = Pair<TN>;
     static std::atomic<int> known[64];
     int pairs;
-    cudaError_t e = prepare(linear_pair_kernel<TN, CODES>, T::kSmem, known, &pairs, o.sms / 2 * 2);
+    cudaError_t e = prepare(linear_pair_kernel<TN, CODES, LONG>, T::kSmem, known, &pairs, o.sms / 2 * 2);
     if (e != cudaSuccess) return e;
     CUtensorMap wmap, xmap;
     if (!rows_map(&wmap, o.w, o.w_stride, a.N, a.K, a.type, kRowsW) ||
@@ -826,13 +881,13 @@ cudaError_t launch_pair(const LinearArgs &a, const Operands &o, cudaStream_t s) 
     cudaLaunchAttribute at{};
     c.numAttrs = pdl_attr(at);
     c.attrs = &at;
-    return cudaLaunchKernelEx(&c, linear_pair_kernel<TN, CODES>, wmap, xmap, a);
+    return cudaLaunchKernelEx(&c, linear_pair_kernel<TN, CODES, LONG>, wmap, xmap, a);
 }
 
 template <bool CODES>
 cudaError_t launch_split(const LinearArgs &a, const Operands &o, const Cut &cut, cudaStream_t s) {
     // (the parts lie where the stages were)
-    if (cut.stages < 2 || cut.tn * kRowsW * 4 > cut.stages * cut.stage_bytes()) return cudaErrorInvalidValue;
+    if (cut.stages < 2 || cut.tn * cut.sums > 512 || cut.tn * kRowsW * 4 > cut.stages * cut.stage_bytes()) return cudaErrorInvalidValue;
     static std::atomic<int> known[64];
     int one;
     cudaError_t e = prepare(linear_split_kernel<CODES>, kMaxSmem, known, &one, 0);
@@ -850,11 +905,12 @@ cudaError_t launch_split(const LinearArgs &a, const Operands &o, const Cut &cut,
     at[1].val.clusterDim.x = (unsigned)cut.split;
     at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     c.attrs = at;
-    return cudaLaunchKernelEx(&c, linear_split_kernel<CODES>, wmap, xmap, a, cut.tn, cut.stages);
+    return cudaLaunchKernelEx(&c, linear_split_kernel<CODES>, wmap, xmap, a, cut.tn, cut.stages, cut.sums);
 }
 
-Cut make_cut(int tn, int split, int per_sm) {
-    Cut c{tn, split, 0};
+// sums: wanted (tensor memory bounds them)
+Cut make_cut(int tn, int split, int per_sm, int sums) {
+    Cut c{tn, split, 0, std::min(sums, 512 / per_sm / tn)};
     c.stages = (kMaxSmem / per_sm - 1024 * per_sm) / c.stage_bytes();
     if (c.stages > kMaxStages) c.stages = kMaxStages;
     return c;
@@ -874,7 +930,7 @@ Cut make_cut(int tn, int split, int per_sm) {
 //    epilogue of the tile before, 6.2 and 3.7 us; 3 us for its start.
 struct Size {
     int M, N, kb, sms;
-    bool even, lined;  // columns go in pairs; rows begin at multiples of 128 bytes
+    bool even, lined, exact;  // columns go in pairs; rows begin at multiples of 128 bytes; fp32 result
     double hbm() const { return ((double)N + M) * kb * kLine / 6.6e6; }
 };
 
@@ -910,7 +966,9 @@ Cut best_cut(const Size &z, const int (&fits)[2][kMaxSplit + 1], double *time) {
         const int64_t tiles = (int64_t)((z.N + kRowsW - 1) / kRowsW) * ((z.M + tn - 1) / tn);
         for (int split = 1; split <= kMaxSplit && split * 3 <= std::max(z.kb, 3); ++split)
             for (int per_sm = 1; per_sm <= 2; ++per_sm) {
-                const Cut c = make_cut(tn, split, per_sm);
+                const int sums = z.exact ? ((z.kb + split - 1) / split + kExactLines - 1) / kExactLines : 1;
+                const Cut c = make_cut(tn, split, per_sm, sums);
+                if (c.sums < sums) continue;
                 if (c.stages < 3 || (split > 1 && tiles * split > fits[per_sm - 1][split])) continue;
                 const double t = split_time(z, c, per_sm);
                 if (t < *time) {
@@ -964,15 +1022,17 @@ cudaError_t by_size(const LinearArgs &a, const Operands &o, cudaStream_t s) {
         return (uintptr_t)p % kLine == 0 && (rows == 1 || stride * size % kLine == 0);
     };
     const Size z{a.M, a.N, (a.K * size + kLine - 1) / kLine, o.sms, a.vec2,
-                 at_lines(o.x, o.x_stride, a.M) && at_lines(o.w, o.w_stride, a.N)};
+                 at_lines(o.x, o.x_stride, a.M) && at_lines(o.w, o.w_stride, a.N), a.out.type == MOE_T_F32};
     int fits[2][kMaxSplit + 1];
     cudaError_t e = cluster_room<CODES>(fits);
     if (e != cudaSuccess) return e;
     double split;
     const Cut cut = best_cut(z, fits, &split);
-    const double wide = pair_time(z, 256), half = pair_time(z, 128);
+    const bool parts = z.exact && z.kb > kExactLines;
+    const double wide = parts ? 1e30 : pair_time(z, 256), half = pair_time(z, 128);
     if (split <= wide && split <= half) return launch_split<CODES>(a, o, cut, s);
-    return half < wide ? launch_pair<128, CODES>(a, o, s) : launch_pair<256, CODES>(a, o, s);
+    if (parts) return launch_pair<128, CODES, true>(a, o, s);
+    return half < wide ? launch_pair<128, CODES, false>(a, o, s) : launch_pair<256, CODES, false>(a, o, s);
 }
 
 // `count` neighbours of a row may be one access.
