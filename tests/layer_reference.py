@@ -4,7 +4,6 @@ import math
 
 import torch
 
-HALF_STEP = {torch.bfloat16: 2.0 ** -9, torch.float16: 2.0 ** -12, torch.float32: 2.0 ** -25}
 U = 2.0 ** -24  # half a step of fp32, relative
 
 

@@ -129,3 +129,33 @@ def test_reference_routing():
     assert ids.tolist() == [[3, 2]] and w.tolist() == [[1.0, 0.0]]
     ids, w = ref.route_experts(torch.full((1, 4), -inf), 2, "sigmoid")
     assert ids.tolist() == [[0, 1]] and w.tolist() == [[0.0, 0.0]]
+
+
+def test_header_is_plain_c(tmp_path):
+    """The header by itself in a pedantic C11 program that links the library and is refused
+    its arguments."""
+    import shutil
+    import subprocess
+    gcc = shutil.which("gcc")
+    if gcc is None:
+        pytest.skip("no C compiler")
+    layer.load_library()
+    lib = ops.library_path()
+    src, exe = tmp_path / "use.c", tmp_path / "use"
+    src.write_text("""#include "moe_layer.h"
+#include <stdio.h>
+int main(void) {
+    printf("%d\\n", moe_add_norm(0, MOE_T_BF16, 8, 0, 0, 0, 0, 0, 1e-6f, 1, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0));
+    printf("%d\\n", moe_linear(0, 8, 0, 0, 8, 0, MOE_T_E4M3, 0, MOE_ACT_SILU, 0, 0, 0, 0, 0, 0, 0,
+                              MOE_T_F32, 8, 1, 8, 8, 0, 0));
+    printf("%d\\n", moe_route_experts(0, MOE_T_F32, 8, 0, 0, 8, 2, MOE_SCORE_SIGMOID, 1, 1, 1, 1, 1.0f, 0, 0,
+                                     0));
+    return 0;
+}
+""")
+    r = subprocess.run([gcc, "-std=c11", "-pedantic", "-Wall", "-Wextra", "-Werror", "-I",
+                        os.path.join(ROOT, "include"), str(src), lib, "-Wl,-rpath," + os.path.dirname(lib),
+                        "-o", str(exe)], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    out = subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout.split()
+    assert [int(v) for v in out] == [SHAPE, NULL, 0]

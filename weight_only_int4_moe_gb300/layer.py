@@ -269,3 +269,27 @@ def moe_route_experts(logits, top_k: int, scoring: str = "softmax", bias=None, g
             topk_weights.data_ptr(), _raw_stream(stream, dev))
     _call((_lib or load_library()).moe_route_experts, "moe_route_experts", dev, args)
     return topk_ids, topk_weights
+
+
+def moe_int4_forward_hidden(x, experts: ops.PackedWeights, router: Linear, scoring: str = "softmax",
+                            bias=None, groups: int = 1, top_groups: int | None = None,
+                            group_best: int = 2, renormalize: bool = True, scale: float = 1.0,
+                            out=None, workspace=None, stream=None):
+    """The expert layer from the tokens alone: router logits in fp32 (moe_linear; router's
+    bias, if it has one, is added to them), their routing (moe_route_experts) and
+    moe_int4_forward.  x bf16 [M, hidden].  Returns (out, topk_ids, topk_weights)."""
+    shape = experts.shape
+    if (router.N, router.K) != (shape.E, shape.hidden):
+        raise ValueError(f"router: expected [{shape.E}, {shape.hidden}], got "
+                         f"[{router.N}, {router.K}]")
+    logits = moe_linear(x, router, out_dtype=_F32, stream=stream)
+    ids, weights = moe_route_experts(logits, shape.top_k, scoring, bias, groups, top_groups, group_best,
+                                     renormalize, scale, stream=stream)
+    if out is None:
+        out = _empty((x.shape[0], shape.hidden), shape.torch_out_dtype, x.device, stream)
+    if workspace is None:
+        n = max(ops.moe_int4_workspace_bytes(x.shape[0], shape), 256)
+        workspace = _empty((n,), torch.uint8, x.device, stream)
+        ops.moe_int4_clear_errors(workspace, stream)
+    experts.forward(x, ids, weights, out=out, workspace=workspace, stream=stream)
+    return out, ids, weights
