@@ -53,6 +53,9 @@ struct LinearArgs {
     uint32_t *err;
     bool vec_gate, vec_residual, vec_out;  // four neighbours of a row may be one access
     bool vec2;  // two may, in each of the three
+    // Debug-bounds builds: block 0 leaves the copy of w for its i-th line out, so that a wait runs
+    // out.  -1: none.
+    int skip_line;
 };
 
 struct RouteExpertsArgs {

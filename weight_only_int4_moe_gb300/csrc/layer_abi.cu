@@ -3,6 +3,7 @@
 #include <stdint.h>
 
 #include <cmath>
+#include <cstdlib>
 
 #include "layer.cuh"
 
@@ -112,6 +113,10 @@ int moe_linear(const void *x, int64_t x_stride, const float *x_scale, const void
     a.residual = MatIn{residual, residual_stride, residual_type};
     a.out = MatOut{out, out_stride, out_type};
     a.err = err;
+    a.skip_line = -1;
+#ifdef MOE_DEBUG_BOUNDS
+    if (const char *v = getenv("MOE_LINEAR_DEBUG_SKIP_LINE")) a.skip_line = atoi(v);
+#endif
     return done(launch_linear(a, x, x_stride, w, w_stride, sms, str(stream)));
 }
 

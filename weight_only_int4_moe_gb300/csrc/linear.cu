@@ -521,7 +521,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                 if (!mbar_wait(empty + 8 * r.idx, r.ph ^ 1, &abort_flag, a.err)) break;
                 const uint32_t bar = full + 8 * r.idx, s = stages + r.idx * stage_bytes;
                 mbar_arrive_expect_tx(bar, stage_bytes);
-                tma_load_2d(s, &wmap, k * kElems, n0, bar);
+                if (!(kDebugBounds && issued == a.skip_line && blockIdx.x == 0 && blockIdx.y == 0))
+                    tma_load_2d(s, &wmap, k * kElems, n0, bar);
                 tma_load_2d(s + kBytesW, &xmap, k * kElems, m0, bar);
                 ++issued;
             }
@@ -545,7 +546,12 @@ __global__ void __launch_bounds__(kThreads, 2)
             mma_stage<CODES, false>(tmem + sum * tn, smem_desc_sw128(s), smem_desc_sw128(s + kBytesW),
                                     idesc, k >= kb0 + n_sums, empty + 8 * r.idx);
         }
-        tc_commit_elect(done);  // also after giving up: products in flight end first
+        tc_commit_elect(done);
+        if (__any_sync(0xffffffffu, *(volatile int *)&abort_flag)) {
+            // products in flight end before the tensor memory is given back
+            volatile int none = 0;
+            mbar_wait(done, 0, &none, a.err);
+        }
     }
     // The sums are complete, and with them every copy has been used.
     __syncwarp();
@@ -706,7 +712,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
                     if (!ok) break;
                     const uint32_t s = stages + r.idx * T::kStage;
                     if (rank == 0) mbar_arrive_expect_tx(full + 8 * r.idx, 2 * T::kStage);
-                    tma_load_pair(s, &wmap, k * kElems, n0, full0 + 8 * r.idx);
+                    if (!(kDebugBounds && issued == a.skip_line && blockIdx.x == 0))
+                        tma_load_pair(s, &wmap, k * kElems, n0, full0 + 8 * r.idx);
                     tma_load_pair(s + kBytesW, &xmap, k * kElems, m0, full0 + 8 * r.idx);
                     ++issued;
                 }
