@@ -939,6 +939,10 @@ struct Size {
     int M, N, kb, sms;
     bool even, lined, exact;  // columns go in pairs; rows begin at multiples of 128 bytes; fp32 result
     double hbm() const { return ((double)N + M) * kb * kLine / 6.6e6; }
+    bool operator==(const Size &o) const {
+        return M == o.M && N == o.N && kb == o.kb && sms == o.sms && even == o.even && lined == o.lined &&
+               exact == o.exact;
+    }
 };
 
 double split_time(const Size &z, const Cut &c, int per_sm) {
@@ -1022,6 +1026,38 @@ cudaError_t cluster_room(int (&fits)[2][kMaxSplit + 1]) {
     return cudaSuccess;
 }
 
+// What a product's sizes decide: the kernel (pair: rows of x of a pair's tile, or 0) and its cut.
+struct Plan {
+    Size z;
+    int pair;
+    Cut cut;
+};
+
+Plan make_plan(const Size &z, const int (&fits)[2][kMaxSplit + 1]) {
+    double split;
+    Plan p{z, 0, best_cut(z, fits, &split)};
+    const double wide = z.exact && z.kb > kExactLines ? 1e30 : pair_time(z, 256), half = pair_time(z, 128);
+    if (split > std::min(wide, half)) p.pair = half < wide ? 128 : 256;
+    return p;
+}
+
+// The plan of a size, worked out once (5 us) and kept by each thread for its last sizes.
+template <bool CODES>
+cudaError_t plan_of(const Size &z, Plan *plan) {
+    static thread_local Plan kept[64];
+    uint32_t h = (uint32_t)z.M * 2654435761u ^ (uint32_t)z.N * 2246822519u ^ (uint32_t)z.kb * 3266489917u;
+    h ^= (uint32_t)(z.even + 2 * z.lined + 4 * z.exact) * 668265263u;
+    Plan &k = kept[(h ^ h >> 15) % 64];
+    if (!(k.z == z)) {
+        int fits[2][kMaxSplit + 1];
+        const cudaError_t e = cluster_room<CODES>(fits);
+        if (e != cudaSuccess) return e;
+        k = make_plan(z, fits);
+    }
+    *plan = k;
+    return cudaSuccess;
+}
+
 template <bool CODES>
 cudaError_t by_size(const LinearArgs &a, const Operands &o, cudaStream_t s) {
     const int size = CODES ? 1 : 2;
@@ -1030,16 +1066,14 @@ cudaError_t by_size(const LinearArgs &a, const Operands &o, cudaStream_t s) {
     };
     const Size z{a.M, a.N, (a.K * size + kLine - 1) / kLine, o.sms, a.vec2,
                  at_lines(o.x, o.x_stride, a.M) && at_lines(o.w, o.w_stride, a.N), a.out.type == MOE_T_F32};
-    int fits[2][kMaxSplit + 1];
-    cudaError_t e = cluster_room<CODES>(fits);
+    Plan p;
+    const cudaError_t e = plan_of<CODES>(z, &p);
     if (e != cudaSuccess) return e;
-    double split;
-    const Cut cut = best_cut(z, fits, &split);
-    const bool parts = z.exact && z.kb > kExactLines;
-    const double wide = parts ? 1e30 : pair_time(z, 256), half = pair_time(z, 128);
-    if (split <= wide && split <= half) return launch_split<CODES>(a, o, cut, s);
-    if (parts) return launch_pair<128, CODES, true>(a, o, s);
-    return half < wide ? launch_pair<128, CODES, false>(a, o, s) : launch_pair<256, CODES, false>(a, o, s);
+    if (p.pair == 256) return launch_pair<256, CODES, false>(a, o, s);
+    if (p.pair == 128)
+        return z.exact && z.kb > kExactLines ? launch_pair<128, CODES, true>(a, o, s)
+                                             : launch_pair<128, CODES, false>(a, o, s);
+    return launch_split<CODES>(a, o, p.cut, s);
 }
 
 // `count` neighbours of a row may be one access.
