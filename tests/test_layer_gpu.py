@@ -45,7 +45,8 @@ def within(got, want, bound, dtype):
 # rows x hidden: a thread, a warp, several; whole vectors and odd ends; more than one
 # vector a thread; the largest
 SIZES = [(1, 1), (3, 7), (5, 8), (2, 250), (4, 256), (7, 264), (3, 1411), (2, 7168), (2, 8200),
-         (2, 9001), (1, 16392), (1, 32768), (1, 32761), (33, 128)]
+         (2, 9001), (1, 16392), (1, 32768), (1, 32761), (33, 128), (20, 1003), (9, 4095), (10, 5),
+         (17, 1), (9, 8190), (5, 8188), (3, 32763)]
 
 
 @pytest.mark.parametrize("rows,hidden", SIZES)

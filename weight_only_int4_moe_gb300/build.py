@@ -26,9 +26,10 @@ DEBUG_BUILD = os.path.join(BUILD, "debug_bounds")
 DEBUG_LIB = os.path.join(DEBUG_BUILD, "libmoe_int4.so")
 SOURCES = ["abi.cu", "align.cu", "pack.cu", "gemm.cu", "noalloc.cu", "ep.cu", "gemv.cu",
            "kv4_abi.cu", "kv4_append.cu", "kv4_decode.cu", "kv4_pages.cu", "kv4_prefill.cu",
-           "layer_abi.cu", "add_norm.cu", "linear.cu", "router.cu"]
+           "layer_abi.cu", "add_norm.cu", "add_norm_bf16.cu", "add_norm_f16.cu",
+           "add_norm_f32.cu", "linear.cu", "router.cu"]
 HEADERS = ["common.cuh", "kernels.cuh", "dequant.cuh", "gemv.cuh", "kv4.cuh", "kv4_launch.cuh",
-           "layer.cuh"]
+           "layer.cuh", "add_norm.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
               "--expt-relaxed-constexpr", "-I" + os.path.join(ROOT, "include")]

@@ -1,361 +1,33 @@
-// The residual's addition and the root-mean-square norm of each row (moe_add_norm):
-//   h = x + residual,  y = h * (1 / sqrt(sum h^2 / H + eps)) * weight,
-// y rounded to the output's type and, where wanted, to e4m3 codes with one scale a row.
-//
-// Bound by memory: x and the residual are read once, the row stays in registers, and h, y
-// and the codes are written once.  A block has one row; its threads hold vectors of eight
-// elements (single elements where rows do not all begin at multiples of 16 bytes).
-//
-// An 8-bit code is decided by y to the last bit wherever y / scale lies next to the middle
-// of two codes, and y by the sum of squares.  So the sum must not depend on how a row is
-// cut into threads: it is held as a number and its rounding error (two-sum: the error of an
-// addition is itself an fp32 number), some 45 bits in all, and rounded once at the end.
-#include <cfloat>
-
+// Host side of moe_add_norm: how the rows lie, and the kernels of x's type (add_norm.cuh, one file
+// for each type).
 #include "layer.cuh"
 
 namespace moe {
 
 namespace {
 
-// A sum as hi + lo, hi = fl(hi + lo).
-struct Sum2 {
-    float hi, lo;
-};
-// a + b = s + e exactly (Knuth's two-sum).
-MOE_DEV void two_sum(float a, float b, float &s, float &e) {
-    s = __fadd_rn(a, b);
-    const float bb = __fsub_rn(s, a);
-    e = __fadd_rn(__fsub_rn(a, __fsub_rn(s, bb)), __fsub_rn(b, bb));
-}
-MOE_DEV void add_square(Sum2 &t, float h) {
-    const float q = __fmul_rn(h, h);
-    float s, e;
-    two_sum(t.hi, q, s, e);
-    t.hi = s;
-    t.lo = __fadd_rn(t.lo, __fadd_rn(e, __fmaf_rn(h, h, -q)));
-}
-MOE_DEV Sum2 join(Sum2 a, Sum2 b) {
-    float s, e;
-    two_sum(a.hi, b.hi, s, e);
-    e = __fadd_rn(e, __fadd_rn(a.lo, b.lo));
-    // not renormalised: lo stays far below hi, and the order of joining does not matter
-    // beyond lo's own rounding
-    return Sum2{s, e};
-}
-
-// VEC consecutive elements of a type as they lie in memory.
-template <int TYPE, int VEC>
-struct Elems {
-    static constexpr int kWords = TYPE == MOE_T_F32 ? VEC : VEC / 2;
-    uint32_t w[kWords ? kWords : 1];
-
-    MOE_DEV void load(const void *p, int64_t i) {
-        if constexpr (VEC == 1) {
-            if constexpr (TYPE == MOE_T_F32)
-                w[0] = reinterpret_cast<const uint32_t *>(p)[i];
-            else
-                w[0] = reinterpret_cast<const uint16_t *>(p)[i];
-        } else {
-            const uint4 *q = reinterpret_cast<const uint4 *>(
-                reinterpret_cast<const char *>(p) + i * (TYPE == MOE_T_F32 ? 4 : 2));
-#pragma unroll
-            for (int k = 0; k < kWords / 4; ++k) {
-                const uint4 v = q[k];
-                w[4 * k] = v.x;
-                w[4 * k + 1] = v.y;
-                w[4 * k + 2] = v.z;
-                w[4 * k + 3] = v.w;
-            }
-        }
-    }
-    MOE_DEV void store(void *p, int64_t i) const {
-        if constexpr (VEC == 1) {
-            if constexpr (TYPE == MOE_T_F32)
-                reinterpret_cast<uint32_t *>(p)[i] = w[0];
-            else
-                reinterpret_cast<uint16_t *>(p)[i] = (uint16_t)w[0];
-        } else {
-            uint4 *q = reinterpret_cast<uint4 *>(reinterpret_cast<char *>(p) +
-                                                 i * (TYPE == MOE_T_F32 ? 4 : 2));
-#pragma unroll
-            for (int k = 0; k < kWords / 4; ++k)
-                q[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
-        }
-    }
-    MOE_DEV void zero() {
-#pragma unroll
-        for (int k = 0; k < (kWords ? kWords : 1); ++k) w[k] = 0u;
-    }
-    MOE_DEV float get(int j) const {
-        if constexpr (TYPE == MOE_T_F32) return __uint_as_float(w[j]);
-        const uint32_t v = (j & 1) ? w[j / 2] >> 16 : w[j / 2] & 0xFFFFu;
-        if constexpr (TYPE == MOE_T_BF16) return __uint_as_float(v << 16);
-        return __half2float(__ushort_as_half((uint16_t)v));
-    }
-    // Rounds f to the type.
-    MOE_DEV void set(const float (&f)[VEC]) {
-        if constexpr (TYPE == MOE_T_F32) {
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) w[j] = __float_as_uint(f[j]);
-        } else if constexpr (VEC == 1) {
-            w[0] = to_bits16(f[0], TYPE);
-        } else {
-#pragma unroll
-            for (int j = 0; j < VEC / 2; ++j) {
-                if constexpr (TYPE == MOE_T_BF16)
-                    asm("cvt.rn.bf16x2.f32 %0, %1, %2;"
-                        : "=r"(w[j])
-                        : "f"(f[2 * j + 1]), "f"(f[2 * j]));
-                else
-                    asm("cvt.rn.f16x2.f32 %0, %1, %2;"
-                        : "=r"(w[j])
-                        : "f"(f[2 * j + 1]), "f"(f[2 * j]));
-            }
-        }
-    }
-};
-
-template <int VEC>
-MOE_DEV void store_as(const MatOut &o, int64_t i, const float (&f)[VEC]) {
-    if (o.type == MOE_T_F32) {
-        Elems<MOE_T_F32, VEC> v;
-        v.set(f);
-        v.store(o.p, i);
-    } else if (o.type == MOE_T_BF16) {
-        Elems<MOE_T_BF16, VEC> v;
-        v.set(f);
-        v.store(o.p, i);
-    } else {
-        Elems<MOE_T_F16, VEC> v;
-        v.set(f);
-        v.store(o.p, i);
-    }
-}
-
-template <int VEC>
-MOE_DEV void load_weight(const AddNormArgs &a, int i, float (&f)[VEC]) {
-    if (!a.weight) {
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) f[j] = 1.0f;
-    } else if (a.weight_type == MOE_T_F32) {
-        Elems<MOE_T_F32, VEC> v;
-        v.load(a.weight, i);
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) f[j] = v.get(j);
-    } else if (a.weight_type == MOE_T_BF16) {
-        Elems<MOE_T_BF16, VEC> v;
-        v.load(a.weight, i);
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) f[j] = v.get(j);
-    } else {
-        Elems<MOE_T_F16, VEC> v;
-        v.load(a.weight, i);
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) f[j] = v.get(j);
-    }
-}
-
-MOE_DEV uint16_t e4m3x2(float lo, float hi) {
-    uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
-constexpr int kNone = -1;  // no residual
-
-// TX, TS: types of x and of the residual; VEC: elements of a load; NV: loads of a thread;
-// MAX: threads of a block at most.
-template <int TX, int TS, int VEC, int NV, int MAX>
-__global__ void __launch_bounds__(MAX, 1024 / MAX) add_norm_kernel(const AddNormArgs a) {
-    __shared__ float part_hi[32], part_lo[32], part_max[32];
-    __shared__ double part_d[32];
-    const int row = blockIdx.x, tid = threadIdx.x, T = blockDim.x, lane = tid & 31;
-    const int warps = T >> 5, H = a.hidden;
-    constexpr bool kAdd = TS != kNone;
-    constexpr int kHeld = kAdd ? TS : TX;  // h has this type exactly: it is kept as it lies in memory
-    pdl_wait();
-    pdl_launch_dependents();
-
-    Elems<kHeld, VEC> h[NV];
-    float w[NV == 1 ? VEC : 1];
-    if constexpr (kAdd) {
-        Elems<TX, VEC> x[NV];
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int p = (i * T + tid) * VEC;
-            if (p < H) {
-                x[i].load(a.x.p, row * a.x.stride + p);
-                h[i].load(a.residual.p, row * a.residual.stride + p);
-            }
-        }
-        if constexpr (NV == 1)
-            if (tid * VEC < H) load_weight<VEC>(a, tid * VEC, w);
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int p = (i * T + tid) * VEC;
-            if (p < H) {
-                float f[VEC];
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) f[j] = __fadd_rn(x[i].get(j), h[i].get(j));
-                h[i].set(f);
-                if (a.residual_out.p) h[i].store(a.residual_out.p, row * a.residual_out.stride + p);
-            } else {
-                h[i].zero();
-            }
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int p = (i * T + tid) * VEC;
-            h[i].zero();
-            if (p < H) h[i].load(a.x.p, row * a.x.stride + p);
-        }
-        if constexpr (NV == 1)
-            if (tid * VEC < H) load_weight<VEC>(a, tid * VEC, w);
-    }
-
-    Sum2 t{0.0f, 0.0f};
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) add_square(t, h[i].get(j));
-#pragma unroll
-    for (int o = 16; o; o >>= 1)
-        t = join(t, Sum2{__shfl_xor_sync(0xffffffffu, t.hi, o), __shfl_xor_sync(0xffffffffu, t.lo, o)});
-    if (warps > 1) {
-        if (lane == 0) {
-            part_hi[tid >> 5] = t.hi;
-            part_lo[tid >> 5] = t.lo;
-        }
-        __syncthreads();
-        t = lane < warps ? Sum2{part_hi[lane], part_lo[lane]} : Sum2{0.0f, 0.0f};
-#pragma unroll
-        for (int o = 16; o; o >>= 1)
-            t = join(t, Sum2{__shfl_xor_sync(0xffffffffu, t.hi, o),
-                             __shfl_xor_sync(0xffffffffu, t.lo, o)});
-    }
-    // the compensation of an infinite or NaN sum is NaN: the sum itself counts then
-    const float total = fabsf(t.hi) <= FLT_MAX ? __fadd_rn(t.hi, t.lo) : t.hi;
-    float q;
-    if (!(total < 1e37f) || (total < 1e-30f && a.eps < 1e-24f)) {
-        // squares beyond fp32, or below it with nothing added to them
-        double d = 0.0;
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) d += (double)h[i].get(j) * (double)h[i].get(j);
-#pragma unroll
-        for (int o = 16; o; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-        if (warps > 1) {
-            if (lane == 0) part_d[tid >> 5] = d;
-            __syncthreads();
-            d = lane < warps ? part_d[lane] : 0.0;
-#pragma unroll
-            for (int o = 16; o; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-        }
-        q = (float)(1.0 / sqrt(d / H + (double)a.eps));
-    } else {
-        q = __frcp_rn(__fsqrt_rn(__fadd_rn(__fmul_rn(total, a.inv_hidden), a.eps)));
-    }
-
-    float top = 0.0f, y[NV][VEC];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int p = (i * T + tid) * VEC;
-        if (p < H) {
-            float f[VEC];
-            if constexpr (NV > 1) load_weight<VEC>(a, p, f);
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                y[i][j] = __fmul_rn(__fmul_rn(h[i].get(j), q), NV == 1 ? w[j] : f[j]);
-                top = fmaxf(top, fabsf(y[i][j]));  // (NaN is not counted)
-            }
-            if (a.out.p) store_as<VEC>(a.out, row * a.out.stride + p, y[i]);
-        }
-    }
-    if (!a.codes) return;
-#pragma unroll
-    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (warps > 1) {
-        if (lane == 0) part_max[tid >> 5] = top;
-        __syncthreads();
-        top = lane < warps ? part_max[lane] : 0.0f;
-#pragma unroll
-        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    }
-    const float scale = fmaxf(__fmul_rn(top, 1.0f / 448.0f), 0x1p-100f);
-    const float inv = __frcp_rn(scale);
-    if (tid == 0) a.scales[row] = scale;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int p = (i * T + tid) * VEC;
-        if (p >= H) continue;
-        uint8_t *c = a.codes + row * a.codes_stride + p;
-        if constexpr (VEC == 1) {
-            *c = (uint8_t)e4m3x2(__fmul_rn(y[i][0], inv), 0.0f);
-        } else {
-            uint32_t v[2];
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-                v[k] = e4m3x2(__fmul_rn(y[i][4 * k], inv), __fmul_rn(y[i][4 * k + 1], inv)) |
-                       (uint32_t)e4m3x2(__fmul_rn(y[i][4 * k + 2], inv),
-                                        __fmul_rn(y[i][4 * k + 3], inv))
-                           << 16;
-            *reinterpret_cast<uint2 *>(c) = make_uint2(v[0], v[1]);
-        }
-    }
-}
-
-template <int TX, int TS, int VEC, int NV, int MAX>
-cudaError_t launch(const AddNormArgs &a, cudaStream_t s) {
-    const int per = VEC * NV, T = ((a.hidden + per - 1) / per + 31) / 32 * 32;
-    auto c = pdl_config((unsigned)a.rows, (unsigned)T, 0, s);
-    cudaLaunchAttribute at{};
-    c.numAttrs = pdl_attr(at);
-    c.attrs = &at;
-    return cudaLaunchKernelEx(&c, add_norm_kernel<TX, TS, VEC, NV, MAX>, a);
-}
-
-template <int TX, int TS>
-cudaError_t by_size(const AddNormArgs &a, bool vec, int sms, cudaStream_t s) {
-    if (vec) {
-        if (a.hidden <= 8192) {
-            if (a.hidden <= 1024 || a.rows <= 2 * sms) return launch<TX, TS, 8, 1, 1024>(a, s);
-            return launch<TX, TS, 8, 4, 256>(a, s);
-        }
-        return launch<TX, TS, 8, 4, 1024>(a, s);
-    }
-    if (a.hidden <= 4096) return launch<TX, TS, 1, 8, 512>(a, s);
-    return launch<TX, TS, 1, 32, 1024>(a, s);
-}
-
-template <int TX>
-cudaError_t by_stream(const AddNormArgs &a, bool vec, int sms, cudaStream_t s) {
-    if (!a.residual.p) return by_size<TX, kNone>(a, vec, sms, s);
-    if (a.residual.type == MOE_T_BF16) return by_size<TX, MOE_T_BF16>(a, vec, sms, s);
-    if (a.residual.type == MOE_T_F16) return by_size<TX, MOE_T_F16>(a, vec, sms, s);
-    return by_size<TX, MOE_T_F32>(a, vec, sms, s);
-}
-
-// Every row of a matrix begins at a multiple of `to` bytes.
-bool rows_at(const void *p, int64_t stride, int size, int rows, int to) {
-    return !p || (((uintptr_t)p % to) == 0 && (rows == 1 || stride * size % to == 0));
+// Of a matrix (size: bytes of an element): may its rows lie on a grid of eight elements whose
+// place the first matrix's stride gives?
+bool on_grid(const void *p, int64_t stride, int size, int rows, int stride8) {
+    return !p || (((uintptr_t)p % (size == 1 ? 8 : 16)) == 0 && (rows == 1 || (stride & 7) == stride8));
 }
 int size_of(int type) { return type == MOE_T_F32 ? 4 : 2; }
 
 }  // namespace
 
-cudaError_t launch_add_norm(const AddNormArgs &a, int sms, cudaStream_t s) {
+cudaError_t launch_add_norm(AddNormArgs a, int sms, cudaStream_t s) {
     const int n = a.rows;
-    const bool vec = a.hidden % 8 == 0 && rows_at(a.x.p, a.x.stride, size_of(a.x.type), n, 16) &&
-                     rows_at(a.residual.p, a.residual.stride, size_of(a.residual.type), n, 16) &&
-                     rows_at(a.residual_out.p, a.residual_out.stride, size_of(a.residual.type), n, 16) &&
-                     rows_at(a.out.p, a.out.stride, size_of(a.out.type), n, 16) &&
-                     rows_at(a.weight, 0, 2, 1, 16) && rows_at(a.codes, a.codes_stride, 1, n, 8);
-    if (a.x.type == MOE_T_BF16) return by_stream<MOE_T_BF16>(a, vec, sms, s);
-    if (a.x.type == MOE_T_F16) return by_stream<MOE_T_F16>(a, vec, sms, s);
-    return by_stream<MOE_T_F32>(a, vec, sms, s);
+    a.stride8 = n == 1 ? 0 : (int)(a.x.stride & 7);
+    Grid grid = Grid::kNone;
+    if (on_grid(a.x.p, a.x.stride, size_of(a.x.type), n, a.stride8) &&
+        on_grid(a.residual.p, a.residual.stride, size_of(a.residual.type), n, a.stride8) &&
+        on_grid(a.residual_out.p, a.residual_out.stride, size_of(a.residual.type), n, a.stride8) &&
+        on_grid(a.out.p, a.out.stride, size_of(a.out.type), n, a.stride8) &&
+        on_grid(a.weight, 0, 2, 1, 0) && on_grid(a.codes, a.codes_stride, 1, n, a.stride8))
+        grid = a.hidden % 8 == 0 && a.stride8 == 0 ? Grid::kVectors : Grid::kEnds;
+    if (a.x.type == MOE_T_BF16) return add_norm_of<MOE_T_BF16>(a, grid, sms, s);
+    if (a.x.type == MOE_T_F16) return add_norm_of<MOE_T_F16>(a, grid, sms, s);
+    return add_norm_of<MOE_T_F32>(a, grid, sms, s);
 }
 
 }  // namespace moe

@@ -1,0 +1,8 @@
+// moe_add_norm for x of MOE_T_F16.
+#include "add_norm.cuh"
+
+namespace moe {
+
+template cudaError_t add_norm_of<MOE_T_F16>(const AddNormArgs &a, Grid grid, int sms, cudaStream_t s);
+
+}  // namespace moe

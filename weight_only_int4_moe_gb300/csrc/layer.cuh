@@ -43,6 +43,7 @@ struct AddNormArgs {
     uint8_t *codes;
     int64_t codes_stride;
     float *scales;
+    int stride8;  // of the rows, modulo 8 (ENDS kernels)
 };
 
 struct LinearArgs {
@@ -69,7 +70,12 @@ struct RouteExpertsArgs {
     float *weights;
 };
 
-cudaError_t launch_add_norm(const AddNormArgs &a, int sms, cudaStream_t s);
+// How an add and norm's rows lie: vectors of eight throughout, vectors but for the ends, or
+// neither.
+enum class Grid { kVectors, kEnds, kNone };
+template <int TX>
+cudaError_t add_norm_of(const AddNormArgs &a, Grid grid, int sms, cudaStream_t s);
+cudaError_t launch_add_norm(AddNormArgs a, int sms, cudaStream_t s);
 // cudaErrorNotSupported: the operands' tensor maps could not be made.
 cudaError_t launch_linear(LinearArgs a, const void *x, int64_t x_stride, const void *w,
                           int64_t w_stride, int sms, cudaStream_t s);
