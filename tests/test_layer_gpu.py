@@ -285,6 +285,55 @@ def test_linear_rows_do_not_meet(layer):
     assert torch.equal(got.isfinite(), ~bad)
 
 
+@pytest.mark.parametrize("m,n,k,dtype,out", [(3, 40, 70000, FP16, FP16), (140, 130, 40000, BF16, FP32),
+                                             (5, 20, 1 << 20, E4M3, FP16)])
+def test_linear_very_long_sums(layer, m, n, k, dtype, out):
+    check_linear(layer, m, n, k, dtype, 3, out_dtype=out)
+
+
+def test_linear_most_rows(layer):
+    """The largest M, more row tiles than a grid's second dimension has at 16 rows each."""
+    m, n, k = 1 << 20, 3, 16
+    x = torch.randn(m, k, generator=torch.Generator("cuda").manual_seed(1), device="cuda").to(BF16)
+    w = torch.randn(n, k, generator=rng(2)).to(BF16).cuda()
+    lin = layer.Linear(w)
+    got = layer.moe_linear(x, lin, out_dtype=FP32)
+    want = x.double() @ w.double().T
+    bound = (x.double().abs() @ w.double().abs().T) * 2 * ref.U * 33 + ref.U * want.abs()
+    assert ((got.double() - want).abs() <= bound).all() and lin.errors() == 0
+
+
+def test_first_calls_in_a_capture():
+    """Nothing that a kernel's first call sets up keeps it out of a captured graph."""
+    import os
+    import subprocess
+    import sys
+    code = """
+import torch
+from weight_only_int4_moe_gb300 import layer
+x, w = (torch.randn(r, 768, device="cuda").to(torch.bfloat16) for r in (300, 640))
+y, v = (torch.randn(r, 768, device="cuda").to(torch.bfloat16) for r in (4000, 3008))
+a, b = layer.Linear(w), layer.Linear(v)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    p = layer.moe_linear(x, a, out_dtype=torch.float32)
+    q, r = layer.moe_linear(y, b), layer.moe_linear(y, b, out_dtype=torch.float32)
+    s, t = layer.moe_add_norm(p, residual=p), layer.moe_route_experts(p[:, :256], 8, "sigmoid")
+g.replay()
+torch.cuda.synchronize()
+assert torch.equal(p, layer.moe_linear(x, a, out_dtype=torch.float32))
+assert torch.equal(q, layer.moe_linear(y, b))
+assert torch.equal(r, layer.moe_linear(y, b, out_dtype=torch.float32))
+assert torch.equal(s.out, layer.moe_add_norm(p, residual=p).out)
+assert torch.equal(t[0], layer.moe_route_experts(p[:, :256], 8, "sigmoid")[0])
+assert a.errors() == b.errors() == 0
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr
+
+
 def test_linear_without_rows(layer):
     lin = layer.Linear(torch.zeros(64, 64, dtype=BF16, device="cuda"))
     assert layer.moe_linear(torch.zeros(0, 64, dtype=BF16, device="cuda"), lin).shape == (0, 64)

@@ -468,9 +468,10 @@ constexpr int kMaxStages = 12, kMaxSplit = 8;
 
 // Lines of k that one sum in tensor memory takes where the result stays fp32.  The tensor cores
 // cut a sum's last place with every instruction, 4 a line: the error of a random product,
-// relative to it, measured 1.6e-8 an instruction (K = 7168 in one sum 7e-6; 16-bit results do
-// not show it).  So longer products go to several sums, which are added up in fp32.
-constexpr int kExactLines = 12;
+// relative to it, measured 1.6e-8 an instruction (K = 7168 in one sum 7e-6).  So longer products
+// go to several sums, which are added up in fp32.  16-bit results show it from kLongLines on
+// (2048 instructions, 3e-5: a 15th of fp16's half step).
+constexpr int kExactLines = 12, kLongLines = 512;
 
 template <bool CODES>
 __global__ void __launch_bounds__(kThreads, 2)
@@ -937,7 +938,8 @@ Cut make_cut(int tn, int split, int per_sm, int sums) {
 //    epilogue of the tile before, 6.2 and 3.7 us; 3 us for its start.
 struct Size {
     int M, N, kb, sms;
-    bool even, lined, exact;  // columns go in pairs; rows begin at multiples of 128 bytes; fp32 result
+    // columns go in pairs; rows begin at multiples of 128 bytes; no sum takes more than kExactLines
+    bool even, lined, exact;
     double hbm() const { return ((double)N + M) * kb * kLine / 6.6e6; }
     bool operator==(const Size &o) const {
         return M == o.M && N == o.N && kb == o.kb && sms == o.sms && even == o.even && lined == o.lined &&
@@ -975,6 +977,7 @@ Cut best_cut(const Size &z, const int (&fits)[2][kMaxSplit + 1], double *time) {
     for (int tn : {16, 32, 48, 64, 96, 128, whole}) {
         if (tn > whole || tn > 128) continue;
         const int64_t tiles = (int64_t)((z.N + kRowsW - 1) / kRowsW) * ((z.M + tn - 1) / tn);
+        if ((z.M + tn - 1) / tn > 65535) continue;  // (the grid's second dimension)
         for (int split = 1; split <= kMaxSplit && split * 3 <= std::max(z.kb, 3); ++split)
             for (int per_sm = 1; per_sm <= 2; ++per_sm) {
                 const int sums = z.exact ? ((z.kb + split - 1) / split + kExactLines - 1) / kExactLines : 1;
@@ -1064,8 +1067,10 @@ cudaError_t by_size(const LinearArgs &a, const Operands &o, cudaStream_t s) {
     const auto at_lines = [&](const void *p, int64_t stride, int rows) {
         return (uintptr_t)p % kLine == 0 && (rows == 1 || stride * size % kLine == 0);
     };
-    const Size z{a.M, a.N, (a.K * size + kLine - 1) / kLine, o.sms, a.vec2,
-                 at_lines(o.x, o.x_stride, a.M) && at_lines(o.w, o.w_stride, a.N), a.out.type == MOE_T_F32};
+    const int kb = (a.K * size + kLine - 1) / kLine;
+    const Size z{a.M, a.N, kb, o.sms, a.vec2,
+                 at_lines(o.x, o.x_stride, a.M) && at_lines(o.w, o.w_stride, a.N),
+                 a.out.type == MOE_T_F32 || kb > kLongLines};
     Plan p;
     const cudaError_t e = plan_of<CODES>(z, &p);
     if (e != cudaSuccess) return e;

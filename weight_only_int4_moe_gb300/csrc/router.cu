@@ -20,7 +20,7 @@ namespace moe {
 
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kWarps = 2;
 constexpr uint32_t kGone = 0;              // the key of what is taken or not open
 constexpr uint32_t kMasked = 0x007FFFFFu;  // of -inf: what is not available
 
@@ -241,7 +241,7 @@ constexpr int kLogits = 0, kSigmoid = 1, kSoftmax = 2;
 
 // V: experts of a lane.
 template <int V, int KEYS>
-__global__ void __launch_bounds__(32 * kWarps, V <= 12 ? 6 : V <= 16 ? 4 : 2)
+__global__ void __launch_bounds__(32 * kWarps, V <= 12 ? 14 : V <= 16 ? 8 : 4)
     route_experts_kernel(const RouteExpertsArgs a) {
     extern __shared__ uint2 room[];  // of a warp: E pairs (key, expert), or E 64-bit numbers
     __shared__ int order[kWarps][32];
@@ -504,7 +504,7 @@ __global__ void __launch_bounds__(32 * kWarps, V <= 12 ? 6 : V <= 16 ? 4 : 2)
 
 template <int V, int KEYS>
 cudaError_t launch(const RouteExpertsArgs &a, int sms, cudaStream_t s) {
-    const int64_t blocks = ((int64_t)a.M + kWarps - 1) / kWarps, most = (int64_t)sms * 16;
+    const int64_t blocks = ((int64_t)a.M + kWarps - 1) / kWarps, most = (int64_t)sms * 32;
     auto c = pdl_config((unsigned)(blocks < most ? blocks : most), 32 * kWarps, (size_t)kWarps * a.E * 8, s);
     cudaLaunchAttribute at{};
     c.numAttrs = pdl_attr(at);

@@ -169,7 +169,8 @@ def moe_add_norm(x, weight=None, residual=None, eps: float = 1e-6, out_dtype=tor
 class Linear:
     """The weights of a product, built once: weight [N, K] in bf16, fp16 or e4m3 codes
     (rows contiguous, beginning at multiples of 16 bytes), bias [N] (kept in fp32) and, for
-    codes, scale fp32 [N].  ``errors`` reads the device error word of its calls."""
+    codes, scale fp32 [N].  It is made on the current stream, on which, or after which, its
+    calls run.  ``errors`` reads the device error word of its calls."""
 
     def __init__(self, weight: torch.Tensor, bias=None, scale=None):
         dev = _device_of(weight, "weight")
