@@ -626,6 +626,11 @@ __global__ void __launch_bounds__(kThreads, 2)
 }
 
 // ------------------------------------------------ two blocks, many tiles --
+// Lines of k up to which a tile's epilogue takes longer than its products: there the next tile's
+// gate and residual are asked for in L2 (8192 x 7168 from K = 512 with a residual 90 -> 82 us).
+// Behind longer products they come in time by themselves, and asking costs 1 %.
+constexpr int kShortLines = 18;
+
 template <int TN>
 struct Pair {
     static constexpr int kStage = kBytesW + TN / 2 * kLine;  // of one block
@@ -765,9 +770,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
             int tm, tn;
             tile_at(t, tiles_m, tiles_n, tm, tn);
             TileOut<1, kPairEpilogue> out;
-            if (t == first) tile_lines(a, tm * TN, tn * 2 * kRowsW + (int)rank * kRowsW, TN, tid);
             out.begin(a, tm * TN, tn * 2 * kRowsW + (int)rank * kRowsW, min(TN, a.M - tm * TN), w, lane);
-            if (t + step < tiles) {
+            if (kb <= kShortLines && t + step < tiles) {
                 int next_m, next_n;
                 tile_at(t + step, tiles_m, tiles_n, next_m, next_n);
                 tile_lines(a, next_m * TN, next_n * 2 * kRowsW + (int)rank * kRowsW, TN, tid);
