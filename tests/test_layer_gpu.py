@@ -473,6 +473,21 @@ def test_route_masked_experts(layer, scoring, renormalize, groups):
             assert (ids.sort(-1)[0].diff(dim=-1) > 0).all()
 
 
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("best", [1, 2])
+def test_route_infinite_biases(layer, scoring, best):
+    """Biases of +inf in more groups than are chosen, and in fewer: such groups and experts
+    are equal, by the lower index."""
+    g = rng(15)
+    logits = torch.randn(6, 96, generator=g)
+    for at in ([4, 20, 21, 38, 43, 50, 70, 77, 95], [21, 50], [90]):
+        bias = torch.randn(96, generator=g)
+        bias[at] = INF
+        for top_groups in (1, 6, 16):
+            check_route(layer, logits, min(6 * top_groups, 26), bias, scoring=scoring, groups=16,
+                        top_groups=top_groups, group_best=best)
+
+
 def test_route_agrees_with_the_plain_router(layer):
     from weight_only_int4_moe_gb300 import ops
     logits = torch.randn(300, 384, generator=rng(17)).cuda()

@@ -468,7 +468,7 @@ constexpr int kMaxStages = 12, kMaxSplit = 8;
 
 // Lines of k that one sum in tensor memory takes where the result stays fp32.  The tensor cores
 // cut a sum's last place with every instruction, 4 a line: the error of a random product,
-// relative to it, measured 1.6e-8 an instruction (K = 7168 in one sum 7e-6).  So longer products
+// relative to it, measured 1.7e-8 an instruction (K = 7168 in one sum 7.9e-6).  So longer products
 // go to several sums, which are added up in fp32.  16-bit results show it from kLongLines on
 // (2048 instructions, 3e-5: a 15th of fp16's half step).
 constexpr int kExactLines = 12, kLongLines = 512;

@@ -359,7 +359,7 @@ __global__ void __launch_bounds__(32 * kWarps, V <= 12 ? 14 : V <= 16 ? 8 : 4)
                         __ballot_sync(0xffffffffu, lane < a.groups && !(fabsf(mine - edge) > 2.0f * near));
                     if (least > kMasked) {
                         const float v = value_of(least);
-                        least = key_of(v - (unsure + 2.5e-7f * fabsf(v)));
+                        if (v < INFINITY) least = key_of(v - (unsure + 2.5e-7f * fabsf(v)));
                     }
                     least = max(least, kMasked + 1u);
                     int m = 0;
