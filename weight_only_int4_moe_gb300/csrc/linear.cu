@@ -383,7 +383,8 @@ MOE_DEV void tile_lines(const LinearArgs &a, int m0, int n0, int rows, int tid) 
     if (a.residual.p) row_lines(a.residual, m, n0, a.N);
 }
 
-// Four neighbours of a row, n..n+3 (those below N exist).
+// Four neighbours of a row, n..n+3 (those below N exist), as they lie in memory: nothing waits
+// for a load before its values are used.
 struct Quad {
     uint32_t r[4];
     MOE_DEV void load(const MatIn &s, bool vec, int m, int n, int N) {
@@ -401,17 +402,24 @@ struct Quad {
             const uint16_t *p = reinterpret_cast<const uint16_t *>(s.p) + at;
             if (vec && n + 3 < N) {
                 const uint2 v = *reinterpret_cast<const uint2 *>(p);
-                r[0] = v.x & 0xFFFFu, r[1] = v.x >> 16, r[2] = v.y & 0xFFFFu, r[3] = v.y >> 16;
+                r[0] = v.x, r[1] = v.y;
             } else {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) r[j] = n + j < N ? p[j] : 0u;
             }
         }
     }
-    MOE_DEV void get(int type, float (&f)[4]) const {
+    MOE_DEV void get(int type, bool vec, int n, int N, float (&f)[4]) const {
+        if (type == MOE_T_F32) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            f[j] = type == MOE_T_F32 ? __uint_as_float(r[j]) : from_bits16(r[j], type);
+            for (int j = 0; j < 4; ++j) f[j] = __uint_as_float(r[j]);
+        } else if (vec && n + 3 < N) {
+            f[0] = from_bits16(r[0] & 0xFFFFu, type), f[1] = from_bits16(r[0] >> 16, type);
+            f[2] = from_bits16(r[1] & 0xFFFFu, type), f[3] = from_bits16(r[1] >> 16, type);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) f[j] = from_bits16(r[j], type);
+        }
     }
 };
 
@@ -422,12 +430,12 @@ MOE_DEV void quad_out(const LinearArgs &a, int m, int n, float (&v)[4], const fl
     for (int j = 0; j < 4; ++j) v[j] = v[j] * sx * sw[j] + bias[j];
     activate<4>(a.activation, v);
     if (a.gate.p) {
-        gate.get(a.gate.type, f);
+        gate.get(a.gate.type, a.vec_gate, n, a.N, f);
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[j] *= f[j];
     }
     if (a.residual.p) {
-        residual.get(a.residual.type, f);
+        residual.get(a.residual.type, a.vec_residual, n, a.N, f);
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[j] += f[j];
     }
@@ -567,7 +575,19 @@ __global__ void __launch_bounds__(kThreads, 2)
             out.run(a, tmem, w, n_sums, tn);
         }
     } else {
+        // Of the output a warp will take a row of its block's share at a time, a lane four
+        // columns.  A row's gate and residual are asked for while the row before it is worked
+        // on, the first row's before the sums are complete.
+        const int c0 = rows * (int)rank / (int)S, c1 = rows * (int)(rank + 1) / (int)S;
+        const int n = n0 + 4 * lane;
+        Quad gate, residual;
+        const auto ask = [&](int c) {
+            if (c >= c1) return;
+            if (a.gate.p) gate.load(a.gate, a.vec_gate, m0 + c, n, a.N);
+            if (a.residual.p) residual.load(a.residual, a.vec_residual, m0 + c, n, a.N);
+        };
         if (w < kEpilogue) {
+            ask(c0 + w);
             mbar_wait(done, 0, &abort_flag, a.err);
             __syncwarp();
             tc_fence_after();
@@ -587,10 +607,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
         __syncwarp();
         cluster_sync();
-        // a warp takes a row of its block's share, a lane four columns
         if (w < kEpilogue) {
-            const int c0 = rows * (int)rank / (int)S, c1 = rows * (int)(rank + 1) / (int)S;
-            const int n = n0 + 4 * lane;
             float sw[4], bias[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -600,20 +617,19 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll 1
             for (int c = c0 + w; c < c1; c += kEpilogue) {
                 const int m = m0 + c;
-                Quad gate, residual;
-                if (a.gate.p) gate.load(a.gate, a.vec_gate, m, n, a.N);
-                if (a.residual.p) residual.load(a.residual, a.vec_residual, m, n, a.N);
                 const float sx = a.x_scale ? a.x_scale[m] : 1.0f;
                 const uint32_t at = stages + c * 512 + 16 * lane;
                 float4 p[8];
 #pragma unroll
                 for (int q = 0; q < 8; ++q)
                     if (q < S) p[q] = ld_cluster4(map_to(at, q));
+                const Quad g = gate, r = residual;
+                ask(c + kEpilogue);
                 float v[4] = {p[0].x, p[0].y, p[0].z, p[0].w};
 #pragma unroll
                 for (int q = 1; q < 8; ++q)
                     if (q < S) v[0] += p[q].x, v[1] += p[q].y, v[2] += p[q].z, v[3] += p[q].w;
-                quad_out(a, m, n, v, sw, bias, gate, residual, sx);
+                quad_out(a, m, n, v, sw, bias, g, r, sx);
             }
         }
         __syncwarp();
