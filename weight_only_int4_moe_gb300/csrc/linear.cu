@@ -32,6 +32,7 @@ constexpr int kEpilogue = 8;                // warps
 constexpr int kPairThreads = 576;           // of a pair's block: warps 0-15 epilogue, 16 copies, 17 products
 constexpr int kPairEpilogue = 16;
 constexpr int kMaxSmem = 227 * 1024 - 1024; // of a block, beside its few static bytes
+constexpr int kHalfSmem = 110 * 1024;       // where two lie on an SM
 
 MOE_DEV uint32_t cluster_rank() {
     uint32_t r;
@@ -481,8 +482,10 @@ constexpr int kMaxStages = 12, kMaxSplit = 8;
 // (2048 instructions, 3e-5: a 15th of fp16's half step).
 constexpr int kExactLines = 12, kLongLines = 512;
 
+// (Bounded as blocks of 12 warps: 10 lie on an SM's four parts as 3, 3, 2 and 2, so that of two
+// blocks with 96 registers a thread the second did not fit.)
 template <bool CODES>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(384, 2)
     linear_split_kernel(const __grid_constant__ CUtensorMap wmap,
                         const __grid_constant__ CUtensorMap xmap, const LinearArgs a, const int tn,
                         const int n_stages, const int n_sums) {
@@ -939,7 +942,7 @@ cudaError_t launch_split(const LinearArgs &a, const Operands &o, const Cut &cut,
 // sums: wanted (tensor memory bounds them)
 Cut make_cut(int tn, int split, int per_sm, int sums) {
     Cut c{tn, split, 0, std::min(sums, 512 / per_sm / tn)};
-    c.stages = (kMaxSmem / per_sm - 1024 * per_sm) / c.stage_bytes();
+    c.stages = ((per_sm == 1 ? kMaxSmem : kHalfSmem) - 1024) / c.stage_bytes();
     if (c.stages > kMaxStages) c.stages = kMaxStages;
     return c;
 }
@@ -948,12 +951,13 @@ Cut make_cut(int tn, int split, int per_sm, int sums) {
 //  - A block takes a line of k in 170 ns and 0.65 ns for each of its tn rows of x (its waits,
 //    and the copies' requests, one a row); two blocks on an SM get a row in 0.93 ns.  Rows that
 //    do not begin at multiples of 128 bytes take two requests a line: 1.4 times that.
-//  - w comes from HBM once, at 6.6 TB/s.
+//  - w comes from HBM once, at 6.6 TB/s; less by up to 6 % with the blocks that an SM could hold
+//    more.
 //  - An epilogue of two warps a quarter of the lanes takes 0.55 us for 32 rows (twice that where
 //    columns do not go in pairs); parts cost 1.2 us for the two cluster barriers, 0.12 us for
-//    32 rows to write them and 0.35 us for 8 rows of a block's share to add them up.
-//  - 2 us for the launch and the first lines, 1 us more where blocks share an SM; every further
-//    block of an SM adds 1.5 us for its own and its epilogue.
+//    32 rows to write them and 0.25 us for 8 rows of a block's share to add them up.
+//  - 2 us for the launch and the first lines; lines take 1.8 us more where blocks share an SM;
+//    every further block of an SM adds 1.5 us for its own and its epilogue.
 //  - A pair takes a line in 0.33 us (256 rows of x) or 0.22 us (128), under which runs the
 //    epilogue of the tile before, 6.2 and 3.7 us; 3 us for its start.
 struct Size {
@@ -976,8 +980,10 @@ double split_time(const Size &z, const Cut &c, int per_sm) {
     const double rows = std::min(c.tn, z.M);
     const double out = c.split == 1 ? (z.even ? 0.55 : 1.1) * std::ceil(rows / 32)
                                     : 1.2 + 0.12 * std::ceil(rows / 32) +
-                                          0.35 * std::ceil(rows / c.split / 8);
-    return 1 + per_sm + std::max(z.hbm(), waves * line * z.kb / c.split / 1000) + out +
+                                          0.25 * std::ceil(rows / c.split / 8);
+    const double idle = std::max(0.0, 1 - blocks / (z.sms * per_sm));
+    const double lines = waves * line * std::ceil((double)z.kb / c.split) / 1000 + 1.8 * (per_sm - 1);
+    return 2 + std::max(z.hbm() * (1 + 0.06 * idle), lines) + out +
            (waves - 1) * (1.5 + out);
 }
 
@@ -1014,38 +1020,38 @@ Cut best_cut(const Size &z, const int (&fits)[2][kMaxSplit + 1], double *time) {
     return best;
 }
 
-// fits of best_cut on the current device, asked once.
+// fits of best_cut on the current device, asked once.  Of two blocks an SM the clusters of one
+// are counted twice, which is never too many (asked for them, the runtime says one an SM, but
+// two do run).
 template <bool CODES>
 cudaError_t cluster_room(int (&fits)[2][kMaxSplit + 1]) {
-    static std::atomic<int> known[64][2][kMaxSplit + 1];
+    static std::atomic<int> known[64][kMaxSplit + 1];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     const bool keep = dev >= 0 && dev < 64;
-    for (int p = 0; p < 2; ++p)
-        for (int split = 1; split <= kMaxSplit; ++split) {
-            if (keep && known[dev][p][split] > 0) {
-                fits[p][split] = known[dev][p][split];
-                continue;
-            }
+    for (int split = 1; split <= kMaxSplit; ++split) {
+        int n = keep ? known[dev][split].load() : 0;
+        if (n <= 0) {
             cudaLaunchConfig_t c{};
             c.gridDim = dim3((unsigned)split);
             c.blockDim = dim3(kThreads);
-            c.dynamicSmemBytes = (size_t)(kMaxSmem / (p + 1) - 1024 * p);
+            c.dynamicSmemBytes = (size_t)kMaxSmem;
             cudaLaunchAttribute at{};
             at.id = cudaLaunchAttributeClusterDimension;
             at.val.clusterDim.x = (unsigned)split;
             at.val.clusterDim.y = at.val.clusterDim.z = 1;
             c.numAttrs = 1;
             c.attrs = &at;
-            int n = 0;
             e = cudaFuncSetAttribute(linear_split_kernel<CODES>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      kMaxSmem);
             if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&n, linear_split_kernel<CODES>, &c);
             if (e != cudaSuccess) return e;
-            fits[p][split] = n * split;
-            if (keep) known[dev][p][split] = n * split;
+            if (keep) known[dev][split] = n;
         }
+        fits[0][split] = n * split;
+        fits[1][split] = 2 * n * split;
+    }
     return cudaSuccess;
 }
 
