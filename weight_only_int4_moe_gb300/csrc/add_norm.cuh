@@ -7,7 +7,10 @@
 // elements.  Where rows begin elsewhere than at multiples of 16 bytes, but all matrices' rows
 // at the same place between two (contiguous rows of any length), the vectors lie on that grid
 // and the two at the row's ends are moved by elements (ENDS; single elements throughout took
-// 90 instructions each: 4096 rows of 4095 70 us).  What is left goes by single elements.
+// 90 instructions each: 4096 rows of 4095 70 us, now 36).  What is left goes by single elements.
+//
+// Measured: 8192 rows of 7168 bf16 with a residual 75 us, 6.2 TB/s of the 6.8 that a copy reaches;
+// 2048 rows of 4096, fp32 into a bf16 stream, with codes 16.4 us (5.6 TB/s); one row 2.9 us.
 //
 // An 8-bit code is decided by y to the last bit wherever y / scale lies next to the middle
 // of two codes, and y by the sum of squares.  So the sum must not depend on how a row is

@@ -12,6 +12,10 @@
 // formed in fp32, whose error against the real number is bounded (`unsure`); where two
 // neighbours in the order are nearer to each other than that, the candidates are compared
 // again in 64 bits.  That is seldom: the 9 gaps of a top-8 choice are some 1e-2 wide.
+//
+// Measured: 8192 tokens of 384 experts, sigmoid and bias, 13.7 us, of them 2 for the dozen near
+// ties (each 1 to 2 us of 64-bit latency in one warp); 1130 instructions a token, 58 % of the issue
+// slots.  One token 3.1 us.  4096 tokens, 4 of 8 groups of 32: 12 us.
 #include <cfloat>
 
 #include "layer.cuh"
