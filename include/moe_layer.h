@@ -78,8 +78,10 @@ int moe_add_norm(const void *x, int x_type, int64_t x_stride, const void *residu
  * Out: out       [M][N] of out_type (those three); may be gate or residual itself
  *                where type and stride are the same, must not overlap x or w
  * Products are added up in fp32 by the tensor cores, the epilogue is fp32, and the
- * result is rounded once.  The order of the sum depends on the sizes only, so the same
- * call gives the same bits.
+ * result is rounded once.  Where the result stays fp32 (or K is beyond 32 768 two-byte
+ * elements) long sums are made of parts of 768 elements (1536 codes), since the tensor
+ * cores cut a sum's last place again and again.  The order of the sum depends on the
+ * sizes, types and alignments only, so the same call gives the same bits.
  * x and w: rows begin at multiples of 16 bytes (pointers 16-byte aligned, strides
  * multiples of 16 bytes); K itself may be any number.  The others need their type's
  * alignment only.  err: device uint32 or NULL; MOE_DEVERR_TIMEOUT is set where a wait

@@ -303,6 +303,31 @@ def test_linear_most_rows(layer):
     assert ((got.double() - want).abs() <= bound).all() and lin.errors() == 0
 
 
+def test_offsets_beyond_32_bits(layer):
+    """Matrices of more than 2^31 elements: the last rows are those of a small call."""
+    g = torch.Generator("cuda").manual_seed(5)
+    m, h = 540_000, 4096  # 2.2e9 elements
+    tail = slice(m - 40, m)
+    x = torch.zeros(m, h, dtype=BF16, device="cuda")
+    r = torch.zeros(m, h, dtype=BF16, device="cuda")
+    x[tail], r[tail] = torch.randn(40, h, generator=g, device="cuda"), torch.randn(40, h, generator=g, device="cuda")
+    got = layer.moe_add_norm(x, None, r, codes=True, residual_out=r)
+    again = layer.moe_add_norm(r[tail], out_dtype=BF16, codes=True)
+    assert torch.equal(got.out[tail], again.out) and torch.equal(got.scales[tail], again.scales)
+    assert torch.equal(got.codes.view(torch.uint8)[tail], again.codes.view(torch.uint8))
+    assert not got.out[:8].any() and not got.codes.view(torch.uint8)[m // 2].any()
+    del got, r
+    w = torch.randn(4200, 64, generator=g, device="cuda").to(BF16)
+    lin = layer.Linear(w)
+    out = layer.moe_linear(x[:, :64], lin, residual=None)  # rows 8 KB apart, 2.27e9 results
+    assert torch.equal(out[tail], layer.moe_linear(x[tail, :64].contiguous(), lin))
+    del out
+    ids, wts = layer.moe_route_experts(x[:, :1024], 4)  # rows of a wider matrix
+    one = layer.moe_route_experts(x[tail, :1024].contiguous(), 4)
+    assert torch.equal(ids[tail], one[0]) and torch.equal(wts[tail], one[1])
+    assert lin.errors() == 0
+
+
 def test_first_calls_in_a_capture():
     """Nothing that a kernel's first call sets up keeps it out of a captured graph."""
     import os
