@@ -29,7 +29,7 @@ SOURCES = ["abi.cu", "align.cu", "pack.cu", "gemm.cu", "noalloc.cu", "ep.cu", "g
            "layer_abi.cu", "add_norm.cu", "add_norm_bf16.cu", "add_norm_f16.cu",
            "add_norm_f32.cu", "linear.cu", "router.cu"]
 HEADERS = ["common.cuh", "kernels.cuh", "dequant.cuh", "gemv.cuh", "kv4.cuh", "kv4_launch.cuh",
-           "layer.cuh", "add_norm.cuh"]
+           "layer.cuh", "add_norm.cuh", "device.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
               "--expt-relaxed-constexpr", "-I" + os.path.join(ROOT, "include")]

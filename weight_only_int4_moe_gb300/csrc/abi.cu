@@ -12,6 +12,7 @@
 #include <utility>
 
 #include "moe_int4.h"
+#include "device.cuh"
 #include "kernels.cuh"
 #include "gemv.cuh"
 

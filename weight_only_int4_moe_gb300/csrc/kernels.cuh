@@ -26,15 +26,6 @@ inline unsigned pdl_attr(cudaLaunchAttribute &a) {
     return 1;
 }
 
-// SM count of the current device; MOE_ERR_UNSUPPORTED unless it is sm_103.
-int device_sms(int *sms);
-// The driver's tensor map encoder (NULL if it has none).
-typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
-                                  const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
-                                  const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-EncodeTiledFn encode_fn();
-
 struct AlignArgs {
     const int32_t *ids;    // [P]
     int P, E, block_m;

@@ -6,6 +6,7 @@
 #include <cmath>
 #include <cstdlib>
 
+#include "device.cuh"
 #include "kv4_launch.cuh"
 
 using namespace moe;
