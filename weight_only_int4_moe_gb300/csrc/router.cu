@@ -9,9 +9,12 @@
 //
 // Which experts are chosen must not depend on how an exponential was rounded.  Without a bias
 // the scores order as the logits do, and the logits are the keys.  With one, c = s + bias is
-// formed in fp32, whose error against the real number is bounded (`unsure`); where two
-// neighbours in the order are nearer to each other than that, the candidates are compared
-// again in 64 bits.  That is seldom: the 9 gaps of a top-8 choice are some 1e-2 wide.
+// formed in fp32, whose error against the real number is bounded (`unsure`, and c's own
+// rounding); where two neighbours in the order are nearer to each other than that, the
+// candidates are compared again in 64 bits.  That is seldom: the 9 gaps of a top-8 choice are
+// some 1e-2 wide.  A group's sum of two c is off by the roundings of its terms, which may be far
+// larger than the sum (biases of either sign).  So each group has a bound of its own, and the
+// groups whose intervals reach the border between chosen and other ones are compared in 64 bits.
 //
 // Measured: 8192 tokens of 384 experts, sigmoid and bias, 13.7 us, of them 2 for the dozen near
 // ties (each 1 to 2 us of 64-bit latency in one warp); 1130 instructions a token, 58 % of the issue
@@ -134,18 +137,18 @@ __device__ __noinline__ int order_exactly(const RouteExpertsArgs &a, int64_t row
     return list[lane];
 }
 
-// The groups of a token where some lie too near to the border for fp32: lane g has group g's
-// value, and for the groups in `close` the best experts' c are formed in 64 bits: lane j < n
-// has one, expert e.  -> the chosen groups.
+// The groups of a token where fp32 leaves some open: `surely` are chosen, and of those in `close`
+// the best, by their best experts' c in 64 bits: lane j < n has one, expert e.  -> the chosen
+// groups.
 __device__ __noinline__ uint32_t groups_exactly(const RouteExpertsArgs &a, int64_t row, int lane, int n,
-                                                int e, float value, uint32_t close) {
+                                                int e, uint32_t surely, uint32_t close) {
     double top, inv;
     softmax_exactly(a, row, lane, top, inv);
     const double c = lane < n ? score_exactly(a, row, e, top, inv) : -INFINITY;
     const int mine = lane < n ? e / (a.E / a.groups) : -1;
-    double of_group = (double)value;
-    for (; close; close &= close - 1) {
-        const int g = __ffs(close) - 1;
+    double of_group = -INFINITY;
+    for (uint32_t left = close; left; left &= left - 1) {
+        const int g = __ffs(left) - 1;
         double x = mine == g ? c : -INFINITY, y = -INFINITY;  // the two best
 #pragma unroll
         for (int o = 16; o; o >>= 1) {
@@ -156,8 +159,13 @@ __device__ __noinline__ uint32_t groups_exactly(const RouteExpertsArgs &a, int64
         }
         if (lane == g) of_group = a.group_best == 2 && y > -INFINITY ? x + y : x;
     }
-    double gap, edge;
-    return choose_groups(a, of_group, lane, gap, edge);
+    int before = __popc(surely);
+    for (uint32_t left = close; left; left &= left - 1) {
+        const int g = __ffs(left) - 1;
+        const double o = __shfl_sync(0xffffffffu, of_group, g);
+        before += o > of_group || (o == of_group && g < lane);
+    }
+    return surely | __ballot_sync(0xffffffffu, ((close >> lane) & 1u) && before < a.top_groups);
 }
 
 // The whole choice in 64 bits; c: room for E numbers.  -> the lane's expert.
@@ -313,7 +321,7 @@ __global__ void __launch_bounds__(32 * kWarps, V <= 12 ? 14 : V <= 16 ? 8 : 4)
             key[i] = lane + 32 * i < a.E ? key_of(c) : kGone;
         }
         if (a.groups > 1) {
-            float mine = -INFINITY;
+            float mine = -INFINITY, slack = 0.0f;  // lane g: group g's value, and a bound on its error
             uint32_t least = kMasked;  // the last of the group's experts that count
             // the warp's two best of a group -> its value, in lane g
             auto value = [&](int g, uint32_t x, uint32_t y) {
@@ -324,8 +332,14 @@ __global__ void __launch_bounds__(32 * kWarps, V <= 12 ? 14 : V <= 16 ? 8 : 4)
                     second = __popc(who) > 1 ? best : __reduce_max_sync(0xffffffffu, x == best ? y : x);
                 }
                 if (lane == g) least = sums ? second : best;
-                if (lane == g && best > kMasked)
-                    mine = second > kMasked ? value_of(best) + value_of(second) : value_of(best);
+                if (lane == g && best > kMasked) {
+                    const float b = value_of(best), s = second > kMasked ? value_of(second) : 0.0f;
+                    // (a sum of numbers beyond fp32 is unsure, not infinite)
+                    mine = b < INFINITY ? fminf(fmaxf(b + s, -FLT_MAX), FLT_MAX) : b;
+                    // two scores; the roundings of the two c, of their sum and of the interval's ends
+                    // below, each 2^-24 of the terms at most
+                    slack = b < INFINITY ? unsure + 2e-7f * (fabsf(b) + fabsf(s)) : 0.0f;
+                }
             };
             if (size % 32 == 0) {
                 // a group is some of every lane's registers
@@ -357,10 +371,24 @@ __global__ void __launch_bounds__(32 * kWarps, V <= 12 ? 14 : V <= 16 ? 8 : 4)
             uint32_t open = choose_groups(a, mine, lane, gap, edge);
             if (KEYS != kLogits) {
                 // (-inf: fewer groups than that have an expert left)
-                const float near = 2.0f * unsure + 2.5e-7f * fabsf(edge);
-                if (!(gap > near) && edge > -INFINITY) {
-                    const uint32_t close =
-                        __ballot_sync(0xffffffffu, lane < a.groups && !(fabsf(mine - edge) > 2.0f * near));
+                const float most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(slack)));
+                uint32_t surely = 0, close = 0;
+                if (!(gap > 2.0f * most) && edge > -INFINITY) {
+                    // which groups surely are among the best, and which surely are not
+                    const bool finite = fabsf(mine) < INFINITY;
+                    const float lo = finite ? fmaxf(mine - slack, -FLT_MAX) : mine;
+                    const float hi = finite ? fminf(mine + slack, FLT_MAX) : mine;
+                    int may = 0, must = 0;  // groups that may, and that must, be before this one
+                    for (int g = 0; g < a.groups; ++g) {
+                        const float h = __shfl_sync(0xffffffffu, hi, g), l = __shfl_sync(0xffffffffu, lo, g);
+                        may += h >= lo ? 1 : 0;  // (itself among them)
+                        must += l > hi ? 1 : 0;
+                    }
+                    surely = __ballot_sync(0xffffffffu, lane < a.groups && may <= a.top_groups);
+                    close = __ballot_sync(0xffffffffu,
+                                          lane < a.groups && may > a.top_groups && must < a.top_groups);
+                }
+                if (close) {
                     if (least > kMasked) {
                         const float v = value_of(least);
                         if (v < INFINITY) least = key_of(v - (unsure + 2.5e-7f * fabsf(v)));
@@ -377,7 +405,7 @@ __global__ void __launch_bounds__(32 * kWarps, V <= 12 ? 14 : V <= 16 ? 8 : 4)
                     }
                     __syncwarp();
                     if (m <= 32)
-                        open = groups_exactly(a, t, lane, m, lane < m ? (int)list[lane].y : 0, mine, close);
+                        open = groups_exactly(a, t, lane, m, lane < m ? (int)list[lane].y : 0, surely, close);
                     else
                         sure = false;
                     __syncwarp();
