@@ -53,8 +53,10 @@ extern "C" {
  * rounded to one at the end: total * fp32(1/hidden), + eps, square root, reciprocal,
  * h * that, * weight; for the codes y * (1 / scale) with scale = max|y| * fp32(1/448).
  * Rows whose sum leaves fp32 (values beyond 1e18, or tiny ones with eps = 0) are added
- * up in 64 bits.  A row that holds NaN becomes NaN; one that holds an infinity (and no
- * NaN) becomes 0, and NaN where the infinity was.  max|y| does not count NaN.
+ * up in 64 bits, and where 1 / sqrt leaves it too, multiplied by a power of two first.  A
+ * row of zeros with eps = 0 becomes NaN (0 / 0).  A row that holds NaN becomes NaN; one
+ * that holds an infinity (and no NaN) becomes 0, and NaN where the infinity was.  max|y|
+ * does not count NaN.
  * Sizes: 0 <= rows <= 1<<20, 1 <= hidden <= 32768, 0 <= eps (finite).  Pointers need
  * their type's alignment only; rows that all begin at multiples of 16 bytes are
  * faster.  Errors: MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_ALIGN, MOE_ERR_UNSUPPORTED,

@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(MAX, 1024 / MAX) add_norm_kernel(const AddNorm
     }
     // the compensation of an infinite or NaN sum is NaN: the sum itself counts then
     const float total = fabsf(t.hi) <= FLT_MAX ? __fadd_rn(t.hi, t.lo) : t.hi;
-    float q;
+    float q, up = 1.0f;
     if (!(total < 1e37f) || (total < 1e-30f && a.eps < 1e-24f)) {
         // squares beyond fp32, or below it with nothing added to them
         double d = 0.0;
@@ -324,7 +324,13 @@ __global__ void __launch_bounds__(MAX, 1024 / MAX) add_norm_kernel(const AddNorm
 #pragma unroll
             for (int o = 16; o; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
         }
-        q = (float)(1.0 / sqrt(d / H + (double)a.eps));
+        // 1 / sqrt is a normal number for root mean squares between 2^-100 and 2^100.  Rows
+        // beyond them come to the middle by a power of two, which costs their elements nothing
+        // that y could show.
+        const double ms = d / H + (double)a.eps;
+        if (ms > 0.0 && ms < 0x1p-200) up = 0x1p96f;
+        if (ms > 0x1p200 && ms < INFINITY) up = 0x1p-32f;
+        q = (float)(1.0 / (sqrt(ms) * (double)up));
     } else {
         q = __frcp_rn(__fsqrt_rn(__fadd_rn(__fmul_rn(total, a.inv_hidden), a.eps)));
     }
@@ -341,7 +347,7 @@ __global__ void __launch_bounds__(MAX, 1024 / MAX) add_norm_kernel(const AddNorm
             if (a.weight) weights.get(a, i, p, f);
 #pragma unroll
             for (int j = 0; j < VEC; ++j) {
-                y[i][j] = __fmul_rn(__fmul_rn(h[i].get(j), q), f[j]);
+                y[i][j] = __fmul_rn(__fmul_rn(__fmul_rn(h[i].get(j), up), q), f[j]);
                 // (NaN is not counted, nor what lies beyond the row's ends: 0 times an
                 // infinite 1 / sqrt is NaN)
                 top = fmaxf(top, fabsf(y[i][j]));
