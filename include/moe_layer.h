@@ -28,8 +28,8 @@ extern "C" {
 /* Activations of moe_linear. */
 #define MOE_ACT_NONE 0
 #define MOE_ACT_RELU 1 /* max(y, 0); NaN stays NaN */
-#define MOE_ACT_SILU 2 /* y / (1 + e^-y) */
-#define MOE_ACT_GELU 3 /* y (1 + erf(y / sqrt 2)) / 2 */
+#define MOE_ACT_SILU 2 /* y / (1 + e^-y); 0 below -88.7, where e^-y leaves fp32 */
+#define MOE_ACT_GELU 3 /* y (1 + erf(y / sqrt 2)) / 2, within 2^-23 |y| where 1 + erf cancels */
 
 /* Scores of moe_route_experts. */
 #define MOE_SCORE_SOFTMAX 0
