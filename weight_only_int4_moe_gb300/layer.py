@@ -15,7 +15,7 @@ from typing import NamedTuple
 import torch
 
 from . import ops
-from .kv4 import _empty, _like, _raw_stream
+from .kv4 import _INT_MAX, _empty, _like, _raw_stream
 
 MOE_T_BF16 = 0
 MOE_T_F32 = 1
@@ -120,6 +120,8 @@ def moe_add_norm(x, weight=None, residual=None, eps: float = 1e-6, out_dtype=tor
         raise ValueError(f"x: expected [rows, hidden], got {tuple(x.shape)}")
     shape = x.shape
     rows, hidden = shape
+    if rows > _INT_MAX or hidden > _INT_MAX:
+        raise ValueError(f"x: {tuple(shape)} is too large")
     xp, xt, xs = _matrix(x, "x", dev, shape, _TYPES)
     rp, rt, rs, np_, ns = None, 0, 0, None, hidden
     if residual is not None:
@@ -178,6 +180,8 @@ class Linear:
             raise ValueError(f"weight: expected [N, K], got {tuple(weight.shape)}")
         self.weight, self.index, self.device = weight, dev, weight.device
         self.N, self.K = weight.shape
+        if self.N > _INT_MAX or self.K > _INT_MAX:
+            raise ValueError(f"weight: {tuple(weight.shape)} is too large")
         self.ptr, self.type, self.stride = _matrix(weight, "weight", dev, weight.shape, _OPERANDS)
         self.dtype = weight.dtype
         self.scale, self.scale_ptr, self.bias, self.bias_ptr = scale, None, None, None
@@ -215,6 +219,8 @@ def moe_linear(x, linear: Linear, activation=None, gate=None, residual=None, x_s
     if x.dtype is not linear.dtype:
         raise TypeError(f"x: expected {linear.dtype}, got {x.dtype}")
     m = x.shape[0]
+    if m > _INT_MAX:
+        raise ValueError(f"x: {tuple(x.shape)} is too large")
     act = ACTIVATIONS.get(activation)
     if act is None:
         raise ValueError(f"activation: {activation!r} is not one of {list(ACTIVATIONS)}")
@@ -251,6 +257,12 @@ def moe_route_experts(logits, top_k: int, scoring: str = "softmax", bias=None, g
     if logits.dim() != 2:
         raise ValueError(f"logits: expected [M, E], got {tuple(logits.shape)}")
     m, e = shape = logits.shape
+    top_groups = groups if top_groups is None else top_groups
+    if m > _INT_MAX or e > _INT_MAX:
+        raise ValueError(f"logits: {tuple(shape)} is too large")
+    how = (top_k, groups, top_groups, group_best)
+    if max(how) > _INT_MAX or min(how) < -_INT_MAX:
+        raise ValueError(f"(top_k, groups, top_groups, group_best): {how} is out of range")
     kind = SCORES.get(scoring)
     if kind is None:
         raise ValueError(f"scoring: {scoring!r} is not one of {list(SCORES)}")
@@ -265,9 +277,9 @@ def moe_route_experts(logits, top_k: int, scoring: str = "softmax", bias=None, g
         topk_weights = _empty(size, _F32, logits.device, stream)
     else:
         _like(topk_weights, "topk_weights", dev, _F32, size)
-    args = (lp, lt, ls, bp, m, e, top_k, kind, groups, groups if top_groups is None else top_groups,
-            group_best, 1 if renormalize else 0, scale, topk_ids.data_ptr(),
-            topk_weights.data_ptr(), _raw_stream(stream, dev))
+    args = (lp, lt, ls, bp, m, e, top_k, kind, groups, top_groups, group_best,
+            1 if renormalize else 0, scale, topk_ids.data_ptr(), topk_weights.data_ptr(),
+            _raw_stream(stream, dev))
     _call((_lib or load_library()).moe_route_experts, "moe_route_experts", dev, args)
     return topk_ids, topk_weights
 
