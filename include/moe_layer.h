@@ -31,6 +31,12 @@ extern "C" {
 #define MOE_ACT_SILU 2 /* y / (1 + e^-y); 0 below -88.7, where e^-y leaves fp32 */
 #define MOE_ACT_GELU 3 /* y (1 + erf(y / sqrt 2)) / 2, within 2^-23 |y| where 1 + erf cancels */
 
+/* Kernels of moe_linear. */
+#define MOE_LINEAR_SPLIT 1          /* a tile a cluster, whose blocks share the sum */
+#define MOE_LINEAR_PAIRS_128 2      /* tiles of 256 x 128 on two SMs */
+#define MOE_LINEAR_PAIRS_128_SUMS 3 /* the same, with the sum in parts */
+#define MOE_LINEAR_PAIRS_256 4      /* tiles of 256 x 256 on two SMs */
+
 /* Scores of moe_route_experts. */
 #define MOE_SCORE_SOFTMAX 0
 #define MOE_SCORE_SIGMOID 1
@@ -97,6 +103,10 @@ int moe_linear(const void *x, int64_t x_stride, const float *x_scale, const void
                const void *residual, int residual_type, int64_t residual_stride, void *out,
                int out_type, int64_t out_stride, int M, int N, int K, uint32_t *err,
                moe_stream_t stream);
+
+/* The kernel that this thread's last moe_linear launched (sizes, types and alignments decide);
+ * 0: none yet. */
+int moe_linear_last_kernel(void);
 
 /*
  * moe_route_experts: the experts of each token and their weights.

@@ -80,6 +80,7 @@ cudaError_t launch_add_norm(AddNormArgs a, int sms, cudaStream_t s);
 // cudaErrorNotSupported: the operands' tensor maps could not be made.
 cudaError_t launch_linear(LinearArgs a, const void *x, int64_t x_stride, const void *w,
                           int64_t w_stride, int sms, cudaStream_t s);
+int linear_last_kernel();
 cudaError_t launch_route_experts(const RouteExpertsArgs &a, int sms, cudaStream_t s);
 
 }  // namespace moe

@@ -120,6 +120,8 @@ int moe_linear(const void *x, int64_t x_stride, const float *x_scale, const void
     return done(launch_linear(a, x, x_stride, w, w_stride, sms, str(stream)));
 }
 
+int moe_linear_last_kernel(void) { return linear_last_kernel(); }
+
 int moe_route_experts(const void *logits, int type, int64_t stride, const float *bias, int M,
                       int E, int top_k, int scoring, int groups, int top_groups, int group_best,
                       int renormalize, float scale, int32_t *topk_ids, float *topk_weights,

@@ -902,6 +902,8 @@ cudaError_t prepare(K kernel, int smem, std::atomic<int> *known, int *n, int pai
     return cudaSuccess;
 }
 
+thread_local int last_kernel = 0;  // MOE_LINEAR_*
+
 template <int TN, bool CODES, bool LONG>
 cudaError_t launch_pair(const LinearArgs &a, const Operands &o, cudaStream_t s) {
     using T = Pair<TN>;
@@ -918,7 +920,10 @@ cudaError_t launch_pair(const LinearArgs &a, const Operands &o, cudaStream_t s) 
     cudaLaunchAttribute at{};
     c.numAttrs = pdl_attr(at);
     c.attrs = &at;
-    return cudaLaunchKernelEx(&c, linear_pair_kernel<TN, CODES, LONG>, wmap, xmap, a);
+    e = cudaLaunchKernelEx(&c, linear_pair_kernel<TN, CODES, LONG>, wmap, xmap, a);
+    if (e == cudaSuccess)
+        last_kernel = TN == 256 ? MOE_LINEAR_PAIRS_256 : LONG ? MOE_LINEAR_PAIRS_128_SUMS : MOE_LINEAR_PAIRS_128;
+    return e;
 }
 
 template <bool CODES>
@@ -942,7 +947,9 @@ cudaError_t launch_split(const LinearArgs &a, const Operands &o, const Cut &cut,
     at[1].val.clusterDim.x = (unsigned)cut.split;
     at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     c.attrs = at;
-    return cudaLaunchKernelEx(&c, linear_split_kernel<CODES>, wmap, xmap, a, cut.tn, cut.stages, cut.sums);
+    e = cudaLaunchKernelEx(&c, linear_split_kernel<CODES>, wmap, xmap, a, cut.tn, cut.stages, cut.sums);
+    if (e == cudaSuccess) last_kernel = MOE_LINEAR_SPLIT;
+    return e;
 }
 
 // sums: wanted (tensor memory bounds them)
@@ -1120,6 +1127,8 @@ bool together(const void *p, int64_t stride, int type, int rows, int count) {
 }
 
 }  // namespace
+
+int linear_last_kernel() { return last_kernel; }
 
 cudaError_t launch_linear(LinearArgs a, const void *x, int64_t x_stride, const void *w,
                           int64_t w_stride, int sms, cudaStream_t s) {

@@ -24,7 +24,9 @@ MOE_T_E4M3 = 3
 ACTIVATIONS = {"none": 0, None: 0, "relu": 1, "silu": 2, "gelu": 3}
 SCORES = {"softmax": 0, "sigmoid": 1}
 
-EXPORTED = ["moe_add_norm", "moe_linear", "moe_route_experts"]
+KERNELS = {0: None, 1: "split", 2: "pairs_128", 3: "pairs_128_sums", 4: "pairs_256"}  # of moe_linear
+
+EXPORTED = ["moe_add_norm", "moe_linear", "moe_linear_last_kernel", "moe_route_experts"]
 
 _TYPES = {torch.bfloat16: MOE_T_BF16, torch.float32: MOE_T_F32, torch.float16: MOE_T_F16}
 _OPERANDS = {torch.bfloat16: MOE_T_BF16, torch.float16: MOE_T_F16,
@@ -43,6 +45,7 @@ def load_library():
             "moe_add_norm": ([p, i, i64, p, i, i64, p, i, f, i, i, p, i64, p, i, i64, p, i64, p, p], i),
             "moe_linear": ([p, i64, p, p, i64, p, i, p, i, p, i, i64, p, i, i64, p, i, i64, i, i, i, p,
                             p], i),
+            "moe_linear_last_kernel": ([], i),
             "moe_route_experts": ([p, i, i64, p, i, i, i, i, i, i, i, i, f, p, p, p], i),
         }
         for name, (args, res) in sig.items():
@@ -243,6 +246,11 @@ def moe_linear(x, linear: Linear, activation=None, gate=None, residual=None, x_s
             _raw_stream(stream, dev))
     _call((_lib or load_library()).moe_linear, "moe_linear", dev, args)
     return out
+
+
+def moe_linear_last_kernel() -> str | None:
+    """Which of its kernels (KERNELS) this thread's last moe_linear launched."""
+    return KERNELS[(_lib or load_library()).moe_linear_last_kernel()]
 
 
 def moe_route_experts(logits, top_k: int, scoring: str = "softmax", bias=None, groups: int = 1,
