@@ -412,22 +412,21 @@ cudaError_t by_size(const AddNormArgs &a, Grid grid, int sms, cudaStream_t s) {
     // fp32 rows take twice the registers: two loads (8192 rows of 7168 fp32 with an fp32 residual
     // 117 us, four 157)
     constexpr bool kWide = TS != kNone && (TX == MOE_T_F32 || TS == MOE_T_F32);
+    constexpr int kLoads = kWide ? 2 : 4, kMost = 8192 / (8 * kLoads);
     if (grid == Grid::kVectors) {
         if (a.hidden <= 8192) {
             if (a.hidden <= 1024 || a.rows <= 2 * sms) return launch<TX, TS, 8, 1, 1024, false>(a, s);
-            return kWide ? launch<TX, TS, 8, 2, 512, false>(a, s) : launch<TX, TS, 8, 4, 256, false>(a, s);
+            return launch<TX, TS, 8, kLoads, kMost, false>(a, s);
         }
         return launch<TX, TS, 8, 4, 1024, false>(a, s);
     }
     if (grid == Grid::kEnds) {
-        if (a.hidden <= 8184)
-            return kWide ? launch<TX, TS, 8, 2, 512, true>(a, s) : launch<TX, TS, 8, 4, 256, true>(a, s);
+        if (a.hidden <= 8184) return launch<TX, TS, 8, kLoads, kMost, true>(a, s);
         if (a.hidden <= 32760) return launch<TX, TS, 8, 4, 1024, true>(a, s);
     }
     if (a.hidden <= 4096) return launch<TX, TS, 1, 8, 512, false>(a, s);
     return launch<TX, TS, 1, 32, 1024, false>(a, s);
 }
-
 
 }  // namespace
 
