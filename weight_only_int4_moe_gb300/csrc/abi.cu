@@ -231,30 +231,7 @@ Plan make_plan(int M, const moe_int4_shape *sh) {
     return p;
 }
 
-struct DeviceInfo {
-    int sms = 0;
-    int ok = -1;  // -1 unknown, 0 unsupported, 1 sm_103
-};
 std::mutex g_mu;
-DeviceInfo g_dev[64];
-
-int device_info(int *sms) {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MOE_ERR_CUDA;
-    std::lock_guard<std::mutex> lk(g_mu);
-    DeviceInfo &d = g_dev[dev];
-    if (d.ok < 0) {
-        int major = 0, minor = 0;
-        if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-            cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
-            cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-            return MOE_ERR_CUDA;
-        d.ok = (major == 10 && minor == 3) ? 1 : 0;
-    }
-    if (!d.ok) return MOE_ERR_UNSUPPORTED;
-    *sms = d.sms;
-    return MOE_OK;
-}
 
 // Tensor map over fp16 rows [rows][cols] (bucketed x or the intermediate), box
 // = 64 columns x BM rows, 128-byte swizzle (the MMA's K-major B layout).
@@ -440,7 +417,7 @@ int forward_impl(const uint16_t *x, const void *w13_packed, const void *w13_scal
     const Plan pl = make_plan(M, shape);
     if (workspace_bytes < pl.total) return MOE_ERR_WORKSPACE;
     int sms = 0;
-    rc = device_info(&sms);
+    rc = device_sms(&sms);
     if (rc != MOE_OK) return rc;
     const int grid = sms < kMaxGrid ? sms : kMaxGrid;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -706,7 +683,7 @@ int moe_route(const float *router_logits, int M, int E, int top_k, int32_t *topk
     if (M == 0) return MOE_OK;
     if (!router_logits || !topk_ids || !topk_weights) return MOE_ERR_NULL;
     int sms = 0;
-    const int rc = device_info(&sms);
+    const int rc = device_sms(&sms);
     if (rc != MOE_OK) return rc;
     RouteArgs ra{};
     ra.logits = router_logits;
