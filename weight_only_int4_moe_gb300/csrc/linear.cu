@@ -857,9 +857,16 @@ bool rows_map(CUtensorMap *m, const void *p, int64_t stride, int rows, int K, in
     const CUtensorMapDataType t = type == MOE_T_BF16  ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                   : type == MOE_T_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                                       : CU_TENSOR_MAP_DATA_TYPE_UINT8;
-    return fn(m, t, 2, const_cast<void *>(p), dims, &pitch, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    const auto encode = [&] {
+        return fn(m, t, 2, const_cast<void *>(p), dims, &pitch, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    };
+    if (encode()) return true;
+    // The driver wants a current context, which a thread does not have before its first call
+    // that needs one; this one may be its first.
+    int dev = 0;
+    return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess && encode();
 }
 
 // What a launch needs to know of the operands.
