@@ -261,6 +261,14 @@ def moe_align_noalloc(topk_ids: torch.Tensor, E: int, block_m: int, out=None, st
 
 
 # ----------------------------------------------------------------- forward --
+def _room(M, shape, x, out, topk_ids, topk_weights):
+    """Refuses tensors that hold less than a forward of M tokens reads or writes."""
+    for t, n, what in ((x, shape.hidden, "x"), (out, shape.hidden, "out"), (topk_ids, shape.top_k, "topk_ids"),
+                       (topk_weights, shape.top_k, "topk_weights")):
+        if t.numel() < M * n:
+            raise ValueError(f"{what}: expected {M} rows of {n}, got {tuple(t.shape)}")
+
+
 def moe_int4_workspace_bytes(M: int, shape: Shape, flags: int = 0) -> int:
     return load_library().moe_int4_workspace_bytes(M, ctypes.byref(shape), flags)
 
@@ -313,6 +321,7 @@ def moe_int4_forward(x, w13_packed, w13_scales, w2_packed, w2_scales, topk_ids, 
         out = torch.empty((M, shape.hidden), dtype=shape.torch_out_dtype, device=x.device)
     if out.dtype != shape.torch_out_dtype:
         raise TypeError(f"out must be {shape.torch_out_dtype}")
+    _room(M, shape, x, out, topk_ids, topk_weights)
     if workspace is None:
         workspace = alloc_workspace(M, shape, device=x.device)
     with _on(x, w13_packed, w13_scales, w2_packed, w2_scales, topk_ids, topk_weights, out,
@@ -392,6 +401,9 @@ def moe_int4_forward_routed(x, w13, w13_scales, w2, w2_scales, router_logits, sh
         topk_ids = torch.empty((M, shape.top_k), dtype=torch.int32, device=dev)
     if topk_weights is None:
         topk_weights = torch.empty((M, shape.top_k), dtype=torch.float32, device=dev)
+    _room(M, shape, x, out, topk_ids, topk_weights)
+    if router_logits.numel() < M * shape.E:
+        raise ValueError(f"router_logits: expected {M} rows of {shape.E}, got {tuple(router_logits.shape)}")
     if workspace is None:
         workspace = alloc_workspace(M, shape, device=dev)
     with _on(x, w13, w13_scales, w2, w2_scales, router_logits, topk_ids, topk_weights, out,
