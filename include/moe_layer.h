@@ -55,8 +55,8 @@ extern "C" {
  *      codes     e4m3 codes of y / scale, nearest even, with one scale for each row:
  *                scales[row] = max(max|y| / 448, 2^-100); both NULL: not wanted
  * Everything is fp32 with each operation rounded on its own.  The sum of squares is
- * held in two fp32 numbers, so that it does not depend on the order of its parts, and
- * rounded to one at the end: total * fp32(1/hidden), + eps, square root, reciprocal,
+ * held in two fp32 numbers (some 45 bits) and rounded to one at the end, so that the order
+ * of its parts shows in about one row of a million, whose sum lies next to a rounding: total * fp32(1/hidden), + eps, square root, reciprocal,
  * h * that, * weight; for the codes y * (1 / scale) with scale = max|y| * fp32(1/448).
  * Rows whose sum leaves fp32 (values beyond 1e18, or tiny ones with eps = 0) are added
  * up in 64 bits, and where 1 / sqrt leaves it too, multiplied by a power of two first.  A

@@ -10,12 +10,14 @@
 // 90 instructions each: 4096 rows of 4095 70 us, now 36).  What is left goes by single elements.
 //
 // Measured: 8192 rows of 7168 bf16 with a residual 75 us, 6.2 TB/s of the 6.8 that a copy reaches;
-// 2048 rows of 4096, fp32 into a bf16 stream, with codes 16.4 us (5.6 TB/s); one row 2.9 us.
+// 2048 rows of 4096, fp32 into a bf16 stream, with codes 16.5 us (5.6 TB/s); one row 2.9 us.
 //
 // An 8-bit code is decided by y to the last bit wherever y / scale lies next to the middle
-// of two codes, and y by the sum of squares.  So the sum must not depend on how a row is
+// of two codes, and y by the sum of squares.  So the sum should not depend on how a row is
 // cut into threads: it is held as a number and its rounding error (two-sum: the error of an
-// addition is itself an fp32 number), some 45 bits in all, and rounded once at the end.
+// addition is itself an fp32 number), some 45 bits in all, and rounded once at the end.  One
+// row in a million or fewer then has another sum than 64 bits give (measured: 1 of 3.1 million
+// rows of 4096), where the sum lies next to the middle of two fp32 numbers.
 #pragma once
 
 #include <cfloat>
@@ -404,6 +406,10 @@ cudaError_t launch(const AddNormArgs &a, cudaStream_t s) {
     return cudaLaunchKernelEx(&c, add_norm_kernel<TX, TS, VEC, NV, MAX, ENDS>, a);
 }
 
+// Rows beyond 8192 take 1024 threads with 64 registers each, which spill 32 to 376 bytes a thread
+// (2048 rows of 16384 with a residual: bf16 47 us, 5.8 TB/s; fp32 96, 4.9 TB/s; bf16 with codes
+// 53), as do the kernels without vectors (up to 684).
+//
 // Loads of a thread: one for short rows and for a row or two an SM, where the latency counts;
 // else four, so that more rows are in flight on an SM (8192 rows of 7168 bf16 with a residual:
 // 132 us with one, 91 with two, 75 with four).

@@ -15,11 +15,11 @@
 // tile's k and add their parts up through distributed shared memory, in the order of the
 // blocks: no workspace, and the same bits every time.
 //
-// What bounds them: a few tokens the weights' way from HBM (1 x 7168 x 7168 18.3 us, 5.6 TB/s of
-// the 6.8 that a copy reaches), sizes between a block's stages (a 128-byte row is one request of
-// the copy engine: about 100 GB/s a block; 256 x 2048 x 7168 13.2 us), large products the tensor
-// cores (8192 x 7168 x 7168 438 us, 1920 TFLOP/s, where cuBLAS reached 1951 at 8192^3; in a row
-// the power cap, 520 us).
+// What bounds them: a few tokens the weights' way from HBM (1 x 7168 x 7168 18.2 us, 5.7 TB/s of
+// the 6.7 that a copy reaches), sizes between a block's stages (a 128-byte row is one request of
+// the copy engine: about 100 GB/s a block; 256 x 2048 x 7168 with SiLU and gate 14.5 us, 13.2 with
+// the weights in L2), large products the tensor cores (8192 x 7168 x 7168 427 us, 1970 TFLOP/s,
+// where cuBLAS reached 1929 at 8192^3; in a row the power cap, 500 us).
 #include <algorithm>
 #include <atomic>
 #include <cmath>
