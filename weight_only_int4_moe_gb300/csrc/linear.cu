@@ -519,7 +519,11 @@ __global__ void __launch_bounds__(384, 2)
     // The first lines of w come to L2 while the previous kernel ends.
     if (w == 8 && lane < n_stages && kb0 + lane < kb1) prefetch_2d(&wmap, (kb0 + lane) * kElems, n0);
     // Tensor memory is taken behind the previous kernel, whose blocks may still want theirs, and
-    // before the next one may start.
+    // before the next one may start.  Kernels of other streams do not want it beside this one: two
+    // blocks of this kernel take 256 columns each where they share an SM, and for any other kernel
+    // that has tensor memory an SM has too few registers left (the expert GEMMs 768 x 80, the
+    // prefill attention 896 x 72) or too little shared memory (pairs).  A block that waited for
+    // columns while its cluster waits for it could wait for ever.
     pdl_wait();
     if (w == 9) {
         tmem_alloc(smem_u32(&tmem_slot), cols);
